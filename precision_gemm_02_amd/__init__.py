@@ -332,3 +332,14 @@ def gemm(A, B, C, alpha=1.0, beta=0.0, stream=None):
     else:
         raise ValueError("A, B and C must share one layout")
     return C
+
+
+# The layer operators (include/pgemm_layers.h)
+from . import layer_ops as _layer_ops  # noqa: E402
+
+_layer_ops._bind(_lib, _check)
+from .layer_ops import (  # noqa: E402,F401
+    combine, combine_backward, expert_linear, expert_linear_backward,
+    expert_linear_backward_workspace, linear, linear_backward, linear_backward_workspace,
+    linear_workspace, route, route_backward, route_workspace)
+LAYER_EXPORTS = _layer_ops.EXPORTS

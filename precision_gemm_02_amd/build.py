@@ -1,4 +1,4 @@
-"""Build libpgemm.so from csrc/ with hipcc for gfx950.
+"""Build libpgemm.so from csrc/ and layers/ with hipcc for gfx950.
 
 Each .hip file is compiled to an object in parallel, then linked into one
 shared library next to this file.  Usage: ``python precision_gemm_02_amd/build.py``
@@ -18,7 +18,10 @@ CSRC = os.path.join(HERE, "csrc")
 INCLUDE = os.path.join(os.path.dirname(HERE), "include")
 BUILD_DIR = os.path.join(HERE, "_build")
 LIB_PATH = os.path.join(HERE, "libpgemm.so")
-SOURCES = ["api.hip", "sgemm.hip", "dgemm.hip"]
+LAYERS = os.path.join(HERE, "layers")
+SOURCES = [os.path.join(CSRC, f) for f in ("api.hip", "sgemm.hip", "dgemm.hip")] + [
+    os.path.join(LAYERS, f)
+    for f in ("layers_api.hip", "prod_f32.hip", "prod_f16.hip", "prod_bf16.hip")]
 ARCH = "gfx950"
 
 HIPCC = os.environ.get("HIPCC", shutil.which("hipcc") or "/opt/rocm/bin/hipcc")
@@ -27,15 +30,15 @@ CFLAGS = [
     "-ffp-contract=fast",
     # never emit packed fp32 VALU ops (v_pk_*_f32)
     "-Xclang", "-target-feature", "-Xclang", "-packed-fp32-ops",
-    "-I" + CSRC, "-I" + INCLUDE,
+    "-I" + CSRC, "-I" + LAYERS, "-I" + INCLUDE,
     "-Wall", "-Wno-unused-result",
 ]
 
 
 def source_digest(extra_flags=()) -> str:
-    """sha256 (first 16 hex digits) of what determines the built kernels: the
-    compiler flags and the bytes of every file under csrc/ and of the public
-    header.  Unlike a hash of libpgemm.so it does not depend on the directory
+    """sha256 (first 16 hex digits) of what determines the built matrix-multiply
+    kernels: the compiler flags and the bytes of every file under csrc/ and of
+    pgemm.h (the layer operators are compiled apart, from layers/).  Unlike a hash of libpgemm.so it does not depend on the directory
     the library is built in (hipcc derives per-file symbols from the path)."""
     import hashlib
     h = hashlib.sha256()
@@ -52,8 +55,9 @@ def source_digest(extra_flags=()) -> str:
 
 
 def _compile(src: str, extra) -> str:
-    obj = os.path.join(BUILD_DIR, os.path.splitext(src)[0] + ".o")
-    cmd = [HIPCC, *CFLAGS, *extra, "-c", os.path.join(CSRC, src), "-o", obj]
+    name = os.path.splitext(os.path.basename(src))[0]
+    obj = os.path.join(BUILD_DIR, name + ".o")
+    cmd = [HIPCC, *CFLAGS, *extra, "-c", src, "-o", obj]
     proc = subprocess.run(cmd, capture_output=True, text=True)
     noise = "is not a recognized feature for this target"
     err = "\n".join(ln for ln in proc.stderr.splitlines() if noise not in ln)

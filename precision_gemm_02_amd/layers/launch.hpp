@@ -1,0 +1,42 @@
+// Internal: what the entry points launch.  One translation unit per element
+// type compiles its kernels (prod_f32.hip, prod_f16.hip, prod_bf16.hip).
+#pragma once
+
+#include <hip/hip_runtime.h>
+
+#include "prod.hpp"
+#include "rows.hpp"
+#include "route.hpp"
+
+namespace pgemm {
+namespace layers {
+
+// The tile classes and the few-rows kernels of the products.
+enum Kernel { kTile256 = 0, kTile128 = 1, kTile64 = 2, kFew16 = 3, kFew32 = 4 };
+
+struct KernelShape {
+  int bm, bn;
+};
+constexpr KernelShape kShape[3] = {{256, 256}, {128, 128}, {64, 64}};
+
+// Columns of a workgroup of the few-rows kernels.
+constexpr int few_columns(int lb) { return lb == kInner ? 16 : 64; }
+
+struct TypeOps {
+  hipError_t (*prod)(const ProdArgs& a, int la, int lb, int mode, int kernel, bool direct,
+                     hipStream_t s);
+  hipError_t (*slope)(const SlopeArgs& a, int groups, hipStream_t s);
+  hipError_t (*column_sum)(const float* partial, void* out, int n, int groups, int chunks,
+                           int out32, hipStream_t s);
+  hipError_t (*combine)(const CombineArgs& a, hipStream_t s);
+  hipError_t (*combine_back)(const CombineBackArgs& a, hipStream_t s);
+  hipError_t (*route)(const RouteArgs& a, hipStream_t s);
+  hipError_t (*route_back)(const RouteBackArgs& a, hipStream_t s);
+};
+
+const TypeOps& ops_f32();
+const TypeOps& ops_f16();
+const TypeOps& ops_bf16();
+
+}  // namespace layers
+}  // namespace pgemm

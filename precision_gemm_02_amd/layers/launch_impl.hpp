@@ -1,0 +1,141 @@
+// Internal: the launches of one element type (included by prod_*.hip).
+#pragma once
+
+#include "launch.hpp"
+#include "prod_rows.hpp"
+#include "prod_tile.hpp"
+
+namespace pgemm {
+namespace layers {
+namespace {
+
+template <typename A>
+hipError_t launch(void (*kernel)(const A), dim3 grid, int threads, const A& a, hipStream_t s) {
+  A copy = a;
+  void* args[] = {&copy};
+  return hipLaunchKernel(reinterpret_cast<const void*>(kernel), grid, dim3(threads), args, 0, s);
+}
+
+template <typename T, int LA, int LB, int BM, int BN, int WGM, int WGN, bool DIRECT, int MODE>
+hipError_t launch_tile(const ProdArgs& a, hipStream_t s) {
+  long long tiles = (long long)a.tiles_m * a.tiles_n;
+  if (MODE == kSums) tiles *= a.groups;
+  return launch(&prod_tile_kernel<T, LA, LB, BM, BN, WGM, WGN, DIRECT, MODE>,
+                dim3((unsigned)tiles, MODE == kDense ? (unsigned)a.splits : 1), WGM * WGN * 64, a,
+                s);
+}
+
+template <typename T, int LA, int LB, int MODE>
+hipError_t prod_tile(const ProdArgs& a, int kernel, bool direct, hipStream_t s) {
+  if constexpr (sizeof(T) == 2) {
+    if (kernel == kTile256 && direct) return launch_tile<T, LA, LB, 256, 256, 2, 4, true, MODE>(a, s);
+  }
+  if (kernel == kTile128)
+    return direct ? launch_tile<T, LA, LB, 128, 128, 2, 2, true, MODE>(a, s)
+                  : launch_tile<T, LA, LB, 128, 128, 2, 2, false, MODE>(a, s);
+  if (kernel == kTile64)
+    return direct ? launch_tile<T, LA, LB, 64, 64, 2, 2, true, MODE>(a, s)
+                  : launch_tile<T, LA, LB, 64, 64, 2, 2, false, MODE>(a, s);
+  return hipErrorInvalidValue;
+}
+
+template <typename T, int LB, int MODE>
+hipError_t prod_few(const ProdArgs& a, int kernel, hipStream_t s) {
+  const dim3 grid((unsigned)(MODE == kRows ? a.tiles_n * a.groups : a.tiles_n),
+                  MODE == kDense ? (unsigned)a.splits : 1);
+  if (kernel == kFew16) return launch(&prod_rows_kernel<T, LB, 1, MODE>, grid, 512, a, s);
+  return launch(&prod_rows_kernel<T, LB, 2, MODE>, grid, 512, a, s);
+}
+
+template <typename T>
+hipError_t prod(const ProdArgs& a, int la, int lb, int mode, int kernel, bool direct,
+                hipStream_t s) {
+  hipError_t e;
+  const bool few = kernel >= kFew16;
+  if (mode == kDense) {
+    if (few)
+      e = lb == kInner ? prod_few<T, kInner, kDense>(a, kernel, s)
+                       : prod_few<T, kOuter, kDense>(a, kernel, s);
+    else if (la == kOuter)
+      e = prod_tile<T, kOuter, kOuter, kDense>(a, kernel, direct, s);
+    else
+      e = lb == kInner ? prod_tile<T, kInner, kInner, kDense>(a, kernel, direct, s)
+                       : prod_tile<T, kInner, kOuter, kDense>(a, kernel, direct, s);
+    if (e == hipSuccess && a.splits > 1) {
+      const long long items = (long long)a.M * ((a.N + 7) / 8);
+      e = launch(&prod_reduce_kernel<T>, dim3((unsigned)((items + 255) / 256)), 256, a, s);
+    }
+    return e;
+  }
+  if (mode == kRows) {
+    if (few)
+      return lb == kInner ? prod_few<T, kInner, kRows>(a, kernel, s)
+                          : prod_few<T, kOuter, kRows>(a, kernel, s);
+    return lb == kInner ? prod_tile<T, kInner, kInner, kRows>(a, kernel, direct, s)
+                        : prod_tile<T, kInner, kOuter, kRows>(a, kernel, direct, s);
+  }
+  return prod_tile<T, kOuter, kOuter, kSums>(a, kernel, direct, s);
+}
+
+template <typename T>
+hipError_t slope(const SlopeArgs& a, int groups, hipStream_t s) {
+  const unsigned cols = (unsigned)((a.n + a.tpr * 8 - 1) / (a.tpr * 8));
+  return launch(&slope_kernel<T>, dim3(cols, (unsigned)a.chunks, (unsigned)groups), 256, a, s);
+}
+
+template <typename T>
+hipError_t column_sum(const float* partial, void* out, int n, int groups, int chunks, int out32,
+                      hipStream_t s) {
+  void* args[] = {&partial, &out, &n, &chunks, &out32};
+  return hipLaunchKernel(reinterpret_cast<const void*>(&column_sum_kernel<T>),
+                         dim3((unsigned)((n + 255) / 256), (unsigned)groups), dim3(256), args, 0, s);
+}
+
+template <typename T>
+hipError_t combine(const CombineArgs& a, hipStream_t s) {
+  const int tpb = 256 / a.tpr;
+  return launch(&combine_kernel<T>,
+                dim3((unsigned)((a.m + tpb - 1) / tpb),
+                     (unsigned)((a.n + a.tpr * 8 - 1) / (a.tpr * 8))),
+                256, a, s);
+}
+
+template <typename T>
+hipError_t combine_back(const CombineBackArgs& a, hipStream_t s) {
+  const long long waves = (long long)a.m * a.top;
+  return launch(&combine_back_kernel<T>, dim3((unsigned)((waves + 3) / 4)), 256, a, s);
+}
+
+template <typename T>
+hipError_t route(const RouteArgs& a, hipStream_t s) {
+  const dim3 grid((unsigned)a.blocks);
+  hipError_t e;
+  if (a.experts <= 64) e = launch(&route_kernel<T, 1>, grid, 1024, a, s);
+  else if (a.experts <= 128) e = launch(&route_kernel<T, 2>, grid, 1024, a, s);
+  else if (a.experts <= 256) e = launch(&route_kernel<T, 4>, grid, 1024, a, s);
+  else e = launch(&route_kernel<T, 16>, grid, 1024, a, s);
+  if (e != hipSuccess || a.blocks == 1) return e;
+  e = launch(&route_sum_kernel<T>, dim3((unsigned)a.experts), 64, a, s);
+  if (e != hipSuccess) return e;
+  return launch(&route_place_kernel<T>, grid, 1024, a, s);
+}
+
+template <typename T>
+hipError_t route_back(const RouteBackArgs& a, hipStream_t s) {
+  const dim3 grid((unsigned)((a.m + 3) / 4));
+  if (a.experts <= 64) return launch(&route_back_kernel<T, 1>, grid, 256, a, s);
+  if (a.experts <= 128) return launch(&route_back_kernel<T, 2>, grid, 256, a, s);
+  if (a.experts <= 256) return launch(&route_back_kernel<T, 4>, grid, 256, a, s);
+  return launch(&route_back_kernel<T, 16>, grid, 256, a, s);
+}
+
+template <typename T>
+const TypeOps& type_ops() {
+  static const TypeOps ops = {&prod<T>,         &slope<T>, &column_sum<T>, &combine<T>,
+                              &combine_back<T>, &route<T>, &route_back<T>};
+  return ops;
+}
+
+}  // namespace
+}  // namespace layers
+}  // namespace pgemm

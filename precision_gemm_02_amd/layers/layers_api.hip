@@ -1,0 +1,632 @@
+// C ABI of the layer operators: argument checks, the choice of kernels and
+// their launches.  Declarations and the contract are in pgemm_layers.h.
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include "launch.hpp"
+#include "pgemm_layers.h"
+
+namespace pgemm {
+namespace layers {
+namespace {
+
+constexpr int kUnits = 256;                       // compute units of an MI355X
+constexpr long long kMaxGrid = 1LL << 24;         // workgroups in one launch
+
+int size_of(int dtype) { return dtype == PGEMM_F32 ? 4 : 2; }
+bool known(int dtype) { return dtype == PGEMM_F32 || dtype == PGEMM_F16 || dtype == PGEMM_BF16; }
+
+const TypeOps& ops_of(int dtype) {
+  return dtype == PGEMM_F32 ? ops_f32() : dtype == PGEMM_F16 ? ops_f16() : ops_bf16();
+}
+
+bool kind_ok(const pgemm_kind& k) {
+  return known(k.dtype) && (k.out_dtype == k.dtype || k.out_dtype == PGEMM_F32) &&
+         k.act >= PGEMM_ACT_NONE && k.act <= PGEMM_ACT_SILU;
+}
+
+long long ceil_div(long long a, long long b) { return (a + b - 1) / b; }
+long long round_up(long long a, long long b) { return ceil_div(a, b) * b; }
+size_t align256(size_t b) { return (b + 255) & ~(size_t)255; }
+
+bool aligned_to(const void* p, int bytes) {
+  return reinterpret_cast<uintptr_t>(p) % (unsigned)bytes == 0;
+}
+
+// A matrix of `cols` columns that the call touches (need) or may touch.
+bool rows_ok(const pgemm_rows& x, int cols, int size, bool need) {
+  if (x.data == nullptr) return !need;
+  return aligned_to(x.data, size) && x.ld >= (cols > 1 ? cols : 1);
+}
+bool weight_ok(const pgemm_weight& w, int k, int n, int size, bool need, int experts) {
+  if (w.data == nullptr) return !need;
+  if (w.order != PGEMM_KN && w.order != PGEMM_NK) return false;
+  const int cols = w.order == PGEMM_KN ? n : k, rows = w.order == PGEMM_KN ? k : n;
+  if (!aligned_to(w.data, size) || w.ld < (cols > 1 ? cols : 1)) return false;
+  if (experts <= 1) return true;
+  return w.stride >= (rows > 0 ? (long long)(rows - 1) * w.ld + cols : 0);
+}
+bool vector_ok(const void* p, int size, bool need) {
+  return p == nullptr ? !need : aligned_to(p, size);
+}
+
+// offsets are read by a call that touches anything (need).
+bool plan_ok(const pgemm_plan& p, int rows, bool need) {
+  return p.experts >= 1 && p.experts <= kMaxExperts && vector_ok(p.offsets, 4, need) &&
+         vector_ok(p.tokens, 4, false) && p.x_rows >= 0 &&
+         (p.tokens != nullptr || p.x_rows >= rows);
+}
+
+// ---- the choice of a product's kernel ----------------------------------------
+
+struct Plan {
+  int kernel = kTile64;
+  int splits = 1;
+  int k_split = 0;
+  bool direct = false;
+};
+
+bool operand_direct(const void* p, long long ld, int size, int inner, long long stride) {
+  const int v = 16 / size;
+  return aligned_to(p, 16) && ld % v == 0 && inner % v == 0 && stride % v == 0;
+}
+
+// Sustained rate of one compute unit's tiles (flop/s) and the fixed time of a
+// tile (seconds), by class.
+double class_rate(int kernel, int size) {
+  static const double r16[3] = {1.1e15, 0.85e15, 0.4e15};
+  static const double r32[3] = {0, 130e12, 100e12};
+  return (size == 2 ? r16[kernel] : r32[kernel]) / kUnits;
+}
+
+// Splits of the summed index that give every compute unit about `want`
+// workgroups, each at least `least` inner indices (multiples of `unit`).
+int split_for(long long wgs, long long want, int k, int least) {
+  long long s = want / (wgs > 0 ? wgs : 1);
+  if (s > k / least) s = k / least;
+  if (s > 64) s = 64;
+  return s < 1 ? 1 : (int)s;
+}
+
+// rows: the rows of D that one launch expects per group (an average; any
+// distribution is correct).
+Plan plan_product(int size, int la, int lb, int mode, long long rows, int groups, int n, int k,
+                  bool direct, size_t ws_bytes, bool any_ws) {
+  Plan p;
+  p.direct = direct;
+  const int bk = 128 / size;
+  const long long per = mode == kRows ? ceil_div(rows, groups > 0 ? groups : 1) : rows;
+  if (la == kInner && per <= 32) {
+    // Few rows: B is read once, the rest is latency.  The few-rows kernel
+    // takes 16 or 32 rows per pass and never needs a tile of operands.
+    p.kernel = per <= 16 ? kFew16 : kFew32;
+    if (mode == kDense) {
+      const int cols = few_columns(lb);
+      p.splits = split_for(ceil_div(n, cols), 2 * kUnits, k, 8 * bk);
+    }
+  } else {
+    double best = 0;
+    for (int c = 0; c < 3; ++c) {
+      if (c == kTile256 && (size == 4 || !direct)) continue;
+      const int bm = kShape[c].bm, bn = kShape[c].bn;
+      const int co = c == kTile256 ? 1 : c == kTile128 ? 2 : 4;   // workgroups that share a unit
+      long long tiles = ceil_div(n, bn);
+      if (mode == kRows) tiles *= ceil_div(rows, bm) + (groups < rows ? groups : rows) / 2;
+      else tiles *= ceil_div(rows, bm);
+      if (mode == kSums) tiles *= groups;
+      const double depth = mode == kSums ? (double)k / (groups > 0 ? groups : 1) : (double)k;
+      int s = 1;
+      if (mode == kDense && tiles < kUnits) s = split_for(tiles, kUnits * co, k, 4 * bk);
+      const double waves = (double)ceil_div(tiles * s, kUnits);
+      double t = waves * (2.0 * bm * bn * (depth / s) / class_rate(c, size)) +
+                 (double)ceil_div(tiles * s, kUnits * co) * 2e-6;
+      if (s > 1) t += 3e-6 + (double)s * (double)rows * n * 8 / 4e12;
+      if (best == 0 || t < best) {
+        best = t;
+        p.kernel = c;
+        p.splits = s;
+      }
+    }
+  }
+  if (p.splits > 1) {
+    p.k_split = (int)round_up(ceil_div(k, p.splits), bk);
+    p.splits = (int)ceil_div(k, p.k_split);
+    const size_t need = (size_t)p.splits * (size_t)rows * (size_t)n * 4;
+    if (!any_ws && ws_bytes < need) p.splits = 1;
+  }
+  return p;
+}
+
+// Workspace that plan_product may use for a dense product, over any alignment.
+size_t split_bytes(int size, int la, int lb, int rows, int n, int k) {
+  size_t most = 0;
+  for (int d = 0; d < 2; ++d) {
+    const Plan p = plan_product(size, la, lb, kDense, rows, 1, n, k, d != 0, 0, true);
+    const size_t b = p.splits > 1 ? (size_t)p.splits * (size_t)rows * (size_t)n * 4 : 0;
+    if (b > most) most = b;
+  }
+  return most;
+}
+
+// Fill in what depends on the plan and launch.  `rows` as in plan_product.
+int run_product(ProdArgs a, int dtype, int la, int lb, int mode, long long rows, void* ws,
+                size_t ws_bytes, hipStream_t s) {
+  const int size = size_of(dtype);
+  const bool direct =
+      operand_direct(a.A, a.lda, size, la == kInner ? (mode == kSums ? 0 : a.K) : a.M, 0) &&
+      operand_direct(a.B, a.ldb, size, lb == kInner ? a.K : a.N, mode == kRows ? a.strideB : 0);
+  const Plan p = plan_product(size, la, lb, mode, rows, a.groups, a.N, mode == kSums ? a.rows : a.K,
+                              direct, ws == nullptr ? 0 : ws_bytes, false);
+  a.splits = p.splits;
+  a.k_split = p.k_split;
+  a.partial = static_cast<float*>(ws);
+  if (p.kernel >= kFew16) {
+    a.tiles_m = 1;
+    a.tiles_n = (int)ceil_div(a.N, few_columns(lb));
+  } else {
+    const int bm = kShape[p.kernel].bm;
+    long long tm = ceil_div(rows, bm);
+    if (mode == kRows) tm += a.groups < rows ? a.groups : rows;   // partly filled tiles
+    a.tiles_m = (int)tm;
+    a.tiles_n = (int)ceil_div(a.N, kShape[p.kernel].bn);
+  }
+  if ((long long)a.tiles_m * a.tiles_n * (a.groups > 0 ? a.groups : 1) > kMaxGrid)
+    return PGEMM_EHIP;
+  return ops_of(dtype).prod(a, la, lb, mode, p.kernel, p.direct, s) == hipSuccess ? PGEMM_OK
+                                                                                : PGEMM_EHIP;
+}
+
+// Threads per row of a row-wise kernel with 8 columns per thread.
+int threads_per_row(int n, int most) {
+  int t = 1;
+  while (t < most && t * 8 < n) t *= 2;
+  return t;
+}
+
+// Row chunks per group of the slope kernel: enough workgroups for every
+// compute unit, at least 16 rows of an average group each.
+int slope_chunks(long long rows, int groups, int n) {
+  if (n < 1) return 1;
+  const long long cols = ceil_div(n, threads_per_row(n, 64) * 8);
+  long long c = 4 * kUnits / (cols * groups);
+  const long long most = ceil_div(ceil_div(rows, groups), 16);
+  if (c > most) c = most;
+  return c < 1 ? 1 : (int)c;
+}
+
+// The parts of a backward call's workspace: dZ, then partial sums (column sums
+// of the bias gradient, then the products' splits, one after the other in
+// stream order).
+struct BackSpace {
+  size_t dz = 0, rest = 0;
+  long long ldz = 0;
+  int chunks = 1;
+  size_t total() const { return dz + rest; }
+};
+
+BackSpace back_space(const pgemm_kind& kind, long long rows, int n, int k, int groups) {
+  BackSpace b;
+  const int size = size_of(kind.dtype);
+  b.ldz = round_up(n, 8);
+  if (kind.act != PGEMM_ACT_NONE) b.dz = align256((size_t)rows * (size_t)b.ldz * (size_t)size);
+  if (rows < 1) rows = 1;
+  b.chunks = slope_chunks(rows, groups, n);
+  b.rest = (size_t)groups * (size_t)b.chunks * (size_t)n * 4;
+  if (groups == 1 && rows <= INT32_MAX) {
+    for (int lb = 0; lb < 2; ++lb) {
+      const size_t x = split_bytes(size, kInner, lb, (int)rows, k, n);
+      if (x > b.rest) b.rest = x;
+    }
+    const size_t w = split_bytes(size, kOuter, kOuter, k, n, (int)rows),
+                 v = split_bytes(size, kOuter, kOuter, n, k, (int)rows);
+    if (w > b.rest) b.rest = w;
+    if (v > b.rest) b.rest = v;
+  }
+  b.rest = align256(b.rest);
+  return b;
+}
+
+// dZ (or dY itself) and the bias gradient, then the two products.
+struct BackArgs {
+  pgemm_kind kind;
+  int rows, n, k, groups;
+  const int* offsets;
+  const int* tokens;
+  int x_rows;
+  pgemm_rows dY, Z, X, dX;
+  pgemm_weight W, dW;
+  void* dbias;
+};
+
+int run_backward(const BackArgs& b, void* ws, const BackSpace& space, hipStream_t s) {
+  const TypeOps& ops = ops_of(b.kind.dtype);
+  const bool grouped = b.offsets != nullptr;
+  char* base = static_cast<char*>(ws);
+  void* rest = base + space.dz;
+  const void* dz = b.dY.data;
+  long long ldz = b.dY.ld;
+  const bool slope = b.kind.act != PGEMM_ACT_NONE && (b.dX.data != nullptr || b.dW.data != nullptr);
+  const bool out32 = b.kind.out_dtype == PGEMM_F32;
+  if (slope || b.dbias != nullptr) {
+    SlopeArgs a{};
+    a.dY = b.dY.data;
+    a.ldy = b.dY.ld;
+    if (b.kind.act != PGEMM_ACT_NONE) {
+      a.Z = b.Z.data;
+      a.ldz = b.Z.ld;
+      a.dZ = base;
+      a.ldd = space.ldz;
+      dz = base;
+      ldz = space.ldz;
+    }
+    a.n = b.n;
+    a.act = b.kind.act;
+    a.offsets = b.offsets;
+    a.rows = b.rows;
+    a.chunks = space.chunks;
+    a.tpr = threads_per_row(b.n, 64);
+    a.partial = b.dbias != nullptr ? static_cast<float*>(rest) : nullptr;
+    if (ops.slope(a, b.groups, s) != hipSuccess) return PGEMM_EHIP;
+    if (b.dbias != nullptr &&
+        ops.column_sum(a.partial, b.dbias, b.n, b.groups, a.chunks, out32, s) != hipSuccess)
+      return PGEMM_EHIP;
+  }
+  if (b.dX.data != nullptr && b.rows > 0 && b.k > 0) {
+    ProdArgs a{};
+    a.A = dz;
+    a.lda = ldz;
+    a.B = b.W.data;
+    a.ldb = b.W.ld;
+    a.strideB = b.W.stride;
+    a.D = b.dX.data;
+    a.ldd = b.dX.ld;
+    a.out32 = b.kind.dtype == PGEMM_F32;
+    a.M = b.rows;
+    a.N = b.k;
+    a.K = b.n;
+    a.offsets = b.offsets;
+    a.groups = grouped ? b.groups : 0;
+    a.rows = b.rows;
+    const int st = run_product(a, b.kind.dtype, kInner, b.W.order == PGEMM_KN ? kInner : kOuter,
+                               grouped ? kRows : kDense, b.rows, rest, space.rest, s);
+    if (st != PGEMM_OK) return st;
+  }
+  if (b.dW.data != nullptr && b.k > 0 && b.n > 0) {
+    ProdArgs a{};
+    const bool kn = b.dW.order == PGEMM_KN;
+    a.A = kn ? b.X.data : dz;
+    a.lda = kn ? b.X.ld : ldz;
+    a.B = kn ? dz : b.X.data;
+    a.ldb = kn ? ldz : b.X.ld;
+    a.gather = kn ? b.tokens : nullptr;
+    a.gather_b = kn ? nullptr : b.tokens;
+    a.gather_rows = b.x_rows;
+    a.D = const_cast<void*>(b.dW.data);
+    a.ldd = b.dW.ld;
+    a.strideD = b.dW.stride;
+    a.out32 = out32;
+    a.M = kn ? b.k : b.n;
+    a.N = kn ? b.n : b.k;
+    a.K = b.rows;
+    a.offsets = b.offsets;
+    a.groups = grouped ? b.groups : 0;
+    a.rows = b.rows;
+    const int st = run_product(a, b.kind.dtype, kOuter, kOuter, grouped ? kSums : kDense, a.M,
+                               rest, space.rest, s);
+    if (st != PGEMM_OK) return st;
+  }
+  return PGEMM_OK;
+}
+
+}  // namespace
+}  // namespace layers
+}  // namespace pgemm
+
+using namespace pgemm::layers;
+
+extern "C" {
+
+int pgemm_linear(pgemm_kind kind, int m, int n, int k, pgemm_rows X, pgemm_weight W,
+                 const void* bias, pgemm_rows residual, pgemm_rows Z, pgemm_rows Y,
+                 void* workspace, size_t workspace_bytes, void* stream) {
+  if (!kind_ok(kind)) return -1;
+  if (m < 0) return -2;
+  if (n < 0) return -3;
+  if (k < 0) return -4;
+  const bool touch = m > 0 && n > 0, read = touch && k > 0;
+  const int size = size_of(kind.dtype), osize = size_of(kind.out_dtype);
+  if (!rows_ok(X, k, size, read)) return -5;
+  if (!weight_ok(W, k, n, size, read, 1)) return -6;
+  if (!vector_ok(bias, size, false)) return -7;
+  if (!rows_ok(residual, n, osize, false)) return -8;
+  if (!rows_ok(Z, n, size, false)) return -9;
+  if (!rows_ok(Y, n, osize, touch)) return -10;
+  if (workspace != nullptr && !aligned_to(workspace, 16)) return -11;
+  if (!touch) return PGEMM_OK;
+  ProdArgs a{};
+  a.A = X.data;
+  a.lda = X.ld;
+  a.B = W.data;
+  a.ldb = W.ld;
+  a.D = Y.data;
+  a.ldd = Y.ld;
+  a.M = m;
+  a.N = n;
+  a.K = k;
+  a.bias = bias;
+  a.R = residual.data;
+  a.ldr = residual.ld;
+  a.Z = Z.data;
+  a.ldz = Z.ld;
+  a.act = kind.act;
+  a.out32 = kind.out_dtype == PGEMM_F32;
+  return run_product(a, kind.dtype, kInner, W.order == PGEMM_KN ? kOuter : kInner, kDense, m,
+                     workspace, workspace_bytes, static_cast<hipStream_t>(stream));
+}
+
+size_t pgemm_linear_workspace(int dtype, int m, int n, int k) {
+  if (!known(dtype) || m <= 0 || n <= 0 || k <= 0) return 0;
+  const size_t a = split_bytes(size_of(dtype), kInner, kInner, m, n, k);
+  const size_t b = split_bytes(size_of(dtype), kInner, kOuter, m, n, k);
+  return a > b ? a : b;
+}
+
+int pgemm_linear_backward(pgemm_kind kind, int m, int n, int k, pgemm_rows dY, pgemm_rows Z,
+                          pgemm_rows X, pgemm_weight W, pgemm_rows dX, pgemm_weight dW,
+                          void* dbias, void* workspace, size_t workspace_bytes, void* stream) {
+  if (!kind_ok(kind)) return -1;
+  if (m < 0) return -2;
+  if (n < 0) return -3;
+  if (k < 0) return -4;
+  const int size = size_of(kind.dtype), osize = size_of(kind.out_dtype);
+  const bool read = m > 0 && n > 0;
+  if (!rows_ok(dY, n, size, read)) return -5;
+  if (!rows_ok(Z, n, size, read && kind.act != PGEMM_ACT_NONE)) return -6;
+  if (!rows_ok(X, k, size, read && k > 0 && dW.data != nullptr)) return -7;
+  if (!weight_ok(W, k, n, size, read && k > 0 && dX.data != nullptr, 1)) return -8;
+  if (!rows_ok(dX, k, size, false)) return -9;
+  if (!weight_ok(dW, k, n, osize, false, 1)) return -10;
+  if (!vector_ok(dbias, osize, false)) return -11;
+  const BackSpace space = back_space(kind, m, n, k, 1);
+  if (space.total() > 0 && (workspace == nullptr || !aligned_to(workspace, 16))) return -12;
+  if (workspace_bytes < space.total()) return -13;
+  if (n == 0) {
+    // no columns: dX is a sum of nothing
+    if (dX.data == nullptr || m == 0 || k == 0) return PGEMM_OK;
+  }
+  BackArgs b{kind, m, n, k, 1, nullptr, nullptr, 0, dY, Z, X, dX, W, dW, n > 0 ? dbias : nullptr};
+  if (n == 0) b.kind.act = PGEMM_ACT_NONE;
+  return run_backward(b, workspace, space, static_cast<hipStream_t>(stream));
+}
+
+size_t pgemm_linear_backward_workspace(pgemm_kind kind, int m, int n, int k) {
+  if (!kind_ok(kind) || m < 0 || n <= 0 || k < 0) return 0;
+  return back_space(kind, m, n, k, 1).total();
+}
+
+int pgemm_route(int dtype, int m, int experts, int top, int score, int groups, int top_groups,
+                int renorm, float scale, pgemm_rows logits, const float* bias, pgemm_route_out out,
+                void* workspace, size_t workspace_bytes, void* stream) {
+  if (!known(dtype)) return -1;
+  if (m < 0 || m > (1 << 30) / kMaxTop) return -2;
+  if (experts < 1 || experts > kMaxExperts) return -3;
+  if (top < 1 || top > kMaxTop || top > experts) return -4;
+  if (score != PGEMM_SOFTMAX && score != PGEMM_SIGMOID) return -5;
+  if (groups < 1 || groups > 64 || experts % groups != 0) return -6;
+  if (top_groups < 1 || top_groups > groups) return -7;
+  if (top > experts / groups * top_groups) return -4;
+  if (!rows_ok(logits, experts, size_of(dtype), m > 0)) return -10;
+  if (!vector_ok(bias, 4, false)) return -11;
+  if (!vector_ok(out.offsets, 4, true)) return -12;
+  if (!vector_ok(out.weights, 4, m > 0) || !vector_ok(out.expert_index, 4, m > 0) ||
+      !vector_ok(out.tokens, 4, m > 0) || !vector_ok(out.slots, 4, m > 0))
+    return -12;
+  const size_t need = pgemm_route_workspace(m, experts, top);
+  if (need > 0 && (workspace == nullptr || !aligned_to(workspace, 16))) return -13;
+  if (workspace_bytes < need) return -14;
+  RouteArgs a{};
+  a.logits = logits.data;
+  a.ld = logits.ld;
+  a.bias = bias;
+  a.m = m;
+  a.experts = experts;
+  a.top = top;
+  a.score = score;
+  a.groups = groups;
+  a.top_groups = top_groups;
+  a.renorm = renorm != 0;
+  a.scale = scale;
+  a.weights = out.weights;
+  a.index = out.expert_index;
+  a.offsets = out.offsets;
+  a.tokens = out.tokens;
+  a.slots = out.slots;
+  a.blocks = m > 0 ? (int)ceil_div(m, kRouteTokens) : 1;
+  a.counts = static_cast<int*>(workspace);
+  a.totals = a.counts == nullptr ? nullptr : a.counts + (size_t)experts * (size_t)a.blocks;
+  return ops_of(dtype).route(a, static_cast<hipStream_t>(stream)) == hipSuccess ? PGEMM_OK
+                                                                             : PGEMM_EHIP;
+}
+
+size_t pgemm_route_workspace(int m, int experts, int top) {
+  (void)top;
+  if (m <= kRouteTokens || experts < 1) return 0;
+  return align256((size_t)experts * (size_t)(ceil_div(m, kRouteTokens) + 1) * 4);
+}
+
+int pgemm_route_backward(int dtype, int m, int experts, int top, int score, int renorm,
+                         float scale, const float* dweights, pgemm_rows logits,
+                         const int* expert_index, pgemm_rows dlogits, void* stream) {
+  if (!known(dtype)) return -1;
+  if (m < 0 || m > (1 << 30) / kMaxTop) return -2;
+  if (experts < 1 || experts > kMaxExperts) return -3;
+  if (top < 1 || top > kMaxTop) return -4;
+  if (score != PGEMM_SOFTMAX && score != PGEMM_SIGMOID) return -5;
+  if (!vector_ok(dweights, 4, m > 0)) return -8;
+  if (!rows_ok(logits, experts, size_of(dtype), m > 0)) return -9;
+  if (!vector_ok(expert_index, 4, m > 0)) return -10;
+  if (!rows_ok(dlogits, experts, size_of(dtype), m > 0)) return -11;
+  if (m == 0) return PGEMM_OK;
+  RouteBackArgs a{};
+  a.dweights = dweights;
+  a.logits = logits.data;
+  a.ld = logits.ld;
+  a.index = expert_index;
+  a.dlogits = dlogits.data;
+  a.ldd = dlogits.ld;
+  a.m = m;
+  a.experts = experts;
+  a.top = top;
+  a.score = score;
+  a.renorm = renorm != 0;
+  a.scale = scale;
+  return ops_of(dtype).route_back(a, static_cast<hipStream_t>(stream)) == hipSuccess ? PGEMM_OK
+                                                                                  : PGEMM_EHIP;
+}
+
+int pgemm_expert_linear(pgemm_kind kind, int rows, int n, int k, pgemm_plan plan, pgemm_rows X,
+                        pgemm_weight W, const void* bias, pgemm_rows Z, pgemm_rows Y,
+                        void* stream) {
+  if (!kind_ok(kind)) return -1;
+  if (rows < 0) return -2;
+  if (n < 0) return -3;
+  if (k < 0) return -4;
+  const bool touch = rows > 0 && n > 0, read = touch && k > 0;
+  const int size = size_of(kind.dtype), osize = size_of(kind.out_dtype);
+  if (!plan_ok(plan, rows, touch)) return -5;
+  if (!rows_ok(X, k, size, read && plan.x_rows > 0)) return -6;
+  if (!weight_ok(W, k, n, size, read, plan.experts)) return -7;
+  if (!vector_ok(bias, size, false)) return -8;
+  if (!rows_ok(Z, n, size, false)) return -9;
+  if (!rows_ok(Y, n, osize, touch)) return -10;
+  if (!touch) return PGEMM_OK;
+  ProdArgs a{};
+  a.A = X.data;
+  a.lda = X.ld;
+  a.B = W.data;
+  a.ldb = W.ld;
+  a.strideB = W.stride;
+  a.D = Y.data;
+  a.ldd = Y.ld;
+  a.M = rows;
+  a.N = n;
+  a.K = k;
+  a.bias = bias;
+  a.strideBias = n;
+  a.Z = Z.data;
+  a.ldz = Z.ld;
+  a.act = kind.act;
+  a.out32 = kind.out_dtype == PGEMM_F32;
+  a.offsets = plan.offsets;
+  a.groups = plan.experts;
+  a.rows = rows;
+  a.gather = plan.tokens;
+  a.gather_rows = plan.x_rows;
+  return run_product(a, kind.dtype, kInner, W.order == PGEMM_KN ? kOuter : kInner, kRows, rows,
+                     nullptr, 0, static_cast<hipStream_t>(stream));
+}
+
+int pgemm_expert_linear_backward(pgemm_kind kind, int rows, int n, int k, pgemm_plan plan,
+                                 pgemm_rows dY, pgemm_rows Z, pgemm_rows X, pgemm_weight W,
+                                 pgemm_rows dX, pgemm_weight dW, void* dbias, void* workspace,
+                                 size_t workspace_bytes, void* stream) {
+  if (!kind_ok(kind)) return -1;
+  if (rows < 0) return -2;
+  if (n < 0) return -3;
+  if (k < 0) return -4;
+  const int size = size_of(kind.dtype), osize = size_of(kind.out_dtype);
+  const bool read = rows > 0 && n > 0;
+  if (!plan_ok(plan, rows, true)) return -5;
+  if (!rows_ok(dY, n, size, read)) return -6;
+  if (!rows_ok(Z, n, size, read && kind.act != PGEMM_ACT_NONE)) return -7;
+  if (!rows_ok(X, k, size, read && k > 0 && plan.x_rows > 0 && dW.data != nullptr)) return -8;
+  if (!weight_ok(W, k, n, size, read && k > 0 && dX.data != nullptr, plan.experts)) return -9;
+  if (!rows_ok(dX, k, size, false)) return -10;
+  if (!weight_ok(dW, k, n, osize, false, plan.experts)) return -11;
+  if (!vector_ok(dbias, osize, false)) return -12;
+  const int experts = plan.experts;
+  const BackSpace space = back_space(kind, rows, n, k, experts);
+  if (space.total() > 0 && (workspace == nullptr || !aligned_to(workspace, 16))) return -13;
+  if (workspace_bytes < space.total()) return -14;
+  BackArgs b{kind, rows, n, k, experts, plan.offsets, plan.tokens, plan.x_rows,
+             dY,   Z,    X, dX, W,      dW,           n > 0 ? dbias : nullptr};
+  if (n == 0) b.kind.act = PGEMM_ACT_NONE;
+  return run_backward(b, workspace, space, static_cast<hipStream_t>(stream));
+}
+
+size_t pgemm_expert_linear_backward_workspace(pgemm_kind kind, int rows, int n, int k,
+                                              int experts) {
+  if (!kind_ok(kind) || rows < 0 || n <= 0 || k < 0 || experts < 1) return 0;
+  return back_space(kind, rows, n, k, experts).total();
+}
+
+int pgemm_combine(int dtype, int m, int n, int top, int rows, pgemm_rows Y, const int* slots,
+                  const float* weights, pgemm_rows residual, pgemm_rows out, void* stream) {
+  if (!known(dtype)) return -1;
+  if (m < 0 || m > (1 << 30) / kMaxTop) return -2;
+  if (n < 0) return -3;
+  if (top < 1 || top > kMaxTop) return -4;
+  if (rows < 0) return -5;
+  const bool touch = m > 0 && n > 0;
+  const int size = size_of(dtype);
+  if (!rows_ok(Y, n, size, touch && rows > 0)) return -6;
+  if (!vector_ok(slots, 4, touch)) return -7;
+  if (!vector_ok(weights, 4, false)) return -8;
+  if (!rows_ok(residual, n, size, false)) return -9;
+  if (!rows_ok(out, n, size, touch)) return -10;
+  if (!touch) return PGEMM_OK;
+  CombineArgs a{};
+  a.Y = Y.data;
+  a.slots = slots;
+  a.weights = weights;
+  a.R = residual.data;
+  a.out = out.data;
+  a.ldy = Y.ld;
+  a.ldr = residual.ld;
+  a.ldo = out.ld;
+  a.m = m;
+  a.n = n;
+  a.top = top;
+  a.rows = rows;
+  a.tpr = threads_per_row(n, 256);
+  return ops_of(dtype).combine(a, static_cast<hipStream_t>(stream)) == hipSuccess ? PGEMM_OK
+                                                                               : PGEMM_EHIP;
+}
+
+int pgemm_combine_backward(int dtype, int m, int n, int top, int rows, pgemm_rows dout,
+                           pgemm_rows Y, const int* slots, const float* weights, pgemm_rows dY,
+                           float* dweights, void* stream) {
+  if (!known(dtype)) return -1;
+  if (m < 0 || m > (1 << 30) / kMaxTop) return -2;
+  if (n < 0) return -3;
+  if (top < 1 || top > kMaxTop) return -4;
+  if (rows < 0) return -5;
+  const int size = size_of(dtype);
+  const bool read = m > 0 && n > 0;
+  if (!rows_ok(dout, n, size, read)) return -6;
+  if (!rows_ok(Y, n, size, read && rows > 0 && dweights != nullptr)) return -7;
+  if (!vector_ok(slots, 4, m > 0)) return -8;
+  if (!vector_ok(weights, 4, false)) return -9;
+  if (!rows_ok(dY, n, size, false)) return -10;
+  if (!vector_ok(dweights, 4, false)) return -11;
+  if (m == 0 || (dY.data == nullptr && dweights == nullptr)) return PGEMM_OK;
+  CombineBackArgs a{};
+  a.dout = dout.data;
+  a.Y = Y.data;
+  a.slots = slots;
+  a.weights = weights;
+  a.dY = dY.data;
+  a.dweights = dweights;
+  a.ldo = dout.ld;
+  a.ldy = Y.ld;
+  a.ldd = dY.ld;
+  a.m = m;
+  a.n = n;
+  a.top = top;
+  a.rows = rows;
+  return ops_of(dtype).combine_back(a, static_cast<hipStream_t>(stream)) == hipSuccess
+             ? PGEMM_OK
+             : PGEMM_EHIP;
+}
+
+}  // extern "C"

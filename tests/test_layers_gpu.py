@@ -1,0 +1,679 @@
+"""The layer operators on the GPU against plain 64-bit arithmetic on the CPU.
+
+Sizes are small and chosen where the kernels can go wrong: one row, one
+column, one inner index, one more or less than a tile, padded and unaligned
+rows, experts without rows, tokens without experts.  Inputs of small whole
+numbers make every sum exact in fp32, so that those results have to be equal
+bit by bit; random inputs are held to bounds that count the roundings:
+
+  a product of k terms summed in fp32: |error| <= (k + 2) 2^-24 sum |x||w|
+  an activation: its slope is below 1.13, and its own evaluation is off by at
+  most (|z| + 8) 2^-23 |z|
+  each result: half a step of its type.
+"""
+import math
+
+import pytest
+import torch
+
+import precision_gemm_02_amd as pg
+from layer_util import (Guarded, act64, half_step, ints, plan64, route64, slope64, weight)
+
+pytestmark = [pytest.mark.gpu,
+              pytest.mark.skipif(not torch.cuda.is_available(), reason="needs a GPU")]
+
+F32, F16, BF16 = torch.float32, torch.float16, torch.bfloat16
+TYPES = [F32, F16, BF16]
+ids = {F32: "f32", F16: "f16", BF16: "bf16"}.get
+
+
+def gen(seed):
+    return torch.Generator().manual_seed(seed)
+
+
+def space(n):
+    return torch.full((n + 16,), 0x7F, dtype=torch.uint8, device="cuda") if n else None
+
+
+# (m, n, k): few-rows kernels (m <= 32), tiles of every class, edges of each
+SHAPES = [(1, 1, 1), (1, 64, 64), (1, 257, 1023), (3, 17, 5), (16, 130, 72), (17, 64, 129),
+          (32, 72, 520), (33, 65, 31), (64, 64, 128), (65, 129, 64), (128, 256, 40),
+          (200, 136, 1), (300, 263, 264)]
+
+
+@pytest.mark.parametrize("dtype", TYPES, ids=ids)
+@pytest.mark.parametrize("order", ["kn", "nk"])
+@pytest.mark.parametrize("shape", SHAPES, ids=str)
+@pytest.mark.parametrize("pad", [0, 5, 8])
+def test_linear_exact_integers(dtype, order, shape, pad):
+    m, n, k = shape
+    g = gen(1)
+    X = Guarded(m, k, dtype, pad=pad, data=ints(g, m, k).to(dtype))
+    W = weight(g, (), k, n, order, dtype, integer=True, pad=pad)
+    bias, R = ints(g, n).to(dtype).cuda(), ints(g, m, n).cuda()
+    Y = Guarded(m, n, F32, pad=pad)
+    Z = Guarded(m, n, dtype, pad=pad)
+    pg.linear(X.t, W, Y.t, bias=bias, act="relu", residual=R, Z=Z.t)
+    z = X.t.double().cpu() @ W.double().cpu() + bias.double().cpu()
+    assert torch.equal(Y.t.double().cpu(), z.clamp(min=0) + R.double().cpu())
+    assert torch.equal(Z.t.cpu(), z.to(dtype))       # one rounding, to nearest even
+    Y.check("Y")
+    Z.check("Z")
+    # the same with the summed index shared between workgroups
+    ws = space(pg.linear_workspace(m, n, k, dtype))
+    Y2 = Guarded(m, n, F32, pad=pad)
+    pg.linear(X.t, W, Y2.t, bias=bias, act="relu", residual=R, Z=Z.t, ws=ws)
+    assert torch.equal(Y2.t, Y.t)
+    Y2.check("Y")
+
+
+# one more, one less and exactly whole tiles of the large class, long k over
+# several workgroups
+LARGE = [(2304, 2304, 192), (2305, 2312, 200), (4096, 2048, 64), (100, 96, 8192), (8, 64, 16384),
+         (2, 3000, 4096), (515, 517, 999), (48, 2048, 2048), (1000, 1000, 1000)]
+
+
+@pytest.mark.parametrize("dtype", TYPES, ids=ids)
+@pytest.mark.parametrize("order", ["kn", "nk"])
+@pytest.mark.parametrize("shape", LARGE, ids=str)
+def test_linear_exact_integers_large(dtype, order, shape):
+    m, n, k = shape
+    g = gen(2)
+    X = ints(g, m, k).to(dtype).cuda()
+    W = weight(g, (), k, n, order, dtype, integer=True)
+    R = ints(g, m, n).cuda()
+    want = X.double() @ W.double()
+    for ws in (None, space(pg.linear_workspace(m, n, k, dtype))):
+        Y = Guarded(m, n, F32, data=R)
+        pg.linear(X, W, Y.t, residual=Y.t, ws=ws)    # in place
+        assert torch.equal(Y.t.double(), want + R.double())
+        Y.check("Y")
+
+
+@pytest.mark.parametrize("dtype", TYPES, ids=ids)
+@pytest.mark.parametrize("act", ["none", "relu", "gelu", "gelu_tanh", "silu"])
+@pytest.mark.parametrize("shape", [(1, 200, 300), (70, 130, 96), (130, 67, 33)], ids=str)
+def test_linear_random(dtype, act, shape):
+    m, n, k = shape
+    g = gen(3)
+    X = (torch.randn(m, k, generator=g) * 1.5).to(dtype).cuda()
+    W = weight(g, (), k, n, "nk", dtype, scale=k ** -0.5)
+    bias, R = torch.randn(n, generator=g).to(dtype).cuda(), torch.randn(m, n, generator=g)
+    R = R.to(dtype).cuda()
+    Y, Z = torch.empty(m, n, dtype=dtype, device="cuda"), torch.empty(m, n, dtype=dtype, device="cuda")
+    pg.linear(X, W, Y, bias=bias, act=act, residual=R, Z=Z)
+    x, w = X.double().cpu(), W.double().cpu()
+    z = x @ w + bias.double().cpu()
+    sums = (k + 2) * 2.0 ** -24 * (x.abs() @ w.abs() + bias.double().cpu().abs())
+    h = half_step(dtype)
+    assert ((Z.double().cpu() - z).abs() <= h * z.abs() * (1 + h) + sums * (1 + h) + 1e-30).all()
+    y = act64(z, act) + R.double().cpu()
+    own = 1.13 * sums + (z.abs() + 8) * 2.0 ** -23 * z.abs() + 2.0 ** -23 * y.abs()
+    tiny = torch.finfo(dtype).tiny * torch.finfo(dtype).eps      # a subnormal step
+    assert ((Y.double().cpu() - y).abs() <= h * y.abs() * (1 + h) + own * (1 + h) + tiny).all()
+
+
+@pytest.mark.parametrize("dtype", TYPES, ids=ids)
+def test_linear_special_values(dtype):
+    """Infinities and NaN of one row stay in it; nothing is read past k."""
+    m, n, k = 40, 48, 24
+    g = gen(4)
+    X = Guarded(m, k, dtype, pad=8, data=torch.randn(m, k, generator=g).to(dtype))
+    X.t[3, 5] = math.inf
+    X.t[7, 0] = math.nan
+    W = weight(g, (), k, n, "kn", dtype, pad=8)
+    for act in ("none", "relu", "gelu", "gelu_tanh", "silu"):
+        Y = torch.empty(m, n, dtype=dtype, device="cuda")
+        pg.linear(X.t, W, Y, act=act)
+        assert Y[7].isnan().all()
+        if act == "none":
+            assert torch.equal(Y[3] > 0, W[5] > 0) and Y[3].isinf().all()
+        rest = [r for r in range(m) if r not in (3, 7)]
+        assert Y[rest].isfinite().all()
+
+
+def test_linear_empty_and_zero_k():
+    X, W = torch.zeros(4, 0, device="cuda"), torch.zeros(0, 5, device="cuda")
+    bias = torch.arange(5.0, device="cuda")
+    Y = torch.full((4, 5), 9.0, device="cuda")
+    pg.linear(X, W, Y, bias=bias)
+    assert torch.equal(Y, bias.expand(4, 5))
+    Y = torch.full((4, 5), 9.0, device="cuda")
+    pg.linear(torch.zeros(4, 3, device="cuda")[:0], torch.zeros(3, 5, device="cuda"), Y[:0])
+    assert (Y == 9).all()
+
+
+@pytest.mark.parametrize("dtype", TYPES, ids=ids)
+@pytest.mark.parametrize("order", ["kn", "nk"])
+@pytest.mark.parametrize("shape", [(1, 1, 1), (1, 64, 96), (5, 33, 17), (40, 130, 72),
+                                   (257, 64, 129), (130, 264, 136), (1000, 24, 40)], ids=str)
+@pytest.mark.parametrize("pad", [0, 8])
+def test_linear_backward_exact_integers(dtype, order, shape, pad):
+    m, n, k = shape
+    g = gen(5)
+    X = Guarded(m, k, dtype, pad=pad, data=ints(g, m, k, hi=1).to(dtype))
+    dY = Guarded(m, n, dtype, pad=pad, data=ints(g, m, n, hi=1).to(dtype))
+    Z = Guarded(m, n, dtype, pad=pad, data=ints(g, m, n).to(dtype))
+    W = weight(g, (), k, n, order, dtype, integer=True, pad=pad)
+    for act in ("none", "relu"):
+        dX = Guarded(m, k, dtype, pad=pad)
+        rows, cols = (k, n) if order == "kn" else (n, k)
+        dW = Guarded(rows, cols, F32, pad=pad)
+        db = torch.empty(n, device="cuda")
+        ws = space(pg.linear_backward_workspace(m, n, k, dtype, act))
+        pg.linear_backward(dY.t, X.t, W, Z=Z.t if act != "none" else None, act=act, dX=dX.t,
+                           dW=dW.t if order == "kn" else dW.t.t(), dbias=db, ws=ws)
+        dz = dY.t.double().cpu()
+        if act == "relu":
+            dz = dz * (Z.t.double().cpu() > 0)
+        assert torch.equal(dX.t.cpu(), (dz @ W.double().cpu().t()).to(dtype))
+        dw = X.t.double().cpu().t() @ dz
+        assert torch.equal(dW.t.double().cpu(), dw if order == "kn" else dw.t())
+        assert torch.equal(db.double().cpu(), dz.sum(0))
+        dX.check("dX")
+        dW.check("dW")
+
+
+@pytest.mark.parametrize("dtype", TYPES, ids=ids)
+@pytest.mark.parametrize("act", ["none", "relu", "gelu", "gelu_tanh", "silu"])
+def test_linear_backward_random(dtype, act):
+    m, n, k = 150, 90, 70
+    g = gen(6)
+    X, dY = torch.randn(m, k, generator=g).to(dtype).cuda(), torch.randn(m, n, generator=g)
+    dY, Z = dY.to(dtype).cuda(), (torch.randn(m, n, generator=g) * 2).to(dtype).cuda()
+    W = weight(g, (), k, n, "nk", dtype)
+    dX, dW = torch.empty_like(X), torch.empty(k, n, dtype=dtype, device="cuda")
+    db = torch.empty(n, dtype=dtype, device="cuda")
+    ws = space(pg.linear_backward_workspace(m, n, k, dtype, act))
+    pg.linear_backward(dY, X, W, Z=Z, act=act, dX=dX, dW=dW, dbias=db, ws=ws)
+    slope = slope64(Z.double().cpu(), act)
+    dz = dY.double().cpu() * slope
+    h = half_step(dtype)
+    # dZ is rounded to the type; the slope itself (terms up to 1 + |z|, each
+    # evaluated to (|z| + 8) 2^-23) is off by at most this
+    z = Z.double().cpu().abs()
+    edz = h * dz.abs() + dY.double().cpu().abs() * (1 + z) * (z + 8) * 2.0 ** -23
+    w, x = W.double().cpu(), X.double().cpu()
+    for got, want, err, mag, terms in (
+            (dX, dz @ w.t(), edz @ w.t().abs(), dz.abs() @ w.t().abs(), n),
+            (dW, x.t() @ dz, x.t().abs() @ edz, x.t().abs() @ dz.abs(), m),
+            (db, dz.sum(0), edz.sum(0), dz.abs().sum(0), m)):
+        bound = (err + (terms + 2) * 2.0 ** -24 * mag) * (1 + 2 * h) + h * want.abs()
+        assert ((got.double().cpu() - want).abs() <= bound + 1e-7).all()
+
+
+def test_linear_gradients_against_differences():
+    """f32 gradients of sum(C * linear) against central differences in 64 bits."""
+    m, n, k = 6, 9, 11
+    g = gen(7)
+    X, W0 = torch.randn(m, k, generator=g).cuda(), torch.randn(k, n, generator=g).cuda()
+    b, C = torch.randn(n, generator=g).cuda(), torch.randn(m, n, generator=g).cuda()
+    for act in ("gelu", "gelu_tanh", "silu"):
+        Y, Z = torch.empty(m, n, device="cuda"), torch.empty(m, n, device="cuda")
+        pg.linear(X, W0, Y, bias=b, act=act, Z=Z)
+        dX, dW, db = torch.empty_like(X), torch.empty_like(W0), torch.empty_like(b)
+        ws = space(pg.linear_backward_workspace(m, n, k, F32, act))
+        pg.linear_backward(C, X, W0, Z=Z, act=act, dX=dX, dW=dW, dbias=db, ws=ws)
+
+        def loss(x, w, bb):
+            return float((act64(x @ w + bb, act) * C.double().cpu()).sum())
+        x, w, bb = X.double().cpu(), W0.double().cpu(), b.double().cpu()
+        h = 1e-5       # difference error h^2 f'''/6 ~ 1e-9, rounding 1e-15 / h = 1e-10
+        for grad, t in ((dX, x), (dW, w), (db, bb)):
+            flat, got = t.view(-1), grad.double().cpu().reshape(-1)
+            for i in range(0, flat.numel(), 7):
+                keep = float(flat[i])
+                flat[i] = keep + h
+                up = loss(x, w, bb)
+                flat[i] = keep - h
+                down = loss(x, w, bb)
+                flat[i] = keep
+                assert abs((up - down) / (2 * h) - float(got[i])) < 5e-5
+
+
+def test_linear_backward_parts():
+    """Each gradient alone, without what only the others read."""
+    m, n, k = 64, 48, 32
+    g = gen(8)
+    X, dY = ints(g, m, k).cuda(), ints(g, m, n).cuda()
+    W = weight(g, (), k, n, "kn", F32, integer=True)
+    ws = space(pg.linear_backward_workspace(m, n, k, F32))
+    dX, dW, db = torch.empty(m, k, device="cuda"), torch.empty(k, n, device="cuda"), \
+        torch.empty(n, device="cuda")
+    pg.linear_backward(dY, None, W, dX=dX, ws=ws)
+    pg.linear_backward(dY, X, None, dW=dW, ws=ws)
+    pg.linear_backward(dY, None, None, dbias=db, ws=ws)
+    assert torch.equal(dX, dY @ W.t()) and torch.equal(dW, X.t() @ dY)
+    assert torch.equal(db, dY.sum(0))
+    # no rows: the weight's and bias's gradients are zero
+    dW.fill_(7)
+    db.fill_(7)
+    pg.linear_backward(dY[:0], X[:0], W, dW=dW, dbias=db, ws=ws)
+    assert (dW == 0).all() and (db == 0).all()
+
+
+# ---- routing ---------------------------------------------------------------------
+
+LOWEST = {F32: torch.finfo(F32).min, F16: -65504.0, BF16: torch.finfo(BF16).min}
+
+
+def run_route(logits, top, **kw):
+    m, E = logits.shape
+    w = torch.full((m, top), -7.0, device="cuda")
+    e = torch.full((m, top), -7, dtype=torch.int32, device="cuda")
+    off = torch.full((E + 1,), -7, dtype=torch.int32, device="cuda")
+    tok = torch.full((m * top,), -7, dtype=torch.int32, device="cuda")
+    slots = torch.full((m, top), -7, dtype=torch.int32, device="cuda")
+    ws = space(pg.route_workspace(m, E, top))
+    pg.route(logits, w, e, off, tok, slots, ws=ws, **kw)
+    return w, e, off, tok, slots
+
+
+def check_route(logits, top, **kw):
+    w, e, off, tok, slots = run_route(logits, top, **kw)
+    bias = kw.pop("bias", None)
+    we, ww = route64(logits.float().cpu(), LOWEST[logits.dtype], top,
+                     bias=None if bias is None else bias.cpu(), **kw)
+    assert torch.equal(e.cpu(), we)
+    # 64-bit scores (a few 2^-53), rounded to fp32 once
+    assert ((w.double().cpu() - ww).abs() <= ww.abs() * (2.0 ** -24 + 1e-12) + 1e-38).all()
+    o, rows, s = plan64(we, logits.shape[1])
+    assert off.tolist() == o and slots.tolist() == s
+    assert tok.tolist() == rows + [-7] * (tok.numel() - len(rows))
+
+
+@pytest.mark.parametrize("dtype", TYPES, ids=ids)
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("case", [
+    # m, E, top, groups, top_groups, bias, renorm, scale
+    (1, 1, 1, 1, 1, False, True, 1.0), (4, 64, 6, 1, 1, False, False, 1.0),
+    (3, 8, 8, 1, 1, True, True, 2.5), (64, 60, 4, 4, 2, False, True, 1.0),
+    (65, 128, 2, 8, 3, True, False, 0.5), (200, 100, 5, 1, 1, True, True, 1.0),
+    (130, 256, 8, 8, 4, True, True, 2.0), (70, 300, 32, 1, 1, False, True, 1.0),
+    (66, 1024, 3, 64, 5, True, True, 1.0), (129, 24, 3, 24, 4, False, True, 1.0)], ids=str)
+def test_route(dtype, score, case):
+    m, E, top, groups, top_groups, bias, renorm, scale = case
+    g = gen(9)
+    logits = (torch.randn(m, E, generator=g) * 2).to(dtype).cuda()
+    b = (torch.randn(E, generator=g) * 0.1).cuda() if bias else None
+    check_route(logits, top, bias=b, score=score, groups=groups, top_groups=top_groups,
+                renorm=renorm, scale=scale)
+
+
+@pytest.mark.parametrize("dtype", TYPES, ids=ids)
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+def test_route_masks_ties_and_extremes(dtype, score):
+    m, E = 70, 16
+    g = gen(10)
+    l = (torch.randn(m, E, generator=g)).to(dtype)
+    l[0] = 0                                  # all equal: lowest indices
+    l[1] = -math.inf                          # nothing left
+    l[2] = LOWEST[dtype]                      # the same by the type's lowest value
+    l[3, 2:] = -math.inf                      # fewer than top
+    l[4, ::2] = LOWEST[dtype]
+    l[5, 3] = math.inf
+    l[6] = math.nan
+    l[7, 1] = math.nan
+    l[8] = torch.tensor([60000.0 if i % 2 else -60000.0 for i in range(E)]).to(dtype)
+    l[9, 8:] = l[9, :8].clone()               # pairs of equal logits
+    l[69] = -math.inf
+    want = l.clone()
+    want[want.isnan()] = -math.inf            # NaN counts as masked
+    w, e, off, tok, slots = run_route(l.cuda(), 4, score=score)
+    ref = want.float()
+    ref[5, 3] = 1e30                          # +inf: the limit of a large logit
+    we, ww = route64(ref, LOWEST[dtype], 4, score=score)
+    assert torch.equal(e.cpu(), we)
+    assert ((w.double().cpu() - ww).abs() <= ww * (2.0 ** -24 + 1e-12) + 1e-38).all()
+    o, rows, s = plan64(we, E)
+    assert off.tolist() == o and slots.tolist() == s and tok[:len(rows)].tolist() == rows
+    assert (e[1] == -1).all() and (e[2] == -1).all() and (w[1] == 0).all()
+    for kw in (dict(groups=4, top_groups=2), dict(bias=torch.zeros(E, device="cuda"))):
+        ee = run_route(l.cuda(), 4, score=score, **kw)[1]
+        kw2 = {x: (y.cpu() if x == "bias" else y) for x, y in kw.items()}
+        assert torch.equal(ee.cpu(), route64(ref, LOWEST[dtype], 4, score=score, **kw2)[0])
+
+
+def test_route_no_tokens_and_padded_rows():
+    E, top = 12, 3
+    w, e, off, tok, slots = run_route(torch.zeros(0, E, device="cuda"), top)
+    assert off.tolist() == [0] * (E + 1)
+    big = torch.randn(300, 40, generator=gen(11)).cuda()
+    check_route(big[:, 5:17], top)            # rows of a wider tensor
+
+
+@pytest.mark.parametrize("dtype", TYPES, ids=ids)
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("renorm", [False, True])
+@pytest.mark.parametrize("E,top", [(1, 1), (8, 2), (64, 6), (100, 8), (200, 4), (1000, 32)])
+def test_route_backward(dtype, score, renorm, E, top):
+    m, scale = 37, 1.7
+    g = gen(12)
+    l = (torch.randn(m, E, generator=g) * 2).to(dtype)
+    e = torch.stack([torch.randperm(E, generator=g)[:top] for _ in range(m)]).int()
+    if E > top:
+        l[2, :] = l[2, :].masked_fill(torch.arange(E) >= E - 2, -math.inf)
+        e[2] = torch.arange(top)
+        e[3, top // 2:] = -1
+    e[4] = -1
+    dw = torch.randn(m, top, generator=g)
+    out = Guarded(m, E, dtype, pad=3)
+    pg.route_backward(dw.cuda(), l.cuda(), e.cuda(), out.t, score=score, renorm=renorm, scale=scale)
+    x = l.double().requires_grad_(True)
+    s = torch.softmax(x, 1) if score == "softmax" else torch.sigmoid(x)
+    live = (e >= 0).double()
+    p = s.gather(1, e.clamp(min=0).long()) * live
+    if renorm:
+        p = p / (p.sum(1, keepdim=True) + (live.sum(1, keepdim=True) == 0))
+    ((p * scale * dw.double()).sum()).backward()
+    want = x.grad
+    # fp32 scores (expf to 2 units, sums of E terms) against cancelling terms
+    # no larger than scale * sum |dw|
+    bound = half_step(dtype) * want.abs() + (E + top + 32) * 2.0 ** -24 * scale * \
+        (s.detach() * dw.abs().sum(1, keepdim=True).double() + dw.abs().max(1, keepdim=True)[0])
+    assert ((out.t.double().cpu() - want).abs() <= bound + 1e-7).all()
+    out.check("dlogits")
+
+
+# ---- the experts' products ---------------------------------------------------------
+
+def random_plan(g, m, top, E, drop=0.1, empty=()):
+    allowed = [x for x in range(E) if x not in empty]
+    e = torch.stack([torch.tensor(allowed)[torch.randperm(len(allowed), generator=g)[:top]]
+                     for _ in range(m)]).int()
+    e[torch.rand(m, generator=g) < drop] = -1
+    o, rows, s = plan64(e, E)
+    tok = torch.full((m * top,), -1, dtype=torch.int32)
+    tok[:len(rows)] = torch.tensor(rows, dtype=torch.int32)
+    return e, torch.tensor(o, dtype=torch.int32).cuda(), tok.cuda(), \
+        torch.tensor(s, dtype=torch.int32).cuda()
+
+
+EXPERT_SHAPES = [  # m, top, E, n, k
+    (1, 1, 1, 8, 8), (1, 2, 8, 64, 64), (16, 4, 16, 80, 72), (40, 3, 5, 130, 65),
+    (100, 2, 3, 136, 264), (300, 4, 6, 64, 40), (90, 8, 70, 33, 96), (700, 2, 4, 264, 128)]
+
+
+@pytest.mark.parametrize("dtype", TYPES, ids=ids)
+@pytest.mark.parametrize("order", ["kn", "nk"])
+@pytest.mark.parametrize("shape", EXPERT_SHAPES, ids=str)
+@pytest.mark.parametrize("gather", [True, False])
+def test_expert_linear_exact_integers(dtype, order, shape, gather):
+    m, top, E, n, k = shape
+    g = gen(13)
+    _, off, tok, _ = random_plan(g, m, top, E, empty=(1,) if E - 1 >= top and E > 1 else ())
+    R = m * top
+    X = Guarded(m if gather else R, k, dtype, pad=8, data=ints(g, m if gather else R, k).to(dtype))
+    W = weight(g, (E,), k, n, order, dtype, integer=True)
+    bias = ints(g, E, n).to(dtype).cuda()
+    Y, Z = Guarded(R, n, F32, pad=1), Guarded(R, n, dtype)
+    pg.expert_linear(X.t, W, Y.t, off, tokens=tok if gather else None, bias=bias, act="relu", Z=Z.t)
+    o = off.tolist()
+    x, w = X.t.double().cpu(), W.double().cpu()
+    for e in range(E):
+        r = torch.arange(o[e], o[e + 1])
+        src = tok.cpu()[r].long() if gather else r
+        z = x[src] @ w[e] + bias[e].double().cpu()
+        assert torch.equal(Y.t.double().cpu()[r], z.clamp(min=0))
+        assert torch.equal(Z.t.cpu()[r], z.to(dtype))
+    Y.check("Y", rows=o[-1])
+    Z.check("Z", rows=o[-1])
+
+
+@pytest.mark.parametrize("dtype", TYPES, ids=ids)
+@pytest.mark.parametrize("order", ["kn", "nk"])
+@pytest.mark.parametrize("shape", EXPERT_SHAPES, ids=str)
+@pytest.mark.parametrize("gather", [True, False])
+def test_expert_linear_backward_exact_integers(dtype, order, shape, gather):
+    m, top, E, n, k = shape
+    g = gen(14)
+    _, off, tok, _ = random_plan(g, m, top, E, empty=(1,) if E - 1 >= top and E > 1 else ())
+    R, xr = m * top, m if gather else m * top
+    X = ints(g, xr, k, hi=1).to(dtype).cuda()
+    dY = ints(g, R, n, hi=1).to(dtype).cuda()
+    Z = ints(g, R, n).to(dtype).cuda()
+    o = off.tolist()
+    dY[o[-1]:] = math.nan                            # rows behind the last are not read
+    Z[o[-1]:] = math.nan
+    W = weight(g, (E,), k, n, order, dtype, integer=True)
+    dX = Guarded(R, k, dtype, pad=8)
+    dW = torch.full_like(W, math.nan, dtype=F32)
+    db = torch.full((E, n), math.nan, device="cuda")
+    ws = space(pg.expert_linear_backward_workspace(R, n, k, E, dtype, "relu"))
+    pg.expert_linear_backward(dY, X, W, off, tokens=tok if gather else None, Z=Z, act="relu",
+                              dX=dX.t, dW=dW, dbias=db, ws=ws)
+    for e in range(E):
+        r = torch.arange(o[e], o[e + 1])
+        src = tok.cpu()[r].long() if gather else r
+        dz = dY.double().cpu()[r] * (Z.double().cpu()[r] > 0)
+        assert torch.equal(dX.t.cpu()[r], (dz @ W[e].double().cpu().t()).to(dtype))
+        assert torch.equal(dW[e].double().cpu(), X.double().cpu()[src].t() @ dz)
+        assert torch.equal(db[e].double().cpu(), dz.sum(0))
+    dX.check("dX", rows=o[-1])
+
+
+def test_expert_linear_skewed_and_large():
+    """All rows on one expert of many, with the large tiles and the few-rows
+    kernel's loop over row blocks."""
+    g = gen(15)
+    for m, E, n, k, dtype in ((600, 64, 64, 64, BF16), (60, 8, 512, 264, F16), (3000, 4, 1032, 72, BF16)):
+        off = torch.zeros(E + 1, dtype=torch.int32)
+        off[E // 2 + 1:] = m
+        X = ints(g, m, k).to(dtype).cuda()
+        W = weight(g, (E,), k, n, "nk", dtype, integer=True)
+        Y = torch.empty(m, n, device="cuda")
+        pg.expert_linear(X, W, Y, off.cuda())
+        assert torch.equal(Y.double(), X.double() @ W[E // 2].double())
+
+
+def test_expert_linear_bad_plans_stay_inside():
+    """Bounds and tokens outside the buffers are clamped, or read as zeros."""
+    g = gen(16)
+    m, E, n, k = 20, 3, 24, 16
+    X, W = ints(g, m, k).cuda(), weight(g, (E,), k, n, "kn", F32, integer=True)
+    Y = Guarded(m, n, F32)
+    off = torch.tensor([-5, 8, 4, 1000], dtype=torch.int32, device="cuda")
+    tok = torch.tensor([-1, 1 << 30] + list(range(18)), dtype=torch.int32, device="cuda")
+    pg.expert_linear(X, W, Y.t, off, tokens=tok)
+    Y.check("Y")
+    assert (Y.t[:2] == 0).all()
+    assert torch.equal(Y.t[2:4], X[:2] @ W[0])
+
+
+# ---- rows back to their tokens -------------------------------------------------------
+
+@pytest.mark.parametrize("dtype", TYPES, ids=ids)
+@pytest.mark.parametrize("m,top,n", [(1, 1, 1), (5, 3, 17), (64, 8, 64), (33, 4, 520), (9, 32, 2056)])
+def test_combine_and_gradients(dtype, m, top, n):
+    g = gen(17)
+    E = 40
+    _, off, tok, slots = random_plan(g, m, top, E, drop=0.2)
+    R = m * top
+    Y = torch.randn(R, n, generator=g).to(dtype).cuda()
+    Y[int(off[-1]):] = math.nan
+    w, res = torch.randn(m, top, generator=g).cuda(), torch.randn(m, n, generator=g).to(dtype)
+    dout = torch.randn(m, n, generator=g).to(dtype).cuda()
+    out = Guarded(m, n, dtype, pad=3, data=res)
+    pg.combine(Y, slots, out.t, weights=w, residual=out.t)
+    s, live = slots.cpu().long(), (slots >= 0).cpu()
+    rows = Y.double().cpu()[s.clamp(min=0)].masked_fill(~live[:, :, None], 0)
+    terms = rows * w.double().cpu()[:, :, None]
+    want = terms.sum(1) + res.double()
+    mag = terms.abs().sum(1) + res.double().abs()
+    h = half_step(dtype)
+    bound = h * want.abs() + (top + 3) * 2.0 ** -24 * mag * (1 + h)
+    assert ((out.t.double().cpu() - want).abs() <= bound + 1e-9).all()
+    out.check("out")
+    plain = torch.empty(m, n, dtype=dtype, device="cuda")
+    pg.combine(Y, slots, plain)
+    want = rows.sum(1)
+    bound = h * want.abs() + (top + 3) * 2.0 ** -24 * rows.abs().sum(1) * (1 + h)
+    assert ((plain.double().cpu() - want).abs() <= bound + 1e-9).all()
+
+    dY = Guarded(R, n, dtype, pad=8)
+    dw = torch.full((m, top), math.nan, device="cuda")
+    pg.combine_backward(dout, Y, slots, w, dY=dY.t, dweights=dw)
+    d = dout.double().cpu()
+    # below the type's smallest normal value the step is fixed at tiny * eps
+    # (fp16: 2^-24), so half a step is this much whatever the value
+    flat = torch.finfo(dtype).tiny * torch.finfo(dtype).eps / 2
+    for t in range(m):
+        for j in range(top):
+            if live[t, j]:
+                want = float(w[t, j]) * d[t]
+                got = dY.t[s[t, j]].double().cpu()
+                assert ((got - want).abs() <= (h + 2.0 ** -23) * want.abs() + flat).all()
+                dot = (d[t] * rows[t, j])
+                assert abs(float(dw[t, j]) - float(dot.sum())) <= (n + 2) * 2.0 ** -24 * \
+                    float(dot.abs().sum()) + 1e-30
+            else:
+                assert float(dw[t, j]) == 0
+    dY.check("dY", rows=int(off[-1]))
+
+
+# ---- together, streams, graphs ----------------------------------------------------------
+
+def moe_forward_backward(X, Wr, W1, W2, dout, top):
+    """A routed pair of products and all its gradients, as a model runs it."""
+    m, h = X.shape
+    E, _, f = W1.shape
+    T, new = X.dtype, lambda *s, d=X.dtype: torch.empty(*s, dtype=d, device="cuda")
+    i32 = torch.int32
+    s = {}
+    s["logits"] = pg.linear(X, Wr, new(m, E, d=F32))
+    s["w"], s["e"], s["slots"] = new(m, top, d=F32), new(m, top, d=i32), new(m, top, d=i32)
+    s["off"], s["tok"] = new(E + 1, d=i32), new(m * top, d=i32)
+    pg.route(s["logits"], s["w"], s["e"], s["off"], s["tok"], s["slots"],
+             ws=space(pg.route_workspace(m, E, top)))
+    R = m * top
+    s["Z"], s["H"], s["Y"] = new(R, f), new(R, f), new(R, h)
+    pg.expert_linear(X, W1, s["H"], s["off"], tokens=s["tok"], act="silu", Z=s["Z"])
+    pg.expert_linear(s["H"], W2, s["Y"], s["off"])
+    s["out"] = pg.combine(s["Y"], s["slots"], new(m, h), weights=s["w"], residual=X)
+    # gradients
+    s["dY"], s["dw"] = new(R, h), new(m, top, d=F32)
+    pg.combine_backward(dout, s["Y"], s["slots"], s["w"], dY=s["dY"], dweights=s["dw"])
+    s["dH"], s["dW2"] = new(R, f), torch.empty_like(W2)
+    size = max(pg.expert_linear_backward_workspace(R, h, f, E, T),
+               pg.expert_linear_backward_workspace(R, f, h, E, T, "silu"),
+               pg.linear_backward_workspace(m, E, h, T))
+    ws = space(size)
+    pg.expert_linear_backward(s["dY"], s["H"], W2, s["off"], dX=s["dH"], dW=s["dW2"], ws=ws)
+    s["dXr"], s["dW1"] = new(R, h), torch.empty_like(W1)
+    pg.expert_linear_backward(s["dH"], X, W1, s["off"], tokens=s["tok"], Z=s["Z"], act="silu",
+                              dX=s["dXr"], dW=s["dW1"], ws=ws)
+    s["dlogits"] = pg.route_backward(s["dw"], s["logits"], s["e"], new(m, E, d=F32))
+    s["dl"] = s["dlogits"].to(T)
+    s["dXl"], s["dWr"] = new(m, h), torch.empty_like(Wr)
+    pg.linear_backward(s["dl"], X, Wr, dX=s["dXl"], dW=s["dWr"], ws=ws)
+    s["dX"] = pg.combine(s["dXr"], s["slots"], new(m, h), residual=s["dXl"])
+    s["dX"] = s["dX"] + dout
+    return s
+
+
+def test_routed_layer_matches_autograd_in_64_bits():
+    """The whole chain in fp32 against autograd of the same layer in 64 bits."""
+    m, h, f, E, top = 90, 48, 72, 8, 2
+    g = gen(18)
+    X, dout = torch.randn(m, h, generator=g).cuda(), torch.randn(m, h, generator=g).cuda()
+    Wr = (torch.randn(E, h, generator=g) * h ** -0.5).cuda().t()
+    W1 = (torch.randn(E, f, h, generator=g) * h ** -0.5).cuda().transpose(1, 2)
+    W2 = (torch.randn(E, f, h, generator=g) * f ** -0.5).cuda()
+    s = moe_forward_backward(X, Wr, W1, W2, dout, top)
+    leaves = [t.double().cpu().detach().requires_grad_(True) for t in (X, Wr, W1, W2)]
+    x, wr, w1, w2 = leaves
+    p = torch.softmax(x @ wr, 1)
+    e = s["e"].cpu().long()
+    assert torch.equal(p.topk(top, 1).indices, e)
+    w = p.gather(1, e)
+    w = w / w.sum(1, keepdim=True)
+    out = x
+    for j in range(top):
+        z = torch.bmm(x[:, None], w1[e[:, j]])[:, 0]
+        out = out + w[:, j:j + 1] * torch.bmm(act64(z, "silu")[:, None], w2[e[:, j]])[:, 0]
+    (out * dout.double().cpu()).sum().backward()
+    for name, got, want in (("out", s["out"], out.detach()), ("dX", s["dX"], x.grad),
+                            ("dWr", s["dWr"], wr.grad), ("dW1", s["dW1"], w1.grad),
+                            ("dW2", s["dW2"], w2.grad)):
+        # seven fp32 stages of at most 90-term sums of values of order one: relative
+        # to the largest entry (7 * 92 + 32) 2^-24 = 4e-5
+        err = (got.double().cpu() - want).abs().max() / want.abs().max()
+        assert err < 4e-5, (name, float(err))
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32], ids=ids)
+def test_routed_layer_captured_and_replayed(dtype):
+    """One graph of the chain, replayed with eager work in between; every
+    replay equals the eager result of its inputs."""
+    m, h, f, E, top = 130, 64, 96, 8, 2
+    g = gen(19)
+
+    def inputs():
+        return [torch.randn(*s, generator=g).to(dtype).cuda() for s in
+                ((m, h), (E, h), (E, f, h), (E, f, h), (m, h))]
+    hold = inputs()
+
+    def run():
+        X, Wr, W1, W2, dout = hold
+        return moe_forward_backward(X, Wr.t(), W1.transpose(1, 2), W2, dout, top)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        run()
+    torch.cuda.current_stream().wait_stream(side)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        captured = run()
+    for _ in range(4):
+        for t, v in zip(hold, inputs()):
+            t.copy_(v)
+        graph.replay()
+        torch.cuda.synchronize()
+        want = run()
+        rows = int(want["off"][-1])
+        for name in ("out", "dX", "dWr", "dW1", "dW2", "w", "e", "off", "slots"):
+            assert torch.equal(captured[name], want[name]), name
+        assert torch.equal(captured["tok"][:rows], want["tok"][:rows])
+
+
+def test_streams_and_repeats():
+    """Two calls at once on their own streams; identical inputs, identical bits."""
+    g = gen(20)
+    X = torch.randn(300, 520, generator=g).to(BF16).cuda()
+    W = weight(g, (), 520, 264, "nk", BF16)
+    Y = torch.empty(300, 264, dtype=BF16, device="cuda")
+    ws = space(pg.linear_workspace(300, 264, 520, BF16))
+    pg.linear(X, W, Y, ws=ws, act="gelu")
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    outs = [torch.empty_like(Y) for _ in streams]
+    spaces = [space(pg.linear_workspace(300, 264, 520, BF16)) for _ in streams]
+    torch.cuda.synchronize()
+    for _ in range(5):
+        for s, o, w in zip(streams, outs, spaces):
+            pg.linear(X, W, o, ws=w, act="gelu", stream=s)
+    torch.cuda.synchronize()
+    for o in outs:
+        assert torch.equal(o, Y)
+
+
+def test_offsets_beyond_32_bits():
+    """Rows whose byte offsets pass 2^32 (a gathered row far into X, and Y)."""
+    rows, k = (1 << 31) // 4096 + 70, 4096            # 2^31 elements and more, bf16
+    X = torch.zeros(rows, k, dtype=BF16, device="cuda")
+    X[-64:, 3] = torch.arange(64, dtype=BF16, device="cuda")
+    W = torch.zeros(1, 16, k, dtype=BF16, device="cuda")
+    W[:, :, 3] = 1
+    tok = torch.arange(rows - 64, rows, dtype=torch.int32, device="cuda")
+    off = torch.tensor([0, 64], dtype=torch.int32, device="cuda")
+    Y = torch.empty(64, 16, device="cuda")
+    pg.expert_linear(X, W.transpose(1, 2), Y, off, tokens=tok)
+    assert torch.equal(Y[:, 0].cpu(), torch.arange(64.0))
+    del X
+    # the result itself that long: n = 16, ld = 2^27, 40 rows
+    buf = torch.zeros(39 * (1 << 27) // 2 + 16, dtype=BF16, device="cuda")
+    Yl = buf.as_strided((40, 16), (1 << 26, 1))
+    Xs, Ws = torch.ones(40, 8, dtype=BF16, device="cuda"), torch.ones(8, 16, dtype=BF16, device="cuda")
+    pg.linear(Xs, Ws, Yl)
+    assert (Yl == 8).all()
