@@ -144,7 +144,8 @@ int pgemm_route_backward(int dtype, int m, int experts, int top, int score, int 
 
 /*
  * The plan of an expert product: row bounds by expert (experts + 1) and the
- * row of X of each row (NULL: the row itself), of which there are x_rows.
+ * row of X of each row (NULL: the row itself), of which there are x_rows (at
+ * least one with tokens, at least as many as rows without).
  */
 typedef struct {
   int experts;            /* 1..1024 */
@@ -157,7 +158,7 @@ typedef struct {
  *   Y[r] = act(X[src(r)] W_e + bias_e), rows r in [offsets[e], offsets[e+1]).
  * src(r) is tokens[r], or r itself if tokens is NULL.  Rows of Y and Z behind
  * offsets[experts] are left as they were.  Row bounds are read on the device
- * and clamped to [0, rows]; a token outside [0, x_rows) reads as a zero row.
+ * and clamped to [0, rows], tokens to [0, x_rows).
  *   arguments: 1 kind, 2 rows (capacity of Y), 3 n, 4 k, 5 plan, 6 X, 7 W,
  *   8 bias (experts x n, contiguous, or NULL), 9 Z, 10 Y, 11 stream.
  */

@@ -54,7 +54,7 @@ bool vector_ok(const void* p, int size, bool need) {
 bool plan_ok(const pgemm_plan& p, int rows, bool need) {
   return p.experts >= 1 && p.experts <= kMaxExperts && vector_ok(p.offsets, 4, need) &&
          vector_ok(p.tokens, 4, false) && p.x_rows >= 0 &&
-         (p.tokens != nullptr || p.x_rows >= rows);
+         (p.tokens != nullptr ? p.x_rows > 0 || rows == 0 : p.x_rows >= rows);
 }
 
 // ---- the choice of a product's kernel ----------------------------------------
@@ -494,7 +494,7 @@ int pgemm_expert_linear(pgemm_kind kind, int rows, int n, int k, pgemm_plan plan
   const bool touch = rows > 0 && n > 0, read = touch && k > 0;
   const int size = size_of(kind.dtype), osize = size_of(kind.out_dtype);
   if (!plan_ok(plan, rows, touch)) return -5;
-  if (!rows_ok(X, k, size, read && plan.x_rows > 0)) return -6;
+  if (!rows_ok(X, k, size, read)) return -6;
   if (!weight_ok(W, k, n, size, read, plan.experts)) return -7;
   if (!vector_ok(bias, size, false)) return -8;
   if (!rows_ok(Z, n, size, false)) return -9;
@@ -539,7 +539,7 @@ int pgemm_expert_linear_backward(pgemm_kind kind, int rows, int n, int k, pgemm_
   if (!plan_ok(plan, rows, true)) return -5;
   if (!rows_ok(dY, n, size, read)) return -6;
   if (!rows_ok(Z, n, size, read && kind.act != PGEMM_ACT_NONE)) return -7;
-  if (!rows_ok(X, k, size, read && k > 0 && plan.x_rows > 0 && dW.data != nullptr)) return -8;
+  if (!rows_ok(X, k, size, read && k > 0 && dW.data != nullptr)) return -8;
   if (!weight_ok(W, k, n, size, read && k > 0 && dX.data != nullptr, plan.experts)) return -9;
   if (!rows_ok(dX, k, size, false)) return -10;
   if (!weight_ok(dW, k, n, osize, false, plan.experts)) return -11;

@@ -24,6 +24,7 @@ enum Order { kInner = 0, kOuter = 1 };
 enum Mode { kDense = 0, kRows = 1, kSums = 2 };
 
 typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef float f32x16 __attribute__((ext_vector_type(16)));
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
 typedef short s16x4 __attribute__((ext_vector_type(4)));
@@ -41,36 +42,50 @@ __device__ __forceinline__ u32x4 load16(const void* p) {
 }
 __device__ __forceinline__ void store16(void* p, u32x4 v) { static_cast<Bytes16*>(p)->v = v; }
 
-// D(16 x 16) += A(16 x 16 bytes of k per lane group) B: one step of 64 bytes of
-// the summed index.  Lane l = 16 g + i gives row i of A and column i of B,
-// 16 bytes of chunk g.  fp32 takes it in four instructions of four inner
-// indices each (lane group g: index 4 g + s at instruction s); both
-// operands use the same order, so every product is formed once.
+// D += A B for one 16 x 16 (mfma) or 32 x 32 (mfma32) block: one 16-byte chunk
+// of the summed index per lane.  Lane l = BLK g + i gives row i of A and column
+// i of B, chunk g.  fp32 takes it in four instructions (lane group g: index
+// 4 g + s at instruction s); both operands use the same order, so every product
+// is formed once.
 template <typename T>
 struct Elem;
 template <>
 struct Elem<__bf16> {
-  static constexpr int kSize = 2;
+  static constexpr int kMfmas = 1;
   static __device__ __forceinline__ f32x4 mfma(u32x4 a, u32x4 b, f32x4 c) {
     return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, a),
+                                                   __builtin_bit_cast(bf16x8, b), c, 0, 0, 0);
+  }
+  static __device__ __forceinline__ f32x16 mfma32(u32x4 a, u32x4 b, f32x16 c) {
+    return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, a),
                                                    __builtin_bit_cast(bf16x8, b), c, 0, 0, 0);
   }
 };
 template <>
 struct Elem<_Float16> {
-  static constexpr int kSize = 2;
+  static constexpr int kMfmas = 1;
   static __device__ __forceinline__ f32x4 mfma(u32x4 a, u32x4 b, f32x4 c) {
     return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8, a),
+                                                  __builtin_bit_cast(f16x8, b), c, 0, 0, 0);
+  }
+  static __device__ __forceinline__ f32x16 mfma32(u32x4 a, u32x4 b, f32x16 c) {
+    return __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(f16x8, a),
                                                   __builtin_bit_cast(f16x8, b), c, 0, 0, 0);
   }
 };
 template <>
 struct Elem<float> {
-  static constexpr int kSize = 4;
+  static constexpr int kMfmas = 4;
   static __device__ __forceinline__ f32x4 mfma(u32x4 a, u32x4 b, f32x4 c) {
     const f32x4 x = __builtin_bit_cast(f32x4, a), y = __builtin_bit_cast(f32x4, b);
 #pragma unroll
     for (int s = 0; s < 4; ++s) c = __builtin_amdgcn_mfma_f32_16x16x4f32(x[s], y[s], c, 0, 0, 0);
+    return c;
+  }
+  static __device__ __forceinline__ f32x16 mfma32(u32x4 a, u32x4 b, f32x16 c) {
+    const f32x4 x = __builtin_bit_cast(f32x4, a), y = __builtin_bit_cast(f32x4, b);
+#pragma unroll
+    for (int s = 0; s < 4; ++s) c = __builtin_amdgcn_mfma_f32_32x32x2f32(x[s], y[s], c, 0, 0, 0);
     return c;
   }
 };
@@ -116,11 +131,38 @@ __device__ __forceinline__ float logistic(float z) {
   else return 1.0f / (1.0f + expf(-z));
 }
 
+// The normal distribution function and exp(-z^2/2).  Fast: the rational
+// approximation 7.1.26 of Abramowitz and Stegun for erfc, whose factor exp(-x^2)
+// keeps the lower tail's relative error below 2e-6 down to z = -5 (2e-5 at
+// -13) where 1 + erf would cancel.
+template <bool Fast>
+__device__ __forceinline__ float normal_cdf(float z, float* bell) {
+  if constexpr (Fast) {
+    const float x = fabsf(z) * 0.70710678118654752f;
+    const float e = __expf(-x * x);
+    const float t = __builtin_amdgcn_rcpf(1.0f + 0.3275911f * x);
+    float p = 1.061405429f;
+    p = p * t - 1.453152027f;
+    p = p * t + 1.421413741f;
+    p = p * t - 0.284496736f;
+    p = p * t + 0.254829592f;
+    const float q = 0.5f * p * t * e;
+    *bell = e;
+    return z > 0.0f ? 1.0f - q : q;
+  } else {
+    *bell = expf(-0.5f * z * z);
+    return 0.5f * erfcf(-0.70710678118654752f * z);
+  }
+}
+
 template <bool Fast>
 __device__ __forceinline__ float act_value(float z, int act) {
   switch (act) {
     case kRelu: return z > 0.0f ? z : (z != z ? z : 0.0f);
-    case kGelu: return 0.5f * z * (1.0f + erff(z * 0.70710678118654752f));
+    case kGelu: {
+      float bell;
+      return z * normal_cdf<Fast>(z, &bell);
+    }
     // 0.5 (1 + tanh u) = logistic(2 u)
     case kGeluTanh:
       return z * logistic<Fast>(1.5957691216057308f * (z + 0.044715f * z * z * z));
@@ -134,9 +176,9 @@ __device__ __forceinline__ float act_slope(float z, int act) {
   switch (act) {
     case kRelu: return z > 0.0f ? 1.0f : 0.0f;
     case kGelu: {
-      const float d = -0.5f * z * z;
-      return 0.5f * (1.0f + erff(z * 0.70710678118654752f)) +
-             z * (Fast ? __expf(d) : expf(d)) * 0.39894228040143268f;
+      float bell;
+      const float phi = normal_cdf<Fast>(z, &bell);
+      return phi + z * bell * 0.39894228040143268f;
     }
     case kGeluTanh: {
       const float q = logistic<Fast>(1.5957691216057308f * (z + 0.044715f * z * z * z));
@@ -183,51 +225,119 @@ __device__ __forceinline__ void put8(void* base, long long at, const float* v) {
   }
 }
 
-// Row m, columns n0 .. n0+7 (those below N) of D from the sums v.  The
-// activation sees the fp32 sum; Z and D are each rounded once from it.
+// Eight residual values as they are stored (16-bit types use the first half).
+struct Raw8 {
+  u32x4 lo, hi;
+};
 template <typename T>
-__device__ __forceinline__ void finish8(const ProdArgs& a, const void* bias, void* D, long long m,
-                                        int n0, const float* sum) {
-  float v[8];
+__device__ __forceinline__ Raw8 load_residual(const ProdArgs& a, long long m, int n0) {
+  Raw8 r;
+  if (sizeof(T) == 4 || a.out32) {
+    const float* p = static_cast<const float*>(a.R) + m * a.ldr + n0;
+    r.lo = load16(p);
+    r.hi = load16(p + 4);
+  } else {
+    r.lo = load16(static_cast<const T*>(a.R) + m * a.ldr + n0);
+    r.hi = u32x4{0, 0, 0, 0};
+  }
+  return r;
+}
+template <typename T>
+__device__ __forceinline__ void add_residual(const ProdArgs& a, const Raw8& r, float* v) {
+  if (sizeof(T) == 4 || a.out32) {
+    const f32x4 x = __builtin_bit_cast(f32x4, r.lo), y = __builtin_bit_cast(f32x4, r.hi);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) { v[j] += x[j]; v[4 + j] += y[j]; }
+  } else if constexpr (sizeof(T) == 2) {
+    typedef T t8 __attribute__((ext_vector_type(8)));
+    const t8 x = __builtin_bit_cast(t8, r.lo);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[j] += (float)x[j];
+  }
+}
+
+// The switch stands outside the loops: the kernels' code stays small.
+template <bool Fast>
+__device__ __forceinline__ void act8(float* v, int act) {
+  switch (act) {
+    case kRelu:
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v[j] = act_value<Fast>(v[j], kRelu);
+      break;
+    case kGelu:
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v[j] = act_value<Fast>(v[j], kGelu);
+      break;
+    case kGeluTanh:
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v[j] = act_value<Fast>(v[j], kGeluTanh);
+      break;
+    case kSilu:
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v[j] = act_value<Fast>(v[j], kSilu);
+      break;
+    default: break;
+  }
+}
+
+// The bias of columns n0 .. n0+7, zeros where there is none.
+template <typename T>
+__device__ __forceinline__ void load_bias(const ProdArgs& a, const void* bias, int n0, float* b) {
+#pragma unroll
+  for (int j = 0; j < 8; ++j) b[j] = 0.0f;
+  if (bias == nullptr) return;
+  if (n0 + 8 <= a.N) {
+    get8<T>(bias, n0, b);
+  } else {
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+      if (n0 + j < a.N) b[j] = (float)static_cast<const T*>(bias)[n0 + j];
+  }
+}
+
+// Row m, columns n0 .. n0+7 of D from v, the sums with the bias added.  The
+// activation sees the fp32 value; Z and D are each rounded once from it.
+// `residual` holds a.R's values if there is one and all eight columns exist.
+template <typename T>
+__device__ __forceinline__ void finish_row(const ProdArgs& a, void* D, long long m, int n0,
+                                           float* v, const Raw8& residual) {
+  constexpr bool Fast = sizeof(T) == 2;
   const int live = a.N - n0;
   if (live >= 8) {
-    if (bias != nullptr) {
-      get8<T>(bias, n0, v);
-#pragma unroll
-      for (int j = 0; j < 8; ++j) v[j] += sum[j];
-    } else {
-#pragma unroll
-      for (int j = 0; j < 8; ++j) v[j] = sum[j];
-    }
     if (a.Z != nullptr) put8<T>(a.Z, m * a.ldz + n0, v);
-    if (a.act != kNone)
-#pragma unroll
-      for (int j = 0; j < 8; ++j) v[j] = act_value<sizeof(T) == 2>(v[j], a.act);
-    if (a.R != nullptr) {
-      float r[8];
-      if (a.out32) get8<float>(a.R, m * a.ldr + n0, r);
-      else get8<T>(a.R, m * a.ldr + n0, r);
-#pragma unroll
-      for (int j = 0; j < 8; ++j) v[j] += r[j];
-    }
+    act8<Fast>(v, a.act);
+    if (a.R != nullptr) add_residual<T>(a, residual, v);
     if (a.out32) put8<float>(D, m * a.ldd + n0, v);
     else put8<T>(D, m * a.ldd + n0, v);
     return;
   }
+#pragma unroll 1
   for (int j = 0; j < live; ++j) {
-    const int n = n0 + j;
     float x = 0.0f;
 #pragma unroll
-    for (int q = 0; q < 8; ++q) x = q == j ? sum[q] : x;   // no indexed registers
-    if (bias != nullptr) x += (float)static_cast<const T*>(bias)[n];
+    for (int q = 0; q < 8; ++q) x = q == j ? v[q] : x;   // no indexed registers
+    const int n = n0 + j;
     if (a.Z != nullptr) static_cast<T*>(a.Z)[m * a.ldz + n] = (T)x;
-    x = act_value<sizeof(T) == 2>(x, a.act);
+    x = act_value<Fast>(x, a.act);
     if (a.R != nullptr)
       x += a.out32 ? static_cast<const float*>(a.R)[m * a.ldr + n]
                    : (float)static_cast<const T*>(a.R)[m * a.ldr + n];
     if (a.out32) static_cast<float*>(D)[m * a.ldd + n] = x;
     else static_cast<T*>(D)[m * a.ldd + n] = (T)x;
   }
+}
+
+// The whole epilogue of eight sums.
+template <typename T>
+__device__ __forceinline__ void finish8(const ProdArgs& a, const void* bias, void* D, long long m,
+                                        int n0, const float* sum) {
+  float v[8];
+  load_bias<T>(a, bias, n0, v);
+#pragma unroll
+  for (int j = 0; j < 8; ++j) v[j] += sum[j];
+  Raw8 r{};
+  if (a.R != nullptr && n0 + 8 <= a.N) r = load_residual<T>(a, m, n0);
+  finish_row<T>(a, D, m, n0, v, r);
 }
 
 // ---- groups ------------------------------------------------------------------

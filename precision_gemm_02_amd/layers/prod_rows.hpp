@@ -11,8 +11,6 @@
 // issued before the current ones are used.
 #pragma once
 
-#include <type_traits>
-
 #include "prod_tile.hpp"
 
 namespace pgemm {
@@ -36,7 +34,7 @@ __global__ __launch_bounds__(512) void prod_rows_kernel(const ProdArgs a) {
   constexpr int STG = LB == kOuter ? WAVES * BN * 128 : 0;
   constexpr int LDS = RED > STG ? RED : STG;
   __shared__ __attribute__((aligned(128))) char lds[LDS];
-  using TB = OperandTile<T, kOuter, 64, 64>;
+  using TB = OperandTile<T, kOuter, 64, 64, 16>;
 
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int g = lane >> 4, i = lane & 15;

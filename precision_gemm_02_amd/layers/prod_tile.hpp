@@ -3,6 +3,8 @@
 // groups.
 #pragma once
 
+#include <type_traits>
+
 #include "prod.hpp"
 
 namespace pgemm {
@@ -12,21 +14,25 @@ namespace layers {
 static __device__ const u32x4 kZeroChunk = {0, 0, 0, 0};
 
 // One operand's tile: `EXT` output indices by 128 bytes' worth of the summed
-// index (BK = 64 16-bit or 32 fp32 elements), in 16-byte chunks.
+// index (BK = 64 16-bit or 32 fp32 elements), in 16-byte chunks, read in
+// fragments of BLK output indices (16 or 32, the matrix instruction's block).
+// A fragment's step is one chunk per lane: 64 / BLK chunks of the summed
+// index.
 //
 // Inner order: LDS row r holds output index r, 8 chunks along the summed
-// index; chunk c sits at c ^ (r & 7).  The b128 operand reads (16 rows, one
-// chunk per lane group) then touch every 16-byte bank group once per
-// cycle: of the two 8-row blocks served together, one reads chunk c and the
-// other c ^ 1, so their flipped positions never meet.
+// index; chunk c sits at c ^ flip(r).  A b128 read serves the 8-lane blocks b
+// and b ^ 3 together.  16-blocks: flip(r) = r & 7; of the two 8-row blocks one
+// reads chunk c and the other c ^ 1, so their flipped positions never meet.
+// 32-blocks: both read chunk c of rows 8 or 24 apart, and bit 3 of the row
+// enters the flip.
 //
 // Outer order: LDS row p holds summed index p, EXT contiguous output indices.
 // 16-bit operands are read through the transposing ds_read_b64_tr_b16 (16
 // lanes read a 4 x 16 block by rows and receive it by columns), fp32 with one
 // b32 per inner index.  The 32-byte (16-bit) or 64-byte (fp32) pieces that
-// one 16-column block takes from a row are flipped by the row so that the
-// rows read together fall into different banks.
-template <typename T, int ORDER, int EXT, int NT>
+// 16 columns take from a row are flipped by the row so that the pieces read
+// together fall into different banks.
+template <typename T, int ORDER, int EXT, int NT, int BLK>
 struct OperandTile {
   static constexpr int S = sizeof(T);
   static constexpr int V = 16 / S;              // elements per chunk
@@ -35,19 +41,29 @@ struct OperandTile {
   static constexpr int ROW_CHUNKS = ORDER == kInner ? 8 : EXT / V;
   static constexpr int ROW_BYTES = ROW_CHUNKS * 16;
   static constexpr int LOADS = BYTES / (16 * NT);
+  static constexpr int STEPS = BLK / 8;         // per tile
+  static constexpr int READS = ORDER == kInner ? 1 : S;   // LDS reads per fragment
   static_assert(BYTES % (16 * NT) == 0, "whole chunks per thread");
-  // outer order: pieces per row (of one 16-column block), as a power of two
+  // outer order: pieces of 16 output indices per row
   static constexpr int PIECE = 16 * S;          // bytes
   static constexpr int PIECES = EXT / 16;
+
+  static __device__ __forceinline__ int row_flip(int r) {
+    return BLK == 16 ? r & 7 : (r & 7) ^ ((r >> 3) & 1);
+  }
 
   // The flip of row p's pieces (outer order).
   static __device__ __forceinline__ int flip(int p) {
     if constexpr (S == 2) {
-      const int q = (p & 3) | (((p >> 3) & 1) << 2);
+      // 16-blocks: a half wave reads one piece of 8 rows (p & 3, bit 3);
+      // 32-blocks: two neighbouring pieces of 4 rows
+      const int q = BLK == 16 ? (p & 3) | (((p >> 3) & 1) << 2) : (p & 3) << 1;
       constexpr int b = PIECES >= 8 ? 3 : PIECES == 4 ? 2 : 1;
-      return q >> (3 - b);
+      return BLK == 16 ? q >> (3 - b) : q & ((1 << b) - 1);
     } else {
-      return (p >> 2) & (PIECES >= 4 ? 3 : 1);
+      // 16-blocks: one piece of four rows 4 apart; 32-blocks: two neighbouring
+      // pieces of two such rows
+      return BLK == 16 ? (p >> 2) & (PIECES >= 4 ? 3 : 1) : PIECES >= 4 ? ((p >> 2) & 1) << 1 : 0;
     }
   }
 
@@ -56,29 +72,29 @@ struct OperandTile {
     const int r = s / ROW_CHUNKS, pos = s % ROW_CHUNKS;
     *row = r;
     if constexpr (ORDER == kInner) {
-      *chunk = pos ^ (r & 7);
+      *chunk = pos ^ row_flip(r);
     } else {
       constexpr int CPP = PIECE / 16;           // chunks per piece: 2 or 4
       *chunk = ((pos / CPP) ^ flip(r)) * CPP + pos % CPP;
     }
   }
 
-  // Fragment of 16-index block b (from index `first`), step kk (64 bytes of
-  // the summed index), from the tile at lds.
-  static __device__ __forceinline__ u32x4 frag(const char* lds, int first, int b, int kk) {
-    const int l = threadIdx.x & 63, g = l >> 4, i = l & 15;
+  // Fragment of block b (from index `first`), step s, from the tile at lds.
+  static __device__ __forceinline__ u32x4 frag(const char* lds, int first, int b, int s) {
+    constexpr int GROUPS = 64 / BLK;            // lane groups along the summed index
+    const int l = threadIdx.x & 63, g = l / BLK, i = l % BLK;
     if constexpr (ORDER == kInner) {
-      const int row = first + 16 * b + i;
-      const int c = (4 * kk + g) ^ (i & 7);
+      const int row = first + BLK * b + i;
+      const int c = (GROUPS * s + g) ^ row_flip(i);
       return *reinterpret_cast<const u32x4*>(lds + row * 128 + c * 16);
     } else if constexpr (S == 2) {
       u32x4 out;
-      const int piece = first / 16 + b;
+      const int piece = (first + BLK * b + (i & ~15)) / 16, i16 = i & 15;
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
-        const int p = 32 * kk + 8 * g + 4 * h + (i >> 2);
-        const int f = flip(8 * g + (i >> 2));   // 32 kk and 4 h do not enter
-        const char* at = lds + p * ROW_BYTES + (piece ^ f) * PIECE + (i & 3) * 8;
+        const int p = 8 * (GROUPS * s + g) + 4 * h + (i16 >> 2);
+        const int f = flip(8 * g + (i16 >> 2));  // s and h do not enter
+        const char* at = lds + p * ROW_BYTES + (piece ^ f) * PIECE + (i16 & 3) * 8;
         const s16x4 v = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
             (__attribute__((address_space(3))) s16x4*)(const_cast<char*>(at)));
         const u32x2 w = __builtin_bit_cast(u32x2, v);
@@ -88,12 +104,12 @@ struct OperandTile {
       return out;
     } else {
       u32x4 out;
-      const int piece = first / 16 + b;
+      const int piece = (first + BLK * b + (i & ~15)) / 16, i16 = i & 15;
 #pragma unroll
-      for (int s = 0; s < 4; ++s) {
-        const int p = 16 * kk + 4 * g + s;
-        const char* at = lds + p * ROW_BYTES + (piece ^ flip(4 * g)) * PIECE + i * 4;
-        out[s] = *reinterpret_cast<const uint32_t*>(at);
+      for (int q = 0; q < 4; ++q) {
+        const int p = 4 * (GROUPS * s + g) + q;
+        const char* at = lds + p * ROW_BYTES + (piece ^ flip(p)) * PIECE + i16 * 4;
+        out[q] = *reinterpret_cast<const uint32_t*>(at);
       }
       return out;
     }
@@ -112,14 +128,14 @@ struct Source {
   const int* gather;
   int gather_rows;
 
+  // The gathered row of r: one outside the source reads the nearest inside.
+  __device__ __forceinline__ int token(int r) const {
+    const int t = gather[r];
+    return t < 0 ? 0 : (t < gather_rows ? t : gather_rows - 1);
+  }
   __device__ __forceinline__ const T* row(int r) const {
     if (r >= outer) return nullptr;
-    if (gather != nullptr) {
-      const int t = gather[r];
-      if ((unsigned)t >= (unsigned)gather_rows) return nullptr;
-      return base + (long long)t * ld;
-    }
-    return base + (long long)r * ld;
+    return base + (long long)(gather != nullptr ? token(r) : r) * ld;
   }
 };
 
@@ -143,68 +159,107 @@ __device__ __forceinline__ u32x4 load_whole(const T* row, int c0) {
   return load16(row != nullptr ? (const void*)(row + c0) : (const void*)&kZeroChunk);
 }
 
-// One operand's loads.  DIRECT: straight into LDS (global_load_lds_dwordx4:
-// a wave writes 64 consecutive chunks, so the layout's flips are applied to
-// the global addresses).  It needs 16-byte aligned rows and no chunk that
-// straddles the operand's end.  Otherwise through registers, with guards.
-template <typename T, int ORDER, int EXT, int NT, bool DIRECT>
+// One operand's loads, tile after tile of the summed index.
+//
+// DIRECT: straight into LDS (global_load_lds_dwordx4: a wave writes 64
+// consecutive chunks, so the layout's flips are applied to the global
+// addresses).  It needs 16-byte aligned rows and no chunk that straddles the
+// operand's end.  Each thread keeps one address per chunk and moves it by a
+// constant step.  Output indices outside the operand read its last row or
+// first chunk instead: they reach only results that are never stored.  The
+// last, partly filled tile of the summed index takes zeros there.
+// Otherwise the chunks go through registers, with guards.
+template <typename T, int ORDER, int EXT, int NT, bool DIRECT, bool GATHER>
 struct Loader {
-  using Tile = OperandTile<T, ORDER, EXT, NT>;
+  using Tile = OperandTile<T, ORDER, EXT, NT, 32>;
   static constexpr int L = Tile::LOADS;
   Source<T> src;
   int first;                       // first output index of the tile
-  const T* ptr[L];                 // inner order: the thread's rows
+  int k;                           // first summed index of the next load
+  const T* ptr[L];                 // the next load's addresses
+  int token[L];                    // its gathered rows (outer order, GATHER)
+  long long step;                  // outer order: elements per tile
   u32x4 reg[DIRECT ? 1 : L];
 
-  __device__ __forceinline__ void init(const Source<T>& s, int first_out) {
+  __device__ __forceinline__ void init(const Source<T>& s, int first_out, int k0) {
     src = s;
     first = first_out;
-    if constexpr (ORDER == kInner) {
-#pragma unroll
-      for (int j = 0; j < L; ++j) {
-        int r, c;
-        Tile::slot(j * NT + (int)threadIdx.x, &r, &c);
-        ptr[j] = src.row(first + r);
-      }
-    }
-  }
-
-  // Start the loads of summed indices k0 .. k0+BK-1.
-  __device__ __forceinline__ void load(char* lds, int k0) {
-    // no chunk of this tile straddles the operand's end (the same for the
-    // whole workgroup)
-    const bool whole = ORDER == kInner ? k0 + Tile::BK <= src.inner : first + EXT <= src.inner;
-    if (DIRECT || whole) load_as<true>(lds, k0);
-    else load_as<false>(lds, k0);
-  }
-
-  template <bool WHOLE>
-  __device__ __forceinline__ void load_as(char* lds, int k0) {
+    k = k0;
 #pragma unroll
     for (int j = 0; j < L; ++j) {
       int r, c;
       Tile::slot(j * NT + (int)threadIdx.x, &r, &c);
-      const T* row;
-      int at;
       if constexpr (ORDER == kInner) {
-        row = ptr[j];
-        at = k0 + c * Tile::V;
+        const int row = first + r < src.outer ? first + r : src.outer - 1;
+        ptr[j] = src.row(row) + k + c * Tile::V;
       } else {
-        row = src.row(k0 + r);
-        at = first + c * Tile::V;
+        const int at = first + c * Tile::V;
+        ptr[j] = src.base + (at < src.inner ? at : 0);
+        if constexpr (!GATHER) ptr[j] += (long long)(k + r) * src.ld;
       }
+    }
+    step = (long long)Tile::BK * src.ld;
+    if constexpr (ORDER == kOuter && GATHER) next_tokens();
+  }
+
+  __device__ __forceinline__ void next_tokens() {
+#pragma unroll
+    for (int j = 0; j < L; ++j) {
+      int r, c;
+      Tile::slot(j * NT + (int)threadIdx.x, &r, &c);
+      token[j] = k + r >= src.outer ? 0 : src.gather != nullptr ? src.token(k + r) : k + r;
+    }
+  }
+
+  // Whether a chunk of the next load (through registers) is outside the operand
+  // or straddles its end.  The same for the whole workgroup.
+  __device__ __forceinline__ bool ragged() const {
+    const bool last = k + Tile::BK > (ORDER == kInner ? src.inner : src.outer);
+    return last || (ORDER == kOuter && first + EXT > src.inner);
+  }
+
+  // Chunks J0 .. J1-1 of the load of summed indices k .. k+BK-1.  Direct loads
+  // take no branch: a chunk past the end of the summed index (all of them
+  // past the last tile) comes from the zero chunk.
+  template <int J0, int J1>
+  __device__ __forceinline__ void load(char* lds) {
+    if constexpr (DIRECT) {
+      load_as<false, J0, J1>(lds);
+    } else {
+      if (ragged()) load_as<false, J0, J1>(lds);
+      else load_as<true, J0, J1>(lds);
+    }
+    if constexpr (J1 == L) {
+      k += Tile::BK;
+      if constexpr (ORDER == kOuter && GATHER) next_tokens();
+    }
+  }
+
+  template <bool WHOLE, int J0, int J1>
+  __device__ __forceinline__ void load_as(char* lds) {
+#pragma unroll
+    for (int j = J0; j < J1; ++j) {
+      int r, c;
+      Tile::slot(j * NT + (int)threadIdx.x, &r, &c);
+      const T* p = ptr[j];
+      if constexpr (ORDER == kOuter && GATHER) p += (long long)token[j] * src.ld;
       if constexpr (DIRECT) {
-        const void* p = row != nullptr && at < src.inner ? (const void*)(row + at)
-                                                          : (const void*)&kZeroChunk;
+        const bool in = ORDER == kInner ? k + c * Tile::V < src.inner : k + r < src.outer;
+        const void* from = in ? (const void*)p : (const void*)&kZeroChunk;
         // a wave's 64 chunks; the same LDS base for all its lanes
         char* to = lds + (j * NT + ((int)threadIdx.x & ~63)) * 16;
         __builtin_amdgcn_global_load_lds(
-            (const __attribute__((address_space(1))) void*)p,
+            (const __attribute__((address_space(1))) void*)from,
             (__attribute__((address_space(3))) void*)to, 16, 0, 0);
+      } else if constexpr (WHOLE) {
+        reg[j] = load16(p);
       } else {
-        if constexpr (WHOLE) reg[j] = load_whole(row, at);
-        else reg[j] = load_guarded(row, at, src.inner);
+        const int at = ORDER == kInner ? k + c * Tile::V : first + c * Tile::V;
+        const bool row = ORDER == kInner ? first + r < src.outer : k + r < src.outer;
+        reg[j] = load_guarded(row ? p - at : nullptr, at, src.inner);
       }
+      if constexpr (ORDER == kInner) ptr[j] += Tile::BK;
+      else if constexpr (!GATHER) ptr[j] += step;
     }
   }
 
@@ -232,14 +287,58 @@ __device__ __forceinline__ void map_tile(int id, int tiles_m, int tiles_n, int* 
   *tn = in / rows;
 }
 
+template <int N, typename F>
+__device__ __forceinline__ void static_for(F f) {
+  if constexpr (N > 0) {
+    static_for<N - 1>(f);
+    f(std::integral_constant<int, N - 1>{});
+  }
+}
+
+// All waves of the workgroup are here, and their LDS accesses are done.
+__device__ __forceinline__ void workgroup_barrier() {
+  __builtin_amdgcn_sched_barrier(0);
+  asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
+  __builtin_amdgcn_sched_barrier(0);
+}
+
+// At most N of this wave's global loads are outstanding.
+template <int N>
+__device__ __forceinline__ void wait_loads() {
+  static_assert(N < 64, "the counter's range");
+  __builtin_amdgcn_sched_barrier(0);
+  asm volatile("s_waitcnt vmcnt(%0)" ::"n"(N) : "memory");
+  __builtin_amdgcn_sched_barrier(0);
+}
+
+// Spread READS LDS reads and LOADS global loads evenly over the M matrix
+// instructions of a step.
+template <int READS, int M, int LOADS>
+__device__ __forceinline__ void spread() {
+#pragma unroll
+  for (int i = 0; i < M; ++i) {
+    const int n = (i + 1) * READS / M - i * READS / M;
+    if (n == 1) __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
+    if (n == 2) __builtin_amdgcn_sched_group_barrier(0x100, 2, 0);
+    if (n == 3) __builtin_amdgcn_sched_group_barrier(0x100, 3, 0);
+    if (n == 4) __builtin_amdgcn_sched_group_barrier(0x100, 4, 0);
+    __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+    const int v = (i + 1) * LOADS / M - i * LOADS / M;
+    if (v == 1) __builtin_amdgcn_sched_group_barrier(0x020, 1, 0);
+    if (v == 2) __builtin_amdgcn_sched_group_barrier(0x020, 2, 0);
+    if (v == 3) __builtin_amdgcn_sched_group_barrier(0x020, 3, 0);
+    if (v == 4) __builtin_amdgcn_sched_group_barrier(0x020, 4, 0);
+  }
+}
+
 template <typename T, int LA, int LB, int BM, int BN, int WGM, int WGN, bool DIRECT, int MODE>
 __global__ __launch_bounds__(WGM* WGN * 64) void prod_tile_kernel(const ProdArgs a) {
   constexpr int NT = WGM * WGN * 64;
-  constexpr int WM = BM / WGM, WN = BN / WGN, RB = WM / 16, CB = WN / 16;
+  constexpr int WM = BM / WGM, WN = BN / WGN, RB = WM / 32, CB = WN / 32;
   constexpr int BK = 128 / (int)sizeof(T);
   constexpr int STAGE = (BM + BN) * 128;
   constexpr int EPI_LD = WN + 4;
-  constexpr int EPI = WGM * WGN * 16 * EPI_LD * 4;
+  constexpr int EPI = WGM * WGN * 32 * EPI_LD * 4;
   constexpr int LDS = 2 * STAGE > EPI ? 2 * STAGE : EPI;
   __shared__ __attribute__((aligned(128))) char lds[LDS];
 
@@ -275,7 +374,6 @@ __global__ __launch_bounds__(WGM* WGN * 64) void prod_tile_kernel(const ProdArgs
   const T* Bb = static_cast<const T*>(a.B);
   if constexpr (MODE == kRows) Bb += e * a.strideB;
   Source<T> sa, sb;
-  int k0 = k_lo;
   if constexpr (LA == kInner) {
     sa = {Ab, a.lda, rows, k_hi, a.gather, a.gather_rows};
   } else {
@@ -288,73 +386,100 @@ __global__ __launch_bounds__(WGM* WGN * 64) void prod_tile_kernel(const ProdArgs
   }
   if constexpr (MODE == kDense) sa.gather = nullptr;
 
-  using TA = OperandTile<T, LA, BM, NT>;
-  using TB = OperandTile<T, LB, BN, NT>;
-  Loader<T, LA, BM, NT, DIRECT> la;
-  Loader<T, LB, BN, NT, DIRECT> lb;
-  la.init(sa, row0);
-  lb.init(sb, col0);
+  using TA = OperandTile<T, LA, BM, NT, 32>;
+  using TB = OperandTile<T, LB, BN, NT, 32>;
+  // (a grouped sum's rows may be gathered on either side)
+  using LoadA = Loader<T, LA, BM, NT, DIRECT, MODE == kSums>;
+  using LoadB = Loader<T, LB, BN, NT, DIRECT, MODE == kSums>;
+  LoadA la;
+  LoadB lb;
+  la.init(sa, row0, k_lo);
+  lb.init(sb, col0, k_lo);
 
-  f32x4 acc[RB][CB];
+  f32x16 acc[RB][CB];
 #pragma unroll
   for (int r = 0; r < RB; ++r)
 #pragma unroll
-    for (int c = 0; c < CB; ++c) acc[r][c] = f32x4{0, 0, 0, 0};
+    for (int c = 0; c < CB; ++c)
+#pragma unroll
+      for (int q = 0; q < 16; ++q) acc[r][c][q] = 0;
+
+  // The K loop, in steps of 32 bytes of the summed index (G per tile).  While
+  // the matrix cores run a step, the operands of the next are read from LDS
+  // into the other registers; the last step of a tile reads the next tile's
+  // first operands.  The one barrier per tile stands before that last step,
+  // whose operands are already in registers: behind it every wave has read all
+  // of this tile and the next tile has landed, so this tile's stage is free
+  // for the tile after the next.
+  constexpr int G = TA::STEPS;
+  u32x4 fa[2][RB], fb[2][CB];
+  auto read = [&](const char* stage, int s, int into) {
+#pragma unroll
+    for (int c = 0; c < CB; ++c) fb[into][c] = TB::frag(stage + BM * 128, wn, c, s);
+#pragma unroll
+    for (int r = 0; r < RB; ++r) fa[into][r] = TA::frag(stage, wm, r, s);
+  };
+  // A tile's loads, in P parts over its first steps (in one block they would
+  // hold up every wave's issue at once).  Direct loads fetch the next tile into
+  // the stage that the last barrier freed; register loads store the next tile
+  // there and fetch the one after.
+  constexpr int P = G / 2;
+  auto load = [&](auto part, char* stage) {
+    constexpr int q = decltype(part)::value;
+    la.template load<LoadA::L * q / P, LoadA::L*(q + 1) / P>(stage);
+    lb.template load<LoadB::L * q / P, LoadB::L*(q + 1) / P>(stage + BM * 128);
+  };
+  auto load_all = [&](char* stage) { static_for<P>([&](auto q) { load(q, stage); }); };
 
   const int nk = (k_hi - k_lo + BK - 1) / BK;
   if (nk > 0) {
-    la.load(lds, k0);
-    lb.load(lds + BM * 128, k0);
-    if constexpr (!DIRECT) {
+    load_all(lds);
+    if constexpr (DIRECT) {
+      wait_loads<0>();
+    } else {
       la.store(lds);
       lb.store(lds + BM * 128);
-      if (nk > 1) {
-        la.load(nullptr, k0 + BK);
-        lb.load(nullptr, k0 + BK);
-      }
+      if (nk > 1) load_all(nullptr);
     }
-  }
-  for (int kt = 0; kt < nk; ++kt) {
-    char* cur = lds + (kt & 1) * STAGE;
-    char* nxt = lds + ((kt + 1) & 1) * STAGE;
-    // this wave's loads of tile kt have landed; then every wave's have, and
-    // nobody reads the other stage any more
-    if constexpr (DIRECT) asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
-    __syncthreads();
-    k0 += BK;
-    if constexpr (DIRECT) {
-      if (kt + 1 < nk) {
-        la.load(nxt, k0);
-        lb.load(nxt + BM * 128, k0);
+    workgroup_barrier();
+    read(lds, 0, 0);
+    for (int kt = 0; kt < nk; ++kt) {
+      char* cur = lds + (kt & 1) * STAGE;
+      char* nxt = lds + ((kt + 1) & 1) * STAGE;
+      if constexpr (!DIRECT) {
+        if (kt + 1 < nk) {
+          la.store(nxt);
+          lb.store(nxt + BM * 128);
+        }
+        if (kt + 2 < nk) load_all(nullptr);
       }
-    } else {
-      if (kt + 1 < nk) {
-        la.store(nxt);
-        lb.store(nxt + BM * 128);
-      }
-      if (kt + 2 < nk) {
-        la.load(nullptr, k0 + BK);
-        lb.load(nullptr, k0 + BK);
-      }
-    }
+      static_for<G>([&](auto gc) {
+        constexpr int g = decltype(gc)::value;
+        if constexpr (g == G - 1) {
+          if constexpr (DIRECT) wait_loads<0>();
+          workgroup_barrier();
+          read(nxt, 0, 0);     // past the last tile: some LDS, never used
+        } else {
+          // reads first: the compiler keeps LDS reads behind loads into LDS
+          read(cur, g + 1, (g + 1) & 1);
+          if constexpr (DIRECT && g < P) load(gc, nxt);
+        }
+        // B's block as the instruction's rows: a lane then holds four
+        // consecutive columns of one row of D per four registers
 #pragma unroll
-    for (int kk = 0; kk < 2; ++kk) {
-      u32x4 fa[RB], fb[CB];
+        for (int r = 0; r < RB; ++r)
 #pragma unroll
-      for (int c = 0; c < CB; ++c) fb[c] = TB::frag(cur + BM * 128, wn, c, kk);
-#pragma unroll
-      for (int r = 0; r < RB; ++r) fa[r] = TA::frag(cur, wm, r, kk);
-      // B's block as the instruction's rows: a lane then holds four
-      // consecutive columns of one row of D
-#pragma unroll
-      for (int r = 0; r < RB; ++r)
-#pragma unroll
-        for (int c = 0; c < CB; ++c) acc[r][c] = Elem<T>::mfma(fb[c], fa[r], acc[r][c]);
+          for (int c = 0; c < CB; ++c)
+            acc[r][c] = Elem<T>::mfma32(fb[g & 1][c], fa[g & 1][r], acc[r][c]);
+        spread<RB * TA::READS + CB * TB::READS, RB * CB * Elem<T>::kMfmas,
+               DIRECT && g < P ? (LoadA::L + LoadB::L) / P : 0>();
+        __builtin_amdgcn_sched_barrier(0);
+      });
     }
   }
   __syncthreads();   // the operands' LDS becomes the epilogue's
 
-  // Epilogue: 16 rows of the wave tile at a time through the wave's own LDS,
+  // Epilogue: 32 rows of the wave tile at a time through the wave's own LDS,
   // so that each lane finishes 8 consecutive columns with 16-byte accesses.
   const void* bias = a.bias;
   char* D = static_cast<char*>(a.D);
@@ -366,25 +491,50 @@ __global__ __launch_bounds__(WGM* WGN * 64) void prod_tile_kernel(const ProdArgs
     D += e * a.strideD * dsize;
     rows = a.M;
   }
-  float* stg = reinterpret_cast<float*>(lds) + wave * 16 * EPI_LD;
-  constexpr int LPR = WN / 8, RPP = 64 / LPR;   // lanes per row, rows per pass
-#pragma unroll
+  float* stg = reinterpret_cast<float*>(lds) + wave * 32 * EPI_LD;
+  constexpr int LPR = WN / 8, RPP = 64 / LPR, PASSES = 32 / RPP;   // lanes per row, rows per pass
+  const int col = (lane % LPR) * 8, n = col0 + wn + col;
+  const bool split = MODE == kDense && a.splits > 1;
+  float b8[8];
+  load_bias<T>(a, split ? nullptr : bias, n, b8);
+#pragma unroll 1
   for (int r = 0; r < RB; ++r) {
+    const int m0 = row0 + wm + 32 * r + lane / LPR;
+    Raw8 res[PASSES] = {};
+    if (a.R != nullptr && !split && n + 8 <= a.N) {
 #pragma unroll
-    for (int c = 0; c < CB; ++c)
-      *reinterpret_cast<f32x4*>(stg + (lane & 15) * EPI_LD + 16 * c + 4 * (lane >> 4)) = acc[r][c];
+      for (int p = 0; p < PASSES; ++p)
+        if (m0 + p * RPP < rows) res[p] = load_residual<T>(a, m0 + p * RPP, n);
+    }
+    static_for<RB>([&](auto rc) {
+      constexpr int q = decltype(rc)::value;
+      if (r == q) {
+#pragma unroll
+        for (int c = 0; c < CB; ++c)
+#pragma unroll
+          for (int x = 0; x < 4; ++x)
+            *reinterpret_cast<f32x4*>(stg + (lane & 31) * EPI_LD + 32 * c + 8 * x +
+                                      4 * (lane >> 5)) =
+                f32x4{acc[q][c][4 * x], acc[q][c][4 * x + 1], acc[q][c][4 * x + 2],
+                      acc[q][c][4 * x + 3]};
+      }
+    });
     __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
     __builtin_amdgcn_wave_barrier();
 #pragma unroll
-    for (int p = 0; p < 16; p += RPP) {
-      const int row = p + lane / LPR, col = (lane % LPR) * 8;
-      const float* from = stg + row * EPI_LD + col;
+    for (int p = 0; p < PASSES; ++p) {
+      const float* from = stg + (p * RPP + lane / LPR) * EPI_LD + col;
       const f32x4 x = *reinterpret_cast<const f32x4*>(from);
       const f32x4 y = *reinterpret_cast<const f32x4*>(from + 4);
-      const int m = row0 + wm + 16 * r + row, n = col0 + wn + col;
+      const int m = m0 + p * RPP;
       if (m < rows && n < a.N) {
-        const float v[8] = {x[0], x[1], x[2], x[3], y[0], y[1], y[2], y[3]};
-        if (MODE == kDense && a.splits > 1) {
+        float v[8];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          v[j] = x[j] + b8[j];
+          v[4 + j] = y[j] + b8[4 + j];
+        }
+        if (split) {
           float* to = a.partial + ((long long)blockIdx.y * a.M + m) * a.N + n;
           if (n + 8 <= a.N) {
             put8<float>(to, 0, v);
@@ -394,7 +544,7 @@ __global__ __launch_bounds__(WGM* WGN * 64) void prod_tile_kernel(const ProdArgs
               if (n + j < a.N) to[j] = v[j];
           }
         } else {
-          finish8<T>(a, bias, D, m, n, v);
+          finish_row<T>(a, D, m, n, v, res[p]);
         }
       }
     }

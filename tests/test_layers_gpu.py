@@ -467,7 +467,7 @@ def test_expert_linear_skewed_and_large():
 
 
 def test_expert_linear_bad_plans_stay_inside():
-    """Bounds and tokens outside the buffers are clamped, or read as zeros."""
+    """Bounds and tokens outside the buffers are clamped."""
     g = gen(16)
     m, E, n, k = 20, 3, 24, 16
     X, W = ints(g, m, k).cuda(), weight(g, (E,), k, n, "kn", F32, integer=True)
@@ -476,7 +476,7 @@ def test_expert_linear_bad_plans_stay_inside():
     tok = torch.tensor([-1, 1 << 30] + list(range(18)), dtype=torch.int32, device="cuda")
     pg.expert_linear(X, W, Y.t, off, tokens=tok)
     Y.check("Y")
-    assert (Y.t[:2] == 0).all()
+    assert torch.equal(Y.t[0], X[0] @ W[0]) and torch.equal(Y.t[1], X[m - 1] @ W[0])
     assert torch.equal(Y.t[2:4], X[:2] @ W[0])
 
 
