@@ -336,10 +336,11 @@ __global__ __launch_bounds__(WGM* WGN * 64) void prod_tile_kernel(const ProdArgs
   constexpr int NT = WGM * WGN * 64;
   constexpr int WM = BM / WGM, WN = BN / WGN, RB = WM / 32, CB = WN / 32;
   constexpr int BK = 128 / (int)sizeof(T);
-  constexpr int STAGE = (BM + BN) * 128;
+  constexpr int SLOT = (BM > BN ? BM : BN) * 128;   // one operand's tile
+  constexpr int SLOTS = DIRECT ? 5 : 4;
   constexpr int EPI_LD = WN + 4;
   constexpr int EPI = WGM * WGN * 32 * EPI_LD * 4;
-  constexpr int LDS = 2 * STAGE > EPI ? 2 * STAGE : EPI;
+  constexpr int LDS = SLOTS * SLOT > EPI ? SLOTS * SLOT : EPI;
   __shared__ __attribute__((aligned(128))) char lds[LDS];
 
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
@@ -404,65 +405,83 @@ __global__ __launch_bounds__(WGM* WGN * 64) void prod_tile_kernel(const ProdArgs
 #pragma unroll
       for (int q = 0; q < 16; ++q) acc[r][c][q] = 0;
 
-  // The K loop, in steps of 32 bytes of the summed index (G per tile).  While
+  // The K loop, in G = 4 steps of 32 bytes of the summed index per tile.  While
   // the matrix cores run a step, the operands of the next are read from LDS
   // into the other registers; the last step of a tile reads the next tile's
   // first operands.  The one barrier per tile stands before that last step,
   // whose operands are already in registers: behind it every wave has read all
-  // of this tile and the next tile has landed, so this tile's stage is free
-  // for the tile after the next.
+  // of this tile and the next tile has landed.
+  //
+  // Operand tiles A(0), B(0), A(1), B(1), ... follow each other through a ring of
+  // LDS slots.  Direct loads use five of them (all of a compute unit's 160 KiB
+  // for the 256 x 256 tiles): A(t + 2) and B(t + 1) are fetched during tile t,
+  // two loads a step, so that the memory pipe never runs empty at a barrier.
+  // (With two whole stages, all of tile t + 1 was fetched within tile t and
+  // awaited at its end: 25.2 against 22 ns per inner index at 4096 x 4096.)
+  // Register loads use four: tile t + 1 is stored during tile t, tile t + 2
+  // fetched.
   constexpr int G = TA::STEPS;
+  static_assert(G == 4, "the loads' places below");
   u32x4 fa[2][RB], fb[2][CB];
-  auto read = [&](const char* stage, int s, int into) {
+  auto read = [&](const char* a_slot, const char* b_slot, int s, int into) {
 #pragma unroll
-    for (int c = 0; c < CB; ++c) fb[into][c] = TB::frag(stage + BM * 128, wn, c, s);
+    for (int c = 0; c < CB; ++c) fb[into][c] = TB::frag(b_slot, wn, c, s);
 #pragma unroll
-    for (int r = 0; r < RB; ++r) fa[into][r] = TA::frag(stage, wm, r, s);
+    for (int r = 0; r < RB; ++r) fa[into][r] = TA::frag(a_slot, wm, r, s);
   };
-  // A tile's loads, in P parts over its first steps (in one block they would
-  // hold up every wave's issue at once).  Direct loads fetch the next tile into
-  // the stage that the last barrier freed; register loads store the next tile
-  // there and fetch the one after.
-  constexpr int P = G / 2;
-  auto load = [&](auto part, char* stage) {
-    constexpr int q = decltype(part)::value;
-    la.template load<LoadA::L * q / P, LoadA::L*(q + 1) / P>(stage);
-    lb.template load<LoadB::L * q / P, LoadB::L*(q + 1) / P>(stage + BM * 128);
-  };
-  auto load_all = [&](char* stage) { static_for<P>([&](auto q) { load(q, stage); }); };
+  auto slot = [&](int i) { return lds + (i >= SLOTS ? i - SLOTS : i) * SLOT; };
+  constexpr int HA = LoadA::L / 2, HB = LoadB::L / 2;
 
   const int nk = (k_hi - k_lo + BK - 1) / BK;
   if (nk > 0) {
-    load_all(lds);
+    la.template load<0, LoadA::L>(slot(0));
+    lb.template load<0, LoadB::L>(slot(1));
     if constexpr (DIRECT) {
-      wait_loads<0>();
+      la.template load<0, LoadA::L>(slot(2));
+      lb.template load<0, HB>(slot(3));
+      wait_loads<LoadA::L + HB>();
     } else {
-      la.store(lds);
-      lb.store(lds + BM * 128);
-      if (nk > 1) load_all(nullptr);
+      la.store(slot(0));
+      lb.store(slot(1));
+      if (nk > 1) {
+        la.template load<0, LoadA::L>(nullptr);
+        lb.template load<0, LoadB::L>(nullptr);
+      }
     }
     workgroup_barrier();
-    read(lds, 0, 0);
+    read(slot(0), slot(1), 0, 0);
+    int at = 0;                                // slot of A(kt)
     for (int kt = 0; kt < nk; ++kt) {
-      char* cur = lds + (kt & 1) * STAGE;
-      char* nxt = lds + ((kt + 1) & 1) * STAGE;
+      char *const a0 = slot(at), *const b0 = slot(at + 1);
+      char *const a1 = slot(at + 2), *const b1 = slot(at + 3);
+      char *const a2 = slot(at + 4), *const b2 = a0;
+      at = at + 2 >= SLOTS ? at + 2 - SLOTS : at + 2;
       if constexpr (!DIRECT) {
         if (kt + 1 < nk) {
-          la.store(nxt);
-          lb.store(nxt + BM * 128);
+          la.store(a1);
+          lb.store(b1);
         }
-        if (kt + 2 < nk) load_all(nullptr);
+        if (kt + 2 < nk) {
+          la.template load<0, LoadA::L>(nullptr);
+          lb.template load<0, LoadB::L>(nullptr);
+        }
       }
       static_for<G>([&](auto gc) {
         constexpr int g = decltype(gc)::value;
         if constexpr (g == G - 1) {
-          if constexpr (DIRECT) wait_loads<0>();
+          // all but A(t + 2) has landed
+          if constexpr (DIRECT) wait_loads<LoadA::L>();
           workgroup_barrier();
-          read(nxt, 0, 0);     // past the last tile: some LDS, never used
+          read(a1, b1, 0, 0);     // past the last tile: some LDS, never used
         } else {
           // reads first: the compiler keeps LDS reads behind loads into LDS
-          read(cur, g + 1, (g + 1) & 1);
-          if constexpr (DIRECT && g < P) load(gc, nxt);
+          read(a0, b0, g + 1, (g + 1) & 1);
+        }
+        if constexpr (DIRECT) {
+          if constexpr (g == 0) lb.template load<HB, LoadB::L>(b1);
+          if constexpr (g == 1) la.template load<0, HA>(a2);
+          if constexpr (g == 2) la.template load<HA, LoadA::L>(a2);
+          if constexpr (g == 3) lb.template load<0, HB>(b2);
         }
         // B's block as the instruction's rows: a lane then holds four
         // consecutive columns of one row of D per four registers
@@ -472,10 +491,11 @@ __global__ __launch_bounds__(WGM* WGN * 64) void prod_tile_kernel(const ProdArgs
           for (int c = 0; c < CB; ++c)
             acc[r][c] = Elem<T>::mfma32(fb[g & 1][c], fa[g & 1][r], acc[r][c]);
         spread<RB * TA::READS + CB * TB::READS, RB * CB * Elem<T>::kMfmas,
-               DIRECT && g < P ? (LoadA::L + LoadB::L) / P : 0>();
+               DIRECT ? (g == 1 || g == 2 ? HA : HB) : 0>();
         __builtin_amdgcn_sched_barrier(0);
       });
     }
+    if constexpr (DIRECT) wait_loads<0>();     // the loads past the end
   }
   __syncthreads();   // the operands' LDS becomes the epilogue's
 
