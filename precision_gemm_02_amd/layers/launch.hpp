@@ -12,7 +12,15 @@ namespace pgemm {
 namespace layers {
 
 // The tile classes and the few-rows kernels of the products.
-enum Kernel { kTile256 = 0, kTile128 = 1, kTile64 = 2, kFew16 = 3, kFew32 = 4 };
+enum Kernel {
+  kTile256 = 0,
+  kTile128 = 1,
+  kTile64 = 2,
+  kFew16 = 3,
+  kFew32 = 4,
+  kFew16Wide = 5,
+  kFew32Wide = 6
+};
 
 struct KernelShape {
   int bm, bn;
@@ -20,7 +28,7 @@ struct KernelShape {
 constexpr KernelShape kShape[3] = {{256, 256}, {128, 128}, {64, 64}};
 
 // Columns of a workgroup of the few-rows kernels.
-constexpr int few_columns(int lb) { return lb == kInner ? 16 : 64; }
+constexpr int few_columns(int kernel) { return kernel >= kFew16Wide ? 64 : 16; }
 
 struct TypeOps {
   hipError_t (*prod)(const ProdArgs& a, int la, int lb, int mode, int kernel, bool direct,

@@ -39,12 +39,19 @@ hipError_t prod_tile(const ProdArgs& a, int kernel, bool direct, hipStream_t s) 
   return hipErrorInvalidValue;
 }
 
-template <typename T, int LB, int MODE>
-hipError_t prod_few(const ProdArgs& a, int kernel, hipStream_t s) {
+template <typename T, int LB, int MB, int MODE>
+hipError_t prod_few(const ProdArgs& a, bool wide, hipStream_t s) {
   const dim3 grid((unsigned)(MODE == kRows ? a.tiles_n * a.groups : a.tiles_n),
                   MODE == kDense ? (unsigned)a.splits : 1);
-  if (kernel == kFew16) return launch(&prod_rows_kernel<T, LB, 1, MODE>, grid, 512, a, s);
-  return launch(&prod_rows_kernel<T, LB, 2, MODE>, grid, 512, a, s);
+  if (wide) return launch(&prod_rows_kernel<T, LB, MB, 4, 8, MODE>, grid, 512, a, s);
+  return launch(&prod_rows_kernel<T, LB, MB, 1, 8, MODE>, grid, 512, a, s);
+}
+
+template <typename T, int LB, int MODE>
+hipError_t prod_few(const ProdArgs& a, int kernel, hipStream_t s) {
+  const bool wide = kernel == kFew16Wide || kernel == kFew32Wide;
+  return kernel == kFew16 || kernel == kFew16Wide ? prod_few<T, LB, 1, MODE>(a, wide, s)
+                                                  : prod_few<T, LB, 2, MODE>(a, wide, s);
 }
 
 template <typename T>

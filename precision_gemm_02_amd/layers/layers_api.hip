@@ -99,11 +99,11 @@ Plan plan_product(int size, int la, int lb, int mode, long long rows, int groups
   if (la == kInner && per <= 32) {
     // Few rows: B is read once, the rest is latency.  The few-rows kernel
     // takes 16 or 32 rows per pass and never needs a tile of operands.
-    p.kernel = per <= 16 ? kFew16 : kFew32;
-    if (mode == kDense) {
-      const int cols = few_columns(lb);
-      p.splits = split_for(ceil_div(n, cols), 2 * kUnits, k, 8 * bk);
-    }
+    const long long wide = ceil_div(n, 64) * (mode == kRows ? groups : 1);
+    if (wide >= 2 * kUnits) p.kernel = per <= 16 ? kFew16Wide : kFew32Wide;
+    else p.kernel = per <= 16 ? kFew16 : kFew32;
+    if (mode == kDense)
+      p.splits = split_for(ceil_div(n, few_columns(p.kernel)), kUnits, k, 16 * bk);
   } else {
     double best = 0;
     for (int c = 0; c < 3; ++c) {
@@ -162,7 +162,7 @@ int run_product(ProdArgs a, int dtype, int la, int lb, int mode, long long rows,
   a.partial = static_cast<float*>(ws);
   if (p.kernel >= kFew16) {
     a.tiles_m = 1;
-    a.tiles_n = (int)ceil_div(a.N, few_columns(lb));
+    a.tiles_n = (int)ceil_div(a.N, few_columns(p.kernel));
   } else {
     const int bm = kShape[p.kernel].bm;
     long long tm = ceil_div(rows, bm);

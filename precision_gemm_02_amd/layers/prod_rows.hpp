@@ -1,14 +1,20 @@
 // Few rows: up to 32 rows of D against the whole of B, bound by reading B
 // once.  A workgroup takes NB blocks of 16 columns and all of the summed index
-// (or one split of it); its 8 waves take units of 128 bytes of the summed
-// index in turn, each adding into its own 16 x 16 accumulators, which are
-// summed over the waves through LDS in a fixed order.
+// (or one split of it); its waves take units of 128 bytes of the summed index
+// in turn, each adding into its own 16 x 16 accumulators, which are summed over
+// the waves through LDS in a fixed order.
 //
 // Inner-order B goes from memory straight into the matrix instruction's
-// operand registers (16 rows of 128 consecutive bytes per unit).  Outer-order
-// B arrives as rows of 64 columns and passes through a wave-private LDS tile,
-// whose transposing reads give the operand.  The loads of the next units are
-// issued before the current ones are used.
+// operand registers (16 rows of 128 consecutive bytes per unit and block).
+// Outer-order B arrives as rows of 16 NB columns and passes through a
+// wave-private LDS tile, whose transposing reads give the operand.  The loads
+// of the next units are issued before the current ones are used.
+//
+// NB = 4 where that gives every compute unit its workgroups; otherwise NB = 1,
+// with more units in flight per wave, so that a small B is still spread over the
+// whole chip and most of it is in flight at
+// once.  Workgroups of neighbouring columns run on one XCD: with NB = 1 they
+// share outer-order B's cache lines.
 #pragma once
 
 #include "prod_tile.hpp"
@@ -16,34 +22,26 @@
 namespace pgemm {
 namespace layers {
 
-template <typename T, int LB, int MB, int MODE>
-struct RowsShape {
-  static constexpr int WAVES = 8;
-  static constexpr int NB = LB == kInner ? 1 : 4;     // column blocks
-  static constexpr int BN = 16 * NB;
-  static constexpr int U = LB == kInner ? 2 : 1;      // units in flight per step
-};
-
-template <typename T, int LB, int MB, int MODE>
-__global__ __launch_bounds__(512) void prod_rows_kernel(const ProdArgs a) {
-  using S = RowsShape<T, LB, MB, MODE>;
-  constexpr int WAVES = S::WAVES, NB = S::NB, BN = S::BN, U = S::U;
+template <typename T, int LB, int MB, int NB, int WAVES, int MODE>
+__global__ __launch_bounds__(WAVES * 64) void prod_rows_kernel(const ProdArgs a) {
+  constexpr int BN = 16 * NB, U = NB == 1 ? (MB == 1 ? 4 : 2) : 1;   // U: units per load
   constexpr int V = 16 / (int)sizeof(T), BK = 128 / (int)sizeof(T);
   constexpr int RED_LD = BN + 4;
   constexpr int RED = WAVES * MB * 16 * RED_LD * 4;
   constexpr int STG = LB == kOuter ? WAVES * BN * 128 : 0;
   constexpr int LDS = RED > STG ? RED : STG;
   __shared__ __attribute__((aligned(128))) char lds[LDS];
-  using TB = OperandTile<T, kOuter, 64, 64, 16>;
+  using TB = OperandTile<T, kOuter, BN, 64, 16>;
 
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int g = lane >> 4, i = lane & 15;
-  int nb = blockIdx.x, e = 0, lo = 0, hi = a.M;
+  const int id = map_range(blockIdx.x, gridDim.x);
+  int nb = id, e = 0, lo = 0, hi = a.M;
   const T* Bb = static_cast<const T*>(a.B);
   const void* bias = a.bias;
   if constexpr (MODE == kRows) {
-    e = blockIdx.x / a.tiles_n;
-    nb = blockIdx.x % a.tiles_n;
+    e = id / a.tiles_n;
+    nb = id % a.tiles_n;
     group_bounds(a.offsets, e, a.rows, &lo, &hi);
     if (lo == hi) return;
     Bb += e * a.strideB;
@@ -55,16 +53,41 @@ __global__ __launch_bounds__(512) void prod_rows_kernel(const ProdArgs a) {
     k_lo = blockIdx.y * a.k_split;
     k_hi = k_lo + a.k_split < a.K ? k_lo + a.k_split : a.K;
   }
+  // Units loaded without guards, and those at the end of the summed index
+  // that need them.  Rows and columns outside the operands read the last row
+  // or the first chunk instead (their results are never stored); a chunk of
+  // outer-order B that straddles its row's end goes on into the next rows,
+  // which is inside B except near its end.
   const int units = (k_hi - k_lo + BK - 1) / BK;
+  int whole = (k_hi - k_lo) / BK;
+  if (LB == kOuter && col0 + BN > a.N) {
+    const int inside = a.K - V - k_lo;
+    whole = inside < 0 ? 0 : (inside / BK < whole ? inside / BK : whole);
+  }
   Source<T> sa = {static_cast<const T*>(a.A), a.lda, hi, k_hi,
                   MODE == kRows ? a.gather : nullptr, a.gather_rows};
-  const T* brow = nullptr;                      // inner order: the lane's row of B
-  if (LB == kInner && col0 + i < a.N) brow = Bb + (long long)(col0 + i) * a.ldb;
+  constexpr int BL = 2 * NB;                    // loads of B per unit and lane
+  const T* bptr[LB == kInner ? NB : BL];        // without the summed index
+#pragma unroll
+  for (int c = 0; c < (LB == kInner ? NB : BL); ++c) {
+    if constexpr (LB == kInner) {
+      const int n = col0 + 16 * c + i;
+      bptr[c] = Bb + (long long)(n < a.N ? n : a.N - 1) * a.ldb;
+    } else {
+      int r, q;
+      TB::slot(c * 64 + lane, &r, &q);
+      const int n = col0 + q * V;
+      bptr[c] = Bb + (long long)r * a.ldb + (n < a.N ? n : 0);
+    }
+  }
 
   for (int m0 = lo; m0 < hi; m0 += 16 * MB) {
     const T* arow[MB];
 #pragma unroll
-    for (int b = 0; b < MB; ++b) arow[b] = sa.row(m0 + 16 * b + i);
+    for (int b = 0; b < MB; ++b) {
+      const int m = m0 + 16 * b + i;
+      arow[b] = sa.row(m < hi ? m : hi - 1);
+    }
 
     f32x4 acc[MB][NB];
 #pragma unroll
@@ -72,79 +95,92 @@ __global__ __launch_bounds__(512) void prod_rows_kernel(const ProdArgs a) {
 #pragma unroll
       for (int c = 0; c < NB; ++c) acc[b][c] = f32x4{0, 0, 0, 0};
 
-    constexpr int BL = LB == kInner ? 2 : 8;    // loads of B per unit and lane
+    // multiply one unit's operands (outer order: through the wave's own LDS)
+    auto use = [&](u32x4(&rb)[BL], u32x4(&ra)[MB][2]) {
+      if constexpr (LB == kInner) {
+#pragma unroll
+        for (int kk = 0; kk < 2; ++kk)
+#pragma unroll
+          for (int c = 0; c < NB; ++c)
+#pragma unroll
+            for (int b = 0; b < MB; ++b)
+              acc[b][c] = Elem<T>::mfma(rb[2 * c + kk], ra[b][kk], acc[b][c]);
+      } else {
+        char* mine = lds + wave * BN * 128;
+#pragma unroll
+        for (int j = 0; j < BL; ++j)
+          *reinterpret_cast<u32x4*>(mine + (j * 64 + lane) * 16) = rb[j];
+        __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+        __builtin_amdgcn_wave_barrier();
+#pragma unroll
+        for (int kk = 0; kk < 2; ++kk)
+#pragma unroll
+          for (int c = 0; c < NB; ++c) {
+            const u32x4 f = TB::frag(mine, 0, c, kk);
+#pragma unroll
+            for (int b = 0; b < MB; ++b) acc[b][c] = Elem<T>::mfma(f, ra[b][kk], acc[b][c]);
+          }
+        __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+        __builtin_amdgcn_wave_barrier();
+      }
+    };
+    // this wave's units: wave, wave + WAVES, ..., U of them per load
+    constexpr int STEP = U * WAVES;
     u32x4 xb[U][BL], xa[U][MB][2], yb[U][BL], ya[U][MB][2];
-    auto load_unit = [&](auto whole, int u, int k0, u32x4(&rb)[U][BL], u32x4(&ra)[U][MB][2]) {
-        constexpr bool W = decltype(whole)::value;
-        if constexpr (LB == kInner) {
+    auto load = [&](int u0, u32x4(&rb)[U][BL], u32x4(&ra)[U][MB][2]) {
 #pragma unroll
-          for (int kk = 0; kk < 2; ++kk)
-            rb[u][kk] = W ? load_whole(brow, k0 + (4 * kk + g) * V)
-                          : load_guarded(brow, k0 + (4 * kk + g) * V, k_hi);
-        } else {
+      for (int u = 0; u < U; ++u) {
+        const int unit = u0 + u * WAVES;
+        if (unit >= whole) break;
+        const int k0 = k_lo + unit * BK;
 #pragma unroll
-          for (int j = 0; j < BL; ++j) {
+        for (int j = 0; j < BL; ++j) {
+          if constexpr (LB == kInner) rb[u][j] = load16(bptr[j >> 1] + k0 + (4 * (j & 1) + g) * V);
+          else rb[u][j] = load16(bptr[j] + (long long)k0 * a.ldb);
+        }
+#pragma unroll
+        for (int b = 0; b < MB; ++b)
+#pragma unroll
+          for (int kk = 0; kk < 2; ++kk) ra[u][b][kk] = load16(arow[b] + k0 + (4 * kk + g) * V);
+      }
+    };
+    auto use_all = [&](int u0, u32x4(&rb)[U][BL], u32x4(&ra)[U][MB][2]) {
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        if (u0 + u * WAVES >= whole) break;
+        use(rb[u], ra[u]);
+      }
+    };
+    load(wave, xb, xa);
+#pragma unroll 1
+    for (int u0 = wave; u0 < whole; u0 += 2 * STEP) {
+      load(u0 + STEP, yb, ya);
+      use_all(u0, xb, xa);
+      load(u0 + 2 * STEP, xb, xa);
+      use_all(u0 + STEP, yb, ya);
+    }
+#pragma unroll 1
+    for (int unit = whole + wave; unit < units; unit += WAVES) {
+      const int k0 = k_lo + unit * BK;
+      {
+        u32x4 rb[BL], ra[MB][2];
+#pragma unroll
+        for (int q = 0; q < BL; ++q) {
+          if constexpr (LB == kInner) {
+            rb[q] = load_guarded(bptr[q >> 1], k0 + (4 * (q & 1) + g) * V, k_hi);
+          } else {
             int r, c;
-            TB::slot(j * 64 + lane, &r, &c);
+            TB::slot(q * 64 + lane, &r, &c);
             const T* row = k0 + r < k_hi ? Bb + (long long)(k0 + r) * a.ldb : nullptr;
-            rb[u][j] = W ? load_whole(row, col0 + c * V) : load_guarded(row, col0 + c * V, a.N);
+            rb[q] = load_guarded(row, col0 + c * V, a.N);
           }
         }
 #pragma unroll
         for (int b = 0; b < MB; ++b)
 #pragma unroll
           for (int kk = 0; kk < 2; ++kk)
-            ra[u][b][kk] = W ? load_whole(arow[b], k0 + (4 * kk + g) * V)
-                             : load_guarded(arow[b], k0 + (4 * kk + g) * V, k_hi);
-    };
-    auto load = [&](int u0, u32x4(&rb)[U][BL], u32x4(&ra)[U][MB][2]) {
-#pragma unroll
-      for (int u = 0; u < U; ++u) {
-        const int k0 = k_lo + (u0 + u * WAVES) * BK;
-        if (k0 + BK <= k_hi && (LB == kInner || col0 + BN <= a.N))
-          load_unit(std::integral_constant<bool, true>{}, u, k0, rb, ra);
-        else
-          load_unit(std::integral_constant<bool, false>{}, u, k0, rb, ra);
-      }
-    };
-    auto use = [&](u32x4(&rb)[U][BL], u32x4(&ra)[U][MB][2]) {
-#pragma unroll
-      for (int u = 0; u < U; ++u) {
-        if constexpr (LB == kInner) {
-#pragma unroll
-          for (int kk = 0; kk < 2; ++kk)
-#pragma unroll
-            for (int b = 0; b < MB; ++b)
-              acc[b][0] = Elem<T>::mfma(rb[u][kk], ra[u][b][kk], acc[b][0]);
-        } else {
-          char* mine = lds + wave * BN * 128;
-#pragma unroll
-          for (int j = 0; j < BL; ++j)
-            *reinterpret_cast<u32x4*>(mine + (j * 64 + lane) * 16) = rb[u][j];
-          __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
-          __builtin_amdgcn_wave_barrier();
-#pragma unroll
-          for (int kk = 0; kk < 2; ++kk)
-#pragma unroll
-            for (int c = 0; c < NB; ++c) {
-              const u32x4 f = TB::frag(mine, 0, c, kk);
-#pragma unroll
-              for (int b = 0; b < MB; ++b) acc[b][c] = Elem<T>::mfma(f, ra[u][b][kk], acc[b][c]);
-            }
-          __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
-          __builtin_amdgcn_wave_barrier();
-        }
-      }
-    };
-    // units of this wave: wave, wave + WAVES, ...; loads past the end give zeros
-    constexpr int STEP = U * WAVES;
-    if (wave < units) load(wave, xb, xa);
-    for (int u0 = wave; u0 < units; u0 += 2 * STEP) {
-      if (u0 + STEP < units) load(u0 + STEP, yb, ya);
-      use(xb, xa);
-      if (u0 + STEP < units) {
-        if (u0 + 2 * STEP < units) load(u0 + 2 * STEP, xb, xa);
-        use(yb, ya);
+            ra[b][kk] = load_guarded(arow[b], k0 + (4 * kk + g) * V, k_hi);
+        use(rb, ra);
       }
     }
 
@@ -158,7 +194,7 @@ __global__ __launch_bounds__(512) void prod_rows_kernel(const ProdArgs a) {
         *reinterpret_cast<f32x4*>(red + ((wave * MB + b) * 16 + i) * RED_LD + 16 * c + 4 * g) =
             acc[b][c];
     __syncthreads();
-    for (int t = threadIdx.x; t < MB * 16 * (BN / 8); t += 512) {
+    for (int t = threadIdx.x; t < MB * 16 * (BN / 8); t += WAVES * 64) {
       const int row = t / (BN / 8), col = (t % (BN / 8)) * 8;
       const int m = m0 + row, n = col0 + col;
       if (m < hi && n < a.N) {

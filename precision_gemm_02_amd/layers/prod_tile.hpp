@@ -58,12 +58,12 @@ struct OperandTile {
       // 16-blocks: a half wave reads one piece of 8 rows (p & 3, bit 3);
       // 32-blocks: two neighbouring pieces of 4 rows
       const int q = BLK == 16 ? (p & 3) | (((p >> 3) & 1) << 2) : (p & 3) << 1;
-      constexpr int b = PIECES >= 8 ? 3 : PIECES == 4 ? 2 : 1;
+      constexpr int b = PIECES >= 8 ? 3 : PIECES == 4 ? 2 : PIECES == 2 ? 1 : 0;
       return BLK == 16 ? q >> (3 - b) : q & ((1 << b) - 1);
     } else {
       // 16-blocks: one piece of four rows 4 apart; 32-blocks: two neighbouring
       // pieces of two such rows
-      return BLK == 16 ? (p >> 2) & (PIECES >= 4 ? 3 : 1) : PIECES >= 4 ? ((p >> 2) & 1) << 1 : 0;
+      return BLK == 16 ? (p >> 2) & (PIECES >= 4 ? 3 : PIECES == 2 ? 1 : 0) : PIECES >= 4 ? ((p >> 2) & 1) << 1 : 0;
     }
   }
 
@@ -272,13 +272,17 @@ struct Loader {
   }
 };
 
-// Tile (tm, tn) of workgroup id: ids are regrouped so that each of the 8 XCDs
-// takes a contiguous range (workgroups go round-robin over XCDs, each with its
-// own L2), then walk down `GM` tile rows before the next tile column.
+// Workgroup ids regrouped so that each of the 8 XCDs takes a contiguous range
+// (workgroups go round-robin over XCDs, each with its own L2).
+__device__ __forceinline__ int map_range(int id, int total) {
+  const int per = total / 8, extra = total % 8, x = id % 8;
+  return x * per + (x < extra ? x : extra) + id / 8;
+}
+
+// Tile (tm, tn) of workgroup id: down `GM` tile rows before the next tile
+// column.
 __device__ __forceinline__ void map_tile(int id, int tiles_m, int tiles_n, int* tm, int* tn) {
-  const int total = tiles_m * tiles_n, per = total / 8, extra = total % 8;
-  const int x = id % 8, at = id / 8;
-  const int t = x * per + (x < extra ? x : extra) + at;
+  const int t = map_range(id, tiles_m * tiles_n);
   constexpr int GM = 8;
   const int span = GM * tiles_n, band = t / span, m0 = band * GM;
   const int rows = tiles_m - m0 < GM ? tiles_m - m0 : GM;
