@@ -95,7 +95,7 @@ hipError_t column_sum(const float* partial, void* out, int n, int groups, int ch
                       hipStream_t s) {
   void* args[] = {&partial, &out, &n, &chunks, &out32};
   return hipLaunchKernel(reinterpret_cast<const void*>(&column_sum_kernel<T>),
-                         dim3((unsigned)((n + 255) / 256), (unsigned)groups), dim3(256), args, 0, s);
+                         dim3((unsigned)((n + 31) / 32), (unsigned)groups), dim3(256), args, 0, s);
 }
 
 template <typename T>
@@ -119,12 +119,15 @@ hipError_t route(const RouteArgs& a, hipStream_t s) {
   hipError_t e;
   if (a.experts <= 64) e = launch(&route_kernel<T, 1>, grid, 1024, a, s);
   else if (a.experts <= 128) e = launch(&route_kernel<T, 2>, grid, 1024, a, s);
+  else if (a.experts <= 192) e = launch(&route_kernel<T, 3>, grid, 1024, a, s);
   else if (a.experts <= 256) e = launch(&route_kernel<T, 4>, grid, 1024, a, s);
+  else if (a.experts <= 512) e = launch(&route_kernel<T, 8>, grid, 1024, a, s);
   else e = launch(&route_kernel<T, 16>, grid, 1024, a, s);
   if (e != hipSuccess || a.blocks == 1) return e;
+  if (a.blocks <= 512) return launch(&route_place_kernel<T, true>, grid, 1024, a, s);
   e = launch(&route_sum_kernel<T>, dim3((unsigned)a.experts), 64, a, s);
   if (e != hipSuccess) return e;
-  return launch(&route_place_kernel<T>, grid, 1024, a, s);
+  return launch(&route_place_kernel<T, false>, grid, 1024, a, s);
 }
 
 template <typename T>

@@ -88,15 +88,25 @@ __global__ __launch_bounds__(256) void slope_kernel(const SlopeArgs a) {
   }
 }
 
-// dbias from the chunks' column sums, in order.
+// dbias from the chunks' column sums: 32 columns per workgroup, 8 threads per
+// column that each add every eighth chunk in order, then their sums in order.
 template <typename T>
 __global__ __launch_bounds__(256) void column_sum_kernel(const float* partial, void* out, int n,
                                                          int chunks, int out32) {
-  const int x = blockIdx.x * 256 + threadIdx.x, e = blockIdx.y;
-  if (x >= n) return;
+  __shared__ float sums[8][32];
+  const int c = threadIdx.x & 31, part = threadIdx.x >> 5;
+  const int x = blockIdx.x * 32 + c, e = blockIdx.y;
   float v = 0.0f;
+  if (x < n) {
+    const float* from = partial + (long long)e * chunks * n + x;
 #pragma unroll 8
-  for (int s = 0; s < chunks; ++s) v += partial[((long long)e * chunks + s) * n + x];
+    for (int s = part; s < chunks; s += 8) v += from[(long long)s * n];
+  }
+  sums[part][c] = v;
+  __syncthreads();
+  if (part != 0 || x >= n) return;
+#pragma unroll
+  for (int p = 1; p < 8; ++p) v += sums[p][c];
   const long long at = (long long)e * n + x;
   if (out32) static_cast<float*>(out)[at] = v;
   else static_cast<T*>(out)[at] = (T)v;

@@ -334,6 +334,31 @@ def test_route_masks_ties_and_extremes(dtype, score):
         assert torch.equal(ee.cpu(), route64(ref, LOWEST[dtype], 4, score=score, **kw2)[0])
 
 
+@pytest.mark.parametrize("groups", [1, 4])
+def test_route_close_keys(groups):
+    """Keys a few 1e-11 apart: below what the integer keys tell apart (2^-28), well
+    above an exp's last bit (1e-16).  The bias of every second expert is chosen
+    so that its key nearly meets its neighbour's."""
+    m, E, top = 100, 32, 5
+    g = gen(23)
+    row = torch.randn(E, generator=g)
+    logits = row.expand(m, E).clone()
+    s = torch.sigmoid(row.double())
+    bias = torch.zeros(E)
+    for e in range(1, E, 2):
+        # neighbours' scores differ by less than 2^-10, so that this bias's fp32
+        # rounding is below 2^-35 = 3e-11
+        row[e] = row[e - 1] + 1e-4 * (e + 1)
+        s[e] = torch.sigmoid(row[e].double())
+        bias[e] = float(s[e - 1] - s[e])
+    logits = row.expand(m, E).contiguous()
+    keys = s + bias.double()
+    gap = (keys[0::2] - keys[1::2]).abs()
+    assert float(gap.max()) < 2.0 ** -30 and float(gap.min()) > 1e-14
+    check_route(logits.cuda(), top, bias=bias.cuda(), score="sigmoid", groups=groups,
+                top_groups=max(1, groups // 2))
+
+
 def test_route_no_tokens_and_padded_rows():
     E, top = 12, 3
     w, e, off, tok, slots = run_route(torch.zeros(0, E, device="cuda"), top)
