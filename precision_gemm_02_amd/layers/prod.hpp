@@ -24,7 +24,6 @@ enum Order { kInner = 0, kOuter = 1 };
 enum Mode { kDense = 0, kRows = 1, kSums = 2 };
 
 typedef float f32x4 __attribute__((ext_vector_type(4)));
-typedef float f32x16 __attribute__((ext_vector_type(16)));
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
 typedef short s16x4 __attribute__((ext_vector_type(4)));
@@ -42,11 +41,11 @@ __device__ __forceinline__ u32x4 load16(const void* p) {
 }
 __device__ __forceinline__ void store16(void* p, u32x4 v) { static_cast<Bytes16*>(p)->v = v; }
 
-// D += A B for one 16 x 16 (mfma) or 32 x 32 (mfma32) block: one 16-byte chunk
-// of the summed index per lane.  Lane l = BLK g + i gives row i of A and column
-// i of B, chunk g.  fp32 takes it in four instructions (lane group g: index
-// 4 g + s at instruction s); both operands use the same order, so every product
-// is formed once.
+// D(16 x 16) += A B: one 16-byte chunk of the summed index per lane.  Lane
+// l = 16 g + i gives row i of A and column i of B, chunk g.  fp32 takes it in
+// four instructions (lane group g: index 4 g + s at instruction s); both
+// operands use the same order, so every product is formed once.  (32 x 32
+// blocks were 3 to 5 % slower in the large tiles on random data.)
 template <typename T>
 struct Elem;
 template <>
@@ -54,10 +53,6 @@ struct Elem<__bf16> {
   static constexpr int kMfmas = 1;
   static __device__ __forceinline__ f32x4 mfma(u32x4 a, u32x4 b, f32x4 c) {
     return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, a),
-                                                   __builtin_bit_cast(bf16x8, b), c, 0, 0, 0);
-  }
-  static __device__ __forceinline__ f32x16 mfma32(u32x4 a, u32x4 b, f32x16 c) {
-    return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, a),
                                                    __builtin_bit_cast(bf16x8, b), c, 0, 0, 0);
   }
 };
@@ -68,10 +63,6 @@ struct Elem<_Float16> {
     return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8, a),
                                                   __builtin_bit_cast(f16x8, b), c, 0, 0, 0);
   }
-  static __device__ __forceinline__ f32x16 mfma32(u32x4 a, u32x4 b, f32x16 c) {
-    return __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(f16x8, a),
-                                                  __builtin_bit_cast(f16x8, b), c, 0, 0, 0);
-  }
 };
 template <>
 struct Elem<float> {
@@ -80,12 +71,6 @@ struct Elem<float> {
     const f32x4 x = __builtin_bit_cast(f32x4, a), y = __builtin_bit_cast(f32x4, b);
 #pragma unroll
     for (int s = 0; s < 4; ++s) c = __builtin_amdgcn_mfma_f32_16x16x4f32(x[s], y[s], c, 0, 0, 0);
-    return c;
-  }
-  static __device__ __forceinline__ f32x16 mfma32(u32x4 a, u32x4 b, f32x16 c) {
-    const f32x4 x = __builtin_bit_cast(f32x4, a), y = __builtin_bit_cast(f32x4, b);
-#pragma unroll
-    for (int s = 0; s < 4; ++s) c = __builtin_amdgcn_mfma_f32_32x32x2f32(x[s], y[s], c, 0, 0, 0);
     return c;
   }
 };

@@ -31,7 +31,7 @@ __global__ __launch_bounds__(WAVES * 64) void prod_rows_kernel(const ProdArgs a)
   constexpr int STG = LB == kOuter ? WAVES * BN * 128 : 0;
   constexpr int LDS = RED > STG ? RED : STG;
   __shared__ __attribute__((aligned(128))) char lds[LDS];
-  using TB = OperandTile<T, kOuter, BN, 64, 16>;
+  using TB = OperandTile<T, kOuter, BN, 64>;
 
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int g = lane >> 4, i = lane & 15;

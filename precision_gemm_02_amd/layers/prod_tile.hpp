@@ -15,16 +15,12 @@ static __device__ const u32x4 kZeroChunk = {0, 0, 0, 0};
 
 // One operand's tile: `EXT` output indices by 128 bytes' worth of the summed
 // index (BK = 64 16-bit or 32 fp32 elements), in 16-byte chunks, read in
-// fragments of BLK output indices (16 or 32, the matrix instruction's block).
-// A fragment's step is one chunk per lane: 64 / BLK chunks of the summed
-// index.
+// fragments of 16 output indices by 64 bytes (two steps per tile).
 //
 // Inner order: LDS row r holds output index r, 8 chunks along the summed
-// index; chunk c sits at c ^ flip(r).  A b128 read serves the 8-lane blocks b
-// and b ^ 3 together.  16-blocks: flip(r) = r & 7; of the two 8-row blocks one
-// reads chunk c and the other c ^ 1, so their flipped positions never meet.
-// 32-blocks: both read chunk c of rows 8 or 24 apart, and bit 3 of the row
-// enters the flip.
+// index; chunk c sits at c ^ (r & 7).  A b128 read serves the 8-lane blocks b
+// and b ^ 3 together; of these one reads chunk c and the other c ^ 1, so their
+// flipped positions never meet.
 //
 // Outer order: LDS row p holds summed index p, EXT contiguous output indices.
 // 16-bit operands are read through the transposing ds_read_b64_tr_b16 (16
@@ -32,7 +28,7 @@ static __device__ const u32x4 kZeroChunk = {0, 0, 0, 0};
 // b32 per inner index.  The 32-byte (16-bit) or 64-byte (fp32) pieces that
 // 16 columns take from a row are flipped by the row so that the pieces read
 // together fall into different banks.
-template <typename T, int ORDER, int EXT, int NT, int BLK>
+template <typename T, int ORDER, int EXT, int NT>
 struct OperandTile {
   static constexpr int S = sizeof(T);
   static constexpr int V = 16 / S;              // elements per chunk
@@ -41,29 +37,21 @@ struct OperandTile {
   static constexpr int ROW_CHUNKS = ORDER == kInner ? 8 : EXT / V;
   static constexpr int ROW_BYTES = ROW_CHUNKS * 16;
   static constexpr int LOADS = BYTES / (16 * NT);
-  static constexpr int STEPS = BLK / 8;         // per tile
   static constexpr int READS = ORDER == kInner ? 1 : S;   // LDS reads per fragment
   static_assert(BYTES % (16 * NT) == 0, "whole chunks per thread");
   // outer order: pieces of 16 output indices per row
   static constexpr int PIECE = 16 * S;          // bytes
   static constexpr int PIECES = EXT / 16;
 
-  static __device__ __forceinline__ int row_flip(int r) {
-    return BLK == 16 ? r & 7 : (r & 7) ^ ((r >> 3) & 1);
-  }
-
   // The flip of row p's pieces (outer order).
   static __device__ __forceinline__ int flip(int p) {
+    constexpr int b = PIECES >= 8 ? 3 : PIECES == 4 ? 2 : PIECES == 2 ? 1 : 0;
     if constexpr (S == 2) {
-      // 16-blocks: a half wave reads one piece of 8 rows (p & 3, bit 3);
-      // 32-blocks: two neighbouring pieces of 4 rows
-      const int q = BLK == 16 ? (p & 3) | (((p >> 3) & 1) << 2) : (p & 3) << 1;
-      constexpr int b = PIECES >= 8 ? 3 : PIECES == 4 ? 2 : PIECES == 2 ? 1 : 0;
-      return BLK == 16 ? q >> (3 - b) : q & ((1 << b) - 1);
+      // a half wave reads one piece of 8 rows (p & 3, bit 3 of p)
+      return ((p & 3) | (((p >> 3) & 1) << 2)) >> (3 - b);
     } else {
-      // 16-blocks: one piece of four rows 4 apart; 32-blocks: two neighbouring
-      // pieces of two such rows
-      return BLK == 16 ? (p >> 2) & (PIECES >= 4 ? 3 : PIECES == 2 ? 1 : 0) : PIECES >= 4 ? ((p >> 2) & 1) << 1 : 0;
+      // one piece of four rows 4 apart
+      return (p >> 2) & (b >= 2 ? 3 : b);
     }
   }
 
@@ -72,44 +60,42 @@ struct OperandTile {
     const int r = s / ROW_CHUNKS, pos = s % ROW_CHUNKS;
     *row = r;
     if constexpr (ORDER == kInner) {
-      *chunk = pos ^ row_flip(r);
+      *chunk = pos ^ (r & 7);
     } else {
       constexpr int CPP = PIECE / 16;           // chunks per piece: 2 or 4
       *chunk = ((pos / CPP) ^ flip(r)) * CPP + pos % CPP;
     }
   }
 
-  // Fragment of block b (from index `first`), step s, from the tile at lds.
+  // Fragment of 16-index block b (from index `first`), step s, from the tile at
+  // lds.
   static __device__ __forceinline__ u32x4 frag(const char* lds, int first, int b, int s) {
-    constexpr int GROUPS = 64 / BLK;            // lane groups along the summed index
-    const int l = threadIdx.x & 63, g = l / BLK, i = l % BLK;
+    const int l = threadIdx.x & 63, g = l >> 4, i = l & 15;
     if constexpr (ORDER == kInner) {
-      const int row = first + BLK * b + i;
-      const int c = (GROUPS * s + g) ^ row_flip(i);
+      const int row = first + 16 * b + i, c = (4 * s + g) ^ (i & 7);
       return *reinterpret_cast<const u32x4*>(lds + row * 128 + c * 16);
-    } else if constexpr (S == 2) {
-      u32x4 out;
-      const int piece = (first + BLK * b + (i & ~15)) / 16, i16 = i & 15;
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const int p = 8 * (GROUPS * s + g) + 4 * h + (i16 >> 2);
-        const int f = flip(8 * g + (i16 >> 2));  // s and h do not enter
-        const char* at = lds + p * ROW_BYTES + (piece ^ f) * PIECE + (i16 & 3) * 8;
-        const s16x4 v = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
-            (__attribute__((address_space(3))) s16x4*)(const_cast<char*>(at)));
-        const u32x2 w = __builtin_bit_cast(u32x2, v);
-        out[2 * h] = w[0];
-        out[2 * h + 1] = w[1];
-      }
-      return out;
     } else {
       u32x4 out;
-      const int piece = (first + BLK * b + (i & ~15)) / 16, i16 = i & 15;
+      const int piece = first / 16 + b;
+      if constexpr (S == 2) {
 #pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        const int p = 4 * (GROUPS * s + g) + q;
-        const char* at = lds + p * ROW_BYTES + (piece ^ flip(p)) * PIECE + i16 * 4;
-        out[q] = *reinterpret_cast<const uint32_t*>(at);
+        for (int h = 0; h < 2; ++h) {
+          const int p = 32 * s + 8 * g + 4 * h + (i >> 2);
+          const int f = flip(8 * g + (i >> 2));   // 32 s and 4 h do not enter
+          const char* at = lds + p * ROW_BYTES + (piece ^ f) * PIECE + (i & 3) * 8;
+          const s16x4 v = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+              (__attribute__((address_space(3))) s16x4*)(const_cast<char*>(at)));
+          const u32x2 w = __builtin_bit_cast(u32x2, v);
+          out[2 * h] = w[0];
+          out[2 * h + 1] = w[1];
+        }
+      } else {
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          const int p = 16 * s + 4 * g + q;
+          const char* at = lds + p * ROW_BYTES + (piece ^ flip(4 * g)) * PIECE + i * 4;
+          out[q] = *reinterpret_cast<const uint32_t*>(at);
+        }
       }
       return out;
     }
@@ -159,6 +145,27 @@ __device__ __forceinline__ u32x4 load_whole(const T* row, int c0) {
   return load16(row != nullptr ? (const void*)(row + c0) : (const void*)&kZeroChunk);
 }
 
+// 16 bytes per lane from its own address straight to LDS: lane l of the wave
+// writes at to + 16 l (`to` is the same for all lanes).  Written as the
+// instruction, without a memory clobber: behind the builtin the compiler waits
+// for all loads before every transposing LDS read (it cannot tell their slots
+// apart), which cost outer-order operands the whole overlap.  The order that
+// matters is kept by hand: wait_loads and workgroup_barrier are volatile, like
+// this, and clobber memory; between two barriers no slot is both loaded and
+// read (see the K loop).  There is no register output, and the address
+// registers are read at issue.  m0 is reserved, so the compiler does not name it
+// as a clobber; these kernels use it for nothing else.
+__device__ __forceinline__ void load_to_lds(const void* from, char* to) {
+  const int at = __builtin_amdgcn_readfirstlane(
+      (int)(uint32_t)(uintptr_t)(__attribute__((address_space(3))) char*)to);
+  asm volatile(
+      "s_mov_b32 m0, %0\n\t"
+      "s_nop 0\n\t"
+      "global_load_lds_dwordx4 %1, off"
+      :
+      : "s"(at), "v"(from));
+}
+
 // One operand's loads, tile after tile of the summed index.
 //
 // DIRECT: straight into LDS (global_load_lds_dwordx4: a wave writes 64
@@ -171,7 +178,7 @@ __device__ __forceinline__ u32x4 load_whole(const T* row, int c0) {
 // Otherwise the chunks go through registers, with guards.
 template <typename T, int ORDER, int EXT, int NT, bool DIRECT, bool GATHER>
 struct Loader {
-  using Tile = OperandTile<T, ORDER, EXT, NT, 32>;
+  using Tile = OperandTile<T, ORDER, EXT, NT>;
   static constexpr int L = Tile::LOADS;
   Source<T> src;
   int first;                       // first output index of the tile
@@ -247,10 +254,7 @@ struct Loader {
         const bool in = ORDER == kInner ? k + c * Tile::V < src.inner : k + r < src.outer;
         const void* from = in ? (const void*)p : (const void*)&kZeroChunk;
         // a wave's 64 chunks; the same LDS base for all its lanes
-        char* to = lds + (j * NT + ((int)threadIdx.x & ~63)) * 16;
-        __builtin_amdgcn_global_load_lds(
-            (const __attribute__((address_space(1))) void*)from,
-            (__attribute__((address_space(3))) void*)to, 16, 0, 0);
+        load_to_lds(from, lds + (j * NT + ((int)threadIdx.x & ~63)) * 16);
       } else if constexpr (WHOLE) {
         reg[j] = load16(p);
       } else {
@@ -338,12 +342,12 @@ __device__ __forceinline__ void spread() {
 template <typename T, int LA, int LB, int BM, int BN, int WGM, int WGN, bool DIRECT, int MODE>
 __global__ __launch_bounds__(WGM* WGN * 64) void prod_tile_kernel(const ProdArgs a) {
   constexpr int NT = WGM * WGN * 64;
-  constexpr int WM = BM / WGM, WN = BN / WGN, RB = WM / 32, CB = WN / 32;
+  constexpr int WM = BM / WGM, WN = BN / WGN, RB = WM / 16, CB = WN / 16;
   constexpr int BK = 128 / (int)sizeof(T);
   constexpr int SLOT = (BM > BN ? BM : BN) * 128;   // one operand's tile
   constexpr int SLOTS = DIRECT ? 5 : 4;
   constexpr int EPI_LD = WN + 4;
-  constexpr int EPI = WGM * WGN * 32 * EPI_LD * 4;
+  constexpr int EPI = WGM * WGN * 32 * EPI_LD * 4;   // 32 rows per wave
   constexpr int LDS = SLOTS * SLOT > EPI ? SLOTS * SLOT : EPI;
   __shared__ __attribute__((aligned(128))) char lds[LDS];
 
@@ -391,8 +395,8 @@ __global__ __launch_bounds__(WGM* WGN * 64) void prod_tile_kernel(const ProdArgs
   }
   if constexpr (MODE == kDense) sa.gather = nullptr;
 
-  using TA = OperandTile<T, LA, BM, NT, 32>;
-  using TB = OperandTile<T, LB, BN, NT, 32>;
+  using TA = OperandTile<T, LA, BM, NT>;
+  using TB = OperandTile<T, LB, BN, NT>;
   // (a grouped sum's rows may be gathered on either side)
   using LoadA = Loader<T, LA, BM, NT, DIRECT, MODE == kSums>;
   using LoadB = Loader<T, LB, BN, NT, DIRECT, MODE == kSums>;
@@ -401,20 +405,19 @@ __global__ __launch_bounds__(WGM* WGN * 64) void prod_tile_kernel(const ProdArgs
   la.init(sa, row0, k_lo);
   lb.init(sb, col0, k_lo);
 
-  f32x16 acc[RB][CB];
+  f32x4 acc[RB][CB];
 #pragma unroll
   for (int r = 0; r < RB; ++r)
 #pragma unroll
-    for (int c = 0; c < CB; ++c)
-#pragma unroll
-      for (int q = 0; q < 16; ++q) acc[r][c][q] = 0;
+    for (int c = 0; c < CB; ++c) acc[r][c] = f32x4{0, 0, 0, 0};
 
-  // The K loop, in G = 4 steps of 32 bytes of the summed index per tile.  While
-  // the matrix cores run a step, the operands of the next are read from LDS
-  // into the other registers; the last step of a tile reads the next tile's
-  // first operands.  The one barrier per tile stands before that last step,
-  // whose operands are already in registers: behind it every wave has read all
-  // of this tile and the next tile has landed.
+  // The K loop.  A tile's two steps (64 bytes of the summed index each) are cut
+  // into G groups of one pair of A blocks against all B blocks.  While the
+  // matrix cores run a group, the operands of the next are read from LDS into
+  // the other registers; the last group of a tile reads the next tile's first
+  // operands.  The one barrier per tile stands before that last group, whose
+  // operands are already in registers: behind it every wave has read all of
+  // this tile and the next tile has landed.
   //
   // Operand tiles A(0), B(0), A(1), B(1), ... follow each other through a ring of
   // LDS slots.  Direct loads use five of them (all of a compute unit's 160 KiB
@@ -424,14 +427,16 @@ __global__ __launch_bounds__(WGM* WGN * 64) void prod_tile_kernel(const ProdArgs
   // awaited at its end: 25.2 against 22 ns per inner index at 4096 x 4096.)
   // Register loads use four: tile t + 1 is stored during tile t, tile t + 2
   // fetched.
-  constexpr int G = TA::STEPS;
-  static_assert(G == 4, "the loads' places below");
-  u32x4 fa[2][RB], fb[2][CB];
-  auto read = [&](const char* a_slot, const char* b_slot, int s, int into) {
+  constexpr int GP = RB / 2, G = 2 * GP;
+  static_assert(RB % 2 == 0 && (G == 2 || G % 4 == 0), "the loads' places below");
+  u32x4 fa[2][2], fb[2][CB];
+  auto read_a = [&](const char* a_slot, int g) {
+    fa[g & 1][0] = TA::frag(a_slot, wm, 2 * (g % GP), g / GP);
+    fa[g & 1][1] = TA::frag(a_slot, wm, 2 * (g % GP) + 1, g / GP);
+  };
+  auto read_b = [&](const char* b_slot, int step) {
 #pragma unroll
-    for (int c = 0; c < CB; ++c) fb[into][c] = TB::frag(b_slot, wn, c, s);
-#pragma unroll
-    for (int r = 0; r < RB; ++r) fa[into][r] = TA::frag(a_slot, wm, r, s);
+    for (int c = 0; c < CB; ++c) fb[step][c] = TB::frag(b_slot, wn, c, step);
   };
   auto slot = [&](int i) { return lds + (i >= SLOTS ? i - SLOTS : i) * SLOT; };
   constexpr int HA = LoadA::L / 2, HB = LoadB::L / 2;
@@ -453,7 +458,8 @@ __global__ __launch_bounds__(WGM* WGN * 64) void prod_tile_kernel(const ProdArgs
       }
     }
     workgroup_barrier();
-    read(slot(0), slot(1), 0, 0);
+    read_a(slot(0), 0);
+    read_b(slot(1), 0);
     int at = 0;                                // slot of A(kt)
     for (int kt = 0; kt < nk; ++kt) {
       char *const a0 = slot(at), *const b0 = slot(at + 1);
@@ -471,31 +477,50 @@ __global__ __launch_bounds__(WGM* WGN * 64) void prod_tile_kernel(const ProdArgs
         }
       }
       static_for<G>([&](auto gc) {
-        constexpr int g = decltype(gc)::value;
+        constexpr int g = decltype(gc)::value, step = g / GP, p = g % GP;
+        // reads first: the compiler keeps LDS reads behind loads into LDS
         if constexpr (g == G - 1) {
           // all but A(t + 2) has landed
           if constexpr (DIRECT) wait_loads<LoadA::L>();
           workgroup_barrier();
-          read(a1, b1, 0, 0);     // past the last tile: some LDS, never used
+          read_a(a1, 0);          // past the last tile: some LDS, never used
+          read_b(b1, 0);
         } else {
-          // reads first: the compiler keeps LDS reads behind loads into LDS
-          read(a0, b0, g + 1, (g + 1) & 1);
+          read_a(a0, g + 1);
+          if constexpr (p == GP - 1) read_b(b0, 1);
         }
-        if constexpr (DIRECT) {
-          if constexpr (g == 0) lb.template load<HB, LoadB::L>(b1);
-          if constexpr (g == 1) la.template load<0, HA>(a2);
-          if constexpr (g == 2) la.template load<HA, LoadA::L>(a2);
-          if constexpr (g == 3) lb.template load<0, HB>(b2);
+        // the rest of B(t + 1), A(t + 2), and behind the barrier the first half
+        // of B(t + 2), by quarters of the tile's groups
+        constexpr int Q = G < 4 ? 1 : G / 4, q = g / Q, h = g % Q;
+        constexpr int IB = LoadB::L - HB, IA = LoadA::L - HA;
+        if constexpr (DIRECT && G == 2) {
+          if constexpr (g == 0) {
+            lb.template load<HB, LoadB::L>(b1);
+            la.template load<0, LoadA::L>(a2);
+          } else {
+            lb.template load<0, HB>(b2);
+          }
+        } else if constexpr (DIRECT) {
+          if constexpr (q == 0) lb.template load<HB + IB * h / Q, HB + IB*(h + 1) / Q>(b1);
+          if constexpr (q == 1) la.template load<HA * h / Q, HA*(h + 1) / Q>(a2);
+          if constexpr (q == 2) la.template load<HA + IA * h / Q, HA + IA*(h + 1) / Q>(a2);
+          if constexpr (g == G - 1) lb.template load<0, HB>(b2);
         }
         // B's block as the instruction's rows: a lane then holds four
-        // consecutive columns of one row of D per four registers
+        // consecutive columns of one row of D
 #pragma unroll
-        for (int r = 0; r < RB; ++r)
+        for (int r = 0; r < 2; ++r)
 #pragma unroll
           for (int c = 0; c < CB; ++c)
-            acc[r][c] = Elem<T>::mfma32(fb[g & 1][c], fa[g & 1][r], acc[r][c]);
-        spread<RB * TA::READS + CB * TB::READS, RB * CB * Elem<T>::kMfmas,
-               DIRECT ? (g == 1 || g == 2 ? HA : HB) : 0>();
+            acc[2 * p + r][c] = Elem<T>::mfma(fb[step][c], fa[g & 1][r], acc[2 * p + r][c]);
+        constexpr int loads = !DIRECT        ? 0
+                              : G == 2       ? (g == 0 ? LoadA::L + IB : HB)
+                              : g == G - 1   ? HB
+                              : q == 3       ? 0
+                              : q == 0       ? IB / Q
+                                             : HA / Q;
+        spread<2 * TA::READS + (p == GP - 1 ? CB * TB::READS : 0), 2 * CB * Elem<T>::kMfmas,
+               loads>();
         __builtin_amdgcn_sched_barrier(0);
       });
     }
@@ -522,7 +547,7 @@ __global__ __launch_bounds__(WGM* WGN * 64) void prod_tile_kernel(const ProdArgs
   float b8[8];
   load_bias<T>(a, split ? nullptr : bias, n, b8);
 #pragma unroll 1
-  for (int r = 0; r < RB; ++r) {
+  for (int r = 0; r < RB / 2; ++r) {
     const int m0 = row0 + wm + 32 * r + lane / LPR;
     Raw8 res[PASSES] = {};
     if (a.R != nullptr && !split && n + 8 <= a.N) {
@@ -530,17 +555,15 @@ __global__ __launch_bounds__(WGM* WGN * 64) void prod_tile_kernel(const ProdArgs
       for (int p = 0; p < PASSES; ++p)
         if (m0 + p * RPP < rows) res[p] = load_residual<T>(a, m0 + p * RPP, n);
     }
-    static_for<RB>([&](auto rc) {
+    static_for<RB / 2>([&](auto rc) {
       constexpr int q = decltype(rc)::value;
       if (r == q) {
 #pragma unroll
-        for (int c = 0; c < CB; ++c)
+        for (int h = 0; h < 2; ++h)
 #pragma unroll
-          for (int x = 0; x < 4; ++x)
-            *reinterpret_cast<f32x4*>(stg + (lane & 31) * EPI_LD + 32 * c + 8 * x +
-                                      4 * (lane >> 5)) =
-                f32x4{acc[q][c][4 * x], acc[q][c][4 * x + 1], acc[q][c][4 * x + 2],
-                      acc[q][c][4 * x + 3]};
+          for (int c = 0; c < CB; ++c)
+            *reinterpret_cast<f32x4*>(stg + (16 * h + (lane & 15)) * EPI_LD + 16 * c +
+                                      4 * (lane >> 4)) = acc[2 * q + h][c];
       }
     });
     __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
