@@ -71,60 +71,85 @@ bool operand_direct(const void* p, long long ld, int size, int inner, long long 
   return aligned_to(p, 16) && ld % v == 0 && inner % v == 0 && stride % v == 0;
 }
 
-// Sustained rate of one compute unit's tiles (flop/s) and the fixed time of a
-// tile (seconds), by class.
-double class_rate(int kernel, int size) {
-  static const double r16[3] = {1.1e15, 0.85e15, 0.4e15};
-  static const double r32[3] = {0, 130e12, 100e12};
-  return (size == 2 ? r16[kernel] : r32[kernel]) / kUnits;
+// A tile class's time, fitted to 15 dense shapes in both weight orders (64 to
+// 8192 rows) and 5 expert shapes, every class timed on each: the flop rate of
+// `together` workgroups that share a compute unit, the share of it that fewer
+// of them reach, and the fixed time of each such group (prologue, epilogue).
+struct ClassTime {
+  double rate;             // of the whole chip
+  double fixed;            // seconds
+  int together;
+  double part[4];          // by workgroups left over (0: unused)
+};
+ClassTime class_time(int kernel, int size) {
+  static const ClassTime t16[3] = {{1.35e15, 10e-6, 1, {0, 0, 0, 0}},
+                                   {1.10e15, 7e-6, 2, {0, 0.7, 0, 0}},
+                                   {0.60e15, 3.5e-6, 4, {0, 0.5, 0.75, 0.9}}};
+  static const ClassTime t32[3] = {{0, 0, 1, {0, 0, 0, 0}},
+                                   {130e12, 4e-6, 2, {0, 0.93, 0, 0}},
+                                   {119e12, 3e-6, 4, {0, 0.8, 0.9, 0.95}}};
+  return (size == 2 ? t16 : t32)[kernel];
 }
 
-// Splits of the summed index that give every compute unit about `want`
-// workgroups, each at least `least` inner indices (multiples of `unit`).
-int split_for(long long wgs, long long want, int k, int least) {
-  long long s = want / (wgs > 0 ? wgs : 1);
-  if (s > k / least) s = k / least;
-  if (s > 64) s = 64;
-  return s < 1 ? 1 : (int)s;
+double tiles_time(const ClassTime& c, double tiles, double tile_flops) {
+  const long long whole = (long long)tiles;
+  const long long per = ceil_div(whole + (tiles > (double)whole ? 1 : 0), kUnits);
+  const double one = tile_flops / (c.rate / kUnits);
+  const long long full = per / c.together, left = per % c.together;
+  double t = (double)full * (c.together * one + c.fixed);
+  if (left > 0) t += (double)left * one / c.part[left] + c.fixed;
+  return t;
 }
 
-// rows: the rows of D that one launch expects per group (an average; any
-// distribution is correct).
-Plan plan_product(int size, int la, int lb, int mode, long long rows, int groups, int n, int k,
-                  bool direct, size_t ws_bytes, bool any_ws) {
+// rows: the rows of D over all groups (how they are distributed is not known
+// here; any distribution is correct).  may_split: the summed index may be
+// shared by workgroups, through partial sums in `ws_bytes` bytes (any_ws: as
+// many as it takes).
+Plan plan_product(int size, int la, int mode, long long rows, int groups, int n, int k,
+                  bool direct, size_t ws_bytes, bool any_ws, bool may_split = true) {
   Plan p;
   p.direct = direct;
   const int bk = 128 / size;
-  const long long per = mode == kRows ? ceil_div(rows, groups > 0 ? groups : 1) : rows;
+  if (mode != kDense) may_split = false;
+  if (mode == kRows && groups > rows) groups = (int)rows;
+  const double per = mode == kRows ? (double)rows / groups : (double)rows;
   if (la == kInner && per <= 32) {
     // Few rows: B is read once, the rest is latency.  The few-rows kernel
     // takes 16 or 32 rows per pass and never needs a tile of operands.
     const long long wide = ceil_div(n, 64) * (mode == kRows ? groups : 1);
     if (wide >= 2 * kUnits) p.kernel = per <= 16 ? kFew16Wide : kFew32Wide;
     else p.kernel = per <= 16 ? kFew16 : kFew32;
-    if (mode == kDense)
-      p.splits = split_for(ceil_div(n, few_columns(p.kernel)), kUnits, k, 16 * bk);
+    if (may_split) {
+      // one split per free compute unit, each of 16 units of 128 bytes at least
+      long long s = kUnits / ceil_div(n, few_columns(p.kernel));
+      if (s > k / (16 * bk)) s = k / (16 * bk);
+      p.splits = s < 1 ? 1 : s > 64 ? 64 : (int)s;
+    }
   } else {
     double best = 0;
     for (int c = 0; c < 3; ++c) {
       if (c == kTile256 && (size == 4 || !direct)) continue;
       const int bm = kShape[c].bm, bn = kShape[c].bn;
-      const int co = c == kTile256 ? 1 : c == kTile128 ? 2 : 4;   // workgroups that share a unit
-      long long tiles = ceil_div(n, bn);
-      if (mode == kRows) tiles *= ceil_div(rows, bm) + (groups < rows ? groups : rows) / 2;
-      else tiles *= ceil_div(rows, bm);
-      if (mode == kSums) tiles *= groups;
-      const double depth = mode == kSums ? (double)k / (groups > 0 ? groups : 1) : (double)k;
-      int s = 1;
-      if (mode == kDense && tiles < kUnits) s = split_for(tiles, kUnits * co, k, 4 * bk);
-      const double waves = (double)ceil_div(tiles * s, kUnits);
-      double t = waves * (2.0 * bm * bn * (depth / s) / class_rate(c, size)) +
-                 (double)ceil_div(tiles * s, kUnits * co) * 2e-6;
-      if (s > 1) t += 3e-6 + (double)s * (double)rows * n * 8 / 4e12;
-      if (best == 0 || t < best) {
-        best = t;
-        p.kernel = c;
-        p.splits = s;
+      // tiles that are half empty waste the loads too (512 tokens, top 8 of
+      // 64 experts, 1024 x 1024: 39 us with 64-row tiles, 45 with 128)
+      if (mode == kRows && c != kTile64 && 2 * per <= bm) continue;
+      double tiles = (double)ceil_div(n, bn);
+      if (mode == kRows) tiles *= groups * (per / bm > 0.5 ? per / bm + 0.5 : 1.0);
+      else tiles *= (double)ceil_div(rows, bm) * (mode == kSums ? groups : 1);
+      const double depth = mode == kSums ? (double)k / groups : (double)k;
+      const ClassTime ct = class_time(c, size);
+      for (int s = 1; s <= 64; s *= 2) {
+        if (s > 1 &&
+            (!may_split || k / s < 4 * bk || tiles * s > (double)kUnits * ct.together))
+          break;
+        // the partial sums' traffic, and the launch that adds them
+        const double split = s > 1 ? 4e-6 + (double)s * (double)rows * n * 8 / 6e12 : 0;
+        const double t = tiles_time(ct, tiles * s, 2.0 * bm * bn * depth / s) + split;
+        if (best == 0 || t < best) {
+          best = t;
+          p.kernel = c;
+          p.splits = s;
+        }
       }
     }
   }
@@ -132,16 +157,17 @@ Plan plan_product(int size, int la, int lb, int mode, long long rows, int groups
     p.k_split = (int)round_up(ceil_div(k, p.splits), bk);
     p.splits = (int)ceil_div(k, p.k_split);
     const size_t need = (size_t)p.splits * (size_t)rows * (size_t)n * 4;
-    if (!any_ws && ws_bytes < need) p.splits = 1;
+    if (!any_ws && ws_bytes < need)   // the best plan that needs no space
+      return plan_product(size, la, mode, rows, groups, n, k, direct, 0, false, false);
   }
   return p;
 }
 
 // Workspace that plan_product may use for a dense product, over any alignment.
-size_t split_bytes(int size, int la, int lb, int rows, int n, int k) {
+size_t split_bytes(int size, int la, int rows, int n, int k) {
   size_t most = 0;
   for (int d = 0; d < 2; ++d) {
-    const Plan p = plan_product(size, la, lb, kDense, rows, 1, n, k, d != 0, 0, true);
+    const Plan p = plan_product(size, la, kDense, rows, 1, n, k, d != 0, 0, true);
     const size_t b = p.splits > 1 ? (size_t)p.splits * (size_t)rows * (size_t)n * 4 : 0;
     if (b > most) most = b;
   }
@@ -155,7 +181,7 @@ int run_product(ProdArgs a, int dtype, int la, int lb, int mode, long long rows,
   const bool direct =
       operand_direct(a.A, a.lda, size, la == kInner ? (mode == kSums ? 0 : a.K) : a.M, 0) &&
       operand_direct(a.B, a.ldb, size, lb == kInner ? a.K : a.N, mode == kRows ? a.strideB : 0);
-  const Plan p = plan_product(size, la, lb, mode, rows, a.groups, a.N, mode == kSums ? a.rows : a.K,
+  const Plan p = plan_product(size, la, mode, rows, a.groups, a.N, mode == kSums ? a.rows : a.K,
                               direct, ws == nullptr ? 0 : ws_bytes, false);
   a.splits = p.splits;
   a.k_split = p.k_split;
@@ -213,14 +239,11 @@ BackSpace back_space(const pgemm_kind& kind, long long rows, int n, int k, int g
   b.chunks = slope_chunks(rows, groups, n);
   b.rest = (size_t)groups * (size_t)b.chunks * (size_t)n * 4;
   if (groups == 1 && rows <= INT32_MAX) {
-    for (int lb = 0; lb < 2; ++lb) {
-      const size_t x = split_bytes(size, kInner, lb, (int)rows, k, n);
+    const size_t parts[3] = {split_bytes(size, kInner, (int)rows, k, n),
+                             split_bytes(size, kOuter, k, n, (int)rows),
+                             split_bytes(size, kOuter, n, k, (int)rows)};
+    for (const size_t x : parts)
       if (x > b.rest) b.rest = x;
-    }
-    const size_t w = split_bytes(size, kOuter, kOuter, k, n, (int)rows),
-                 v = split_bytes(size, kOuter, kOuter, n, k, (int)rows);
-    if (w > b.rest) b.rest = w;
-    if (v > b.rest) b.rest = v;
   }
   b.rest = align256(b.rest);
   return b;
@@ -366,9 +389,7 @@ int pgemm_linear(pgemm_kind kind, int m, int n, int k, pgemm_rows X, pgemm_weigh
 
 size_t pgemm_linear_workspace(int dtype, int m, int n, int k) {
   if (!known(dtype) || m <= 0 || n <= 0 || k <= 0) return 0;
-  const size_t a = split_bytes(size_of(dtype), kInner, kInner, m, n, k);
-  const size_t b = split_bytes(size_of(dtype), kInner, kOuter, m, n, k);
-  return a > b ? a : b;
+  return split_bytes(size_of(dtype), kInner, m, n, k);
 }
 
 int pgemm_linear_backward(pgemm_kind kind, int m, int n, int k, pgemm_rows dY, pgemm_rows Z,
