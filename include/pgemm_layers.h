@@ -202,6 +202,23 @@ int pgemm_combine_backward(int dtype, int m, int n, int top, int rows, pgemm_row
                            pgemm_rows Y, const int *slots, const float *weights, pgemm_rows dY,
                            float *dweights, void *stream);
 
+/*
+ * For bindings: a call with all its arguments in one struct, in the order and
+ * types of the function's parameters (each at its natural alignment, the
+ * stream last).  Returns the function's status, or -1 for an unknown op.
+ */
+enum {
+  PGEMM_OP_LINEAR = 0,
+  PGEMM_OP_LINEAR_BACKWARD = 1,
+  PGEMM_OP_ROUTE = 2,
+  PGEMM_OP_ROUTE_BACKWARD = 3,
+  PGEMM_OP_EXPERT_LINEAR = 4,
+  PGEMM_OP_EXPERT_LINEAR_BACKWARD = 5,
+  PGEMM_OP_COMBINE = 6,
+  PGEMM_OP_COMBINE_BACKWARD = 7
+};
+int pgemm_layer_call(int op, const void *args);
+
 #ifdef __cplusplus
 }
 #endif

@@ -13,6 +13,7 @@ enqueued on ``stream`` (default: torch's current stream) and returns at once.
 from __future__ import annotations
 
 import ctypes
+import struct
 
 import torch
 
@@ -49,17 +50,47 @@ class _Plan(ctypes.Structure):
 EXPORTS = ("pgemm_linear", "pgemm_linear_workspace", "pgemm_linear_backward",
            "pgemm_linear_backward_workspace", "pgemm_route", "pgemm_route_workspace",
            "pgemm_route_backward", "pgemm_expert_linear", "pgemm_expert_linear_backward",
-           "pgemm_expert_linear_backward_workspace", "pgemm_combine", "pgemm_combine_backward")
+           "pgemm_expert_linear_backward_workspace", "pgemm_combine", "pgemm_combine_backward",
+           "pgemm_layer_call")
 
 _lib = None
 _check = None
-_NO_ROWS = _Rows(None, 1)
-_NO_WEIGHT = _Weight(None, 1, _KN, 0)
+_call = None            # pgemm_layer_call
+
+# The arguments of pgemm_layer_call, by op: a call's parameters in order (P
+# pointers, q and N 64-bit sizes, each at its natural alignment).  Packed
+# arguments cost a call about 4 us less than structures built one by one.
+_KIND, _ROWS, _WEIGHT, _PLAN = "3i", "Pq", "Pqiq", "iPPi"
+
+
+def _struct(*parts):
+    """A struct of nested C structs, each padded to its alignment."""
+    fmt = "@"
+    for p in parts:
+        fmt += p + ("0q" if p in (_PLAN, _WEIGHT) else "")
+    return struct.Struct(fmt).pack
+
+
+_PACK = (
+    _struct(_KIND, "3i", _ROWS, _WEIGHT, "P", _ROWS, _ROWS, _ROWS, "PNP"),
+    _struct(_KIND, "3i", _ROWS, _ROWS, _ROWS, _WEIGHT, _ROWS, _WEIGHT, "PPNP"),
+    _struct("8if", "0q", _ROWS, "P", "5P", "PNP"),
+    _struct("6if", "P", _ROWS, "P", _ROWS, "P"),
+    _struct(_KIND, "3i", _PLAN, _ROWS, _WEIGHT, "P", _ROWS, _ROWS, "P"),
+    _struct(_KIND, "3i", _PLAN, _ROWS, _ROWS, _ROWS, _WEIGHT, _ROWS, _WEIGHT, "PPNP"),
+    _struct("5i", "0q", _ROWS, "PP", _ROWS, _ROWS, "P"),
+    _struct("5i", "0q", _ROWS, _ROWS, "PP", _ROWS, "PP"),
+)
+(_LINEAR, _LINEAR_BACKWARD, _ROUTE, _ROUTE_BACKWARD, _EXPERT_LINEAR, _EXPERT_LINEAR_BACKWARD,
+ _COMBINE, _COMBINE_BACKWARD) = range(8)
+
+_NO_ROWS = (0, 1)
+_NO_WEIGHT = (0, 1, _KN, 0)
 
 
 def _bind(lib, check):
     """Declare the entry points' types (called once, by the package)."""
-    global _lib, _check
+    global _lib, _check, _call
     missing = [n for n in EXPORTS if not hasattr(lib, n)]
     if missing:
         raise ImportError("libpgemm.so is older than this binding (no %s); rebuild it with "
@@ -85,96 +116,99 @@ def _bind(lib, check):
         fn = getattr(lib, name)
         fn.argtypes = args
         fn.restype = z if name.endswith("_workspace") else i
-    _lib, _check = lib, check
+    lib.pgemm_layer_call.argtypes = [i, ctypes.c_char_p]
+    lib.pgemm_layer_call.restype = i
+    _lib, _check, _call = lib, check, lib.pgemm_layer_call
 
 
 # ---- arguments -----------------------------------------------------------------
 
 def _device(t, name):
-    """The current device's index, which must be the tensor's."""
+    """The current device's index, which must be the tensor's (an address
+    elsewhere would be a fault on the GPU, not an error code)."""
     device = t.get_device()
-    if device < 0 or device != torch.cuda.current_device():
+    if device < 0 or device != torch._C._cuda_getDevice():
         raise TypeError("%s is on %s; pgemm needs memory of the current device" % (name, t.device))
     return device
 
 
-def _place(t, name, device):
-    """The tensor is on the current device (an address elsewhere would be a
-    fault on the GPU, not an error code)."""
-    if t.get_device() != device:
-        raise TypeError("%s is on %s; pgemm needs memory of the current device (cuda:%d)"
-                        % (name, t.device, device))
-
-
-def _typed(t, name, dtype):
+def _wrong(t, name, dtype, shape, device):
+    """Raise for the first thing that is not as expected."""
     if t.dtype is not dtype:
         raise TypeError("%s is %s, expected %s" % (name, t.dtype, dtype))
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError("%s is %s, expected %s" % (name, tuple(t.shape), tuple(shape)))
+    raise TypeError("%s is on %s; pgemm needs memory of the current device (cuda:%d)"
+                    % (name, t.device, device))
 
 
 def _rows(t, name, rows, cols, dtype, device):
+    """(address, row stride) of a matrix with contiguous rows (None: none)."""
     if t is None:
         return _NO_ROWS
-    _typed(t, name, dtype)
-    if t.dim() != 2 or t.shape[0] != rows or t.shape[1] != cols:
-        raise ValueError("%s is %s, expected (%d, %d)" % (name, tuple(t.shape), rows, cols))
-    _place(t, name, device)
-    if rows == 0 or cols == 0:
-        return _Rows(t.data_ptr() or None, max(1, cols))
+    if t.dtype is not dtype or t.shape != (rows, cols) or t.get_device() != device:
+        _wrong(t, name, dtype, (rows, cols), device)
     s0, s1 = t.stride()
+    if s1 == 1 and s0 >= cols and rows > 1:
+        return t.data_ptr(), s0 or 1
+    if rows == 0 or cols == 0:
+        return t.data_ptr(), max(1, cols)
     if cols > 1 and s1 != 1:
         raise ValueError("%s must have contiguous rows (strides %s)" % (name, (s0, s1)))
     if rows == 1:
         s0 = cols
     if s0 < cols:
         raise ValueError("%s has overlapping rows (strides %s)" % (name, (s0, s1)))
-    return _Rows(t.data_ptr(), s0)
+    return t.data_ptr(), s0
 
 
 def _weight(t, name, experts, k, n, dtype, device):
-    """A k x n weight, or `experts` of them (experts None: one, 2-D)."""
+    """(address, ld, order, expert stride) of a k x n weight, or `experts` of
+    them (experts None: one, 2-D)."""
     if t is None:
         return _NO_WEIGHT
-    _typed(t, name, dtype)
     shape = (k, n) if experts is None else (experts, k, n)
-    if tuple(t.shape) != shape:
-        raise ValueError("%s is %s, expected %s" % (name, tuple(t.shape), shape))
-    _place(t, name, device)
-    if t.numel() == 0:
-        return _Weight(t.data_ptr() or None, max(1, n), _KN, max(1, k) * max(1, n))
-    sk, sn = t.stride()[-2:]
-    stride = 0 if experts is None else t.stride(0)
+    if t.dtype is not dtype or t.shape != shape or t.get_device() != device:
+        _wrong(t, name, dtype, shape, device)
+    if experts is None:
+        stride, (sk, sn) = 0, t.stride()
+    else:
+        stride, sk, sn = t.stride()
+    if k == 0 or n == 0 or experts == 0:
+        return t.data_ptr(), max(1, n), _KN, max(1, k) * max(1, n)
     if (n == 1 or sn == 1) and (k == 1 or sk >= n):
-        order, ld, span = _KN, (sk if k > 1 else n), (k - 1) * (sk if k > 1 else n) + n
+        order, ld = _KN, (sk if k > 1 else n)
+        span = (k - 1) * ld + n
     elif (k == 1 or sk == 1) and (n == 1 or sn >= k):
-        order, ld, span = _NK, (sn if n > 1 else k), (n - 1) * (sn if n > 1 else k) + k
+        order, ld = _NK, (sn if n > 1 else k)
+        span = (n - 1) * ld + k
     else:
         raise ValueError("%s with strides %s has neither contiguous rows nor contiguous columns"
                          % (name, t.stride()))
     if experts is not None and experts > 1 and stride < span:
         raise ValueError("%s: the experts' weights overlap (strides %s)" % (name, t.stride()))
-    return _Weight(t.data_ptr(), ld, order, stride)
+    return t.data_ptr(), ld, order, stride
 
 
 def _flat(t, name, shape, dtype, device):
-    """A contiguous tensor's address (None: NULL)."""
+    """A contiguous tensor's address (None: 0)."""
     if t is None:
-        return None
-    _typed(t, name, dtype)
-    if tuple(t.shape) != shape:
-        raise ValueError("%s is %s, expected %s" % (name, tuple(t.shape), shape))
+        return 0
+    if t.dtype is not dtype or t.shape != shape or t.get_device() != device:
+        _wrong(t, name, dtype, shape, device)
     if not t.is_contiguous():
         raise ValueError("%s must be contiguous" % name)
-    _place(t, name, device)
-    return t.data_ptr() or None
+    return t.data_ptr()
 
 
 def _space(ws, device):
     if ws is None:
-        return None, 0
+        return 0, 0
     if not ws.is_contiguous():
         raise ValueError("ws must be contiguous")
-    _place(ws, "ws", device)
-    return ws.data_ptr() or None, ws.numel() * ws.element_size()
+    if ws.get_device() != device:
+        raise TypeError("ws is on %s; pgemm needs memory of the current device" % ws.device)
+    return ws.data_ptr(), ws.nbytes
 
 
 def _stream(stream, device):
@@ -225,13 +259,14 @@ def linear(X, W, Y, *, bias=None, act="none", residual=None, Z=None, ws=None, st
     m, k = _shape2(X, "X")
     n = _shape2(Y, "Y")[1]
     T = X.dtype
-    kind = _Kind(_dtype(X, "X"), _out(Y, "Y", T), _act(act))
-    w, size = _space(ws, dev)
-    _check(_lib.pgemm_linear(
-        kind, m, n, k, _rows(X, "X", m, k, T, dev), _weight(W, "W", None, k, n, T, dev),
-        _flat(bias, "bias", (n,), T, dev), _rows(residual, "residual", m, n, Y.dtype, dev),
-        _rows(Z, "Z", m, n, T, dev), _rows(Y, "Y", m, n, Y.dtype, dev), w, size,
-        _stream(stream, dev)), "linear")
+    out = Y.dtype
+    st = _call(_LINEAR, _PACK[_LINEAR](
+        _dtype(X, "X"), _out(Y, "Y", T), _act(act), m, n, k, *_rows(X, "X", m, k, T, dev),
+        *_weight(W, "W", None, k, n, T, dev), _flat(bias, "bias", (n,), T, dev),
+        *_rows(residual, "residual", m, n, out, dev), *_rows(Z, "Z", m, n, T, dev),
+        *_rows(Y, "Y", m, n, out, dev), *_space(ws, dev), _stream(stream, dev)))
+    if st != 0:
+        _check(st, "linear")
     return Y
 
 
@@ -271,13 +306,14 @@ def linear_backward(dY, X, W, *, Z=None, act="none", dX=None, dW=None, dbias=Non
     code = _dtype(dY, "dY")
     if out is not T and out is not torch.float32:
         raise TypeError("dW and dbias are %s, expected %s or float32" % (out, T))
-    kind = _Kind(code, _DTYPES[out], _act(act))
-    w, size = _space(ws, dev)
-    _check(_lib.pgemm_linear_backward(
-        kind, m, n, k, _rows(dY, "dY", m, n, T, dev), _rows(Z, "Z", m, n, T, dev),
-        _rows(X, "X", m, k, T, dev), _weight(W, "W", None, k, n, T, dev),
-        _rows(dX, "dX", m, k, T, dev), _weight(dW, "dW", None, k, n, out, dev),
-        _flat(dbias, "dbias", (n,), out, dev), w, size, _stream(stream, dev)), "linear_backward")
+    st = _call(_LINEAR_BACKWARD, _PACK[_LINEAR_BACKWARD](
+        code, _DTYPES[out], _act(act), m, n, k, *_rows(dY, "dY", m, n, T, dev),
+        *_rows(Z, "Z", m, n, T, dev), *_rows(X, "X", m, k, T, dev),
+        *_weight(W, "W", None, k, n, T, dev), *_rows(dX, "dX", m, k, T, dev),
+        *_weight(dW, "dW", None, k, n, out, dev), _flat(dbias, "dbias", (n,), out, dev),
+        *_space(ws, dev), _stream(stream, dev)))
+    if st != 0:
+        _check(st, "linear_backward")
 
 
 def linear_backward_workspace(m, n, k, dtype, act="none") -> int:
@@ -310,16 +346,16 @@ def route(logits, weights, experts, offsets, tokens, slots, *, bias=None, score=
     m, E = _shape2(logits, "logits")
     top = _shape2(weights, "weights")[1]
     i32, f32 = torch.int32, torch.float32
-    out = _RouteOut(_flat(weights, "weights", (m, top), f32, dev),
-                    _flat(experts, "experts", (m, top), i32, dev),
-                    _flat(offsets, "offsets", (E + 1,), i32, dev),
-                    _flat(tokens, "tokens", (m * top,), i32, dev),
-                    _flat(slots, "slots", (m, top), i32, dev))
-    w, size = _space(ws, dev)
-    _check(_lib.pgemm_route(
+    st = _call(_ROUTE, _PACK[_ROUTE](
         _dtype(logits, "logits"), m, E, top, _score(score), groups, top_groups, bool(renorm),
-        scale, _rows(logits, "logits", m, E, logits.dtype, dev),
-        _flat(bias, "bias", (E,), f32, dev), out, w, size, _stream(stream, dev)), "route")
+        scale, *_rows(logits, "logits", m, E, logits.dtype, dev),
+        _flat(bias, "bias", (E,), f32, dev), _flat(weights, "weights", (m, top), f32, dev),
+        _flat(experts, "experts", (m, top), i32, dev),
+        _flat(offsets, "offsets", (E + 1,), i32, dev),
+        _flat(tokens, "tokens", (m * top,), i32, dev), _flat(slots, "slots", (m, top), i32, dev),
+        *_space(ws, dev), _stream(stream, dev)))
+    if st != 0:
+        _check(st, "route")
 
 
 def route_workspace(m, experts, top) -> int:
@@ -335,17 +371,20 @@ def route_backward(dweights, logits, experts, dlogits, *, score="softmax", renor
     m, E = _shape2(logits, "logits")
     top = _shape2(experts, "experts")[1]
     T = logits.dtype
-    _check(_lib.pgemm_route_backward(
+    st = _call(_ROUTE_BACKWARD, _PACK[_ROUTE_BACKWARD](
         _dtype(logits, "logits"), m, E, top, _score(score), bool(renorm), scale,
         _flat(dweights, "dweights", (m, top), torch.float32, dev),
-        _rows(logits, "logits", m, E, T, dev), _flat(experts, "experts", (m, top), torch.int32, dev),
-        _rows(dlogits, "dlogits", m, E, T, dev), _stream(stream, dev)), "route_backward")
+        *_rows(logits, "logits", m, E, T, dev),
+        _flat(experts, "experts", (m, top), torch.int32, dev),
+        *_rows(dlogits, "dlogits", m, E, T, dev), _stream(stream, dev)))
+    if st != 0:
+        _check(st, "route_backward")
     return dlogits
 
 
 def _plan(E, offsets, tokens, rows, x_rows, device):
-    return _Plan(E, _flat(offsets, "offsets", (E + 1,), torch.int32, device),
-                 _flat(tokens, "tokens", (rows,), torch.int32, device), x_rows)
+    return (E, _flat(offsets, "offsets", (E + 1,), torch.int32, device),
+            _flat(tokens, "tokens", (rows,), torch.int32, device), x_rows)
 
 
 def expert_linear(X, W, Y, offsets, *, tokens=None, bias=None, act="none", Z=None, stream=None):
@@ -362,12 +401,14 @@ def expert_linear(X, W, Y, offsets, *, tokens=None, bias=None, act="none", Z=Non
         raise ValueError("W must be 3-D")
     E = W.shape[0]
     T = X.dtype
-    kind = _Kind(_dtype(X, "X"), _out(Y, "Y", T), _act(act))
-    _check(_lib.pgemm_expert_linear(
-        kind, rows, n, k, _plan(E, offsets, tokens, rows, xr, dev), _rows(X, "X", xr, k, T, dev),
-        _weight(W, "W", E, k, n, T, dev), _flat(bias, "bias", (E, n), T, dev),
-        _rows(Z, "Z", rows, n, T, dev), _rows(Y, "Y", rows, n, Y.dtype, dev),
-        _stream(stream, dev)), "expert_linear")
+    st = _call(_EXPERT_LINEAR, _PACK[_EXPERT_LINEAR](
+        _dtype(X, "X"), _out(Y, "Y", T), _act(act), rows, n, k,
+        *_plan(E, offsets, tokens, rows, xr, dev), *_rows(X, "X", xr, k, T, dev),
+        *_weight(W, "W", E, k, n, T, dev), _flat(bias, "bias", (E, n), T, dev),
+        *_rows(Z, "Z", rows, n, T, dev), *_rows(Y, "Y", rows, n, Y.dtype, dev),
+        _stream(stream, dev)))
+    if st != 0:
+        _check(st, "expert_linear")
     return Y
 
 
@@ -388,14 +429,14 @@ def expert_linear_backward(dY, X, W, offsets, *, tokens=None, Z=None, act="none"
     code = _dtype(dY, "dY")
     if out is not T and out is not torch.float32:
         raise TypeError("dW and dbias are %s, expected %s or float32" % (out, T))
-    kind = _Kind(code, _DTYPES[out], _act(act))
-    w, size = _space(ws, dev)
-    _check(_lib.pgemm_expert_linear_backward(
-        kind, rows, n, k, _plan(E, offsets, tokens, rows, xr, dev), _rows(dY, "dY", rows, n, T, dev),
-        _rows(Z, "Z", rows, n, T, dev), _rows(X, "X", xr, k, T, dev),
-        _weight(W, "W", E, k, n, T, dev), _rows(dX, "dX", rows, k, T, dev),
-        _weight(dW, "dW", E, k, n, out, dev), _flat(dbias, "dbias", (E, n), out, dev), w, size,
-        _stream(stream, dev)), "expert_linear_backward")
+    st = _call(_EXPERT_LINEAR_BACKWARD, _PACK[_EXPERT_LINEAR_BACKWARD](
+        code, _DTYPES[out], _act(act), rows, n, k, *_plan(E, offsets, tokens, rows, xr, dev),
+        *_rows(dY, "dY", rows, n, T, dev), *_rows(Z, "Z", rows, n, T, dev),
+        *_rows(X, "X", xr, k, T, dev), *_weight(W, "W", E, k, n, T, dev),
+        *_rows(dX, "dX", rows, k, T, dev), *_weight(dW, "dW", E, k, n, out, dev),
+        _flat(dbias, "dbias", (E, n), out, dev), *_space(ws, dev), _stream(stream, dev)))
+    if st != 0:
+        _check(st, "expert_linear_backward")
 
 
 def expert_linear_backward_workspace(rows, n, k, experts, dtype, act="none") -> int:
@@ -415,12 +456,14 @@ def combine(Y, slots, out, *, weights=None, residual=None, stream=None):
     rows, n = _shape2(Y, "Y")
     m, top = _shape2(slots, "slots")
     T = Y.dtype
-    _check(_lib.pgemm_combine(
-        _dtype(Y, "Y"), m, n, top, rows, _rows(Y, "Y", rows, n, T, dev),
+    st = _call(_COMBINE, _PACK[_COMBINE](
+        _dtype(Y, "Y"), m, n, top, rows, *_rows(Y, "Y", rows, n, T, dev),
         _flat(slots, "slots", (m, top), torch.int32, dev),
         _flat(weights, "weights", (m, top), torch.float32, dev),
-        _rows(residual, "residual", m, n, T, dev), _rows(out, "out", m, n, T, dev),
-        _stream(stream, dev)), "combine")
+        *_rows(residual, "residual", m, n, T, dev), *_rows(out, "out", m, n, T, dev),
+        _stream(stream, dev)))
+    if st != 0:
+        _check(st, "combine")
     return out
 
 
@@ -438,10 +481,11 @@ def combine_backward(dout, Y, slots, weights, *, dY=None, dweights=None, stream=
         raise ValueError("dweights needs Y")
     some = Y if Y is not None else dY
     rows = 0 if some is None else _shape2(some, "Y")[0]
-    _check(_lib.pgemm_combine_backward(
-        _dtype(dout, "dout"), m, n, top, rows, _rows(dout, "dout", m, n, T, dev),
-        _rows(Y, "Y", rows, n, T, dev), _flat(slots, "slots", (m, top), torch.int32, dev),
+    st = _call(_COMBINE_BACKWARD, _PACK[_COMBINE_BACKWARD](
+        _dtype(dout, "dout"), m, n, top, rows, *_rows(dout, "dout", m, n, T, dev),
+        *_rows(Y, "Y", rows, n, T, dev), _flat(slots, "slots", (m, top), torch.int32, dev),
         _flat(weights, "weights", (m, top), torch.float32, dev),
-        _rows(dY, "dY", rows, n, T, dev),
-        _flat(dweights, "dweights", (m, top), torch.float32, dev), _stream(stream, dev)),
-        "combine_backward")
+        *_rows(dY, "dY", rows, n, T, dev),
+        _flat(dweights, "dweights", (m, top), torch.float32, dev), _stream(stream, dev)))
+    if st != 0:
+        _check(st, "combine_backward")

@@ -650,4 +650,140 @@ int pgemm_combine_backward(int dtype, int m, int n, int top, int rows, pgemm_row
              : PGEMM_EHIP;
 }
 
+namespace {
+
+struct LinearCall {
+  pgemm_kind kind;
+  int m, n, k;
+  pgemm_rows X;
+  pgemm_weight W;
+  const void* bias;
+  pgemm_rows residual, Z, Y;
+  void* workspace;
+  size_t workspace_bytes;
+  void* stream;
+};
+struct LinearBackwardCall {
+  pgemm_kind kind;
+  int m, n, k;
+  pgemm_rows dY, Z, X;
+  pgemm_weight W;
+  pgemm_rows dX;
+  pgemm_weight dW;
+  void* dbias;
+  void* workspace;
+  size_t workspace_bytes;
+  void* stream;
+};
+struct RouteCall {
+  int dtype, m, experts, top, score, groups, top_groups, renorm;
+  float scale;
+  pgemm_rows logits;
+  const float* bias;
+  pgemm_route_out out;
+  void* workspace;
+  size_t workspace_bytes;
+  void* stream;
+};
+struct RouteBackwardCall {
+  int dtype, m, experts, top, score, renorm;
+  float scale;
+  const float* dweights;
+  pgemm_rows logits;
+  const int* expert_index;
+  pgemm_rows dlogits;
+  void* stream;
+};
+struct ExpertLinearCall {
+  pgemm_kind kind;
+  int rows, n, k;
+  pgemm_plan plan;
+  pgemm_rows X;
+  pgemm_weight W;
+  const void* bias;
+  pgemm_rows Z, Y;
+  void* stream;
+};
+struct ExpertLinearBackwardCall {
+  pgemm_kind kind;
+  int rows, n, k;
+  pgemm_plan plan;
+  pgemm_rows dY, Z, X;
+  pgemm_weight W;
+  pgemm_rows dX;
+  pgemm_weight dW;
+  void* dbias;
+  void* workspace;
+  size_t workspace_bytes;
+  void* stream;
+};
+struct CombineCall {
+  int dtype, m, n, top, rows;
+  pgemm_rows Y;
+  const int* slots;
+  const float* weights;
+  pgemm_rows residual, out;
+  void* stream;
+};
+struct CombineBackwardCall {
+  int dtype, m, n, top, rows;
+  pgemm_rows dout, Y;
+  const int* slots;
+  const float* weights;
+  pgemm_rows dY;
+  float* dweights;
+  void* stream;
+};
+
+}  // namespace
+
+int pgemm_layer_call(int op, const void* args) {
+  if (args == nullptr) return -2;
+  switch (op) {
+    case PGEMM_OP_LINEAR: {
+      const LinearCall& c = *static_cast<const LinearCall*>(args);
+      return pgemm_linear(c.kind, c.m, c.n, c.k, c.X, c.W, c.bias, c.residual, c.Z, c.Y,
+                          c.workspace, c.workspace_bytes, c.stream);
+    }
+    case PGEMM_OP_LINEAR_BACKWARD: {
+      const LinearBackwardCall& c = *static_cast<const LinearBackwardCall*>(args);
+      return pgemm_linear_backward(c.kind, c.m, c.n, c.k, c.dY, c.Z, c.X, c.W, c.dX, c.dW,
+                                   c.dbias, c.workspace, c.workspace_bytes, c.stream);
+    }
+    case PGEMM_OP_ROUTE: {
+      const RouteCall& c = *static_cast<const RouteCall*>(args);
+      return pgemm_route(c.dtype, c.m, c.experts, c.top, c.score, c.groups, c.top_groups,
+                         c.renorm, c.scale, c.logits, c.bias, c.out, c.workspace,
+                         c.workspace_bytes, c.stream);
+    }
+    case PGEMM_OP_ROUTE_BACKWARD: {
+      const RouteBackwardCall& c = *static_cast<const RouteBackwardCall*>(args);
+      return pgemm_route_backward(c.dtype, c.m, c.experts, c.top, c.score, c.renorm, c.scale,
+                                  c.dweights, c.logits, c.expert_index, c.dlogits, c.stream);
+    }
+    case PGEMM_OP_EXPERT_LINEAR: {
+      const ExpertLinearCall& c = *static_cast<const ExpertLinearCall*>(args);
+      return pgemm_expert_linear(c.kind, c.rows, c.n, c.k, c.plan, c.X, c.W, c.bias, c.Z, c.Y,
+                                 c.stream);
+    }
+    case PGEMM_OP_EXPERT_LINEAR_BACKWARD: {
+      const ExpertLinearBackwardCall& c = *static_cast<const ExpertLinearBackwardCall*>(args);
+      return pgemm_expert_linear_backward(c.kind, c.rows, c.n, c.k, c.plan, c.dY, c.Z, c.X, c.W,
+                                          c.dX, c.dW, c.dbias, c.workspace, c.workspace_bytes,
+                                          c.stream);
+    }
+    case PGEMM_OP_COMBINE: {
+      const CombineCall& c = *static_cast<const CombineCall*>(args);
+      return pgemm_combine(c.dtype, c.m, c.n, c.top, c.rows, c.Y, c.slots, c.weights, c.residual,
+                           c.out, c.stream);
+    }
+    case PGEMM_OP_COMBINE_BACKWARD: {
+      const CombineBackwardCall& c = *static_cast<const CombineBackwardCall*>(args);
+      return pgemm_combine_backward(c.dtype, c.m, c.n, c.top, c.rows, c.dout, c.Y, c.slots,
+                                    c.weights, c.dY, c.dweights, c.stream);
+    }
+    default: return -1;
+  }
+}
+
 }  // extern "C"

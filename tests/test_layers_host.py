@@ -132,6 +132,52 @@ def test_combine_argument_codes():
         assert L.pgemm_combine_backward(*args) == -pos, pos
 
 
+def flat(args):
+    """A call's arguments as pgemm_layer_call's packed members."""
+    out = []
+    for a in args:
+        if isinstance(a, ctypes.Structure):
+            out += flat(getattr(a, f) for f, _ in a._fields_)
+        else:
+            out.append(0 if a is None else a)
+    return out
+
+
+def test_packed_calls_equal_the_functions():
+    """Every argument reaches its place: a bad value gives the same code."""
+    out, plan = lo._RouteOut(FAKE, FAKE, FAKE, FAKE, FAKE), lo._Plan(4, FAKE, FAKE, 8)
+    silu = lo._Kind(2, 2, 4)
+    need = L.pgemm_linear_backward_workspace(silu, 8, 64, 64)
+    needr = L.pgemm_route_workspace(100, 64, 4)
+    neede = L.pgemm_expert_linear_backward_workspace(silu, 32, 64, 64, 4)
+    calls = [
+        (L.pgemm_linear, [KIND, 8, 64, 64, R(), Wt(), FAKE, R(), R(), R(), FAKE + 8, 0, None]),
+        (L.pgemm_linear_backward, [silu, 8, 64, 64, R(), R(), R(), Wt(), R(), Wt(), FAKE, FAKE,
+                                   need - 1, None]),
+        (L.pgemm_route, [0, 100, 64, 4, 0, 8, 4, 1, 1.0, R(), FAKE, out, FAKE, needr - 1, None]),
+        (L.pgemm_route_backward, [0, 10, 64, 4, 0, 1, 1.0, FAKE, R(), FAKE, R(FAKE, 3), None]),
+        (L.pgemm_expert_linear, [KIND, 32, 64, 64, plan, R(), Wt(), FAKE, R(), R(FAKE, 3), None]),
+        (L.pgemm_expert_linear_backward, [silu, 32, 64, 64, plan, R(), R(), R(), Wt(), R(), Wt(),
+                                          FAKE, FAKE, neede - 1, None]),
+        (L.pgemm_combine, [2, 8, 64, 2, 16, R(), FAKE, FAKE, R(), R(FAKE, 3), None]),
+        (L.pgemm_combine_backward, [2, 8, 64, 2, 16, R(), R(), FAKE, FAKE, R(), FAKE + 2, None])]
+    bad = {ctypes.c_int: -1, lo._Rows: R(FAKE + 1, 64), lo._Weight: Wt(FAKE, 64, 9),
+           lo._Kind: lo._Kind(7, 7, 0), lo._Plan: lo._Plan(0, FAKE, FAKE, 8),
+           lo._RouteOut: lo._RouteOut(FAKE, FAKE, FAKE + 1, FAKE, FAKE),
+           ctypes.c_void_p: FAKE + 1}
+    for op, (fn, args) in enumerate(calls):
+        # the last bad argument alone, then also each earlier one
+        assert fn(*args) < 0
+        for pos, kind in enumerate(fn.argtypes[:-1]):
+            a = list(args)
+            if kind in bad:
+                a[pos] = bad[kind]
+            want = fn(*a)
+            assert want < 0 and want > -100
+            assert L.pgemm_layer_call(op, lo._PACK[op](*flat(a))) == want, (fn.__name__, pos)
+    assert L.pgemm_layer_call(8, b"") == -1 and L.pgemm_layer_call(0, None) == -2
+
+
 def test_workspace_sizes():
     # enough rows need none; one row of a long sum can use some
     assert pg.linear_workspace(8192, 8192, 4096, BF) == 0
@@ -152,7 +198,7 @@ def anywhere(monkeypatch):
     """Let CPU tensors past the device checks: a call that is not refused
     before the library would be, by its own checks, or fail to launch."""
     monkeypatch.setattr(lo, "_device", lambda t, name: -1)
-    monkeypatch.setattr(lo, "_stream", lambda s, d: None)
+    monkeypatch.setattr(lo, "_stream", lambda s, d: 0)
 
 
 def z(*shape, dtype=BF):
