@@ -31,7 +31,7 @@ constexpr KernelShape kShape[3] = {{256, 256}, {128, 128}, {64, 64}};
 constexpr int few_columns(int kernel) { return kernel >= kFew16Wide ? 64 : 16; }
 
 struct TypeOps {
-  hipError_t (*prod)(const ProdArgs& a, int la, int lb, int mode, int kernel, bool direct,
+  hipError_t (*prod)(const ProdArgs& a, int la, int lb, int mode, int kernel, int loading,
                      hipStream_t s);
   hipError_t (*slope)(const SlopeArgs& a, int groups, hipStream_t s);
   hipError_t (*column_sum)(const float* partial, void* out, int n, int groups, int chunks,

@@ -16,27 +16,32 @@ hipError_t launch(void (*kernel)(const A), dim3 grid, int threads, const A& a, h
   return hipLaunchKernel(reinterpret_cast<const void*>(kernel), grid, dim3(threads), args, 0, s);
 }
 
-template <typename T, int LA, int LB, int BM, int BN, int WGM, int WGN, bool DIRECT, int MODE>
+template <typename T, int LA, int LB, int BM, int BN, int WGM, int WGN, int LOADING, int MODE>
 hipError_t launch_tile(const ProdArgs& a, hipStream_t s) {
   long long tiles = (long long)a.tiles_m * a.tiles_n;
   if (MODE == kSums) tiles *= a.groups;
-  return launch(&prod_tile_kernel<T, LA, LB, BM, BN, WGM, WGN, DIRECT, MODE>,
+  return launch(&prod_tile_kernel<T, LA, LB, BM, BN, WGM, WGN, LOADING, MODE>,
                 dim3((unsigned)tiles, MODE == kDense ? (unsigned)a.splits : 1), WGM * WGN * 64, a,
                 s);
 }
 
-template <typename T, int LA, int LB, int MODE>
-hipError_t prod_tile(const ProdArgs& a, int kernel, bool direct, hipStream_t s) {
-  if constexpr (sizeof(T) == 2) {
-    if (kernel == kTile256 && direct) return launch_tile<T, LA, LB, 256, 256, 2, 4, true, MODE>(a, s);
+template <typename T, int LA, int LB, int MODE, int LOADING>
+hipError_t prod_tile(const ProdArgs& a, int kernel, hipStream_t s) {
+  if constexpr (LOADING == kDirect) {
+    if (kernel == kTile256) return launch_tile<T, LA, LB, 256, 256, 2, 4, LOADING, MODE>(a, s);
   }
-  if (kernel == kTile128)
-    return direct ? launch_tile<T, LA, LB, 128, 128, 2, 2, true, MODE>(a, s)
-                  : launch_tile<T, LA, LB, 128, 128, 2, 2, false, MODE>(a, s);
-  if (kernel == kTile64)
-    return direct ? launch_tile<T, LA, LB, 64, 64, 2, 2, true, MODE>(a, s)
-                  : launch_tile<T, LA, LB, 64, 64, 2, 2, false, MODE>(a, s);
+  if (kernel == kTile128) return launch_tile<T, LA, LB, 128, 128, 2, 2, LOADING, MODE>(a, s);
+  if (kernel == kTile64) return launch_tile<T, LA, LB, 64, 64, 2, 2, LOADING, MODE>(a, s);
   return hipErrorInvalidValue;
+}
+
+template <typename T, int LA, int LB, int MODE>
+hipError_t prod_tile(const ProdArgs& a, int kernel, int loading, hipStream_t s) {
+  if (loading == kDirect) return prod_tile<T, LA, LB, MODE, kDirect>(a, kernel, s);
+  if constexpr (MODE != kSums && sizeof(T) == 2) {
+    if (loading == kRagged) return prod_tile<T, LA, LB, MODE, kRagged>(a, kernel, s);
+  }
+  return prod_tile<T, LA, LB, MODE, kThrough>(a, kernel, s);
 }
 
 template <typename T, int LB, int MB, int MODE>
@@ -55,7 +60,7 @@ hipError_t prod_few(const ProdArgs& a, int kernel, hipStream_t s) {
 }
 
 template <typename T>
-hipError_t prod(const ProdArgs& a, int la, int lb, int mode, int kernel, bool direct,
+hipError_t prod(const ProdArgs& a, int la, int lb, int mode, int kernel, int loading,
                 hipStream_t s) {
   hipError_t e;
   const bool few = kernel >= kFew16;
@@ -64,10 +69,10 @@ hipError_t prod(const ProdArgs& a, int la, int lb, int mode, int kernel, bool di
       e = lb == kInner ? prod_few<T, kInner, kDense>(a, kernel, s)
                        : prod_few<T, kOuter, kDense>(a, kernel, s);
     else if (la == kOuter)
-      e = prod_tile<T, kOuter, kOuter, kDense>(a, kernel, direct, s);
+      e = prod_tile<T, kOuter, kOuter, kDense>(a, kernel, loading, s);
     else
-      e = lb == kInner ? prod_tile<T, kInner, kInner, kDense>(a, kernel, direct, s)
-                       : prod_tile<T, kInner, kOuter, kDense>(a, kernel, direct, s);
+      e = lb == kInner ? prod_tile<T, kInner, kInner, kDense>(a, kernel, loading, s)
+                       : prod_tile<T, kInner, kOuter, kDense>(a, kernel, loading, s);
     if (e == hipSuccess && a.splits > 1) {
       const long long items = (long long)a.M * ((a.N + 7) / 8);
       e = launch(&prod_reduce_kernel<T>, dim3((unsigned)((items + 255) / 256)), 256, a, s);
@@ -78,10 +83,10 @@ hipError_t prod(const ProdArgs& a, int la, int lb, int mode, int kernel, bool di
     if (few)
       return lb == kInner ? prod_few<T, kInner, kRows>(a, kernel, s)
                           : prod_few<T, kOuter, kRows>(a, kernel, s);
-    return lb == kInner ? prod_tile<T, kInner, kInner, kRows>(a, kernel, direct, s)
-                        : prod_tile<T, kInner, kOuter, kRows>(a, kernel, direct, s);
+    return lb == kInner ? prod_tile<T, kInner, kInner, kRows>(a, kernel, loading, s)
+                        : prod_tile<T, kInner, kOuter, kRows>(a, kernel, loading, s);
   }
-  return prod_tile<T, kOuter, kOuter, kSums>(a, kernel, direct, s);
+  return prod_tile<T, kOuter, kOuter, kSums>(a, kernel, loading, s);
 }
 
 template <typename T>

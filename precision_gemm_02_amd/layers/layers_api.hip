@@ -63,12 +63,16 @@ struct Plan {
   int kernel = kTile64;
   int splits = 1;
   int k_split = 0;
-  bool direct = false;
+  int loading = kThrough;
 };
 
-bool operand_direct(const void* p, long long ld, int size, int inner, long long stride) {
+// The loading that an operand allows: `inner` is its contiguous extent.
+int operand_loading(const void* p, long long ld, int size, int inner, long long stride) {
   const int v = 16 / size;
-  return aligned_to(p, 16) && ld % v == 0 && inner % v == 0 && stride % v == 0;
+  if (aligned_to(p, 16) && ld % v == 0 && inner % v == 0 && stride % v == 0) return kDirect;
+  // fp32 goes through registers instead: 4098 x 3002 x 1022 k x n 230 us, with
+  // kRagged 247 (bf16 78 us through registers, 57 so)
+  return size == 2 && aligned_to(p, 4) && ld % 2 == 0 && stride % 2 == 0 ? kRagged : kThrough;
 }
 
 // A tile class's time, fitted to 15 dense shapes in both weight orders (64 to
@@ -85,7 +89,7 @@ ClassTime class_time(int kernel, int size) {
   static const ClassTime t16[3] = {{1.35e15, 10e-6, 1, {0, 0, 0, 0}},
                                    {1.10e15, 7e-6, 2, {0, 0.7, 0, 0}},
                                    {0.60e15, 3.5e-6, 4, {0, 0.5, 0.75, 0.9}}};
-  static const ClassTime t32[3] = {{0, 0, 1, {0, 0, 0, 0}},
+  static const ClassTime t32[3] = {{142e12, 6e-6, 1, {0, 0, 0, 0}},
                                    {130e12, 4e-6, 2, {0, 0.93, 0, 0}},
                                    {119e12, 3e-6, 4, {0, 0.8, 0.9, 0.95}}};
   return (size == 2 ? t16 : t32)[kernel];
@@ -106,9 +110,9 @@ double tiles_time(const ClassTime& c, double tiles, double tile_flops) {
 // shared by workgroups, through partial sums in `ws_bytes` bytes (any_ws: as
 // many as it takes).
 Plan plan_product(int size, int la, int mode, long long rows, int groups, int n, int k,
-                  bool direct, size_t ws_bytes, bool any_ws, bool may_split = true) {
+                  int loading, size_t ws_bytes, bool any_ws, bool may_split = true) {
   Plan p;
-  p.direct = direct;
+  p.loading = loading;
   const int bk = 128 / size;
   if (mode != kDense) may_split = false;
   if (mode == kRows && groups > rows) groups = (int)rows;
@@ -128,7 +132,7 @@ Plan plan_product(int size, int la, int mode, long long rows, int groups, int n,
   } else {
     double best = 0;
     for (int c = 0; c < 3; ++c) {
-      if (c == kTile256 && (size == 4 || !direct)) continue;
+      if (c == kTile256 && loading != kDirect) continue;
       const int bm = kShape[c].bm, bn = kShape[c].bn;
       // tiles that are half empty waste the loads too (512 tokens, top 8 of
       // 64 experts, 1024 x 1024: 39 us with 64-row tiles, 45 with 128)
@@ -158,7 +162,7 @@ Plan plan_product(int size, int la, int mode, long long rows, int groups, int n,
     p.splits = (int)ceil_div(k, p.k_split);
     const size_t need = (size_t)p.splits * (size_t)rows * (size_t)n * 4;
     if (!any_ws && ws_bytes < need)   // the best plan that needs no space
-      return plan_product(size, la, mode, rows, groups, n, k, direct, 0, false, false);
+      return plan_product(size, la, mode, rows, groups, n, k, loading, 0, false, false);
   }
   return p;
 }
@@ -166,8 +170,8 @@ Plan plan_product(int size, int la, int mode, long long rows, int groups, int n,
 // Workspace that plan_product may use for a dense product, over any alignment.
 size_t split_bytes(int size, int la, int rows, int n, int k) {
   size_t most = 0;
-  for (int d = 0; d < 2; ++d) {
-    const Plan p = plan_product(size, la, kDense, rows, 1, n, k, d != 0, 0, true);
+  for (const int loading : {kThrough, kDirect}) {
+    const Plan p = plan_product(size, la, kDense, rows, 1, n, k, loading, 0, true);
     const size_t b = p.splits > 1 ? (size_t)p.splits * (size_t)rows * (size_t)n * 4 : 0;
     if (b > most) most = b;
   }
@@ -178,11 +182,16 @@ size_t split_bytes(int size, int la, int rows, int n, int k) {
 int run_product(ProdArgs a, int dtype, int la, int lb, int mode, long long rows, void* ws,
                 size_t ws_bytes, hipStream_t s) {
   const int size = size_of(dtype);
-  const bool direct =
-      operand_direct(a.A, a.lda, size, la == kInner ? (mode == kSums ? 0 : a.K) : a.M, 0) &&
-      operand_direct(a.B, a.ldb, size, lb == kInner ? a.K : a.N, mode == kRows ? a.strideB : 0);
+  const int al = operand_loading(a.A, a.lda, size,
+                                 la == kInner ? (mode == kSums ? 0 : a.K) : a.M, 0);
+  const int bl = operand_loading(a.B, a.ldb, size, lb == kInner ? a.K : a.N,
+                                 mode == kRows ? a.strideB : 0);
+  int loading = al == kDirect && bl == kDirect       ? kDirect
+                : al != kThrough && bl != kThrough   ? kRagged
+                                                     : kThrough;
+  if (mode == kSums && loading == kRagged) loading = kThrough;   // see Loader
   const Plan p = plan_product(size, la, mode, rows, a.groups, a.N, mode == kSums ? a.rows : a.K,
-                              direct, ws == nullptr ? 0 : ws_bytes, false);
+                              loading, ws == nullptr ? 0 : ws_bytes, false);
   a.splits = p.splits;
   a.k_split = p.k_split;
   a.partial = static_cast<float*>(ws);
@@ -198,7 +207,7 @@ int run_product(ProdArgs a, int dtype, int la, int lb, int mode, long long rows,
   }
   if ((long long)a.tiles_m * a.tiles_n * (a.groups > 0 ? a.groups : 1) > kMaxGrid)
     return PGEMM_EHIP;
-  return ops_of(dtype).prod(a, la, lb, mode, p.kernel, p.direct, s) == hipSuccess ? PGEMM_OK
+  return ops_of(dtype).prod(a, la, lb, mode, p.kernel, p.loading, s) == hipSuccess ? PGEMM_OK
                                                                                 : PGEMM_EHIP;
 }
 

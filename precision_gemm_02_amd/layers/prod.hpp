@@ -22,6 +22,8 @@ namespace layers {
 enum Act { kNone = 0, kRelu = 1, kGelu = 2, kGeluTanh = 3, kSilu = 4 };
 enum Order { kInner = 0, kOuter = 1 };
 enum Mode { kDense = 0, kRows = 1, kSums = 2 };
+// How a tile's operands reach LDS (see Loader).
+enum Loading { kThrough = 0, kDirect = 1, kRagged = 2 };
 
 typedef float f32x4 __attribute__((ext_vector_type(4)));
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));

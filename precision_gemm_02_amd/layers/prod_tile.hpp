@@ -170,16 +170,22 @@ __device__ __forceinline__ void load_to_lds(const void* from, char* to) {
 //
 // DIRECT: straight into LDS (global_load_lds_dwordx4: a wave writes 64
 // consecutive chunks, so the layout's flips are applied to the global
-// addresses).  It needs 16-byte aligned rows and no chunk that straddles the
-// operand's end.  Each thread keeps one address per chunk and moves it by a
-// constant step.  Output indices outside the operand read its last row or
+// addresses).  It needs rows at 16-byte boundaries and no chunk that straddles
+// the operand's end.  Each thread keeps one address per chunk and moves it by
+// a constant step.  Output indices outside the operand read its last row or
 // first chunk instead: they reach only results that are never stored.  The
 // last, partly filled tile of the summed index takes zeros there.
-// Otherwise the chunks go through registers, with guards.
-template <typename T, int ORDER, int EXT, int NT, bool DIRECT, bool GATHER>
+// RAGGED: the same for rows at 4-byte boundaries and any sizes.  A chunk that
+// straddles the end of an outer-order row goes on into the next rows; the tiles
+// near the end of the summed index go through registers with guards instead.
+// (Not for gathered outer-order rows, whose next row may be outside.)
+// THROUGH: through registers, with guards, for any alignment.
+template <typename T, int ORDER, int EXT, int NT, int LOADING, bool GATHER>
 struct Loader {
+  static constexpr bool DIRECT = LOADING != kThrough;
   using Tile = OperandTile<T, ORDER, EXT, NT>;
   static constexpr int L = Tile::LOADS;
+  static_assert(LOADING != kRagged || !GATHER, "see above");
   Source<T> src;
   int first;                       // first output index of the tile
   int k;                           // first summed index of the next load
@@ -230,8 +236,15 @@ struct Loader {
   // past the last tile) comes from the zero chunk.
   template <int J0, int J1>
   __device__ __forceinline__ void load(char* lds) {
-    if constexpr (DIRECT) {
+    if constexpr (LOADING == kDirect) {
       load_as<false, J0, J1>(lds);
+    } else if constexpr (LOADING == kRagged) {
+      // near the end: V rows of margin for the chunks that go on into the next
+      if (k + Tile::BK + Tile::V >= (ORDER == kInner ? src.inner : src.outer)) {
+        load_guards<J0, J1>(lds);
+      } else {
+        load_as<true, J0, J1>(lds);
+      }
     } else {
       if (ragged()) load_as<false, J0, J1>(lds);
       else load_as<true, J0, J1>(lds);
@@ -251,8 +264,11 @@ struct Loader {
       const T* p = ptr[j];
       if constexpr (ORDER == kOuter && GATHER) p += (long long)token[j] * src.ld;
       if constexpr (DIRECT) {
-        const bool in = ORDER == kInner ? k + c * Tile::V < src.inner : k + r < src.outer;
-        const void* from = in ? (const void*)p : (const void*)&kZeroChunk;
+        const void* from = p;
+        if constexpr (!WHOLE) {
+          const bool in = ORDER == kInner ? k + c * Tile::V < src.inner : k + r < src.outer;
+          from = in ? from : (const void*)&kZeroChunk;
+        }
         // a wave's 64 chunks; the same LDS base for all its lanes
         load_to_lds(from, lds + (j * NT + ((int)threadIdx.x & ~63)) * 16);
       } else if constexpr (WHOLE) {
@@ -262,6 +278,22 @@ struct Loader {
         const bool row = ORDER == kInner ? first + r < src.outer : k + r < src.outer;
         reg[j] = load_guarded(row ? p - at : nullptr, at, src.inner);
       }
+      if constexpr (ORDER == kInner) ptr[j] += Tile::BK;
+      else if constexpr (!GATHER) ptr[j] += step;
+    }
+  }
+
+  // RAGGED: the same chunks with guards, through registers, at once.
+  template <int J0, int J1>
+  __device__ __forceinline__ void load_guards(char* lds) {
+#pragma unroll
+    for (int j = J0; j < J1; ++j) {
+      int r, c;
+      Tile::slot(j * NT + (int)threadIdx.x, &r, &c);
+      const int at = ORDER == kInner ? k + c * Tile::V : first + c * Tile::V;
+      const bool row = ORDER == kInner ? first + r < src.outer : k + r < src.outer;
+      *reinterpret_cast<u32x4*>(lds + (j * NT + (int)threadIdx.x) * 16) =
+          load_guarded(row ? ptr[j] - at : nullptr, at, src.inner);
       if constexpr (ORDER == kInner) ptr[j] += Tile::BK;
       else if constexpr (!GATHER) ptr[j] += step;
     }
@@ -339,8 +371,9 @@ __device__ __forceinline__ void spread() {
   }
 }
 
-template <typename T, int LA, int LB, int BM, int BN, int WGM, int WGN, bool DIRECT, int MODE>
+template <typename T, int LA, int LB, int BM, int BN, int WGM, int WGN, int LOADING, int MODE>
 __global__ __launch_bounds__(WGM* WGN * 64) void prod_tile_kernel(const ProdArgs a) {
+  constexpr bool DIRECT = LOADING != kThrough;
   constexpr int NT = WGM * WGN * 64;
   constexpr int WM = BM / WGM, WN = BN / WGN, RB = WM / 16, CB = WN / 16;
   constexpr int BK = 128 / (int)sizeof(T);
@@ -398,8 +431,8 @@ __global__ __launch_bounds__(WGM* WGN * 64) void prod_tile_kernel(const ProdArgs
   using TA = OperandTile<T, LA, BM, NT>;
   using TB = OperandTile<T, LB, BN, NT>;
   // (a grouped sum's rows may be gathered on either side)
-  using LoadA = Loader<T, LA, BM, NT, DIRECT, MODE == kSums>;
-  using LoadB = Loader<T, LB, BN, NT, DIRECT, MODE == kSums>;
+  using LoadA = Loader<T, LA, BM, NT, LOADING, MODE == kSums>;
+  using LoadB = Loader<T, LB, BN, NT, LOADING, MODE == kSums>;
   LoadA la;
   LoadB lb;
   la.init(sa, row0, k_lo);

@@ -67,10 +67,43 @@ def test_linear_exact_integers(dtype, order, shape, pad):
     Y2.check("Y")
 
 
+@pytest.mark.parametrize("dtype", TYPES, ids=ids)
+@pytest.mark.parametrize("order", ["kn", "nk"])
+@pytest.mark.parametrize("shape", [(70, 70, 66), (130, 262, 190), (300, 134, 1002), (140, 5, 130),
+                                   (140, 130, 3), (65, 1, 4), (200, 66, 64)], ids=str)
+@pytest.mark.parametrize("pad,shift", [(0, 0), (2, 2), (2, 1), (1, 0), (6, 4)])
+def test_linear_alignments(dtype, order, shape, pad, shift):
+    """Rows at 4-byte and at element boundaries, straddling chunks on every edge;
+    the buffers' ends are the operands' ends."""
+    m, n, k = shape
+    g = gen(21)
+    X = Guarded(m, k, dtype, pad=pad, shift=shift, data=ints(g, m, k).to(dtype))
+    rows, cols = (k, n) if order == "kn" else (n, k)
+    W = Guarded(rows, cols, dtype, pad=pad, shift=shift, data=ints(g, rows, cols).to(dtype))
+    w = W.t if order == "kn" else W.t.t()
+    Y = Guarded(m, n, F32, pad=pad, shift=shift)
+    pg.linear(X.t, w, Y.t)
+    want = X.t.double().cpu() @ w.double().cpu()
+    assert torch.equal(Y.t.double().cpu(), want)
+    Y.check("Y")
+    # the gradients' products of the same operands
+    dX = Guarded(m, n, dtype, pad=pad, shift=shift)
+    dW = Guarded(n, n, F32, pad=pad, shift=shift)
+    ws = space(pg.linear_backward_workspace(m, k, n, dtype))
+    pg.linear_backward(X.t, dX.t, w.t(), dX=dX.t, ws=ws)
+    assert torch.equal(dX.t.cpu(), want.to(dtype))
+    dX.check("dX")
+    D = Guarded(m, n, dtype, pad=pad, shift=shift, data=ints(g, m, n).to(dtype))
+    ws = space(pg.linear_backward_workspace(m, n, n, dtype))
+    pg.linear_backward(D.t, D.t, None, dW=dW.t, ws=ws)
+    assert torch.equal(dW.t.double().cpu(), D.t.double().cpu().t() @ D.t.double().cpu())
+    dW.check("dW")
+
+
 # one more, one less and exactly whole tiles of the large class, long k over
 # several workgroups
 LARGE = [(2304, 2304, 192), (2305, 2312, 200), (4096, 2048, 64), (100, 96, 8192), (8, 64, 16384),
-         (2, 3000, 4096), (515, 517, 999), (48, 2048, 2048), (1000, 1000, 1000)]
+         (2, 3000, 4096), (515, 517, 999), (1030, 1026, 1002), (48, 2048, 2048), (1000, 1000, 1000)]
 
 
 @pytest.mark.parametrize("dtype", TYPES, ids=ids)
