@@ -21,7 +21,7 @@ hipError_t launch_tile(const ProdArgs& a, hipStream_t s) {
   long long tiles = (long long)a.tiles_m * a.tiles_n;
   if (MODE == kSums) tiles *= a.groups;
   return launch(&prod_tile_kernel<T, LA, LB, BM, BN, WGM, WGN, LOADING, MODE>,
-                dim3((unsigned)tiles, MODE == kDense ? (unsigned)a.splits : 1), WGM * WGN * 64, a,
+                dim3((unsigned)tiles, MODE == kRows ? 1 : (unsigned)a.splits), WGM * WGN * 64, a,
                 s);
 }
 
@@ -46,7 +46,9 @@ hipError_t prod_tile(const ProdArgs& a, int kernel, int loading, hipStream_t s) 
 
 template <typename T, int LB, int MB, int MODE>
 hipError_t prod_few(const ProdArgs& a, bool wide, hipStream_t s) {
-  const dim3 grid((unsigned)(MODE == kRows ? a.tiles_n * a.groups : a.tiles_n),
+  // no more groups have rows than there are rows
+  const int groups = a.groups < a.rows ? a.groups : a.rows;
+  const dim3 grid((unsigned)(MODE == kRows ? a.tiles_n * groups : a.tiles_n),
                   MODE == kDense ? (unsigned)a.splits : 1);
   if (wide) return launch(&prod_rows_kernel<T, LB, MB, 4, 8, MODE>, grid, 512, a, s);
   return launch(&prod_rows_kernel<T, LB, MB, 1, 8, MODE>, grid, 512, a, s);
@@ -57,6 +59,12 @@ hipError_t prod_few(const ProdArgs& a, int kernel, hipStream_t s) {
   const bool wide = kernel == kFew16Wide || kernel == kFew32Wide;
   return kernel == kFew16 || kernel == kFew16Wide ? prod_few<T, LB, 1, MODE>(a, wide, s)
                                                   : prod_few<T, LB, 2, MODE>(a, wide, s);
+}
+
+template <typename T>
+hipError_t reduce(const ProdArgs& a, hipStream_t s) {
+  const long long items = (long long)(a.groups > 0 ? a.groups : 1) * a.M * ((a.N + 7) / 8);
+  return launch(&prod_reduce_kernel<T>, dim3((unsigned)((items + 255) / 256)), 256, a, s);
 }
 
 template <typename T>
@@ -73,11 +81,7 @@ hipError_t prod(const ProdArgs& a, int la, int lb, int mode, int kernel, int loa
     else
       e = lb == kInner ? prod_tile<T, kInner, kInner, kDense>(a, kernel, loading, s)
                        : prod_tile<T, kInner, kOuter, kDense>(a, kernel, loading, s);
-    if (e == hipSuccess && a.splits > 1) {
-      const long long items = (long long)a.M * ((a.N + 7) / 8);
-      e = launch(&prod_reduce_kernel<T>, dim3((unsigned)((items + 255) / 256)), 256, a, s);
-    }
-    return e;
+    return e == hipSuccess && a.splits > 1 ? reduce<T>(a, s) : e;
   }
   if (mode == kRows) {
     if (few)
@@ -86,7 +90,8 @@ hipError_t prod(const ProdArgs& a, int la, int lb, int mode, int kernel, int loa
     return lb == kInner ? prod_tile<T, kInner, kInner, kRows>(a, kernel, loading, s)
                         : prod_tile<T, kInner, kOuter, kRows>(a, kernel, loading, s);
   }
-  return prod_tile<T, kOuter, kOuter, kSums>(a, kernel, loading, s);
+  e = prod_tile<T, kOuter, kOuter, kSums>(a, kernel, loading, s);
+  return e == hipSuccess && a.splits > 1 ? reduce<T>(a, s) : e;
 }
 
 template <typename T>

@@ -105,6 +105,12 @@ double tiles_time(const ClassTime& c, double tiles, double tile_flops) {
   return t;
 }
 
+// Bytes of a plan's partial sums.
+size_t split_space(const Plan& p, int mode, long long rows, int groups, int n) {
+  if (p.splits <= 1) return 0;
+  return (size_t)p.splits * (size_t)rows * (size_t)n * 4 * (size_t)(mode == kSums ? groups : 1);
+}
+
 // rows: the rows of D over all groups (how they are distributed is not known
 // here; any distribution is correct).  may_split: the summed index may be
 // shared by workgroups, through partial sums in `ws_bytes` bytes (any_ws: as
@@ -114,7 +120,7 @@ Plan plan_product(int size, int la, int mode, long long rows, int groups, int n,
   Plan p;
   p.loading = loading;
   const int bk = 128 / size;
-  if (mode != kDense) may_split = false;
+  if (mode == kRows) may_split = false;
   if (mode == kRows && groups > rows) groups = (int)rows;
   const double per = mode == kRows ? (double)rows / groups : (double)rows;
   if (la == kInner && per <= 32) {
@@ -142,12 +148,12 @@ Plan plan_product(int size, int la, int mode, long long rows, int groups, int n,
       else tiles *= (double)ceil_div(rows, bm) * (mode == kSums ? groups : 1);
       const double depth = mode == kSums ? (double)k / groups : (double)k;
       const ClassTime ct = class_time(c, size);
-      for (int s = 1; s <= 64; s *= 2) {
-        if (s > 1 &&
-            (!may_split || k / s < 4 * bk || tiles * s > (double)kUnits * ct.together))
-          break;
+      const double matrix = (double)rows * n * (mode == kSums ? groups : 1);
+      for (const int s : {1, 2, 3, 4, 5, 6, 8, 10, 12, 16, 24, 32, 48, 64}) {
+        // (beyond 16 pieces per compute unit nothing is left to balance)
+        if (s > 1 && (!may_split || depth / s < 4 * bk || tiles * s > 16.0 * kUnits)) break;
         // the partial sums' traffic, and the launch that adds them
-        const double split = s > 1 ? 4e-6 + (double)s * (double)rows * n * 8 / 6e12 : 0;
+        const double split = s > 1 ? 4e-6 + s * matrix * 8 / 6e12 : 0;
         const double t = tiles_time(ct, tiles * s, 2.0 * bm * bn * depth / s) + split;
         if (best == 0 || t < best) {
           best = t;
@@ -158,21 +164,23 @@ Plan plan_product(int size, int la, int mode, long long rows, int groups, int n,
     }
   }
   if (p.splits > 1) {
-    p.k_split = (int)round_up(ceil_div(k, p.splits), bk);
-    p.splits = (int)ceil_div(k, p.k_split);
-    const size_t need = (size_t)p.splits * (size_t)rows * (size_t)n * 4;
+    if (mode == kDense) {
+      p.k_split = (int)round_up(ceil_div(k, p.splits), bk);
+      p.splits = (int)ceil_div(k, p.k_split);
+    }
+    const size_t need = split_space(p, mode, rows, groups, n);
     if (!any_ws && ws_bytes < need)   // the best plan that needs no space
       return plan_product(size, la, mode, rows, groups, n, k, loading, 0, false, false);
   }
   return p;
 }
 
-// Workspace that plan_product may use for a dense product, over any alignment.
-size_t split_bytes(int size, int la, int rows, int n, int k) {
+// Workspace that plan_product may use for a product, over any alignment.
+size_t split_bytes(int size, int la, int mode, long long rows, int groups, int n, int k) {
   size_t most = 0;
   for (const int loading : {kThrough, kDirect}) {
-    const Plan p = plan_product(size, la, kDense, rows, 1, n, k, loading, 0, true);
-    const size_t b = p.splits > 1 ? (size_t)p.splits * (size_t)rows * (size_t)n * 4 : 0;
+    const Plan p = plan_product(size, la, mode, rows, groups, n, k, loading, 0, true);
+    const size_t b = split_space(p, mode, rows, groups, n);
     if (b > most) most = b;
   }
   return most;
@@ -239,7 +247,7 @@ struct BackSpace {
   size_t total() const { return dz + rest; }
 };
 
-BackSpace back_space(const pgemm_kind& kind, long long rows, int n, int k, int groups) {
+BackSpace back_space(const pgemm_kind& kind, int rows, int n, int k, int groups, bool grouped) {
   BackSpace b;
   const int size = size_of(kind.dtype);
   b.ldz = round_up(n, 8);
@@ -247,13 +255,12 @@ BackSpace back_space(const pgemm_kind& kind, long long rows, int n, int k, int g
   if (rows < 1) rows = 1;
   b.chunks = slope_chunks(rows, groups, n);
   b.rest = (size_t)groups * (size_t)b.chunks * (size_t)n * 4;
-  if (groups == 1 && rows <= INT32_MAX) {
-    const size_t parts[3] = {split_bytes(size, kInner, (int)rows, k, n),
-                             split_bytes(size, kOuter, k, n, (int)rows),
-                             split_bytes(size, kOuter, n, k, (int)rows)};
-    for (const size_t x : parts)
-      if (x > b.rest) b.rest = x;
-  }
+  const int r = (int)rows, mode = grouped ? kSums : kDense;
+  const size_t parts[3] = {grouped ? 0 : split_bytes(size, kInner, kDense, r, 1, k, n),
+                           split_bytes(size, kOuter, mode, k, groups, n, r),
+                           split_bytes(size, kOuter, mode, n, groups, k, r)};
+  for (const size_t x : parts)
+    if (x > b.rest) b.rest = x;
   b.rest = align256(b.rest);
   return b;
 }
@@ -398,7 +405,7 @@ int pgemm_linear(pgemm_kind kind, int m, int n, int k, pgemm_rows X, pgemm_weigh
 
 size_t pgemm_linear_workspace(int dtype, int m, int n, int k) {
   if (!known(dtype) || m <= 0 || n <= 0 || k <= 0) return 0;
-  return split_bytes(size_of(dtype), kInner, m, n, k);
+  return split_bytes(size_of(dtype), kInner, kDense, m, 1, n, k);
 }
 
 int pgemm_linear_backward(pgemm_kind kind, int m, int n, int k, pgemm_rows dY, pgemm_rows Z,
@@ -417,7 +424,7 @@ int pgemm_linear_backward(pgemm_kind kind, int m, int n, int k, pgemm_rows dY, p
   if (!rows_ok(dX, k, size, false)) return -9;
   if (!weight_ok(dW, k, n, osize, false, 1)) return -10;
   if (!vector_ok(dbias, osize, false)) return -11;
-  const BackSpace space = back_space(kind, m, n, k, 1);
+  const BackSpace space = back_space(kind, m, n, k, 1, false);
   if (space.total() > 0 && (workspace == nullptr || !aligned_to(workspace, 16))) return -12;
   if (workspace_bytes < space.total()) return -13;
   if (n == 0) {
@@ -431,7 +438,7 @@ int pgemm_linear_backward(pgemm_kind kind, int m, int n, int k, pgemm_rows dY, p
 
 size_t pgemm_linear_backward_workspace(pgemm_kind kind, int m, int n, int k) {
   if (!kind_ok(kind) || m < 0 || n <= 0 || k < 0) return 0;
-  return back_space(kind, m, n, k, 1).total();
+  return back_space(kind, m, n, k, 1, false).total();
 }
 
 int pgemm_route(int dtype, int m, int experts, int top, int score, int groups, int top_groups,
@@ -575,7 +582,7 @@ int pgemm_expert_linear_backward(pgemm_kind kind, int rows, int n, int k, pgemm_
   if (!weight_ok(dW, k, n, osize, false, plan.experts)) return -11;
   if (!vector_ok(dbias, osize, false)) return -12;
   const int experts = plan.experts;
-  const BackSpace space = back_space(kind, rows, n, k, experts);
+  const BackSpace space = back_space(kind, rows, n, k, experts, true);
   if (space.total() > 0 && (workspace == nullptr || !aligned_to(workspace, 16))) return -13;
   if (workspace_bytes < space.total()) return -14;
   BackArgs b{kind, rows, n, k, experts, plan.offsets, plan.tokens, plan.x_rows,
@@ -587,7 +594,7 @@ int pgemm_expert_linear_backward(pgemm_kind kind, int rows, int n, int k, pgemm_
 size_t pgemm_expert_linear_backward_workspace(pgemm_kind kind, int rows, int n, int k,
                                               int experts) {
   if (!kind_ok(kind) || rows < 0 || n <= 0 || k < 0 || experts < 1) return 0;
-  return back_space(kind, rows, n, k, experts).total();
+  return back_space(kind, rows, n, k, experts, true).total();
 }
 
 int pgemm_combine(int dtype, int m, int n, int top, int rows, pgemm_rows Y, const int* slots,

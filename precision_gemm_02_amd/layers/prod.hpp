@@ -341,8 +341,9 @@ __device__ __forceinline__ void group_bounds(const int* offsets, int e, int rows
 }
 
 // The group that holds row tile t when every group takes ceil(rows / bm)
-// tiles: its index (-1: t is past the last tile), first row and rows left.
-// Every lane of the calling wave takes part and gets the same answer.
+// tiles (bm 0: one, if it has rows): its index (-1: t is past the last tile),
+// first row and rows left.  Every lane of the calling wave takes part and gets
+// the same answer.
 __device__ __forceinline__ int find_group(const int* offsets, int groups, int rows, int bm, int t,
                                           int* row, int* left) {
   const int lane = threadIdx.x & 63;
@@ -351,7 +352,7 @@ __device__ __forceinline__ int find_group(const int* offsets, int groups, int ro
     const int e = e0 + lane;
     int lo = 0, hi = 0;
     if (e < groups) group_bounds(offsets, e, rows, &lo, &hi);
-    const int n = (hi - lo + bm - 1) / bm;
+    const int n = bm == 0 ? (hi > lo ? 1 : 0) : (int)(((long long)(hi - lo) + bm - 1) / bm);
     int sum = n;   // inclusive prefix sum over the wave
 #pragma unroll
     for (int d = 1; d < 64; d <<= 1) {

@@ -40,10 +40,19 @@ __global__ __launch_bounds__(WAVES * 64) void prod_rows_kernel(const ProdArgs a)
   const T* Bb = static_cast<const T*>(a.B);
   const void* bias = a.bias;
   if constexpr (MODE == kRows) {
-    e = id / a.tiles_n;
     nb = id % a.tiles_n;
-    group_bounds(a.offsets, e, a.rows, &lo, &hi);
-    if (lo == hi) return;
+    e = id / a.tiles_n;
+    if (a.rows < a.groups) {
+      // fewer rows than groups: the e-th group that has some (the search takes
+      // longer than to end a workgroup: 64 rows over 64 groups 46 us, so 58)
+      int left;
+      e = find_group(a.offsets, a.groups, a.rows, 0, e, &lo, &left);
+      if (e < 0) return;
+      hi = lo + left;
+    } else {
+      group_bounds(a.offsets, e, a.rows, &lo, &hi);
+      if (lo == hi) return;
+    }
     Bb += e * a.strideB;
     if (bias != nullptr) bias = static_cast<const T*>(bias) + e * a.strideBias;
   }
@@ -219,18 +228,19 @@ __global__ __launch_bounds__(WAVES * 64) void prod_rows_kernel(const ProdArgs a)
   }
 }
 
-// Sums the splits of a product in order and runs its epilogue: 8 columns per
-// thread.
+// Sums the splits of a product (of every group's, for grouped sums) in order and
+// runs its epilogue: 8 columns per thread.
 template <typename T>
 __global__ __launch_bounds__(256) void prod_reduce_kernel(const ProdArgs a) {
-  const int per_row = (a.N + 7) / 8;
+  const int per_row = (a.N + 7) / 8, groups = a.groups > 0 ? a.groups : 1;
   const long long id = (long long)blockIdx.x * 256 + threadIdx.x;
-  if (id >= (long long)a.M * per_row) return;
-  const long long m = id / per_row;
+  if (id >= (long long)groups * a.M * per_row) return;
+  const long long row = id / per_row;
   const int n = (int)(id % per_row) * 8;
   float v[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+#pragma unroll 4
   for (int s = 0; s < a.splits; ++s) {
-    const float* from = a.partial + ((long long)s * a.M + m) * a.N + n;
+    const float* from = a.partial + ((long long)s * groups * a.M + row) * a.N + n;
     if (n + 8 <= a.N) {
       float x[8];
       get8<float>(from, 0, x);
@@ -242,7 +252,9 @@ __global__ __launch_bounds__(256) void prod_reduce_kernel(const ProdArgs a) {
         if (n + j < a.N) v[j] += from[j];
     }
   }
-  finish8<T>(a, a.bias, a.D, m, n, v);
+  const long long e = row / a.M, m = row - e * a.M;
+  char* D = static_cast<char*>(a.D) + e * a.strideD * (a.out32 ? 4 : (int)sizeof(T));
+  finish8<T>(a, a.bias, D, m, n, v);
 }
 
 }  // namespace layers

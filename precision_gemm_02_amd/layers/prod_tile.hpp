@@ -119,6 +119,10 @@ struct Source {
     const int t = gather[r];
     return t < 0 ? 0 : (t < gather_rows ? t : gather_rows - 1);
   }
+  // Behind the last element of the last row.
+  __device__ __forceinline__ const T* end() const {
+    return base + (long long)((gather != nullptr ? gather_rows : outer) - 1) * ld + inner;
+  }
   __device__ __forceinline__ const T* row(int r) const {
     if (r >= outer) return nullptr;
     return base + (long long)(gather != nullptr ? token(r) : r) * ld;
@@ -138,11 +142,15 @@ __device__ __forceinline__ u32x4 load_guarded(const T* row, int c0, int inner) {
   return __builtin_bit_cast(u32x4, v);
 }
 
-// The same where the whole chunk is known to be inside: no branch, a row that
-// is not there reads the zero chunk.
+// A chunk at p, outer order, of which `live` elements exist in its row: what
+// follows them only reaches results that are never stored, so the whole chunk
+// is read wherever it ends before the operand's end.
 template <typename T>
-__device__ __forceinline__ u32x4 load_whole(const T* row, int c0) {
-  return load16(row != nullptr ? (const void*)(row + c0) : (const void*)&kZeroChunk);
+__device__ __forceinline__ u32x4 load_edge(const T* p, int live, const T* end) {
+  constexpr int V = 16 / (int)sizeof(T);
+  if (live <= 0) return u32x4{0, 0, 0, 0};
+  if (p + V <= end) return load16(p);
+  return load_guarded(p, 0, live);
 }
 
 // 16 bytes per lane from its own address straight to LDS: lane l of the wave
@@ -227,8 +235,8 @@ struct Loader {
   // Whether a chunk of the next load (through registers) is outside the operand
   // or straddles its end.  The same for the whole workgroup.
   __device__ __forceinline__ bool ragged() const {
-    const bool last = k + Tile::BK > (ORDER == kInner ? src.inner : src.outer);
-    return last || (ORDER == kOuter && first + EXT > src.inner);
+    if constexpr (ORDER == kInner) return k + Tile::BK > src.inner;
+    return k + Tile::BK > src.outer || first + EXT > src.inner;
   }
 
   // Chunks J0 .. J1-1 of the load of summed indices k .. k+BK-1.  Direct loads
@@ -274,12 +282,21 @@ struct Loader {
       } else if constexpr (WHOLE) {
         reg[j] = load16(p);
       } else {
-        const int at = ORDER == kInner ? k + c * Tile::V : first + c * Tile::V;
-        const bool row = ORDER == kInner ? first + r < src.outer : k + r < src.outer;
-        reg[j] = load_guarded(row ? p - at : nullptr, at, src.inner);
+        reg[j] = guarded(p, r, c);
       }
       if constexpr (ORDER == kInner) ptr[j] += Tile::BK;
       else if constexpr (!GATHER) ptr[j] += step;
+    }
+  }
+
+  // Chunk c of row r, at p, with guards.
+  __device__ __forceinline__ u32x4 guarded(const T* p, int r, int c) const {
+    if constexpr (ORDER == kInner) {
+      const int at = k + c * Tile::V;
+      return load_guarded(first + r < src.outer ? p - at : nullptr, at, src.inner);
+    } else {
+      const int at = first + c * Tile::V;
+      return load_edge(p, k + r < src.outer ? src.inner - at : 0, src.end());
     }
   }
 
@@ -290,10 +307,7 @@ struct Loader {
     for (int j = J0; j < J1; ++j) {
       int r, c;
       Tile::slot(j * NT + (int)threadIdx.x, &r, &c);
-      const int at = ORDER == kInner ? k + c * Tile::V : first + c * Tile::V;
-      const bool row = ORDER == kInner ? first + r < src.outer : k + r < src.outer;
-      *reinterpret_cast<u32x4*>(lds + (j * NT + (int)threadIdx.x) * 16) =
-          load_guarded(row ? ptr[j] - at : nullptr, at, src.inner);
+      *reinterpret_cast<u32x4*>(lds + (j * NT + (int)threadIdx.x) * 16) = guarded(ptr[j], r, c);
       if constexpr (ORDER == kInner) ptr[j] += Tile::BK;
       else if constexpr (!GATHER) ptr[j] += step;
     }
@@ -395,6 +409,12 @@ __global__ __launch_bounds__(WGM* WGN * 64) void prod_tile_kernel(const ProdArgs
     map_tile(blockIdx.x % tiles, a.tiles_m, a.tiles_n, &tm, &tn);
     group_bounds(a.offsets, e, a.rows, &k_lo, &k_hi);
     row0 = tm * BM;
+    if (a.splits > 1) {
+      const int part = ((k_hi - k_lo + a.splits - 1) / a.splits + BK - 1) / BK * BK;
+      const long long from = k_lo + (long long)part * blockIdx.y;
+      k_lo = from < k_hi ? (int)from : k_hi;
+      k_hi = k_hi - k_lo < part ? k_hi : k_lo + part;
+    }
   } else {
     map_tile(blockIdx.x, a.tiles_m, a.tiles_n, &tm, &tn);
     if constexpr (MODE == kRows) {
@@ -576,7 +596,7 @@ __global__ __launch_bounds__(WGM* WGN * 64) void prod_tile_kernel(const ProdArgs
   float* stg = reinterpret_cast<float*>(lds) + wave * 32 * EPI_LD;
   constexpr int LPR = WN / 8, RPP = 64 / LPR, PASSES = 32 / RPP;   // lanes per row, rows per pass
   const int col = (lane % LPR) * 8, n = col0 + wn + col;
-  const bool split = MODE == kDense && a.splits > 1;
+  const bool split = MODE != kRows && a.splits > 1;
   float b8[8];
   load_bias<T>(a, split ? nullptr : bias, n, b8);
 #pragma unroll 1
@@ -615,7 +635,8 @@ __global__ __launch_bounds__(WGM* WGN * 64) void prod_tile_kernel(const ProdArgs
           v[4 + j] = y[j] + b8[4 + j];
         }
         if (split) {
-          float* to = a.partial + ((long long)blockIdx.y * a.M + m) * a.N + n;
+          const long long matrix = MODE == kSums ? (long long)blockIdx.y * a.groups + e : blockIdx.y;
+          float* to = a.partial + (matrix * a.M + m) * a.N + n;
           if (n + 8 <= a.N) {
             put8<float>(to, 0, v);
           } else {
