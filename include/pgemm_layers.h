@@ -18,7 +18,9 @@
  *   content on entry is ignored.  Calls that share one must be ordered.
  * Capture.  Every call only launches kernels (no allocation, memset or
  *   synchronization), so it can be captured into a HIP graph.
- * Determinism.  Identical inputs give identical bits.  No atomics are used.
+ * Determinism.  Identical inputs give identical bits.
+ * Reads.  Rows of a matrix may be read up to 16 bytes past their end where that
+ *   is still before the end of its last row (such values reach no result).
  */
 #ifndef PGEMM_LAYERS_H
 #define PGEMM_LAYERS_H
@@ -103,7 +105,8 @@ size_t pgemm_linear_backward_workspace(pgemm_kind kind, int m, int n, int k);
  *   scores: softmax over the experts, or the sigmoid, of the logits (m x
  *   experts, of dtype).  A logit of -inf or of the type's lowest value is
  *   masked, and so is NaN: such an expert has score 0 and is never chosen.
- *   key: score + bias (fp32, or NULL); with neither bias nor groups the logit
+ *   key: score + bias (fp32, or NULL; a bias that is not finite, or beyond
+ *   3e38, masks its expert); with neither bias nor groups the logit
  *   itself (the scores' own order, also where they underflow).  Keys are
  *   compared in 64 bits; ties go to the lower index.
  *   groups: the experts in `groups` equal ranges; only the top_groups with the

@@ -449,7 +449,8 @@ def random_plan(g, m, top, E, drop=0.1, empty=()):
 
 EXPERT_SHAPES = [  # m, top, E, n, k
     (1, 1, 1, 8, 8), (1, 2, 8, 64, 64), (16, 4, 16, 80, 72), (40, 3, 5, 130, 65),
-    (100, 2, 3, 136, 264), (300, 4, 6, 64, 40), (90, 8, 70, 33, 96), (700, 2, 4, 264, 128)]
+    (100, 2, 3, 136, 264), (300, 4, 6, 64, 40), (90, 8, 70, 33, 96), (700, 2, 4, 264, 128),
+    (300, 2, 3, 134, 262)]
 
 
 @pytest.mark.parametrize("dtype", TYPES, ids=ids)
@@ -508,6 +509,45 @@ def test_expert_linear_backward_exact_integers(dtype, order, shape, gather):
         assert torch.equal(dW[e].double().cpu(), X.double().cpu()[src].t() @ dz)
         assert torch.equal(db[e].double().cpu(), dz.sum(0))
     dX.check("dX", rows=o[-1])
+
+
+@pytest.mark.parametrize("dtype", TYPES, ids=ids)
+@pytest.mark.parametrize("order", ["kn", "nk"])
+@pytest.mark.parametrize("bounds", [[0, 0, 4500, 4501, 6000], [0, 1500, 3000, 4500, 6000],
+                                    [0, 6000, 6000, 6000, 6000], [0, 0, 0, 0, 0],
+                                    [0, 63, 64, 65, 321]], ids=str)
+@pytest.mark.parametrize("n,k", [(72, 40), (33, 70)])
+def test_expert_gradients_over_long_rows(dtype, order, bounds, n, k):
+    """Few tiles and many rows: each expert's rows are shared by workgroups."""
+    R, E = 6000, 4
+    g = gen(24)
+    X, dY = ints(g, R, k, hi=1).to(dtype).cuda(), ints(g, R, n, hi=1).to(dtype).cuda()
+    tok = torch.randperm(R, generator=g).int()
+    off = torch.tensor(bounds, dtype=torch.int32, device="cuda")
+    rows, cols = (k, n) if order == "kn" else (n, k)
+    dW = torch.full((E, rows, cols), math.nan, device="cuda")
+    dW = dW if order == "kn" else dW.transpose(1, 2)
+    db = torch.full((E, n), math.nan, device="cuda")
+    size = pg.expert_linear_backward_workspace(R, n, k, E, dtype)
+    assert size > E * n * k * 4                  # the plan has room for partial sums
+    W = weight(g, (E,), k, n, order, dtype, integer=True)
+    pg.expert_linear_backward(dY, X, W, off, tokens=tok.cuda(), dW=dW, dbias=db, ws=space(size))
+    x, dy = X.double().cpu()[tok.long()], dY.double().cpu()
+    for e in range(E):
+        s = slice(bounds[e], bounds[e + 1])
+        assert torch.equal(dW[e].double().cpu(), x[s].t() @ dy[s])
+        assert torch.equal(db[e].double().cpu(), dy[s].sum(0))
+
+
+def test_zero_inner_size_in_tiles():
+    bias = torch.arange(130.0, device="cuda")
+    Y = torch.full((70, 130), 9.0, device="cuda")
+    pg.linear(torch.zeros(70, 0, device="cuda"), torch.zeros(0, 130, device="cuda"), Y, bias=bias)
+    assert torch.equal(Y, bias.expand(70, 130))
+    dX = torch.full((70, 5), 9.0, device="cuda")
+    pg.linear_backward(torch.zeros(70, 0, device="cuda"), None, torch.zeros(5, 0, device="cuda"),
+                       dX=dX, ws=space(1 << 20))
+    assert (dX == 0).all()
 
 
 def test_expert_linear_skewed_and_large():
