@@ -13,6 +13,9 @@ the layout from their strides: a column-major view (stride (1, ld)) is used
 as is; a row-major tensor (stride (ld, 1)) is served by the operand swap
 C^T = B^T A^T, which moves no data.
 
+The layer operators (``linear``, ``route``, ``expert_linear``, ``combine`` and
+their gradients, see ``layer_ops``) take tensors and are imported here.
+
 The library must be built (``python precision_gemm_02_amd/build.py``, which
 does not import this package); if it is missing or older than this binding,
 importing this package raises ImportError.  There is no CPU or

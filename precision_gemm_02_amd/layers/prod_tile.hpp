@@ -1,6 +1,15 @@
 // The tile kernel: one BM x BN tile of D per workgroup, WGM x WGN waves,
 // matrix cores fed from LDS.  See prod.hpp for the operands' orders and the
 // groups.
+//
+// Large products are bound by the matrix cores at the power-limited clock:
+// 8192 x 8192 x 4096 bf16 with activation and Z 455 us (1.21 PFLOP/s; a plain
+// library product of that shape 420 to 440), 4096^3 114 to 118 us, fp32 4096^3
+// 966 us (142 TFLOP/s).  256 x 256 tiles (8 waves of 128 x 64, all of a compute
+// unit's LDS) halve the LDS and cache traffic per flop of 128 x 128 ones (two
+// workgroups per unit), which win where 256 x 256 would leave units idle; 64 x
+// 64 (four per unit) for small products.  4 waves of 128 x 128 measured 6 to 9
+// % slower than 8.
 #pragma once
 
 #include <type_traits>
@@ -477,7 +486,9 @@ __global__ __launch_bounds__(WGM* WGN * 64) void prod_tile_kernel(const ProdArgs
   // for the 256 x 256 tiles): A(t + 2) and B(t + 1) are fetched during tile t,
   // two loads a step, so that the memory pipe never runs empty at a barrier.
   // (With two whole stages, all of tile t + 1 was fetched within tile t and
-  // awaited at its end: 25.2 against 22 ns per inner index at 4096 x 4096.)
+  // awaited at its end: 25.3 ns per inner index at 4096 x 4096 bf16, with the
+  // ring 24.4, with the loads written as the instruction 22.8; the matrix
+  // cores alone, no loads in the loop, take 20.4 at the clock this load leaves.)
   // Register loads use four: tile t + 1 is stored during tile t, tile t + 2
   // fetched.
   constexpr int GP = RB / 2, G = 2 * GP;
