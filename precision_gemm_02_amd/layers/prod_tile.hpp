@@ -183,6 +183,15 @@ __device__ __forceinline__ void load_to_lds(const void* from, char* to) {
       : "s"(at), "v"(from));
 }
 
+// At most N of this wave's global loads are outstanding.
+template <int N>
+__device__ __forceinline__ void wait_loads() {
+  static_assert(N < 64, "the counter's range");
+  __builtin_amdgcn_sched_barrier(0);
+  asm volatile("s_waitcnt vmcnt(%0)" ::"n"(N) : "memory");
+  __builtin_amdgcn_sched_barrier(0);
+}
+
 // One operand's loads, tile after tile of the summed index.
 //
 // DIRECT: straight into LDS (global_load_lds_dwordx4: a wave writes 64
@@ -309,9 +318,13 @@ struct Loader {
     }
   }
 
-  // RAGGED: the same chunks with guards, through registers, at once.
+  // RAGGED: the same chunks with guards, through registers, at once.  The K loop
+  // counts on these chunks as loads in flight behind the tile it waits for; here
+  // there may be none (a wave whose rows are all outside), so that everything
+  // issued before them has to land first.
   template <int J0, int J1>
   __device__ __forceinline__ void load_guards(char* lds) {
+    if constexpr (J0 < J1) wait_loads<0>();
 #pragma unroll
     for (int j = J0; j < J1; ++j) {
       int r, c;
@@ -362,15 +375,6 @@ __device__ __forceinline__ void static_for(F f) {
 __device__ __forceinline__ void workgroup_barrier() {
   __builtin_amdgcn_sched_barrier(0);
   asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
-  __builtin_amdgcn_sched_barrier(0);
-}
-
-// At most N of this wave's global loads are outstanding.
-template <int N>
-__device__ __forceinline__ void wait_loads() {
-  static_assert(N < 64, "the counter's range");
-  __builtin_amdgcn_sched_barrier(0);
-  asm volatile("s_waitcnt vmcnt(%0)" ::"n"(N) : "memory");
   __builtin_amdgcn_sched_barrier(0);
 }
 

@@ -100,6 +100,29 @@ def test_linear_alignments(dtype, order, shape, pad, shift):
     dW.check("dW")
 
 
+@pytest.mark.parametrize("dtype", [F16, BF16], ids=ids)
+@pytest.mark.parametrize("order", ["kn", "nk"])
+@pytest.mark.parametrize("k", [66, 126, 130, 186, 188, 190, 194, 258, 1026])
+@pytest.mark.parametrize("shape", [(65, 40), (129, 65), (257, 514)], ids=str)
+def test_linear_waves_without_rows(dtype, order, k, shape):
+    """Rows at 4-byte boundaries where whole waves of the last tiles have none, at
+    inner sizes around the last whole tile: such a wave issues no loads of its
+    own for the tiles that are read with guards, and still has to wait for the
+    ones before."""
+    m, n = shape
+    g = gen(k)
+    X = Guarded(m, k, dtype, pad=2, shift=2, data=ints(g, m, k).to(dtype))
+    rows, cols = (k, n) if order == "kn" else (n, k)
+    W = Guarded(rows, cols, dtype, pad=2, shift=2, data=ints(g, rows, cols).to(dtype))
+    w = W.t if order == "kn" else W.t.t()
+    want = X.t.double().cpu() @ w.double().cpu()
+    for _ in range(8):
+        Y = Guarded(m, n, F32, pad=2)
+        pg.linear(X.t, w, Y.t)
+        assert torch.equal(Y.t.double().cpu(), want)
+        Y.check("Y")
+
+
 # one more, one less and exactly whole tiles of the large class, long k over
 # several workgroups
 LARGE = [(2304, 2304, 192), (2305, 2312, 200), (4096, 2048, 64), (100, 96, 8192), (8, 64, 16384),
