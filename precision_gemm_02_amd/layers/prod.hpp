@@ -47,7 +47,7 @@ __device__ __forceinline__ void store16(void* p, u32x4 v) { static_cast<Bytes16*
 // l = 16 g + i gives row i of A and column i of B, chunk g.  fp32 takes it in
 // four instructions (lane group g: index 4 g + s at instruction s); both
 // operands use the same order, so every product is formed once.  (32 x 32
-// blocks were 3 to 5 % slower in the large tiles on random data.)
+// blocks were 2 to 4 % slower in the large tiles on random data.)
 template <typename T>
 struct Elem;
 template <>

@@ -15,6 +15,10 @@
 // whole chip and most of it is in flight at
 // once.  Workgroups of neighbouring columns run on one XCD: with NB = 1 they
 // share outer-order B's cache lines.
+//
+// Measured, bf16: one row through 4096 x 4096 8.2 us a call (33.6 MB: 4.1 TB/s
+// with the launch); 64 rows over the experts of 64 that 16 tokens chose, 1024 x
+// 2048 each, 47 us (213 MB: 4.5 TB/s; a large copy reaches 5.1).
 #pragma once
 
 #include "prod_tile.hpp"
