@@ -410,7 +410,7 @@ __global__ __launch_bounds__(1024) void route_kernel(const RouteArgs a) {
     int pick;
     float chosen_x;
     for (bool fine = false;; fine = true) {
-      int near = -1;              // integers no further apart than this are not in order
+      int near = 0;               // integers no further apart than this are not in order
       if (!logit_key) {
         if (!fine) {
           near = coarse_near;
@@ -499,7 +499,8 @@ __global__ __launch_bounds__(1024) void route_kernel(const RouteArgs a) {
                                  out = __ballot(first && rank == a.top_groups);
         const int vi = __builtin_amdgcn_readlane(sum, __ffsll((long long)in) - 1),
                   vo = __builtin_amdgcn_readlane(sum, __ffsll((long long)out) - 1);
-        unclear = vo != kNoKey && vi - vo <= 3 * near;
+        // (vi >= vo; sums reach +-2^30, so that the difference needs 32 bits unsigned)
+        unclear = vo != kNoKey && (unsigned)vi - (unsigned)vo <= 3u * (unsigned)near;
 #pragma unroll
         for (int q = 0; q < Q; ++q)
           if (!((keep >> group_bit[q]) & 1)) key[q] = kNoKey;
@@ -518,7 +519,8 @@ __global__ __launch_bounds__(1024) void route_kernel(const RouteArgs a) {
         for (int q = 1; q < Q; ++q) b = key[q] > b ? key[q] : b;
         b = wave_max_int(b);
         if (b == kNoKey) break;
-        if (j > 0 && last - b <= near) unclear = true;
+        // (logits as keys are exact, and their difference can pass 32 bits)
+        if (!logit_key && j > 0 && last - b <= near) unclear = true;
         last = b;
         if (j == a.top) break;
         bool done = false;                       // the lowest index that has it

@@ -390,6 +390,22 @@ def test_route_masks_ties_and_extremes(dtype, score):
         assert torch.equal(ee.cpu(), route64(ref, LOWEST[dtype], 4, score=score, **kw2)[0])
 
 
+@pytest.mark.parametrize("dtype", TYPES, ids=ids)
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("renorm", [False, True])
+@pytest.mark.parametrize("top", [2, 5, 8])
+def test_route_logits_far_apart(dtype, score, renorm, top):
+    """Peaked rows without bias or groups: neighbours among the chosen logits whose
+    bit patterns, as ordered integers, are more than 2^31 apart."""
+    big = min(1e30, torch.finfo(dtype).max / 2)
+    logits = torch.tensor([
+        [10, -1, -2, -3, -4, -5, -6, -7], [2.5, -2.5, 0.5, -0.5, 1.5, -1.5, 0, -4],
+        [big, -1e-3, -2e-3, -1, -2, -3, -4, -5], [-1, math.inf, -2, -3, -4, -5, -6, -7],
+        [9, -0.6, -0.7, -0.8, -0.9, -1, -1.1, -1.2], [big, -big, 1, -1, 3, -3, 2, -2],
+        [-3, -2, -1, 10, 4, -5, 7, -8]]).to(dtype)
+    check_route(logits.repeat(11, 1).cuda(), top, score=score, renorm=renorm)
+
+
 @pytest.mark.parametrize("groups", [1, 4])
 def test_route_close_keys(groups):
     """Keys a few 1e-11 apart: below what the integer keys tell apart (2^-28), well
