@@ -30,6 +30,26 @@ constexpr KernelShape kShape[3] = {{256, 256}, {128, 128}, {64, 64}};
 // Columns of a workgroup of the few-rows kernels.
 constexpr int few_columns(int kernel) { return kernel >= kFew16Wide ? 64 : 16; }
 
+// The launch of a product: workgroups (x, and the splits of the summed index in
+// y) and the threads of each.
+struct ProdGrid {
+  long long x;
+  int y;
+};
+inline ProdGrid prod_grid(const ProdArgs& a, int mode, int kernel) {
+  ProdGrid g = {(long long)a.tiles_m * a.tiles_n, mode == kRows ? 1 : a.splits};
+  if (kernel >= kFew16) {
+    // no more groups have rows than there are rows
+    if (mode == kRows) g.x *= a.groups < a.rows ? a.groups : a.rows;
+  } else if (mode == kSums) {
+    g.x *= a.groups;   // (tiles_m of grouped rows already counts every group's)
+  }
+  return g;
+}
+constexpr int prod_threads(int kernel) {
+  return kernel == kTile128 || kernel == kTile64 ? 256 : 512;
+}
+
 struct TypeOps {
   hipError_t (*prod)(const ProdArgs& a, int la, int lb, int mode, int kernel, int loading,
                      hipStream_t s);

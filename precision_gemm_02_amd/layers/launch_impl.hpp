@@ -16,22 +16,26 @@ hipError_t launch(void (*kernel)(const A), dim3 grid, int threads, const A& a, h
   return hipLaunchKernel(reinterpret_cast<const void*>(kernel), grid, dim3(threads), args, 0, s);
 }
 
-template <typename T, int LA, int LB, int BM, int BN, int WGM, int WGN, int LOADING, int MODE>
+inline dim3 grid_of(const ProdArgs& a, int mode, int kernel) {
+  const ProdGrid g = prod_grid(a, mode, kernel);
+  return dim3((unsigned)g.x, (unsigned)g.y);
+}
+
+template <typename T, int LA, int LB, int KERNEL, int WGM, int WGN, int LOADING, int MODE>
 hipError_t launch_tile(const ProdArgs& a, hipStream_t s) {
-  long long tiles = (long long)a.tiles_m * a.tiles_n;
-  if (MODE == kSums) tiles *= a.groups;
+  constexpr int BM = kShape[KERNEL].bm, BN = kShape[KERNEL].bn;
+  static_assert(WGM * WGN * 64 == prod_threads(KERNEL), "the checked launch");
   return launch(&prod_tile_kernel<T, LA, LB, BM, BN, WGM, WGN, LOADING, MODE>,
-                dim3((unsigned)tiles, MODE == kRows ? 1 : (unsigned)a.splits), WGM * WGN * 64, a,
-                s);
+                grid_of(a, MODE, KERNEL), WGM * WGN * 64, a, s);
 }
 
 template <typename T, int LA, int LB, int MODE, int LOADING>
 hipError_t prod_tile(const ProdArgs& a, int kernel, hipStream_t s) {
   if constexpr (LOADING == kDirect) {
-    if (kernel == kTile256) return launch_tile<T, LA, LB, 256, 256, 2, 4, LOADING, MODE>(a, s);
+    if (kernel == kTile256) return launch_tile<T, LA, LB, kTile256, 2, 4, LOADING, MODE>(a, s);
   }
-  if (kernel == kTile128) return launch_tile<T, LA, LB, 128, 128, 2, 2, LOADING, MODE>(a, s);
-  if (kernel == kTile64) return launch_tile<T, LA, LB, 64, 64, 2, 2, LOADING, MODE>(a, s);
+  if (kernel == kTile128) return launch_tile<T, LA, LB, kTile128, 2, 2, LOADING, MODE>(a, s);
+  if (kernel == kTile64) return launch_tile<T, LA, LB, kTile64, 2, 2, LOADING, MODE>(a, s);
   return hipErrorInvalidValue;
 }
 
@@ -45,20 +49,18 @@ hipError_t prod_tile(const ProdArgs& a, int kernel, int loading, hipStream_t s) 
 }
 
 template <typename T, int LB, int MB, int MODE>
-hipError_t prod_few(const ProdArgs& a, bool wide, hipStream_t s) {
-  // no more groups have rows than there are rows
-  const int groups = a.groups < a.rows ? a.groups : a.rows;
-  const dim3 grid((unsigned)(MODE == kRows ? a.tiles_n * groups : a.tiles_n),
-                  MODE == kDense ? (unsigned)a.splits : 1);
-  if (wide) return launch(&prod_rows_kernel<T, LB, MB, 4, 8, MODE>, grid, 512, a, s);
+hipError_t prod_few(const ProdArgs& a, int kernel, hipStream_t s) {
+  const dim3 grid = grid_of(a, MODE, kernel);
+  static_assert(prod_threads(kFew16) == 512, "the checked launch");
+  if (kernel >= kFew16Wide)
+    return launch(&prod_rows_kernel<T, LB, MB, 4, 8, MODE>, grid, 512, a, s);
   return launch(&prod_rows_kernel<T, LB, MB, 1, 8, MODE>, grid, 512, a, s);
 }
 
 template <typename T, int LB, int MODE>
 hipError_t prod_few(const ProdArgs& a, int kernel, hipStream_t s) {
-  const bool wide = kernel == kFew16Wide || kernel == kFew32Wide;
-  return kernel == kFew16 || kernel == kFew16Wide ? prod_few<T, LB, 1, MODE>(a, wide, s)
-                                                  : prod_few<T, LB, 2, MODE>(a, wide, s);
+  return kernel == kFew16 || kernel == kFew16Wide ? prod_few<T, LB, 1, MODE>(a, kernel, s)
+                                                  : prod_few<T, LB, 2, MODE>(a, kernel, s);
 }
 
 template <typename T>

@@ -11,7 +11,7 @@ namespace layers {
 namespace {
 
 constexpr int kUnits = 256;                       // compute units of an MI355X
-constexpr long long kMaxGrid = 1LL << 24;         // workgroups in one launch
+constexpr long long kMaxThreads = 0xffffffffLL;   // of a launch, along x
 
 int size_of(int dtype) { return dtype == PGEMM_F32 ? 4 : 2; }
 bool known(int dtype) { return dtype == PGEMM_F32 || dtype == PGEMM_F16 || dtype == PGEMM_BF16; }
@@ -60,7 +60,7 @@ bool plan_ok(const pgemm_plan& p, int rows, bool need) {
 // ---- the choice of a product's kernel ----------------------------------------
 
 struct Plan {
-  int kernel = kTile64;
+  int kernel = -1;         // (-1: none, the product has more tiles than a launch takes)
   int splits = 1;
   int k_split = 0;
   int loading = kThrough;
@@ -111,6 +111,30 @@ size_t split_space(const Plan& p, int mode, long long rows, int groups, int n) {
   return (size_t)p.splits * (size_t)rows * (size_t)n * 4 * (size_t)(mode == kSums ? groups : 1);
 }
 
+// The tiles of a product.  `rows` as in plan_product.
+void set_tiles(ProdArgs* a, int kernel, int mode, long long rows) {
+  if (kernel >= kFew16) {
+    a->tiles_m = 1;
+    a->tiles_n = (int)ceil_div(a->N, few_columns(kernel));
+    return;
+  }
+  long long tm = ceil_div(rows, kShape[kernel].bm);
+  if (mode == kRows) tm += a->groups < rows ? a->groups : rows;   // partly filled tiles
+  a->tiles_m = (int)tm;
+  a->tiles_n = (int)ceil_div(a->N, kShape[kernel].bn);
+}
+
+// Whether one launch takes all of them.
+bool launch_fits(int kernel, int mode, long long rows, int groups, int n) {
+  ProdArgs a{};
+  a.N = n;
+  a.groups = groups;
+  a.rows = (int)rows;
+  a.splits = 1;
+  set_tiles(&a, kernel, mode, rows);
+  return prod_grid(a, mode, kernel).x * prod_threads(kernel) <= kMaxThreads;
+}
+
 // rows: the rows of D over all groups (how they are distributed is not known
 // here; any distribution is correct).  may_split: the summed index may be
 // shared by workgroups, through partial sums in `ws_bytes` bytes (any_ws: as
@@ -123,12 +147,13 @@ Plan plan_product(int size, int la, int mode, long long rows, int groups, int n,
   if (mode == kRows) may_split = false;
   if (mode == kRows && groups > rows) groups = (int)rows;
   const double per = mode == kRows ? (double)rows / groups : (double)rows;
-  if (la == kInner && per <= 32) {
-    // Few rows: B is read once, the rest is latency.  The few-rows kernel
-    // takes 16 or 32 rows per pass and never needs a tile of operands.
-    const long long wide = ceil_div(n, 64) * (mode == kRows ? groups : 1);
-    if (wide >= 2 * kUnits) p.kernel = per <= 16 ? kFew16Wide : kFew32Wide;
-    else p.kernel = per <= 16 ? kFew16 : kFew32;
+  // Few rows: B is read once, the rest is latency.  The few-rows kernel
+  // takes 16 or 32 rows per pass and never needs a tile of operands.
+  const long long wide = ceil_div(n, 64) * (mode == kRows ? groups : 1);
+  const int few = wide >= 2 * kUnits ? (per <= 16 ? kFew16Wide : kFew32Wide)
+                                     : (per <= 16 ? kFew16 : kFew32);
+  if (la == kInner && per <= 32 && launch_fits(few, mode, rows, groups, n)) {
+    p.kernel = few;
     if (may_split) {
       // one split per free compute unit, each of 16 units of 128 bytes at least
       long long s = kUnits / ceil_div(n, few_columns(p.kernel));
@@ -139,10 +164,13 @@ Plan plan_product(int size, int la, int mode, long long rows, int groups, int n,
     double best = 0;
     for (int c = 0; c < 3; ++c) {
       if (c == kTile256 && loading != kDirect) continue;
+      if (!launch_fits(c, mode, rows, groups, n)) continue;
       const int bm = kShape[c].bm, bn = kShape[c].bn;
       // tiles that are half empty waste the loads too (512 tokens, top 8 of
       // 64 experts, 1024 x 1024: 39 us with 64-row tiles, 45 with 128)
-      if (mode == kRows && c != kTile64 && 2 * per <= bm) continue;
+      if (mode == kRows && c != kTile64 && 2 * per <= bm &&
+          launch_fits(kTile64, mode, rows, groups, n))
+        continue;
       double tiles = (double)ceil_div(n, bn);
       if (mode == kRows) tiles *= groups * (per / bm > 0.5 ? per / bm + 0.5 : 1.0);
       else tiles *= (double)ceil_div(rows, bm) * (mode == kSums ? groups : 1);
@@ -186,10 +214,18 @@ size_t split_bytes(int size, int la, int mode, long long rows, int groups, int n
   return most;
 }
 
-// Fill in what depends on the plan and launch.  `rows` as in plan_product.
-int run_product(ProdArgs a, int dtype, int la, int lb, int mode, long long rows, void* ws,
-                size_t ws_bytes, hipStream_t s) {
-  const int size = size_of(dtype);
+// A product with its plan, ready to be launched.
+struct Product {
+  ProdArgs a;
+  int dtype, la, lb, mode;
+  Plan plan;
+};
+
+// Fill in what depends on the plan; false if no launch takes the product.
+// `rows` as in plan_product.
+bool plan_call(Product* p, long long rows, void* ws, size_t ws_bytes) {
+  ProdArgs& a = p->a;
+  const int size = size_of(p->dtype), la = p->la, lb = p->lb, mode = p->mode;
   const int al = operand_loading(a.A, a.lda, size,
                                  la == kInner ? (mode == kSums ? 0 : a.K) : a.M, 0);
   const int bl = operand_loading(a.B, a.ldb, size, lb == kInner ? a.K : a.N,
@@ -198,25 +234,21 @@ int run_product(ProdArgs a, int dtype, int la, int lb, int mode, long long rows,
                 : al != kThrough && bl != kThrough   ? kRagged
                                                      : kThrough;
   if (mode == kSums && loading == kRagged) loading = kThrough;   // see Loader
-  const Plan p = plan_product(size, la, mode, rows, a.groups, a.N, mode == kSums ? a.rows : a.K,
-                              loading, ws == nullptr ? 0 : ws_bytes, false);
-  a.splits = p.splits;
-  a.k_split = p.k_split;
+  p->plan = plan_product(size, la, mode, rows, a.groups, a.N, mode == kSums ? a.rows : a.K,
+                         loading, ws == nullptr ? 0 : ws_bytes, false);
+  if (p->plan.kernel < 0) return false;
+  a.splits = p->plan.splits;
+  a.k_split = p->plan.k_split;
   a.partial = static_cast<float*>(ws);
-  if (p.kernel >= kFew16) {
-    a.tiles_m = 1;
-    a.tiles_n = (int)ceil_div(a.N, few_columns(p.kernel));
-  } else {
-    const int bm = kShape[p.kernel].bm;
-    long long tm = ceil_div(rows, bm);
-    if (mode == kRows) tm += a.groups < rows ? a.groups : rows;   // partly filled tiles
-    a.tiles_m = (int)tm;
-    a.tiles_n = (int)ceil_div(a.N, kShape[p.kernel].bn);
-  }
-  if ((long long)a.tiles_m * a.tiles_n * (a.groups > 0 ? a.groups : 1) > kMaxGrid)
-    return PGEMM_EHIP;
-  return ops_of(dtype).prod(a, la, lb, mode, p.kernel, p.loading, s) == hipSuccess ? PGEMM_OK
-                                                                                : PGEMM_EHIP;
+  set_tiles(&a, p->plan.kernel, mode, rows);
+  return true;
+}
+
+int launch_product(const Product& p, hipStream_t s) {
+  return ops_of(p.dtype).prod(p.a, p.la, p.lb, p.mode, p.plan.kernel, p.plan.loading, s) ==
+                 hipSuccess
+             ? PGEMM_OK
+             : PGEMM_EHIP;
 }
 
 // Threads per row of a row-wise kernel with 8 columns per thread.
@@ -277,6 +309,7 @@ struct BackArgs {
   void* dbias;
 };
 
+// All of the call is planned before any of it is launched.
 int run_backward(const BackArgs& b, void* ws, const BackSpace& space, hipStream_t s) {
   const TypeOps& ops = ops_of(b.kind.dtype);
   const bool grouped = b.offsets != nullptr;
@@ -284,34 +317,18 @@ int run_backward(const BackArgs& b, void* ws, const BackSpace& space, hipStream_
   void* rest = base + space.dz;
   const void* dz = b.dY.data;
   long long ldz = b.dY.ld;
-  const bool slope = b.kind.act != PGEMM_ACT_NONE && (b.dX.data != nullptr || b.dW.data != nullptr);
+  const bool act = b.kind.act != PGEMM_ACT_NONE;
+  const bool slope = (act && (b.dX.data != nullptr || b.dW.data != nullptr)) || b.dbias != nullptr;
   const bool out32 = b.kind.out_dtype == PGEMM_F32;
-  if (slope || b.dbias != nullptr) {
-    SlopeArgs a{};
-    a.dY = b.dY.data;
-    a.ldy = b.dY.ld;
-    if (b.kind.act != PGEMM_ACT_NONE) {
-      a.Z = b.Z.data;
-      a.ldz = b.Z.ld;
-      a.dZ = base;
-      a.ldd = space.ldz;
-      dz = base;
-      ldz = space.ldz;
-    }
-    a.n = b.n;
-    a.act = b.kind.act;
-    a.offsets = b.offsets;
-    a.rows = b.rows;
-    a.chunks = space.chunks;
-    a.tpr = threads_per_row(b.n, 64);
-    a.partial = b.dbias != nullptr ? static_cast<float*>(rest) : nullptr;
-    if (ops.slope(a, b.groups, s) != hipSuccess) return PGEMM_EHIP;
-    if (b.dbias != nullptr &&
-        ops.column_sum(a.partial, b.dbias, b.n, b.groups, a.chunks, out32, s) != hipSuccess)
-      return PGEMM_EHIP;
+  if (slope && act) {
+    dz = base;
+    ldz = space.ldz;
   }
-  if (b.dX.data != nullptr && b.rows > 0 && b.k > 0) {
-    ProdArgs a{};
+  const bool want_dx = b.dX.data != nullptr && b.rows > 0 && b.k > 0;
+  const bool want_dw = b.dW.data != nullptr && b.k > 0 && b.n > 0;
+  Product dx{}, dw{};
+  if (want_dx) {
+    ProdArgs& a = dx.a;
     a.A = dz;
     a.lda = ldz;
     a.B = b.W.data;
@@ -326,12 +343,14 @@ int run_backward(const BackArgs& b, void* ws, const BackSpace& space, hipStream_
     a.offsets = b.offsets;
     a.groups = grouped ? b.groups : 0;
     a.rows = b.rows;
-    const int st = run_product(a, b.kind.dtype, kInner, b.W.order == PGEMM_KN ? kInner : kOuter,
-                               grouped ? kRows : kDense, b.rows, rest, space.rest, s);
-    if (st != PGEMM_OK) return st;
+    dx.dtype = b.kind.dtype;
+    dx.la = kInner;
+    dx.lb = b.W.order == PGEMM_KN ? kInner : kOuter;
+    dx.mode = grouped ? kRows : kDense;
+    if (!plan_call(&dx, b.rows, rest, space.rest)) return -2;
   }
-  if (b.dW.data != nullptr && b.k > 0 && b.n > 0) {
-    ProdArgs a{};
+  if (want_dw) {
+    ProdArgs& a = dw.a;
     const bool kn = b.dW.order == PGEMM_KN;
     a.A = kn ? b.X.data : dz;
     a.lda = kn ? b.X.ld : ldz;
@@ -350,11 +369,38 @@ int run_backward(const BackArgs& b, void* ws, const BackSpace& space, hipStream_
     a.offsets = b.offsets;
     a.groups = grouped ? b.groups : 0;
     a.rows = b.rows;
-    const int st = run_product(a, b.kind.dtype, kOuter, kOuter, grouped ? kSums : kDense, a.M,
-                               rest, space.rest, s);
+    dw.dtype = b.kind.dtype;
+    dw.la = dw.lb = kOuter;
+    dw.mode = grouped ? kSums : kDense;
+    if (!plan_call(&dw, a.M, rest, space.rest)) return -2;
+  }
+  if (slope) {
+    SlopeArgs a{};
+    a.dY = b.dY.data;
+    a.ldy = b.dY.ld;
+    if (act) {
+      a.Z = b.Z.data;
+      a.ldz = b.Z.ld;
+      a.dZ = base;
+      a.ldd = space.ldz;
+    }
+    a.n = b.n;
+    a.act = b.kind.act;
+    a.offsets = b.offsets;
+    a.rows = b.rows;
+    a.chunks = space.chunks;
+    a.tpr = threads_per_row(b.n, 64);
+    a.partial = b.dbias != nullptr ? static_cast<float*>(rest) : nullptr;
+    if (ops.slope(a, b.groups, s) != hipSuccess) return PGEMM_EHIP;
+    if (b.dbias != nullptr &&
+        ops.column_sum(a.partial, b.dbias, b.n, b.groups, a.chunks, out32, s) != hipSuccess)
+      return PGEMM_EHIP;
+  }
+  if (want_dx) {
+    const int st = launch_product(dx, s);
     if (st != PGEMM_OK) return st;
   }
-  return PGEMM_OK;
+  return want_dw ? launch_product(dw, s) : PGEMM_OK;
 }
 
 }  // namespace
@@ -382,7 +428,8 @@ int pgemm_linear(pgemm_kind kind, int m, int n, int k, pgemm_rows X, pgemm_weigh
   if (!rows_ok(Y, n, osize, touch)) return -10;
   if (workspace != nullptr && !aligned_to(workspace, 16)) return -11;
   if (!touch) return PGEMM_OK;
-  ProdArgs a{};
+  Product p{};
+  ProdArgs& a = p.a;
   a.A = X.data;
   a.lda = X.ld;
   a.B = W.data;
@@ -399,8 +446,12 @@ int pgemm_linear(pgemm_kind kind, int m, int n, int k, pgemm_rows X, pgemm_weigh
   a.ldz = Z.ld;
   a.act = kind.act;
   a.out32 = kind.out_dtype == PGEMM_F32;
-  return run_product(a, kind.dtype, kInner, W.order == PGEMM_KN ? kOuter : kInner, kDense, m,
-                     workspace, workspace_bytes, static_cast<hipStream_t>(stream));
+  p.dtype = kind.dtype;
+  p.la = kInner;
+  p.lb = W.order == PGEMM_KN ? kOuter : kInner;
+  p.mode = kDense;
+  if (!plan_call(&p, m, workspace, workspace_bytes)) return -2;
+  return launch_product(p, static_cast<hipStream_t>(stream));
 }
 
 size_t pgemm_linear_workspace(int dtype, int m, int n, int k) {
@@ -537,7 +588,8 @@ int pgemm_expert_linear(pgemm_kind kind, int rows, int n, int k, pgemm_plan plan
   if (!rows_ok(Z, n, size, false)) return -9;
   if (!rows_ok(Y, n, osize, touch)) return -10;
   if (!touch) return PGEMM_OK;
-  ProdArgs a{};
+  Product p{};
+  ProdArgs& a = p.a;
   a.A = X.data;
   a.lda = X.ld;
   a.B = W.data;
@@ -559,8 +611,12 @@ int pgemm_expert_linear(pgemm_kind kind, int rows, int n, int k, pgemm_plan plan
   a.rows = rows;
   a.gather = plan.tokens;
   a.gather_rows = plan.x_rows;
-  return run_product(a, kind.dtype, kInner, W.order == PGEMM_KN ? kOuter : kInner, kRows, rows,
-                     nullptr, 0, static_cast<hipStream_t>(stream));
+  p.dtype = kind.dtype;
+  p.la = kInner;
+  p.lb = W.order == PGEMM_KN ? kOuter : kInner;
+  p.mode = kRows;
+  if (!plan_call(&p, rows, nullptr, 0)) return -2;
+  return launch_product(p, static_cast<hipStream_t>(stream));
 }
 
 int pgemm_expert_linear_backward(pgemm_kind kind, int rows, int n, int k, pgemm_plan plan,

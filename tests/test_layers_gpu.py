@@ -603,6 +603,31 @@ def test_expert_linear_skewed_and_large():
         assert torch.equal(Y.double(), X.double() @ W[E // 2].double())
 
 
+@pytest.mark.parametrize("dtype,E,R", [(BF16, 384, 24576), (F16, 1024, 33000), (F32, 300, 30000)],
+                         ids=str)
+def test_many_experts_with_many_columns(dtype, E, R):
+    """Hundreds of experts with tens of tiles each, forwards and backwards."""
+    n, k = 4096, 64
+    g = gen(30)
+    cut = torch.randint(0, R + 1, (E - 1,), generator=g).sort()[0].tolist()
+    o = [0] + cut + [R]
+    off = torch.tensor(o, dtype=torch.int32, device="cuda")
+    X, D = ints(g, R, k, hi=1).to(dtype).cuda(), ints(g, R, k, hi=1).to(dtype).cuda()
+    W = weight(g, (E,), k, n, "kn", dtype, integer=True)
+    Y = torch.full((R, n), 9.0, dtype=dtype, device="cuda")
+    pg.expert_linear(X, W, Y, off)
+    dX = torch.full((R, n), 9.0, dtype=dtype, device="cuda")
+    dW = torch.full((E, n, k), 9.0, device="cuda")
+    ws = space(pg.expert_linear_backward_workspace(R, k, n, E, dtype))
+    pg.expert_linear_backward(D, Y, W.transpose(1, 2), off, dX=dX, dW=dW, ws=ws)
+    for e in range(E):
+        r = slice(o[e], o[e + 1])
+        y = X[r].double() @ W[e].double()          # sums of 64 terms up to 3: exact in 16 bits too
+        assert torch.equal(Y[r].double(), y)
+        assert torch.equal(dX[r].double(), D[r].double() @ W[e].double())
+        assert torch.equal(dW[e].double(), y.t() @ D[r].double())
+
+
 def test_expert_linear_bad_plans_stay_inside():
     """Bounds and tokens outside the buffers are clamped."""
     g = gen(16)
