@@ -99,7 +99,11 @@ hipError_t prod(const ProdArgs& a, int la, int lb, int mode, int kernel, int loa
 template <typename T>
 hipError_t slope(const SlopeArgs& a, int groups, hipStream_t s) {
   const unsigned cols = (unsigned)((a.n + a.tpr * 8 - 1) / (a.tpr * 8));
-  return launch(&slope_kernel<T>, dim3(cols, (unsigned)a.chunks, (unsigned)groups), 256, a, s);
+  const dim3 grid(cols, (unsigned)a.chunks, (unsigned)groups);
+  if constexpr (sizeof(T) == 2) {
+    if (!a.sums32) return launch(&slope_kernel<T, true>, grid, 256, a, s);
+  }
+  return launch(&slope_kernel<T, false>, grid, 256, a, s);
 }
 
 template <typename T>

@@ -391,6 +391,7 @@ int run_backward(const BackArgs& b, void* ws, const BackSpace& space, hipStream_
     a.chunks = space.chunks;
     a.tpr = threads_per_row(b.n, 64);
     a.partial = b.dbias != nullptr ? static_cast<float*>(rest) : nullptr;
+    a.sums32 = b.dbias != nullptr && out32;
     if (ops.slope(a, b.groups, s) != hipSuccess) return PGEMM_EHIP;
     if (b.dbias != nullptr &&
         ops.column_sum(a.partial, b.dbias, b.n, b.groups, a.chunks, out32, s) != hipSuccess)

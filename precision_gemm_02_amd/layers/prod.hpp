@@ -109,31 +109,36 @@ struct ProdArgs {
 
 // Activations in fp32.  tanh and the logistic function go through one exp and
 // one division; the exp's argument is such that overflow gives the limit.
-// Fast: the hardware's exp2 and reciprocal, off by about |z| + 2 units of
-// 2^-24, far below a 16-bit result's own rounding (2^-9, 2^-12); fp32 takes
-// the exact forms.
+// Fast is for results of 16 bits: the hardware's exp2 and reciprocal, off by
+// about |z| + 2 units of 2^-24 (of the tanh form, by its argument's), far below
+// half a step of the result (2^-8 of bf16, 2^-11 of fp16).  fp32 results take the
+// exact forms, whatever the inputs' type.
 template <bool Fast>
 __device__ __forceinline__ float logistic(float z) {
   if constexpr (Fast) return __builtin_amdgcn_rcpf(1.0f + __expf(-z));
   else return 1.0f / (1.0f + expf(-z));
 }
 
-// The normal distribution function and exp(-z^2/2).  Fast: the rational
-// approximation 7.1.26 of Abramowitz and Stegun for erfc, whose factor exp(-x^2)
-// keeps the lower tail's relative error below 2e-6 down to z = -5 (2e-5 at
-// -13) where 1 + erf would cancel.
+// The normal distribution function Phi and exp(-z^2/2).  The lower tail is
+// computed as such: 1 + erf would cancel there.  Fast: Phi(-|z|) exp(z^2/2) as a
+// polynomial in t = 1/(1 + 0.26 |z|), fitted for the least relative error over
+// |z| <= 14.5 (where every result of 16 bits has become 0): 1.2e-6, 1.5e-6 with
+// fp32 coefficients.  The exp adds 1.25 z^2 + 4 units of 2^-24 (its argument's
+// roundings), so that Phi is off by at most 1.5e-5 of itself at z = -13; results
+// below the smallest normal fp32 value may be 0.
 template <bool Fast>
 __device__ __forceinline__ float normal_cdf(float z, float* bell) {
   if constexpr (Fast) {
-    const float x = fabsf(z) * 0.70710678118654752f;
-    const float e = __expf(-x * x);
-    const float t = __builtin_amdgcn_rcpf(1.0f + 0.3275911f * x);
-    float p = 1.061405429f;
-    p = p * t - 1.453152027f;
-    p = p * t + 1.421413741f;
-    p = p * t - 0.284496736f;
-    p = p * t + 0.254829592f;
-    const float q = 0.5f * p * t * e;
+    const float e = __builtin_amdgcn_exp2f(z * z * -0.72134752044f);   // log2(e) / 2
+    const float t = __builtin_amdgcn_rcpf(1.0f + 0.26f * fabsf(z));
+    float p = -0.07180302f;
+    p = p * t + 0.22505027f;
+    p = p * t - 0.101182476f;
+    p = p * t + 0.16286214f;
+    p = p * t + 0.07458985f;
+    p = p * t + 0.10695134f;
+    p = p * t + 0.103532486f;
+    const float q = p * t * e;
     *bell = e;
     return z > 0.0f ? 1.0f - q : q;
   } else {
@@ -288,11 +293,12 @@ __device__ __forceinline__ void load_bias(const ProdArgs& a, const void* bias, i
 template <typename T>
 __device__ __forceinline__ void finish_row(const ProdArgs& a, void* D, long long m, int n0,
                                            float* v, const Raw8& residual) {
-  constexpr bool Fast = sizeof(T) == 2;
+  const bool fast = sizeof(T) == 2 && !a.out32;
   const int live = a.N - n0;
   if (live >= 8) {
     if (a.Z != nullptr) put8<T>(a.Z, m * a.ldz + n0, v);
-    act8<Fast>(v, a.act);
+    if (fast) act8<true>(v, a.act);
+    else act8<false>(v, a.act);
     if (a.R != nullptr) add_residual<T>(a, residual, v);
     if (a.out32) put8<float>(D, m * a.ldd + n0, v);
     else put8<T>(D, m * a.ldd + n0, v);
@@ -305,7 +311,7 @@ __device__ __forceinline__ void finish_row(const ProdArgs& a, void* D, long long
     for (int q = 0; q < 8; ++q) x = q == j ? v[q] : x;   // no indexed registers
     const int n = n0 + j;
     if (a.Z != nullptr) static_cast<T*>(a.Z)[m * a.ldz + n] = (T)x;
-    x = act_value<Fast>(x, a.act);
+    x = fast ? act_value<true>(x, a.act) : act_value<false>(x, a.act);
     if (a.R != nullptr)
       x += a.out32 ? static_cast<const float*>(a.R)[m * a.ldr + n]
                    : (float)static_cast<const T*>(a.R)[m * a.ldr + n];

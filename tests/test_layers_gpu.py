@@ -169,6 +169,71 @@ def test_linear_random(dtype, act, shape):
     assert ((Y.double().cpu() - y).abs() <= h * y.abs() * (1 + h) + own * (1 + h) + tiny).all()
 
 
+PAIRS = [(F32, F32), (F16, F16), (BF16, BF16), (F16, F32), (BF16, F32)]
+
+
+def logistic_argument(z, act):
+    """x of z / (1 + exp(-x)): silu's z, and 2 u of 0.5 z (1 + tanh u), where 1 +
+    tanh u itself would cancel in 64 bits."""
+    return 2 * math.sqrt(2 / math.pi) * (z + 0.044715 * z ** 3) if act == "gelu_tanh" else z
+
+
+@pytest.mark.parametrize("dtype,out", PAIRS, ids=lambda d: ids(d))
+@pytest.mark.parametrize("act", ["gelu", "gelu_tanh", "silu"])
+def test_linear_activations_keep_their_tails(act, dtype, out):
+    """Y = act(z) to a relative bound, z itself (one inner index, weight 1).
+
+    fp32 results, in units of 2^-24 of the value: gelu 1.5 z^2 (the roundings of
+    erfc's argument, whose condition is z^2 + 1) and 40 (16 units of the last
+    place of erfcf, the products); the tanh form 5 of its argument and 16 (an exp
+    of 3 units, sums, a division); silu 16.  16-bit results: 3e-6 (twice the
+    polynomial's) and 2 z^2 + 16 for gelu, 8 of the argument and 16 for the others,
+    and half a step.  The factor of z may be 0 where it is below the smallest normal
+    number 2^-126 (exp(-2 u) passes 2^128 there): |z| times that."""
+    z = torch.cat([torch.linspace(-12.9, 5, 1791), torch.linspace(-3, 3, 601)]).to(dtype)
+    Y = torch.empty(z.numel(), 9, dtype=out, device="cuda")
+    pg.linear(z[:, None].cuda(), torch.ones(1, 9, dtype=dtype, device="cuda"), Y, act=act)
+    z = z.double()
+    x = logistic_argument(z, act)
+    want, w = act64(z, act) if act == "gelu" else z * torch.sigmoid(x), x.abs()
+    if out is F32:
+        units = {"gelu": 1.5 * z ** 2 + 40, "gelu_tanh": 5 * w + 16, "silu": 16}[act]
+        own, h = units * 2.0 ** -24, 0.0
+    else:
+        own = 3e-6 + (2 * z ** 2 + 16) * 2.0 ** -24 if act == "gelu" else (8 * w + 16) * 2.0 ** -24
+        h = half_step(out)
+    flat = (1 + z.abs()) * torch.finfo(F32).tiny + torch.finfo(out).tiny * torch.finfo(out).eps / 2
+    bound = want.abs() * (own + h + own * h) + flat
+    for col in (0, 8):                       # whole chunks of columns and the edge
+        assert ((Y[:, col].double().cpu() - want).abs() <= bound).all()
+
+
+@pytest.mark.parametrize("dtype", TYPES, ids=ids)
+@pytest.mark.parametrize("act", ["gelu", "gelu_tanh", "silu"])
+def test_bias_gradient_in_32_bits(act, dtype):
+    """dbias of one row of ones is the slope, here as fp32: its terms to the
+    roundings above, and 1 - q (q the logistic function) to 8 units of 1."""
+    z = torch.linspace(-8, 5, 1041).to(dtype)[None]
+    n = z.shape[1]
+    db = torch.empty(n, device="cuda")
+    ws = space(pg.linear_backward_workspace(1, n, 1, dtype, act))
+    x = torch.zeros(1, 1, dtype=dtype, device="cuda")
+    pg.linear_backward(torch.ones_like(z).cuda(), x, None, Z=z.cuda(), act=act, dbias=db, ws=ws)
+    z = z[0].double()
+    if act == "gelu":
+        terms = 0.5 * torch.erfc(-z / math.sqrt(2)) + \
+            z.abs() * torch.exp(-z * z / 2) / math.sqrt(2 * math.pi)
+        bound = (1.5 * z ** 2 + 48) * terms
+        want = slope64(z, act)
+    else:
+        c = 2 * math.sqrt(2 / math.pi) * (1 + 0.134145 * z ** 2) if act == "gelu_tanh" else 1
+        x = logistic_argument(z, act)
+        q, r = torch.sigmoid(x), torch.sigmoid(-x)
+        want = q + z * q * r * c
+        bound = (5 * x.abs() + 24) * (q + z.abs() * q * r * c) + 8 * z.abs() * q * c
+    assert ((db.double().cpu() - want).abs() <= bound * 2.0 ** -24).all()
+
+
 @pytest.mark.parametrize("dtype", TYPES, ids=ids)
 def test_linear_special_values(dtype):
     """Infinities and NaN of one row stay in it; nothing is read past k."""
