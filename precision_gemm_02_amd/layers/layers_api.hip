@@ -154,7 +154,7 @@ Plan plan_product(int size, int la, int mode, long long rows, int groups, int n,
                                      : (per <= 16 ? kFew16 : kFew32);
   if (la == kInner && per <= 32 && launch_fits(few, mode, rows, groups, n)) {
     p.kernel = few;
-    if (may_split) {
+    if (may_split && n > 0) {   // (no columns: the size of a workspace that is not used)
       // one split per free compute unit, each of 16 units of 128 bytes at least
       long long s = kUnits / ceil_div(n, few_columns(p.kernel));
       if (s > k / (16 * bk)) s = k / (16 * bk);

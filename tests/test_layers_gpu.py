@@ -373,6 +373,20 @@ def test_linear_backward_parts():
     assert (dW == 0).all() and (db == 0).all()
 
 
+@pytest.mark.parametrize("m", [1, 16, 32, 33])
+def test_bias_gradient_alone(m):
+    """Neither X nor W: there is no inner size."""
+    dY = ints(gen(32), m, 40).cuda()
+    db = torch.empty(40, device="cuda")
+    ws = space(pg.linear_backward_workspace(m, 40, 0, F32))
+    pg.linear_backward(dY, None, None, dbias=db, ws=ws)
+    assert torch.equal(db, dY.sum(0))
+    pg.linear_backward(dY, torch.zeros(m, 0, device="cuda"), torch.zeros(0, 40, device="cuda"),
+                       dX=torch.zeros(m, 0, device="cuda"), dW=torch.zeros(0, 40, device="cuda"),
+                       dbias=db.fill_(7), ws=ws)
+    assert torch.equal(db, dY.sum(0))
+
+
 # ---- routing ---------------------------------------------------------------------
 
 LOWEST = {F32: torch.finfo(F32).min, F16: -65504.0, BF16: torch.finfo(BF16).min}

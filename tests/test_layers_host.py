@@ -193,6 +193,19 @@ def test_workspace_sizes():
             assert pg.expert_linear_backward_workspace(m, n, 16, 3, F32, "gelu") >= 0
 
 
+@pytest.mark.parametrize("dtype", [BF, torch.float16, F32])
+def test_workspaces_of_empty_sizes(dtype):
+    """No inner size, no rows, no columns: sizes, whatever the others are."""
+    for m in (0, 1, 16, 32, 33, 5000):
+        for n in (0, 1, 64, 5000):
+            for k in (0, 1, 64, 5000):
+                for act in ("none", "silu"):
+                    need = pg.linear_backward_workspace(m, n, k, dtype, act)
+                    assert need >= m * n * dtype.itemsize * (act != "none")
+                    assert pg.expert_linear_backward_workspace(m, n, k, 3, dtype, act) >= 0
+                assert (pg.linear_workspace(m, n, k, dtype) == 0) or m * n * k > 0
+
+
 @pytest.fixture
 def anywhere(monkeypatch):
     """Let CPU tensors past the device checks: a call that is not refused
