@@ -163,8 +163,13 @@ __device__ __forceinline__ float act_value(float z, int act) {
   }
 }
 
+// The slope at z is that at the nearest of [-1e4, 1e4], where each has long reached
+// its limit of 0 or 1 (a NaN stays): past 5e19 the products of the tanh form would
+// be 0 times infinity, and so would all three at an infinite z, which is what a
+// pre-activation beyond fp16 becomes although its activation is finite.
 template <bool Fast>
 __device__ __forceinline__ float act_slope(float z, int act) {
+  z = z < -1e4f ? -1e4f : (z > 1e4f ? 1e4f : z);
   switch (act) {
     case kRelu: return z > 0.0f ? 1.0f : 0.0f;
     case kGelu: {

@@ -323,6 +323,45 @@ def test_linear_backward_random(dtype, act):
         assert ((got.double().cpu() - want).abs() <= bound + 1e-7).all()
 
 
+@pytest.mark.parametrize("dtype", TYPES, ids=ids)
+@pytest.mark.parametrize("act", ["relu", "gelu", "gelu_tanh", "silu"])
+def test_slopes_of_large_values(dtype, act):
+    """The slope's limits, 1 and 0, at infinities and at finite values whose squares
+    and cubes are not; a NaN reaches its own column alone."""
+    big = torch.finfo(dtype).max
+    z = [math.inf, big, min(big, 1e30), min(big, 1e20), 1e4, 2e4, 300, 60]
+    n = 2 * len(z) + 1
+    Z = torch.tensor([z + [-x for x in z] + [math.nan]]).to(dtype).cuda()
+    W = torch.eye(n, dtype=dtype, device="cuda")[:, :n - 1].contiguous()
+    ws = space(pg.linear_backward_workspace(1, n, n, dtype, act))
+    for out in {dtype, F32}:
+        db = torch.empty(n, dtype=out, device="cuda")
+        dW = torch.empty(1, n, dtype=out, device="cuda")
+        one = torch.ones(1, 1, dtype=dtype, device="cuda")
+        pg.linear_backward(torch.ones_like(Z), one, None, Z=Z, act=act, dW=dW, dbias=db, ws=ws)
+        want = [1.0] * len(z) + [0.0] * len(z)
+        # at -60 silu's slope is -5e-25, beyond -10 the others' are below 1e-20
+        assert (db[:-1].cpu().double() - torch.tensor(want)).abs().max() < 1e-20
+        assert (dW[0, :-1].cpu().double() - torch.tensor(want)).abs().max() < 1e-20
+    dX = torch.empty(1, n - 1, dtype=dtype, device="cuda")
+    pg.linear_backward(torch.ones_like(Z)[:, :n - 1].contiguous(), None, W[:n - 1].contiguous(),
+                       Z=Z[:, :n - 1].contiguous(), act=act, dX=dX, ws=ws)
+    assert (dX[0].cpu().double() - torch.tensor(want)).abs().max() < 1e-20
+
+
+def test_gradient_where_the_kept_pre_activation_overflows():
+    """fp16: z = -70000 gives a finite result; Z keeps -inf, and its gradient is 0."""
+    X, W = torch.full((1, 1), 700.0, device="cuda").half(), torch.full((1, 8), -100.0, device="cuda").half()
+    for act in ("relu", "gelu", "gelu_tanh", "silu"):
+        Y, Z = torch.empty(1, 8, device="cuda").half(), torch.empty(1, 8, device="cuda").half()
+        pg.linear(X, W, Y, act=act, Z=Z)
+        assert (Y == 0).all() and (Z == -math.inf).all()
+        dX, dW = torch.empty(1, 1, device="cuda").half(), torch.empty(1, 8, device="cuda").half()
+        ws = space(pg.linear_backward_workspace(1, 8, 1, F16, act))
+        pg.linear_backward(torch.ones_like(Y), X, W, Z=Z, act=act, dX=dX, dW=dW, ws=ws)
+        assert float(dX) == 0 and (dW == 0).all()
+
+
 def test_linear_gradients_against_differences():
     """f32 gradients of sum(C * linear) against central differences in 64 bits."""
     m, n, k = 6, 9, 11
