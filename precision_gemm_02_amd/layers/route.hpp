@@ -709,7 +709,7 @@ struct RouteBackArgs {
 // S the sum of P, otherwise ds_j = g_j; then through the sigmoid,
 // ds p (1 - p), or the softmax, p (ds - sum_i p_i ds_i).  The softmax
 // renormalised is a softmax of the chosen logits alone, which is how it is
-// computed: no score underflows.
+// computed, and the renormalised sigmoid likewise: no score underflows.
 template <typename T, int Q>
 __global__ __launch_bounds__(256) void route_back_kernel(const RouteBackArgs a) {
   const long long t = (long long)blockIdx.x * 4 + (threadIdx.x >> 6);
@@ -776,14 +776,18 @@ __global__ __launch_bounds__(256) void route_back_kernel(const RouteBackArgs a) 
     d = p * g;
     inner = wsum(d);
   } else {
-    const float p = plive ? 1.0f / (1.0f + expf(-px)) : 0.0f;
     // 1 - p without cancellation
     const float not_p = plive ? 1.0f / (1.0f + expf(px)) : 0.0f;
     if (a.renorm) {
+      // sigmoid(x) = exp(min(x, 0)) / (1 + exp(-|x|)): the sum's ratios keep with
+      // the largest exp taken out of them, also where every score underflows
+      const float low = fminf(px, 0.0f), c = wmax(plive ? low : -__builtin_inff());
+      const float p = plive ? expf(low - c) / (1.0f + expf(-fabsf(px))) : 0.0f;
       const float s = wsum(p);
       const float r = s > 0 ? p / s : 0.0f;
       d = r * (g - wsum(r * g)) * not_p;
     } else {
+      const float p = plive ? 1.0f / (1.0f + expf(-px)) : 0.0f;
       d = g * p * not_p;
     }
   }

@@ -590,6 +590,42 @@ def test_route_backward(dtype, score, renorm, E, top):
     out.check("dlogits")
 
 
+def sigmoid_renorm_weights(x):
+    """Sigmoids over their sum in 64 bits, of logits of any size."""
+    low = x.clamp(max=0)
+    p = torch.exp(low - low.amax(1, keepdim=True)) / (1 + torch.exp(-x.abs()))
+    return p / p.sum(1, keepdim=True)
+
+
+LOW = [[-100.0, -101, -102, -103], [-300, -301, -302, -310], [-89, -200, -95, -90],
+       [-5, -120, -7, -6], [-20, 90, -100, 2], [-1000, -1000, -1001, -1004]]
+
+
+@pytest.mark.parametrize("dtype", TYPES, ids=ids)
+@pytest.mark.parametrize("top", [2, 3])
+def test_route_backward_of_low_sigmoids(dtype, top):
+    """Renormalised sigmoids of logits far below -88, where exp(-x) is infinite in 32
+    bits: the weights depend on the logits like a softmax."""
+    l = torch.tensor(LOW).to(dtype)
+    e = torch.tensor([[0, 1, 3], [2, 1, 0], [0, 3, 2], [1, 0, 3], [2, 0, 1], [1, 0, 2]])[:, :top]
+    dw = torch.tensor([[1.0, -2, 0.5], [0.5, 3, -1], [1, 1.5, 2], [3, -1, 1], [-1, 2, 1], [1, -1, 0.25]])
+    dw = dw[:, :top].contiguous()
+    out = torch.empty(l.shape, dtype=dtype, device="cuda")
+    pg.route_backward(dw.cuda(), l.cuda(), e.int().contiguous().cuda(), out, score="sigmoid")
+    x = l.double()
+    px = x.gather(1, e)
+    r = sigmoid_renorm_weights(px)
+    inner = dw.double() - (r * dw.double()).sum(1, keepdim=True)
+    want = torch.zeros_like(x).scatter_(1, e, r * inner * torch.sigmoid(-px))
+    # r to 12 units of 2^-24 (two exps of 3, sums, divisions) and the difference's
+    # rounding in the exponent, |x| exp(x) < 0.37 of one; the same again for inner
+    mag = r * (dw.double().abs() + (r * dw.double().abs()).sum(1, keepdim=True))
+    bound = torch.zeros_like(x).scatter_(1, e, mag * 40 * 2.0 ** -24)
+    bound = bound + want.abs() * half_step(dtype) + torch.finfo(dtype).tiny * torch.finfo(dtype).eps
+    assert ((out.double().cpu() - want).abs() <= bound).all()
+    assert (out[0] != 0).sum() == top
+
+
 # ---- the experts' products ---------------------------------------------------------
 
 def random_plan(g, m, top, E, drop=0.1, empty=()):
