@@ -212,8 +212,9 @@ __device__ __forceinline__ double reciprocal64(double d) {
   return __builtin_fma(y, __builtin_fma(-d, y, 1.0), y);
 }
 
+// (that of -690, 1e-300, for all below)
 __device__ __forceinline__ double sigmoid64(double x) {
-  return reciprocal64(1.0 + exp64(x < -600.0 ? 600.0 : -x));
+  return reciprocal64(1.0 + exp64(x < -690.0 ? 690.0 : -x));
 }
 
 template <int CTRL>
@@ -553,7 +554,12 @@ __global__ __launch_bounds__(1024) void route_kernel(const RouteArgs a) {
     double w = 0;
     const double px = (double)chosen_x;
     if (a.score != 0) {
-      w = pick >= 0 ? sigmoid64(px) : 0.0;
+      // far below 0 the sigmoid is exp(x), whose ratios no shift changes: where all
+      // scores would underflow, the largest logit is taken as -600
+      double shift = 0;
+      if (a.renorm && __ballot(pick >= 0 && chosen_x >= -600.0f) == 0)
+        shift = (double)unordered(wave_max_int(ordered(chosen_x))) + 600.0;
+      w = pick >= 0 ? sigmoid64(px - shift) : 0.0;
       if (a.renorm) {
         const double sum = wave_sum(w);
         w = sum > 0 ? w / sum : 0.0;

@@ -626,6 +626,22 @@ def test_route_backward_of_low_sigmoids(dtype, top):
     assert (out[0] != 0).sum() == top
 
 
+@pytest.mark.parametrize("dtype", TYPES, ids=ids)
+@pytest.mark.parametrize("top", [1, 2, 4])
+def test_route_weights_of_low_sigmoids(dtype, top):
+    """Renormalised sigmoids that are 0 in 64 bits still have their ratios."""
+    l = torch.tensor(LOW + [[-701.0, -700, -702, -703], [-9000, -9001, -8990, -20000],
+                            [-math.inf, -3000, -3001, -math.inf], [-2e4, -6e4, -5e4, -4e4],
+                            [-math.inf, -math.inf, -math.inf, -math.inf]]).to(dtype)
+    w, e, off, tok, slots = run_route(l.cuda(), top, score="sigmoid")
+    we = route64(l.float(), LOWEST[dtype], top, score="sigmoid")[0]
+    assert torch.equal(e.cpu(), we)
+    live = we >= 0
+    x = l.double().gather(1, we.clamp(min=0).long()).masked_fill(~live, -1e300)
+    want = sigmoid_renorm_weights(x).masked_fill(~live, 0)
+    assert ((w.double().cpu() - want).abs() <= want * (2.0 ** -24 + 1e-12) + 1e-38).all()
+
+
 # ---- the experts' products ---------------------------------------------------------
 
 def random_plan(g, m, top, E, drop=0.1, empty=()):
