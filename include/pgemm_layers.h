@@ -108,6 +108,7 @@ size_t pgemm_linear_backward_workspace(pgemm_kind kind, int m, int n, int k);
  *   scores: softmax over the experts, or the sigmoid, of the logits (m x
  *   experts, of dtype).  A logit of -inf or of the type's lowest value is
  *   masked, and so is NaN: such an expert has score 0 and is never chosen.
+ *   +inf counts as the largest fp32 number.
  *   key: score + bias (fp32, or NULL; a bias that is not finite, or beyond
  *   3e38, masks its expert); with neither bias nor groups the logit
  *   itself (the scores' own order, also where they underflow).  Keys are

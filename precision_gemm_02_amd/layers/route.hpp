@@ -50,13 +50,17 @@ __device__ __forceinline__ double lowest<_Float16>() { return -65504.0; }
 template <>
 __device__ __forceinline__ double lowest<__bf16>() { return -3.3895313892515355e38; }
 
-// A logit in 64 bits, +inf (and all above 3e38) as 3e38, a finite number whose
-// score is the limit; `live` is false for masked logits and NaN.
+// +inf counts as the largest fp32 number, whose differences are numbers: the
+// scores are their limits.
+constexpr float kMaxLogit = 3.4028234663852886e38f;
+__device__ __forceinline__ float finite(float x) { return x < kMaxLogit ? x : kMaxLogit; }
+
+// A logit in 64 bits; `live` is false for masked logits and NaN.
 template <typename T>
 __device__ __forceinline__ double logit(const void* base, long long at, bool* live) {
-  const double x = (double)(float)static_cast<const T*>(base)[at];
-  *live = x > lowest<T>();
-  return x < 3.0e38 ? x : (double)3.0e38f;
+  const float x = (float)static_cast<const T*>(base)[at];
+  *live = (double)x > lowest<T>();
+  return (double)finite(x);
 }
 
 // Reductions over the wave by DPP moves (no LDS round trips): row_shr 1, 2, 4,
@@ -397,7 +401,7 @@ __global__ __launch_bounds__(1024) void route_kernel(const RouteArgs a) {
       if (e < a.experts) {
         x[q] = (float)next[q];
         if ((double)x[q] > lowest<T>()) {
-          x[q] = x[q] < 3.0e38f ? x[q] : 3.0e38f;
+          x[q] = finite(x[q]);
           key[q] = ordered(x[q]);
         }
       }
@@ -731,7 +735,7 @@ __global__ __launch_bounds__(256) void route_back_kernel(const RouteBackArgs a) 
     if (e < a.experts) {
       const float l = (float)static_cast<const T*>(a.logits)[t * a.ld + e];
       live[q] = (double)l > lowest<T>();
-      x[q] = l < 3.0e38f ? l : 3.0e38f;
+      x[q] = finite(l);
     }
     if (live[q] && x[q] > top) top = x[q];
   }
@@ -749,7 +753,7 @@ __global__ __launch_bounds__(256) void route_back_kernel(const RouteBackArgs a) 
   if (pick >= 0) {
     const float l = (float)static_cast<const T*>(a.logits)[t * a.ld + pick];
     plive = (double)l > lowest<T>();
-    px = l < 3.0e38f ? l : 3.0e38f;
+    px = finite(l);
   }
   if (!plive) { pick = -1; g = 0; }
 

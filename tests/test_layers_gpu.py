@@ -642,6 +642,41 @@ def test_route_weights_of_low_sigmoids(dtype, top):
     assert ((w.double().cpu() - want).abs() <= want * (2.0 ** -24 + 1e-12) + 1e-38).all()
 
 
+@pytest.mark.parametrize("dtype", [F32, BF16], ids=ids)
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("top", [1, 2, 4])
+def test_route_of_the_largest_logits(dtype, score, top):
+    """Finite logits up to the type's largest keep their order, +inf before them."""
+    big = torch.finfo(dtype).max
+    l = torch.tensor([[1.0, 3.1e38, 3.3e38, 0], [3.05e38, 0, math.inf, 3.3e38],
+                      [-3.3e38, big, 3.2e38, -1], [-3.3e38, -3.1e38, -3.2e38, -math.inf],
+                      [3.1e38, 3.1e38, 3.2e38, math.nan], [-3.3e38, 3.3e38, -big, 5]]).to(dtype)
+    ref = l.float().masked_fill(l.isnan(), -math.inf)
+    w, e, off, tok, slots = run_route(l.cuda(), top, score=score, renorm=False)
+    we, ww = route64(ref, LOWEST[dtype], top, score=score, renorm=False)
+    assert torch.equal(e.cpu(), we)
+    assert ((w.double().cpu() - ww).abs() <= ww * (2.0 ** -24 + 1e-12) + 1e-38).all()
+    # with gradients of 1 the renormalised weights' is 0; otherwise p (1 - p) of the
+    # sigmoid or p (1 - the chosen ones' sum) of the softmax, to 40 units of 2^-24
+    x = ref.double().clamp(max=torch.finfo(F32).max)
+    p = torch.softmax(x, 1) if score == "softmax" else torch.sigmoid(x)
+    chosen = torch.zeros_like(p).scatter_(1, we.clamp(min=0).long(), 1.0) * (ref > LOWEST[dtype])
+    rest = 1 - (p * chosen).sum(1, keepdim=True) if score == "softmax" else 1 - p
+    mag = chosen * p * (1 - p) if score == "sigmoid" else p * rest.abs() + p * (1 - p)
+    d = torch.empty_like(l, device="cuda")
+    for renorm in (False, True):
+        pg.route_backward(torch.ones(6, top, device="cuda"), l.cuda(), e, d, score=score,
+                          renorm=renorm)
+        if renorm:
+            want = torch.zeros_like(p)
+        elif score == "sigmoid":
+            want = chosen * p * (1 - p)
+        else:
+            want = p * (chosen - (p * chosen).sum(1, keepdim=True))
+        bound = half_step(dtype) * want.abs() + 40 * 2.0 ** -24 * mag
+        assert ((d.double().cpu() - want).abs() <= bound).all()
+
+
 # ---- the experts' products ---------------------------------------------------------
 
 def random_plan(g, m, top, E, drop=0.1, empty=()):
