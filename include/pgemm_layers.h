@@ -19,7 +19,7 @@
  * Capture.  Every call only launches kernels (no allocation, memset or
  *   synchronization), so it can be captured into a HIP graph.
  * Determinism.  Identical inputs give identical bits.
- * Sizes.  A product of more tiles than one launch takes (2^32 threads: 2^24 tiles
+ * Sizes are at most 2^31 - 4096 each.  A product of more tiles than one launch takes (2^32 threads: 2^24 tiles
  *   of 64 x 64 to 128 x 128, 2^23 of 256 x 256) is refused as argument 2,
  *   before any launch of its call.
  * Reads.  Rows of a matrix may be read up to 16 bytes past their end where that

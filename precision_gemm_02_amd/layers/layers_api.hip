@@ -11,6 +11,8 @@ namespace layers {
 namespace {
 
 constexpr int kUnits = 256;                       // compute units of an MI355X
+// The kernels step past a size by a few tiles, in 32 bits.
+constexpr int kMaxSize = 0x7fffffff - 4095;
 constexpr long long kMaxThreads = 0xffffffffLL;   // of a launch, along x
 
 int size_of(int dtype) { return dtype == PGEMM_F32 ? 4 : 2; }
@@ -24,6 +26,8 @@ bool kind_ok(const pgemm_kind& k) {
   return known(k.dtype) && (k.out_dtype == k.dtype || k.out_dtype == PGEMM_F32) &&
          k.act >= PGEMM_ACT_NONE && k.act <= PGEMM_ACT_SILU;
 }
+
+bool size_ok(int v) { return v >= 0 && v <= kMaxSize; }
 
 long long ceil_div(long long a, long long b) { return (a + b - 1) / b; }
 long long round_up(long long a, long long b) { return ceil_div(a, b) * b; }
@@ -416,9 +420,9 @@ int pgemm_linear(pgemm_kind kind, int m, int n, int k, pgemm_rows X, pgemm_weigh
                  const void* bias, pgemm_rows residual, pgemm_rows Z, pgemm_rows Y,
                  void* workspace, size_t workspace_bytes, void* stream) {
   if (!kind_ok(kind)) return -1;
-  if (m < 0) return -2;
-  if (n < 0) return -3;
-  if (k < 0) return -4;
+  if (!size_ok(m)) return -2;
+  if (!size_ok(n)) return -3;
+  if (!size_ok(k)) return -4;
   const bool touch = m > 0 && n > 0, read = touch && k > 0;
   const int size = size_of(kind.dtype), osize = size_of(kind.out_dtype);
   if (!rows_ok(X, k, size, read)) return -5;
@@ -464,9 +468,9 @@ int pgemm_linear_backward(pgemm_kind kind, int m, int n, int k, pgemm_rows dY, p
                           pgemm_rows X, pgemm_weight W, pgemm_rows dX, pgemm_weight dW,
                           void* dbias, void* workspace, size_t workspace_bytes, void* stream) {
   if (!kind_ok(kind)) return -1;
-  if (m < 0) return -2;
-  if (n < 0) return -3;
-  if (k < 0) return -4;
+  if (!size_ok(m)) return -2;
+  if (!size_ok(n)) return -3;
+  if (!size_ok(k)) return -4;
   const int size = size_of(kind.dtype), osize = size_of(kind.out_dtype);
   const bool read = m > 0 && n > 0;
   if (!rows_ok(dY, n, size, read)) return -5;
@@ -577,9 +581,9 @@ int pgemm_expert_linear(pgemm_kind kind, int rows, int n, int k, pgemm_plan plan
                         pgemm_weight W, const void* bias, pgemm_rows Z, pgemm_rows Y,
                         void* stream) {
   if (!kind_ok(kind)) return -1;
-  if (rows < 0) return -2;
-  if (n < 0) return -3;
-  if (k < 0) return -4;
+  if (!size_ok(rows)) return -2;
+  if (!size_ok(n)) return -3;
+  if (!size_ok(k)) return -4;
   const bool touch = rows > 0 && n > 0, read = touch && k > 0;
   const int size = size_of(kind.dtype), osize = size_of(kind.out_dtype);
   if (!plan_ok(plan, rows, touch)) return -5;
@@ -625,9 +629,9 @@ int pgemm_expert_linear_backward(pgemm_kind kind, int rows, int n, int k, pgemm_
                                  pgemm_rows dX, pgemm_weight dW, void* dbias, void* workspace,
                                  size_t workspace_bytes, void* stream) {
   if (!kind_ok(kind)) return -1;
-  if (rows < 0) return -2;
-  if (n < 0) return -3;
-  if (k < 0) return -4;
+  if (!size_ok(rows)) return -2;
+  if (!size_ok(n)) return -3;
+  if (!size_ok(k)) return -4;
   const int size = size_of(kind.dtype), osize = size_of(kind.out_dtype);
   const bool read = rows > 0 && n > 0;
   if (!plan_ok(plan, rows, true)) return -5;
@@ -658,7 +662,7 @@ int pgemm_combine(int dtype, int m, int n, int top, int rows, pgemm_rows Y, cons
                   const float* weights, pgemm_rows residual, pgemm_rows out, void* stream) {
   if (!known(dtype)) return -1;
   if (m < 0 || m > (1 << 30) / kMaxTop) return -2;
-  if (n < 0) return -3;
+  if (!size_ok(n)) return -3;
   if (top < 1 || top > kMaxTop) return -4;
   if (rows < 0) return -5;
   const bool touch = m > 0 && n > 0;
@@ -692,7 +696,7 @@ int pgemm_combine_backward(int dtype, int m, int n, int top, int rows, pgemm_row
                            float* dweights, void* stream) {
   if (!known(dtype)) return -1;
   if (m < 0 || m > (1 << 30) / kMaxTop) return -2;
-  if (n < 0) return -3;
+  if (!size_ok(n)) return -3;
   if (top < 1 || top > kMaxTop) return -4;
   if (rows < 0) return -5;
   const int size = size_of(dtype);

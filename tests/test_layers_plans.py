@@ -183,3 +183,35 @@ def test_few_rows_of_a_long_weight(lib):
     for n in (16, 4096, 1 << 20, 1 << 28, 1 << 29):
         st, got = linear(lib, BF16, 1, n, 8)
         assert st == 0 and got[0].x * got[0].threads < 1 << 32, n
+
+
+@pytest.mark.parametrize("over", [1, 2, 4095])
+def test_sizes_that_32_bits_do_not_step_past_are_refused(lib, over):
+    """The kernels' indices go up to a few tiles beyond a size."""
+    top = (1 << 31) - 4096
+    big, kind, none = top + over, lo._Kind(BF16, BF16, 0), rows(1, None)
+    w = lo._Weight(FAKE, 1 << 31, 0, 1 << 62)
+    plan = lo._Plan(4, FAKE, FAKE, 8)
+    for pos in (2, 3, 4):
+        for size, want in ((big, -pos), (top, 0)):
+            sizes = [16, 16, 16]
+            sizes[pos - 2] = size
+            r = rows(1 << 31)
+            assert lib.pgemm_linear(kind, *sizes, r, w, None, none, none, r, None, 0, None) == want
+            assert len(lib.launched()) == (want == 0)
+            assert lib.pgemm_linear_backward(kind, *sizes, r, r, r, w, r, w, FAKE, FAKE, BIG,
+                                             None) == want
+            assert (len(lib.launched()) > 0) == (want == 0)
+            if pos != 2 and want == 0:
+                sizes[pos - 2] = 1 << 28       # (more columns are too many tiles for a launch)
+            assert lib.pgemm_expert_linear(kind, *sizes, plan, r, w, None, none, r, None) == want
+            assert len(lib.launched()) == (want == 0)
+            assert lib.pgemm_expert_linear_backward(kind, *sizes, plan, r, r, r, w, r, w, FAKE, FAKE,
+                                                    BIG, None) == want
+            assert (len(lib.launched()) > 0) == (want == 0)
+    r = rows(1 << 31)
+    assert lib.pgemm_combine(BF16, 8, big, 2, 16, r, FAKE, FAKE, none, r, None) == -3
+    assert lib.pgemm_combine(BF16, 8, top, 2, 16, r, FAKE, FAKE, none, r, None) == 0
+    assert lib.pgemm_combine_backward(BF16, 8, big, 2, 16, r, r, FAKE, FAKE, r, FAKE, None) == -3
+    assert lib.pgemm_combine_backward(BF16, 8, top, 2, 16, r, r, FAKE, FAKE, r, FAKE, None) == 0
+    assert len(lib.launched()) == 2
