@@ -114,19 +114,52 @@ hipError_t column_sum(const float* partial, void* out, int n, int groups, int ch
                          dim3((unsigned)((n + 31) / 32), (unsigned)groups), dim3(256), args, 0, s);
 }
 
-template <typename T>
-hipError_t combine(const CombineArgs& a, hipStream_t s) {
-  const int tpb = 256 / a.tpr;
-  return launch(&combine_kernel<T>,
-                dim3((unsigned)((a.m + tpb - 1) / tpb),
-                     (unsigned)((a.n + a.tpr * 8 - 1) / (a.tpr * 8))),
-                256, a, s);
+// Workgroups of 256 threads in one launch; more tokens take several (a launch
+// has less than 2^32 threads).
+constexpr int kMostGroups = 1 << 23;
+
+// p moved by `rows` rows of `ld` elements of T (nullptr stays).
+template <typename T, typename P>
+P* rows_on(P* p, long long rows, long long ld) {
+  return p == nullptr ? nullptr : (P*)((const char*)p + rows * ld * (long long)sizeof(T));
 }
 
 template <typename T>
-hipError_t combine_back(const CombineBackArgs& a, hipStream_t s) {
-  const long long waves = (long long)a.m * a.top;
-  return launch(&combine_back_kernel<T>, dim3((unsigned)((waves + 3) / 4)), 256, a, s);
+hipError_t combine(const CombineArgs& all, hipStream_t s) {
+  const int tpb = 256 / all.tpr;
+  const long long part = (long long)kMostGroups * tpb;
+  for (long long t0 = 0; t0 < all.m; t0 += part) {
+    CombineArgs a = all;
+    a.m = (int)(all.m - t0 < part ? all.m - t0 : part);
+    a.slots = rows_on<int>(a.slots, t0, a.top);
+    a.weights = rows_on<float>(a.weights, t0, a.top);
+    a.R = rows_on<T>(a.R, t0, a.ldr);
+    a.out = rows_on<T>(a.out, t0, a.ldo);
+    const hipError_t e = launch(&combine_kernel<T>,
+                                dim3((unsigned)((a.m + tpb - 1) / tpb),
+                                     (unsigned)((a.n + a.tpr * 8 - 1) / (a.tpr * 8))),
+                                256, a, s);
+    if (e != hipSuccess) return e;
+  }
+  return hipSuccess;
+}
+
+template <typename T>
+hipError_t combine_back(const CombineBackArgs& all, hipStream_t s) {
+  const int part = kMostGroups * 4 / all.top;
+  for (long long t0 = 0; t0 < all.m; t0 += part) {
+    CombineBackArgs a = all;
+    a.m = (int)(all.m - t0 < part ? all.m - t0 : part);
+    a.dout = rows_on<T>(a.dout, t0, a.ldo);
+    a.slots = rows_on<int>(a.slots, t0, a.top);
+    a.weights = rows_on<float>(a.weights, t0, a.top);
+    a.dweights = rows_on<float>(a.dweights, t0, a.top);
+    const long long waves = (long long)a.m * a.top;
+    const hipError_t e =
+        launch(&combine_back_kernel<T>, dim3((unsigned)((waves + 3) / 4)), 256, a, s);
+    if (e != hipSuccess) return e;
+  }
+  return hipSuccess;
 }
 
 template <typename T>

@@ -1044,3 +1044,34 @@ def test_offsets_beyond_32_bits():
     Xs, Ws = torch.ones(40, 8, dtype=BF16, device="cuda"), torch.ones(8, 16, dtype=BF16, device="cuda")
     pg.linear(Xs, Ws, Yl)
     assert (Yl == 8).all()
+
+
+def test_combine_of_more_tokens_than_a_launch_takes():
+    """2^24 tokens with a workgroup each, and 2^26 choices with a wave each."""
+    m, n, rows = (1 << 24) + 5, 1032, 16
+    g = gen(33)
+    Y = ints(g, rows, n).to(BF16).cuda()
+    slots = torch.randint(-1, rows, (m, 1), generator=g, dtype=torch.int32).cuda()
+    out = torch.empty(m, n, dtype=BF16, device="cuda")
+    pg.combine(Y, slots, out)
+    padded = torch.cat([torch.zeros(1, n, dtype=BF16, device="cuda"), Y])
+    for t0 in range(0, m, 1 << 20):
+        want = padded[slots[t0:t0 + (1 << 20), 0].long() + 1]
+        assert torch.equal(out[t0:t0 + (1 << 20)], want)
+    del out, want
+    m, top, n = (1 << 22) + 3, 16, 8
+    live = torch.tensor([0, 1, m // 2, (1 << 21) - 1, 1 << 21, (1 << 21) + 1, m - 2, m - 1])
+    R = live.numel() * top
+    slots = torch.full((m, top), -1, dtype=torch.int32)
+    slots[live] = torch.randperm(R, generator=g).int().view(-1, top)
+    slots = slots.cuda()
+    dout, Y = ints(g, m, n).to(BF16).cuda(), ints(g, R, n).to(BF16).cuda()
+    w = torch.full((m, top), 2.0, device="cuda")
+    dY = torch.full((R, n), 9.0, dtype=BF16, device="cuda")
+    dw = torch.full((m, top), 9.0, device="cuda")
+    pg.combine_backward(dout, Y, slots, w, dY=dY, dweights=dw)
+    assert int((dw != 0).any(1).sum()) <= live.numel()
+    for t in live.tolist():
+        r = slots[t].long()
+        assert torch.equal(dY[r], (2 * dout[t]).expand(top, n))
+        assert torch.equal(dw[t], Y[r].float() @ dout[t].float())
