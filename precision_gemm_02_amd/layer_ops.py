@@ -416,14 +416,24 @@ def expert_linear_backward(dY, X, W, offsets, *, tokens=None, Z=None, act="none"
                            dbias=None, ws=None, stream=None):
     """Gradients of ``expert_linear``: dX (rows, k) per row (``combine`` sums
     them over a token's rows), dW (E, k, n), dbias (E, n); those given are
-    written, zeros for experts without rows.  ``ws`` has
-    ``expert_linear_backward_workspace`` bytes."""
+    written, zeros for experts without rows.  W may be None without dX, X without
+    dW.  ``ws`` has ``expert_linear_backward_workspace`` bytes."""
     dev = _device(dY, "dY")
     rows, n = _shape2(dY, "dY")
-    xr, k = _shape2(X, "X")
-    if W.dim() != 3:
-        raise ValueError("W must be 3-D")
-    E = W.shape[0]
+    if offsets.dim() != 1 or offsets.shape[0] < 2:
+        raise ValueError("offsets is %s, expected (experts + 1,)" % (tuple(offsets.shape),))
+    E = offsets.shape[0] - 1
+    xr, k = rows, 0
+    if X is not None:
+        xr, k = _shape2(X, "X")
+    elif dX is not None:
+        k = _shape2(dX, "dX")[1]
+    for t, name in ((W, "W"), (dW, "dW")):
+        if t is not None:
+            if t.dim() != 3:
+                raise ValueError("%s must be 3-D" % name)
+            if X is None and dX is None:
+                k = t.shape[1]
     T = dY.dtype
     out = _grad_type(dW, dbias, T)
     code = _dtype(dY, "dY")

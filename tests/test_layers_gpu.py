@@ -783,6 +783,31 @@ def test_expert_gradients_over_long_rows(dtype, order, bounds, n, k):
         assert torch.equal(db[e].double().cpu(), dy[s].sum(0))
 
 
+@pytest.mark.parametrize("gather", [True, False])
+def test_expert_gradients_alone(gather):
+    """Each gradient without what only the others read."""
+    m, top, E, n, k = 30, 2, 5, 24, 40
+    g = gen(34)
+    _, off, tok, _ = random_plan(g, m, top, E)
+    R, o = m * top, off.tolist()
+    X, dY = ints(g, m if gather else R, k).cuda(), ints(g, R, n).cuda()
+    W = weight(g, (E,), k, n, "nk", F32, integer=True)
+    tokens = tok if gather else None
+    ws = space(pg.expert_linear_backward_workspace(R, n, k, E, F32))
+    dX, dW = Guarded(R, k, F32), torch.full((E, k, n), 9.0, device="cuda")
+    db = torch.full((E, n), 9.0, device="cuda")
+    pg.expert_linear_backward(dY, None, W, off, tokens=tokens, dX=dX.t, ws=ws)
+    pg.expert_linear_backward(dY, X, None, off, tokens=tokens, dW=dW, ws=ws)
+    pg.expert_linear_backward(dY, None, None, off, tokens=tokens, dbias=db, ws=ws)
+    src = tok.long() if gather else torch.arange(R, device="cuda")
+    for e in range(E):
+        r = slice(o[e], o[e + 1])
+        assert torch.equal(dX.t[r], dY[r] @ W[e].t())
+        assert torch.equal(dW[e], X[src[r]].t() @ dY[r])
+        assert torch.equal(db[e], dY[r].sum(0))
+    dX.check("dX", rows=o[-1])
+
+
 def test_zero_inner_size_in_tiles():
     bias = torch.arange(130.0, device="cuda")
     Y = torch.full((70, 130), 9.0, device="cuda")

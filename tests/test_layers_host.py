@@ -279,3 +279,19 @@ def test_other_refusals(anywhere):
 
 def test_status_of_late_arguments_reads_as_an_argument():
     assert "argument" in pg.status_string(-14)
+
+
+def test_expert_gradient_refusals(anywhere):
+    i = lambda *s: torch.zeros(*s, dtype=torch.int32)
+    dY, X, W, off = z(4, 5), z(4, 3), z(2, 3, 5), i(3)
+    for args, kw in (((dY, X, W[0], off), {}), ((dY, X, z(3, 3, 5), off), {}),
+                     ((dY, X, z(2, 4, 5), off), {}), ((dY, X, W, i(1)), {}), ((dY, X, W, i(3, 1)), {}),
+                     ((dY, None, W, off), dict(dX=z(4, 4))), ((dY, None, W, off), dict(dX=z(3, 3))),
+                     ((dY, X, None, off), dict(dW=z(2, 5, 3))), ((dY, X, None, off), dict(dW=z(3, 5)))):
+        with pytest.raises(ValueError):
+            pg.expert_linear_backward(*args, **kw)
+    for kw in (dict(dX=z(4, 3)), dict(dW=z(2, 3, 5))):       # each needs the other operand
+        with pytest.raises(pg.PgemmError) as e:
+            pg.expert_linear_backward(dY, X if "dX" in kw else None, W if "dW" in kw else None, off,
+                                      **kw)
+        assert e.value.status == (-9 if "dX" in kw else -8)
