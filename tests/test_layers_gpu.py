@@ -549,6 +549,79 @@ def test_route_close_keys(groups):
                 top_groups=max(1, groups // 2))
 
 
+@pytest.mark.parametrize("dtype", TYPES, ids=ids)
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("groups,top_groups", [(1, 1), (3, 2), (12, 5)])
+def test_route_masks_by_bias(dtype, score, groups, top_groups):
+    """A bias that is infinite, NaN or beyond 3e38 masks its expert; a large
+    finite one does not disturb the others' order."""
+    m, E, top = 70, 12, 4
+    g = gen(31)
+    l = torch.randn(m, E, generator=g).to(dtype)
+    for bad in (math.inf, -math.inf, math.nan, 3.2e38, -3.2e38):
+        b = torch.randn(E, generator=g) * 0.1
+        b[[1, 4, 5]] = bad
+        w, e, off, tok, slots = run_route(l.cuda(), top, score=score, bias=b.cuda(), groups=groups,
+                                          top_groups=top_groups)
+        b[[1, 4, 5]] = -math.inf
+        we, ww = route64(l.float(), LOWEST[dtype], top, bias=b, score=score, groups=groups,
+                         top_groups=top_groups)
+        assert torch.equal(e.cpu(), we), bad
+        assert ((w.double().cpu() - ww).abs() <= ww.abs() * (2.0 ** -24 + 1e-12) + 1e-38).all()
+    for large in (-1e4, -1e9, 1e6):
+        b = torch.randn(E, generator=g) * 0.1
+        b[[2, 7]] = large
+        check_route(l.cuda(), top, bias=b.cuda(), score=score, groups=groups, top_groups=top_groups)
+    every = torch.full((E,), math.nan, device="cuda")
+    w, e, off, tok, slots = run_route(l.cuda(), top, score=score, bias=every, groups=groups,
+                                      top_groups=top_groups)
+    assert (e == -1).all() and (w == 0).all() and (off == 0).all() and (slots == -1).all()
+
+
+def scores64(row, score):
+    return torch.softmax(row.double(), 0) if score == "softmax" else torch.sigmoid(row.double())
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("top", [1, 5, 16])
+@pytest.mark.parametrize("E", [32, 200])
+def test_route_close_scores(score, top, E):
+    """Keys a few 1e-11 apart and not equal, closer than the integer keys tell."""
+    row = torch.randn(E, generator=gen(35))
+    step = 2e-3 if score == "softmax" else 2e-4
+    row[1::2] = row[0::2] + step * (1 + torch.arange(E // 2) / E)
+    s, bias = scores64(row, score), torch.zeros(E)
+    # (one unit of the last place on from the nearest: never exactly equal)
+    bias[1::2] = torch.nextafter((s[0::2] - s[1::2]).float(), torch.zeros(()))
+    keys = s + bias.double()
+    gap = (keys[0::2] - keys[1::2]).abs()
+    # biases below 2^-9 are rounded by less than 2^-34; two sums of a softmax in 64
+    # bits differ by a few 1e-16
+    assert float(bias.abs().max()) < 2.0 ** -9 and float(gap.max()) < 2.0 ** -30
+    assert float(gap.min()) > 2e-15
+    check_route(row.expand(70, E).contiguous().cuda(), top, bias=bias.cuda(), score=score)
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("top_groups", [1, 2, 3, 5, 7])
+def test_route_close_group_sums(score, top_groups):
+    """Groups in pairs whose sums of two keys are a few 1e-11 apart and not equal."""
+    E, groups, top = 32, 8, 3
+    row = torch.randn(groups, E // groups, generator=gen(36))
+    row[1::2] = row[0::2] + 1e-4 * torch.rand(groups // 2, E // groups, generator=gen(37))
+    row = row.reshape(E)
+    s = scores64(row, score).view(groups, -1)
+    two = s.topk(2, 1)
+    bias = torch.zeros(groups, E // groups)
+    for p in range(1, groups, 2):
+        bias[p, two.indices[p, 0]] = float(two.values[p - 1].sum() - two.values[p].sum())
+    sums = (s + bias.double()).topk(2, 1).values.sum(1)
+    gap = (sums[0::2] - sums[1::2]).abs()
+    assert float(gap.max()) < 2.0 ** -30 and float(gap.min()) > 2e-15
+    check_route(row.expand(70, E).contiguous().cuda(), top, bias=bias.view(E).cuda(), score=score,
+                groups=groups, top_groups=top_groups)
+
+
 def test_route_no_tokens_and_padded_rows():
     E, top = 12, 3
     w, e, off, tok, slots = run_route(torch.zeros(0, E, device="cuda"), top)
