@@ -136,7 +136,7 @@ bool launch_fits(int kernel, int mode, long long rows, int groups, int n) {
   a.rows = (int)rows;
   a.splits = 1;
   set_tiles(&a, kernel, mode, rows);
-  return prod_grid(a, mode, kernel).x * prod_threads(kernel) <= kMaxThreads;
+  return prod_grid(a, mode, kernel).x <= kMaxThreads / prod_threads(kernel);
 }
 
 // rows: the rows of D over all groups (how they are distributed is not known
