@@ -191,8 +191,10 @@ constexpr int kNoKey = -0x7fffffff - 1;
 __device__ __forceinline__ double exp64(double x) {
   x = x < -1000.0 ? -1000.0 : (x > 1000.0 ? 1000.0 : x);
   const double n = __builtin_rint(x * 1.4426950408889634074);
-  double r = __builtin_fma(n, -6.93147180369123816490e-01, x);   // ln 2 in two parts
-  r = __builtin_fma(n, -1.90821492927058770002e-10, r);
+  // ln 2 as its nearest 64-bit number and the rest; the fma forms n times the first
+  // without a rounding, so that it need not be short
+  double r = __builtin_fma(n, -0.6931471805599453, x);
+  r = __builtin_fma(n, -2.3190468138462996e-17, r);
   double p = 1.0 / 479001600.0;
   p = __builtin_fma(p, r, 1.0 / 39916800.0);
   p = __builtin_fma(p, r, 1.0 / 3628800.0);
