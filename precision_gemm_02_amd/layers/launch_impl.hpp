@@ -100,10 +100,9 @@ template <typename T>
 hipError_t slope(const SlopeArgs& a, int groups, hipStream_t s) {
   const unsigned cols = (unsigned)((a.n + a.tpr * 8 - 1) / (a.tpr * 8));
   const dim3 grid(cols, (unsigned)a.chunks, (unsigned)groups);
-  if constexpr (sizeof(T) == 2) {
-    if (!a.sums32) return launch(&slope_kernel<T, true>, grid, 256, a, s);
-  }
-  return launch(&slope_kernel<T, false>, grid, 256, a, s);
+  if constexpr (sizeof(T) == 4) return launch(&slope_kernel<T, kExact>, grid, 256, a, s);
+  else if (a.sums32) return launch(&slope_kernel<T, kFine>, grid, 256, a, s);
+  else return launch(&slope_kernel<T, kFast>, grid, 256, a, s);
 }
 
 template <typename T>

@@ -108,82 +108,105 @@ struct ProdArgs {
 // ---- the epilogue ------------------------------------------------------------
 
 // Activations in fp32.  tanh and the logistic function go through one exp and
-// one division; the exp's argument is such that overflow gives the limit.
-// Fast is for results of 16 bits: the hardware's exp2 and reciprocal, off by
-// about |z| + 2 units of 2^-24 (of the tanh form, by its argument's), far below
-// half a step of the result (2^-8 of bf16, 2^-11 of fp16).  fp32 results take the
-// exact forms, whatever the inputs' type.
-template <bool Fast>
+// one division; the exp's argument is such that overflow gives the limit.  By the
+// results' type, not the inputs':
+//  * kFast, for results of 16 bits: the hardware's exp2 and reciprocal, off by
+//    about |z| + 2 units of 2^-24 (of the tanh form, by its argument's), far below
+//    half a step of the result (2^-8 of bf16, 2^-11 of fp16).
+//  * kFine, for fp32 results of 16-bit inputs: the library's exp and the hardware's
+//    reciprocal (one unit of the last place).
+//  * kExact, for fp32 throughout.
+enum Forms { kFast, kFine, kExact };
+
+template <int F>
 __device__ __forceinline__ float logistic(float z) {
-  if constexpr (Fast) return __builtin_amdgcn_rcpf(1.0f + __expf(-z));
+  if constexpr (F == kFast) return __builtin_amdgcn_rcpf(1.0f + __expf(-z));
+  else if constexpr (F == kFine) return __builtin_amdgcn_rcpf(1.0f + expf(-z));
   else return 1.0f / (1.0f + expf(-z));
 }
 
 // The normal distribution function Phi and exp(-z^2/2).  The lower tail is
-// computed as such: 1 + erf would cancel there.  Fast: Phi(-|z|) exp(z^2/2) as a
-// polynomial in t = 1/(1 + 0.26 |z|), fitted for the least relative error over
-// |z| <= 14.5 (where every result of 16 bits has become 0): 1.2e-6, 1.5e-6 with
-// fp32 coefficients.  The exp adds 1.25 z^2 + 4 units of 2^-24 (its argument's
-// roundings), so that Phi is off by at most 1.5e-5 of itself at z = -13; results
-// below the smallest normal fp32 value may be 0.
-template <bool Fast>
+// computed as such: 1 + erf would cancel there.  kFast and kFine: Phi(-|z|)
+// exp(z^2/2) as a polynomial in t = 1/(1 + c |z|), fitted for the least relative
+// error over |z| <= 14.5 (where every result of 16 bits has become 0).  kFast: 1.2e-6,
+// 1.5e-6 with fp32 coefficients; its exp adds 1.25 z^2 + 4 units of 2^-24 (its
+// argument's roundings), so that Phi is off by at most 1.5e-5 of itself at z = -13.
+// kFine: 1.9e-8, 8 units of 2^-24 as evaluated, and z^2/2 from the exp's argument.
+// Results below the smallest normal fp32 value may be 0.
+template <int F>
 __device__ __forceinline__ float normal_cdf(float z, float* bell) {
-  if constexpr (Fast) {
-    const float e = __builtin_amdgcn_exp2f(z * z * -0.72134752044f);   // log2(e) / 2
-    const float t = __builtin_amdgcn_rcpf(1.0f + 0.26f * fabsf(z));
-    float p = -0.07180302f;
-    p = p * t + 0.22505027f;
-    p = p * t - 0.101182476f;
-    p = p * t + 0.16286214f;
-    p = p * t + 0.07458985f;
-    p = p * t + 0.10695134f;
-    p = p * t + 0.103532486f;
-    const float q = p * t * e;
-    *bell = e;
-    return z > 0.0f ? 1.0f - q : q;
-  } else {
+  if constexpr (F == kExact) {
     *bell = expf(-0.5f * z * z);
     return 0.5f * erfcf(-0.70710678118654752f * z);
+  } else {
+    float e, p;
+    if constexpr (F == kFast) {
+      e = __builtin_amdgcn_exp2f(z * z * -0.72134752044f);   // log2(e) / 2
+      const float t = __builtin_amdgcn_rcpf(1.0f + 0.26f * fabsf(z));
+      p = -0.07180302f;
+      p = p * t + 0.22505027f;
+      p = p * t - 0.101182476f;
+      p = p * t + 0.16286214f;
+      p = p * t + 0.07458985f;
+      p = p * t + 0.10695134f;
+      p = (p * t + 0.103532486f) * t;
+    } else {
+      e = expf(-0.5f * z * z);
+      const float t = __builtin_amdgcn_rcpf(1.0f + 0.21f * fabsf(z));
+      p = -0.07129451f;
+      p = p * t + 0.28180316f;
+      p = p * t - 0.3264904f;
+      p = p * t + 0.34498343f;
+      p = p * t - 0.09077039f;
+      p = p * t + 0.12347116f;
+      p = p * t + 0.06956999f;
+      p = p * t + 0.085012406f;
+      p = (p * t + 0.08371515f) * t;
+    }
+    const float q = p * e;
+    *bell = e;
+    return z > 0.0f ? 1.0f - q : q;
   }
 }
 
-template <bool Fast>
+template <int F>
 __device__ __forceinline__ float act_value(float z, int act) {
   switch (act) {
     case kRelu: return z > 0.0f ? z : (z != z ? z : 0.0f);
     case kGelu: {
       float bell;
-      return z * normal_cdf<Fast>(z, &bell);
+      return z * normal_cdf<F>(z, &bell);
     }
     // 0.5 (1 + tanh u) = logistic(2 u)
     case kGeluTanh:
-      return z * logistic<Fast>(1.5957691216057308f * (z + 0.044715f * z * z * z));
-    case kSilu: return z * logistic<Fast>(z);
+      return z * logistic<F>(1.5957691216057308f * (z + 0.044715f * z * z * z));
+    case kSilu: return z * logistic<F>(z);
     default: return z;
   }
 }
 
-// The slope at z is that at the nearest of [-1e4, 1e4], where each has long reached
-// its limit of 0 or 1 (a NaN stays): past 5e19 the products of the tanh form would
-// be 0 times infinity, and so would all three at an infinite z, which is what a
+// Beside Phi and the logistic function, which have their limits at infinities (and
+// keep a NaN), z is taken as the nearest of [-1e4, 1e4], where every slope has long
+// reached its limit of 0 or 1: past 5e19 the products of the tanh form would be 0
+// times infinity, and so would all three at an infinite z, which is what a
 // pre-activation beyond fp16 becomes although its activation is finite.
-template <bool Fast>
+template <int F>
 __device__ __forceinline__ float act_slope(float z, int act) {
-  z = z < -1e4f ? -1e4f : (z > 1e4f ? 1e4f : z);
+  const float c = __builtin_amdgcn_fmed3f(z, -1e4f, 1e4f);
   switch (act) {
     case kRelu: return z > 0.0f ? 1.0f : 0.0f;
     case kGelu: {
       float bell;
-      const float phi = normal_cdf<Fast>(z, &bell);
-      return phi + z * bell * 0.39894228040143268f;
+      const float phi = normal_cdf<F>(z, &bell);
+      return phi + c * bell * 0.39894228040143268f;
     }
     case kGeluTanh: {
-      const float q = logistic<Fast>(1.5957691216057308f * (z + 0.044715f * z * z * z));
-      return q + z * q * (1.0f - q) * 1.5957691216057308f * (1.0f + 0.134145f * z * z);
+      const float q = logistic<F>(1.5957691216057308f * (z + 0.044715f * z * z * z));
+      return q + c * q * (1.0f - q) * 1.5957691216057308f * (1.0f + 0.134145f * c * c);
     }
     case kSilu: {
-      const float q = logistic<Fast>(z);
-      return q * (1.0f + z * (1.0f - q));
+      const float q = logistic<F>(z);
+      return q * (1.0f + c * (1.0f - q));
     }
     default: return 1.0f;
   }
@@ -254,24 +277,24 @@ __device__ __forceinline__ void add_residual(const ProdArgs& a, const Raw8& r, f
 }
 
 // The switch stands outside the loops: the kernels' code stays small.
-template <bool Fast>
+template <int F>
 __device__ __forceinline__ void act8(float* v, int act) {
   switch (act) {
     case kRelu:
 #pragma unroll
-      for (int j = 0; j < 8; ++j) v[j] = act_value<Fast>(v[j], kRelu);
+      for (int j = 0; j < 8; ++j) v[j] = act_value<F>(v[j], kRelu);
       break;
     case kGelu:
 #pragma unroll
-      for (int j = 0; j < 8; ++j) v[j] = act_value<Fast>(v[j], kGelu);
+      for (int j = 0; j < 8; ++j) v[j] = act_value<F>(v[j], kGelu);
       break;
     case kGeluTanh:
 #pragma unroll
-      for (int j = 0; j < 8; ++j) v[j] = act_value<Fast>(v[j], kGeluTanh);
+      for (int j = 0; j < 8; ++j) v[j] = act_value<F>(v[j], kGeluTanh);
       break;
     case kSilu:
 #pragma unroll
-      for (int j = 0; j < 8; ++j) v[j] = act_value<Fast>(v[j], kSilu);
+      for (int j = 0; j < 8; ++j) v[j] = act_value<F>(v[j], kSilu);
       break;
     default: break;
   }
@@ -298,12 +321,13 @@ __device__ __forceinline__ void load_bias(const ProdArgs& a, const void* bias, i
 template <typename T>
 __device__ __forceinline__ void finish_row(const ProdArgs& a, void* D, long long m, int n0,
                                            float* v, const Raw8& residual) {
+  constexpr int Whole = sizeof(T) == 4 ? kExact : kFine;   // fp32 results
   const bool fast = sizeof(T) == 2 && !a.out32;
   const int live = a.N - n0;
   if (live >= 8) {
     if (a.Z != nullptr) put8<T>(a.Z, m * a.ldz + n0, v);
-    if (fast) act8<true>(v, a.act);
-    else act8<false>(v, a.act);
+    if (fast) act8<kFast>(v, a.act);
+    else act8<Whole>(v, a.act);
     if (a.R != nullptr) add_residual<T>(a, residual, v);
     if (a.out32) put8<float>(D, m * a.ldd + n0, v);
     else put8<T>(D, m * a.ldd + n0, v);
@@ -316,7 +340,7 @@ __device__ __forceinline__ void finish_row(const ProdArgs& a, void* D, long long
     for (int q = 0; q < 8; ++q) x = q == j ? v[q] : x;   // no indexed registers
     const int n = n0 + j;
     if (a.Z != nullptr) static_cast<T*>(a.Z)[m * a.ldz + n] = (T)x;
-    x = fast ? act_value<true>(x, a.act) : act_value<false>(x, a.act);
+    x = fast ? act_value<kFast>(x, a.act) : act_value<Whole>(x, a.act);
     if (a.R != nullptr)
       x += a.out32 ? static_cast<const float*>(a.R)[m * a.ldr + n]
                    : (float)static_cast<const T*>(a.R)[m * a.ldr + n];

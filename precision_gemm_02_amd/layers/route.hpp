@@ -436,7 +436,7 @@ __global__ __launch_bounds__(1024) void route_kernel(const RouteArgs a) {
             for (int q = 0; q < Q; ++q) score[q] *= inv;
           } else {
 #pragma unroll
-            for (int q = 0; q < Q; ++q) score[q] = logistic<true>(x[q]);
+            for (int q = 0; q < Q; ++q) score[q] = logistic<kFast>(x[q]);
           }
 #pragma unroll
           for (int q = 0; q < Q; ++q)

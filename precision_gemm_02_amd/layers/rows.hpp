@@ -44,13 +44,13 @@ struct SlopeArgs {
   int chunks;             // row chunks per group (grid y)
   int tpr;                // threads per row (a power of two, at most 64)
   float* partial;         // [group][chunk][n] column sums (nullptr: not wanted)
-  bool sums32;            // their results are fp32: no Fast activations
+  bool sums32;            // their results are fp32 (see Forms)
 };
 
 // dZ = dY * act'(Z) for one group's rows, one chunk of them per workgroup and
 // tpr * 8 columns, and the chunk's column sums: each thread sums its rows in
 // order, the threads of one column are then added in order through LDS.
-template <typename T, bool Fast>
+template <typename T, int F>
 __global__ __launch_bounds__(256) void slope_kernel(const SlopeArgs a) {
   __shared__ float sums[256 * 8];
   const int e = blockIdx.z;
@@ -71,7 +71,7 @@ __global__ __launch_bounds__(256) void slope_kernel(const SlopeArgs a) {
         float z[8];
         get_row8<T>(a.Z, (long long)r * a.ldz, c, a.n, z);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) d[j] *= act_slope<Fast>(z[j], a.act);
+        for (int j = 0; j < 8; ++j) d[j] *= act_slope<F>(z[j], a.act);
         put_row8<T>(a.dZ, (long long)r * a.ldd, c, a.n, d);
       }
 #pragma unroll
