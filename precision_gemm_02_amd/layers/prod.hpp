@@ -326,8 +326,10 @@ __device__ __forceinline__ void finish_row(const ProdArgs& a, void* D, long long
   const int live = a.N - n0;
   if (live >= 8) {
     if (a.Z != nullptr) put8<T>(a.Z, m * a.ldz + n0, v);
-    if (fast) act8<kFast>(v, a.act);
-    else act8<Whole>(v, a.act);
+    if (a.act != kNone) {
+      if (fast) act8<kFast>(v, a.act);
+      else act8<Whole>(v, a.act);
+    }
     if (a.R != nullptr) add_residual<T>(a, residual, v);
     if (a.out32) put8<float>(D, m * a.ldd + n0, v);
     else put8<T>(D, m * a.ldd + n0, v);
