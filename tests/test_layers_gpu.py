@@ -622,6 +622,30 @@ def test_route_close_group_sums(score, top_groups):
                 groups=groups, top_groups=top_groups)
 
 
+@pytest.mark.parametrize("m,E,top", [(32768, 24, 3), (32769, 24, 3), (70001, 100, 5), (33000, 700, 2)])
+def test_route_plan_of_many_tokens(m, E, top):
+    """Around and beyond 512 workgroups, where the counts are summed apart."""
+    logits = torch.randn(m, E, generator=gen(38))
+    logits[torch.rand(m, generator=gen(39)) < 0.05] = -math.inf
+    logits[5, 1:] = -math.inf
+    w, e, off, tok, slots = run_route(logits.cuda(), top)
+    best = logits.cuda().sort(dim=1, descending=True, stable=True)
+    live = best.values[:, :top] > -math.inf
+    want = best.indices[:, :top].masked_fill(~live, -1).int()
+    assert torch.equal(e, want)
+    p = torch.softmax(best.values[:, :top].double(), 1).masked_fill(~live, 0)
+    assert ((w.double() - p).abs() <= p * (2.0 ** -24 + 1e-12) + 1e-38).all()
+    flat = want.flatten().long()
+    rows = int((flat >= 0).sum())
+    order = flat.masked_fill(flat < 0, E).sort(dim=0, stable=True).indices[:rows]
+    place = torch.full((m * top,), -1, dtype=torch.int32, device="cuda")
+    place[order] = torch.arange(rows, dtype=torch.int32, device="cuda")
+    assert torch.equal(slots.flatten(), place)
+    assert torch.equal(tok[:rows], (order // top).int()) and (tok[rows:] == -7).all()
+    count = torch.bincount(flat[flat >= 0], minlength=E)
+    assert off[0] == 0 and torch.equal(off[1:].long(), count.cumsum(0))
+
+
 def test_route_no_tokens_and_padded_rows():
     E, top = 12, 3
     w, e, off, tok, slots = run_route(torch.zeros(0, E, device="cuda"), top)
