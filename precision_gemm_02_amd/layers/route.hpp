@@ -12,8 +12,11 @@
 // places the rows; with more than 512, where every workgroup's own sums would
 // cost more than a launch, a kernel between them sums.
 //
-// Bound by latency: 16384 tokens of 192 experts 41 us a call, where their bytes
-// would take 3.7; 4 tokens 7.4 us, which is the launch.
+// Bound by latency and, above 64 experts, by registers: 16384 tokens of 192 experts
+// 41 us a call, where their bytes would take 3.7; of 512 128 us, of 1024 1030.  The
+// 64-bit decision that few tokens take lies in the same kernel, whose 128
+// registers a lane (1024 threads) then spill: 48 bytes of scratch a lane at 192
+// experts, 480 at 512, 2 KB at 1024.  4 tokens take 7.4 us, which is the launch.
 #pragma once
 
 #include "prod.hpp"
@@ -344,7 +347,9 @@ __device__ __forceinline__ int choose64(const RouteArgs& a, long long t) {
 // A key that is the logit itself is compared as the exact fp32 value.
 // (16384 tokens of 192 experts in 6 groups: 64-bit comparisons throughout 89
 // us; 64-bit scores throughout 53; from fp32 scores straight to 64-bit
-// comparisons, which 0.2 % of the tokens then waited for, 58.)
+// comparisons, which 0.2 % of the tokens then waited for, 58.  That is for fp32
+// logits with a bias.  Equal logits without one have equal keys, which no integers
+// tell apart: 16-bit logits of 256 experts in 8 groups take 119 us, with a bias 59.)
 template <typename T, int Q>
 __global__ __launch_bounds__(1024) void route_kernel(const RouteArgs a) {
   __shared__ unsigned int mask[2 * kMaxExperts];      // [half of the tokens][expert]

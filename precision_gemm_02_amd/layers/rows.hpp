@@ -1,7 +1,8 @@
 // Row-wise kernels of the layer operators: the activation's gradient with the
 // bias gradient's column sums, and the experts' rows back to their tokens.
 // All of them read and write each element once and are bound by memory.  bf16:
-// dZ of 8192 x 4096 37 to 46 us (201 MB: 4.4 to 5.4 TB/s), combine of 8192 tokens'
+// dZ of 8192 x 4096 37 to 47 us (201 MB: 4.3 to 5.4 TB/s; 50 with an fp32 bias
+// gradient's SiLU, 53 its GELU), combine of 8192 tokens'
 // 8 rows of 2048 70 us (336 MB: 4.8), its gradients for 4095 tokens' 6 rows 49 us
 // (36 in a trace; 218 MB: 4.5).
 #pragma once
