@@ -12,6 +12,7 @@ bit by bit; random inputs are held to bounds that count the roundings:
   each result: half a step of its type.
 """
 import math
+import random
 
 import pytest
 import torch
@@ -1197,3 +1198,168 @@ def test_combine_of_more_tokens_than_a_launch_takes():
         r = slots[t].long()
         assert torch.equal(dY[r], (2 * dout[t]).expand(top, n))
         assert torch.equal(dw[t], Y[r].float() @ dout[t].float())
+
+
+# ---- calls over everything the documentation allows -----------------------------------------
+
+def spread(rng, hi):
+    return int(round(math.exp(rng.uniform(0, math.log(hi)))))
+
+
+def placed(rng, rows, cols, dtype, data=None):
+    """Rows at a random stride, from a random element of the buffer on."""
+    return Guarded(rows, cols, dtype, pad=rng.choice((0, 0, 1, 2, 3, 8, 13)),
+                   shift=rng.choice((0, 0, 1, 2, 4, 5)), data=data)
+
+
+def placed_weight(rng, g, experts, k, n, dtype):
+    """Experts' weights (None: one) in a random order, at random strides."""
+    order, pad = rng.choice(("kn", "nk")), rng.choice((0, 0, 1, 2, 8))
+    rows, cols = (k, n) if order == "kn" else (n, k)
+    E, gap = experts or 1, rng.choice((0, 0, 1, 8, 24))
+    size = rows * (cols + pad) + gap
+    buf = torch.full((E * size + 8,), math.nan, dtype=dtype, device="cuda")[rng.choice((0, 1, 2, 8)):]
+    w = buf.as_strided((E, rows, cols), (size, cols + pad, 1))
+    if g is not None:
+        w.copy_(ints(g, E, rows, cols, hi=2).to(dtype))
+    w = w if order == "kn" else w.transpose(1, 2)
+    return w if experts else w[0]
+
+
+def optional(rng, make):
+    return make() if rng.random() < 0.6 else None
+
+
+@pytest.mark.parametrize("seed", range(60))
+def test_random_linear_calls(seed):
+    """Random shapes, strides, alignments, orders, types and options; exact."""
+    rng, g = random.Random(seed), gen(seed)
+    dtype, out32 = rng.choice(TYPES), rng.random() < 0.4
+    m, n, k = spread(rng, 600), spread(rng, 600), spread(rng, 900)
+    out, act = F32 if out32 else dtype, rng.choice(("none", "relu"))
+    X = placed(rng, m, k, dtype, ints(g, m, k, hi=1).to(dtype))
+    W = placed_weight(rng, g, None, k, n, dtype)
+    bias = optional(rng, lambda: ints(g, n).to(dtype).cuda())
+    R = optional(rng, lambda: placed(rng, m, n, out, ints(g, m, n).to(out)))
+    Y = R if R is not None and rng.random() < 0.5 else placed(rng, m, n, out)
+    res = 0 if R is None else R.t.double().cpu()
+    Z = optional(rng, lambda: placed(rng, m, n, dtype))
+    ws = optional(rng, lambda: space(pg.linear_workspace(m, n, k, dtype)))
+    pg.linear(X.t, W, Y.t, bias=bias, act=act, residual=R.t if R else None, Z=Z.t if Z else None, ws=ws)
+    x, w = X.t.double().cpu(), W.double().cpu()
+    z = x @ w + (0 if bias is None else bias.double().cpu())
+    assert torch.equal(Y.t.cpu(), ((z.clamp(min=0) if act == "relu" else z) + res).to(out))
+    Y.check("Y")
+    if Z:
+        assert torch.equal(Z.t.cpu(), z.to(dtype))
+        Z.check("Z")
+    # the gradients of the same layer
+    dY = placed(rng, m, n, dtype, ints(g, m, n, hi=1).to(dtype))
+    Zb = placed(rng, m, n, dtype, ints(g, m, n).to(dtype))
+    dX = optional(rng, lambda: placed(rng, m, k, dtype))
+    dW = optional(rng, lambda: placed_weight(rng, None, None, k, n, out))
+    db = optional(rng, lambda: torch.full((n,), 9.0, dtype=out, device="cuda"))
+    wsb = space(pg.linear_backward_workspace(m, n, k, dtype, act))
+    pg.linear_backward(dY.t, X.t, W, Z=Zb.t if act == "relu" else None, act=act,
+                       dX=dX.t if dX else None, dW=dW, dbias=db, ws=wsb)
+    dz = dY.t.double().cpu()
+    if act == "relu":
+        dz = dz * (Zb.t.double().cpu() > 0)
+    if dX:
+        assert torch.equal(dX.t.cpu(), (dz @ w.t()).to(dtype))
+        dX.check("dX")
+    if dW is not None:
+        assert torch.equal(dW.cpu(), (x.t() @ dz).to(out))
+    if db is not None:
+        assert torch.equal(db.cpu(), dz.sum(0).to(out))
+
+
+@pytest.mark.parametrize("seed", range(60))
+def test_random_expert_calls(seed):
+    """The same over experts, of which some have no rows and one may have most."""
+    rng, g = random.Random(1000 + seed), gen(1000 + seed)
+    dtype, out32 = rng.choice(TYPES), rng.random() < 0.4
+    E, R, n, k = spread(rng, 90), spread(rng, 1500), spread(rng, 400), spread(rng, 400)
+    out, act = F32 if out32 else dtype, rng.choice(("none", "relu"))
+    last = rng.randint(0, R)
+    o = sorted(rng.choice((0, last, rng.randint(0, last))) for _ in range(E - 1))
+    o = [rng.choice((0, 0, min(o + [last]))) if E > 1 else 0] + o + [last]
+    off = torch.tensor(o, dtype=torch.int32, device="cuda")
+    gather = rng.random() < 0.6
+    m = spread(rng, 300) if gather else R + rng.randint(0, 5)
+    tok = torch.randint(0, m, (R,), generator=g, dtype=torch.int32).cuda() if gather else None
+    src = tok.cpu().long() if gather else torch.arange(R)
+    X = placed(rng, m, k, dtype, ints(g, m, k, hi=1).to(dtype))
+    W = placed_weight(rng, g, E, k, n, dtype)
+    bias = optional(rng, lambda: ints(g, E, n).to(dtype).cuda())
+    Y, Z = placed(rng, R, n, out), optional(rng, lambda: placed(rng, R, n, dtype))
+    pg.expert_linear(X.t, W, Y.t, off, tokens=tok, bias=bias, act=act, Z=Z.t if Z else None)
+    dY = placed(rng, R, n, dtype, ints(g, R, n, hi=1).to(dtype))
+    Zb = placed(rng, R, n, dtype, ints(g, R, n).to(dtype))
+    dX = optional(rng, lambda: placed(rng, R, k, dtype))
+    dW = optional(rng, lambda: placed_weight(rng, None, E, k, n, out))
+    db = optional(rng, lambda: torch.full((E, n), 9.0, dtype=out, device="cuda"))
+    ws = space(pg.expert_linear_backward_workspace(R, n, k, E, dtype, act))
+    pg.expert_linear_backward(dY.t, X.t, W, off, tokens=tok, Z=Zb.t if act == "relu" else None,
+                              act=act, dX=dX.t if dX else None, dW=dW, dbias=db, ws=ws)
+    x, w, d = X.t.double().cpu(), W.double().cpu(), dY.t.double().cpu()
+    if act == "relu":
+        d = d * (Zb.t.double().cpu() > 0)
+    for e in range(E):
+        r = slice(o[e], o[e + 1])
+        z = x[src[r]] @ w[e] + (0 if bias is None else bias[e].double().cpu())
+        assert torch.equal(Y.t[r].cpu(), (z.clamp(min=0) if act == "relu" else z).to(out))
+        if Z:
+            assert torch.equal(Z.t[r].cpu(), z.to(dtype))
+        if dX:
+            assert torch.equal(dX.t[r].cpu(), (d[r] @ w[e].t()).to(dtype))
+        if dW is not None:
+            assert torch.equal(dW[e].cpu(), (x[src[r]].t() @ d[r]).to(out))
+        if db is not None:
+            assert torch.equal(db[e].cpu(), d[r].sum(0).to(out))
+    if o[0] == 0:
+        for t in (Y, Z, dX):
+            if t:
+                t.check(rows=last)
+
+
+@pytest.mark.parametrize("seed", range(40))
+def test_random_combine_calls(seed):
+    """Rows at random strides, slots that are used once, twice (forwards), or not."""
+    rng, g = random.Random(2000 + seed), gen(2000 + seed)
+    dtype, m, n, top = rng.choice(TYPES), spread(rng, 300), spread(rng, 3000), rng.randint(1, 8)
+    rows = m * top + rng.randint(0, 9)
+    Y = placed(rng, rows, n, dtype, ints(g, rows, n).to(dtype))
+    slots = torch.randint(-2, rows + 2, (m, top), generator=g, dtype=torch.int32)
+    w = optional(rng, lambda: ints(g, m, top))
+    R = optional(rng, lambda: placed(rng, m, n, dtype, ints(g, m, n).to(dtype)))
+    out = R if R is not None and rng.random() < 0.5 else placed(rng, m, n, dtype)
+    want = 0 if R is None else R.t.double().cpu()
+    pg.combine(Y.t, slots.cuda(), out.t, weights=None if w is None else w.cuda(),
+               residual=R.t if R else None)
+    live = (slots >= 0) & (slots < rows)
+    f = live.double() * (1 if w is None else w.double())
+    y = Y.t.double().cpu()[slots.long().clamp(0, rows - 1)]
+    assert torch.equal(out.t.cpu(), ((y * f[:, :, None]).sum(1) + want).to(dtype))
+    out.check("out")
+    once = torch.full((m * top,), -1, dtype=torch.int32)
+    used = torch.rand(m * top, generator=g) < 0.8
+    once[used] = torch.randperm(rows, generator=g)[:int(used.sum())].int()
+    once = once.view(m, top)
+    dout = placed(rng, m, n, dtype, ints(g, m, n, hi=1).to(dtype))
+    dY = optional(rng, lambda: placed(rng, rows, n, dtype))
+    dw = optional(rng, lambda: torch.full((m, top), 9.0, device="cuda"))
+    pg.combine_backward(dout.t, Y.t, once.cuda(), None if w is None else w.cuda(),
+                        dY=dY.t if dY else None, dweights=dw)
+    d, live = dout.t.double().cpu(), once >= 0
+    if dY:
+        f = torch.ones(m, top).double() if w is None else w.double()
+        got = dY.t.cpu()[once.long().clamp(min=0)]
+        assert torch.equal(got[live], (d[:, None] * f[:, :, None]).to(dtype)[live])
+        rest = torch.ones(rows, dtype=torch.bool)
+        rest[once[live].long()] = False
+        assert dY.t.cpu()[rest].isnan().all()
+        dY.check("dY")
+    if dw is not None:
+        y = Y.t.double().cpu()[once.long().clamp(min=0)]
+        assert torch.equal(dw.double().cpu(), (d[:, None] * y).sum(2) * live)
