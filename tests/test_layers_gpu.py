@@ -1363,3 +1363,28 @@ def test_random_combine_calls(seed):
     if dw is not None:
         y = Y.t.double().cpu()[once.long().clamp(min=0)]
         assert torch.equal(dw.double().cpu(), (d[:, None] * y).sum(2) * live)
+
+
+@pytest.mark.parametrize("seed", range(60))
+def test_random_route_calls(seed):
+    """Random numbers of experts, groups and choices; logits that are close, far
+    apart, equal or masked; biases of all sizes."""
+    rng, g = random.Random(3000 + seed), gen(3000 + seed)
+    dtype, score = rng.choice(TYPES), rng.choice(("softmax", "sigmoid"))
+    groups = rng.choice((1, 1, 1, 2, 3, 5, 8, 13, 40, 64))
+    E = groups * spread(rng, 1024 // groups)
+    top_groups = rng.randint(1, groups)
+    top = rng.randint(1, min(32, E // groups * top_groups))
+    m = spread(rng, 150) if E < 100 else spread(rng, 20)
+    l = torch.randn(m, E, generator=g) * rng.choice((0.01, 1, 1, 3, 10, 100))
+    if rng.random() < 0.4:                        # equal logits
+        l = (l * 2).round() / 2
+    l = l.to(dtype)
+    if rng.random() < 0.5:
+        l[torch.rand(m, E, generator=g) < rng.choice((0.1, 0.9))] = rng.choice((-math.inf, LOWEST[dtype]))
+    wide = torch.zeros(m, E + 3, dtype=dtype, device="cuda")
+    wide[:, 1:E + 1] = l.cuda()
+    bias = optional(rng, lambda: torch.randn(E, generator=g) * rng.choice((1e-6, 0.1, 1, 1e3)))
+    kw = dict(score=score, groups=groups, top_groups=top_groups, renorm=rng.random() < 0.5,
+              scale=rng.choice((1.0, 2.5)))
+    check_route(wide[:, 1:E + 1], top, bias=None if bias is None else bias.cuda(), **kw)
