@@ -35,23 +35,33 @@ CFLAGS = [
 ]
 
 
-def source_digest(extra_flags=()) -> str:
-    """sha256 (first 16 hex digits) of what determines the built matrix-multiply
-    kernels: the compiler flags and the bytes of every file under csrc/ and of
-    pgemm.h (the layer operators are compiled apart, from layers/).  Unlike a hash of libpgemm.so it does not depend on the directory
-    the library is built in (hipcc derives per-file symbols from the path)."""
+def _digest(folder: str, header: str, extra_flags) -> str:
     import hashlib
     h = hashlib.sha256()
     h.update(" ".join([ARCH, *[f for f in CFLAGS if not f.startswith("-I")],
                        *extra_flags]).encode())
-    files = sorted(os.path.join(CSRC, f) for f in os.listdir(CSRC))
-    files.append(os.path.join(INCLUDE, "pgemm.h"))
+    files = sorted(os.path.join(folder, f) for f in os.listdir(folder))
+    files.append(os.path.join(INCLUDE, header))
     for path in files:
         h.update(os.path.basename(path).encode() + b"\0")
         with open(path, "rb") as f:
             h.update(f.read())
         h.update(b"\0")
     return h.hexdigest()[:16]
+
+
+def source_digest(extra_flags=()) -> str:
+    """sha256 (first 16 hex digits) of what determines the built matrix-multiply
+    kernels: the compiler flags and the bytes of every file under csrc/ and of
+    pgemm.h (the layer operators are compiled apart, from layers/).  Unlike a
+    hash of libpgemm.so it does not depend on the directory the library is built
+    in (hipcc derives per-file symbols from the path)."""
+    return _digest(CSRC, "pgemm.h", extra_flags)
+
+
+def layer_digest(extra_flags=()) -> str:
+    """The same of the layer operators: layers/ and pgemm_layers.h."""
+    return _digest(LAYERS, "pgemm_layers.h", extra_flags)
 
 
 def _compile(src: str, extra) -> str:
