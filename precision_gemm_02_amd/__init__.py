@@ -346,3 +346,11 @@ from .layer_ops import (  # noqa: E402,F401
     expert_linear_backward_workspace, linear, linear_backward, linear_backward_workspace,
     linear_workspace, route, route_backward, route_workspace)
 LAYER_EXPORTS = _layer_ops.EXPORTS
+
+# The block operators (include/pgemm_blocks.h)
+from . import block_ops as _block_ops  # noqa: E402
+
+_block_ops._bind(_lib, _check)
+from .block_ops import (  # noqa: E402,F401
+    layer_norm, layer_norm_backward, layer_norm_backward_workspace)
+BLOCK_EXPORTS = _block_ops.EXPORTS

@@ -1,4 +1,4 @@
-"""Build libpgemm.so from csrc/ and layers/ with hipcc for gfx950.
+"""Build libpgemm.so from csrc/, layers/ and blocks/ with hipcc for gfx950.
 
 Each .hip file is compiled to an object in parallel, then linked into one
 shared library next to this file.  Usage: ``python precision_gemm_02_amd/build.py``
@@ -19,9 +19,11 @@ INCLUDE = os.path.join(os.path.dirname(HERE), "include")
 BUILD_DIR = os.path.join(HERE, "_build")
 LIB_PATH = os.path.join(HERE, "libpgemm.so")
 LAYERS = os.path.join(HERE, "layers")
+BLOCKS = os.path.join(HERE, "blocks")
 SOURCES = [os.path.join(CSRC, f) for f in ("api.hip", "sgemm.hip", "dgemm.hip")] + [
     os.path.join(LAYERS, f)
-    for f in ("layers_api.hip", "prod_f32.hip", "prod_f16.hip", "prod_bf16.hip")]
+    for f in ("layers_api.hip", "prod_f32.hip", "prod_f16.hip", "prod_bf16.hip")] + [
+    os.path.join(BLOCKS, f) for f in ("blocks_api.hip", "norm.hip")]
 ARCH = "gfx950"
 
 HIPCC = os.environ.get("HIPCC", shutil.which("hipcc") or "/opt/rocm/bin/hipcc")
