@@ -48,6 +48,58 @@ int pgemm_layer_norm_backward(int dtype, int out_dtype, int m, int n, pgemm_rows
                               void *workspace, size_t workspace_bytes, void *stream);
 size_t pgemm_layer_norm_backward_workspace(int m, int n);
 
+/* 8-bit floating point: e4m3 without infinities (largest 448), e5m2 (largest 57344). */
+enum { PGEMM_E4M3 = 0, PGEMM_E5M2 = 1 };
+/* Scales of the blocks of 128 columns: of block b of row i (rows == 1) or of rows
+ * 128 i .. 128 i + 127 (rows == 128) at data[i * row_stride + b * block_stride]. */
+typedef struct {
+  float *data;
+  long long row_stride, block_stride;
+  int rows;
+} pgemm_scales;
+
+/*
+ * Blocks of 128 columns to 8 bits: with F the type's largest number,
+ *   scale = max(the block's largest |x| / F, 2^-126),  Q = x / scale, rounded to
+ *   nearest even,
+ * so that Q * scale stands for x.  A block that holds an infinity or a NaN gets NaN
+ * for its scale and its values.  The last block of a row may have fewer columns.
+ *   arguments: 1 dtype (of X), 2 type (of Q), 3 r, 4 c, 5 X (r x c, in either
+ *   order: PGEMM_KN with rows contiguous, PGEMM_NK with columns), 6 Q (r x c, rows of
+ *   ld bytes), 7 scales (written; strides that do not overlap), 8 stream.
+ * r == 0 or c == 0: nothing is touched.
+ */
+int pgemm_quantize(int dtype, int type, int r, int c, pgemm_weight X, pgemm_rows Q,
+                   pgemm_scales scales, void *stream);
+
+/*
+ * Product of 8-bit operands with a scale for each block of 128 of the summed index:
+ *   Z = sum over blocks B of x_scale[i, B] w_scale[j, B] (sum over k in B of
+ *       X[i, k] W[j, k]) + bias,  Y(m x n) = act(Z) + residual.
+ *   arguments: 1 kind, 2 m, 3 n, 4 k, 5 X (m x k, rows of ld bytes), 6 x_scales
+ *   (rows 1), 7 W (n x k, rows of ld bytes: a weight kept as n x k), 8 w_scales
+ *   (rows 1 or 128), 9 bias (n, or NULL), 10 residual (data NULL: none), 11 Z (data
+ *   NULL: not kept), 12 Y, 13 workspace (or NULL), 14 workspace_bytes, 15 stream.
+ * bias, residual, Z and Y have kind.out_dtype.  The products are exact, the sums of
+ * blocks and their scaling fp32; a product of two scales should be a normal fp32
+ * number.  For fp32 results the sums within a block are fp32 too; for 16-bit results
+ * the matrix cores' 8-bit instructions form them, which add eight products at a
+ * time, each cut off 13 bits below the largest (far below a 16-bit rounding).
+ * Scales are read only and may have strides of 0.  m == 0 or n == 0: nothing is
+ * touched; k == 0: Z is the bias.  With a workspace of pgemm_linear_fp8_workspace
+ * bytes the summed index may be shared by several workgroups; NULL or a smaller one
+ * never changes more than the order of the sums.
+ */
+typedef struct {
+  int x_type, w_type;     /* PGEMM_E4M3 or PGEMM_E5M2 */
+  int out_dtype, act;
+} pgemm_fp8_kind;
+int pgemm_linear_fp8(pgemm_fp8_kind kind, int m, int n, int k, pgemm_rows X, pgemm_scales x_scales,
+                     pgemm_rows W, pgemm_scales w_scales, const void *bias, pgemm_rows residual,
+                     pgemm_rows Z, pgemm_rows Y, void *workspace, size_t workspace_bytes,
+                     void *stream);
+size_t pgemm_linear_fp8_workspace(int m, int n, int k);
+
 /*
  * For bindings: a call with all its arguments in one struct, in the order and
  * types of the function's parameters (each at its natural alignment, the
@@ -55,7 +107,9 @@ size_t pgemm_layer_norm_backward_workspace(int m, int n);
  */
 enum {
   PGEMM_OP_LAYER_NORM = 0,
-  PGEMM_OP_LAYER_NORM_BACKWARD = 1
+  PGEMM_OP_LAYER_NORM_BACKWARD = 1,
+  PGEMM_OP_QUANTIZE = 2,
+  PGEMM_OP_LINEAR_FP8 = 3
 };
 int pgemm_block_call(int op, const void *args);
 

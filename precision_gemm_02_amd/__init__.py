@@ -352,5 +352,6 @@ from . import block_ops as _block_ops  # noqa: E402
 
 _block_ops._bind(_lib, _check)
 from .block_ops import (  # noqa: E402,F401
-    layer_norm, layer_norm_backward, layer_norm_backward_workspace)
+    layer_norm, layer_norm_backward, layer_norm_backward_workspace, linear_fp8,
+    linear_fp8_workspace, quantize)
 BLOCK_EXPORTS = _block_ops.EXPORTS

@@ -1,4 +1,5 @@
-"""Operators of a feed-forward block on GPU tensors: layer norm with its gradients.
+"""Operators of a feed-forward block on GPU tensors: layer norm with its gradients, and
+products of 8-bit operands with their quantization.
 
 Thin ctypes binding over the entry points of ``include/pgemm_blocks.h``, with the
 conventions of ``layer_ops``: tensors on the current device with contiguous
@@ -13,23 +14,39 @@ import ctypes
 
 import torch
 
-from .layer_ops import (_DTYPES, _ROWS, _device, _dtype, _flat, _grad_type, _Rows, _rows, _shape2,
-                        _space, _stream, _struct)
+from .layer_ops import (_DTYPES, _ROWS, _WEIGHT, _act, _device, _dtype, _flat, _grad_type, _Rows,
+                        _rows, _shape2, _space, _stream, _struct, _Weight, _weight, _wrong)
 
 # every entry point include/pgemm_blocks.h declares
 EXPORTS = ("pgemm_layer_norm", "pgemm_layer_norm_backward", "pgemm_layer_norm_backward_workspace",
-           "pgemm_block_call")
+           "pgemm_quantize", "pgemm_linear_fp8", "pgemm_linear_fp8_workspace", "pgemm_block_call")
+
+_FP8 = {torch.float8_e4m3fn: 0, torch.float8_e5m2: 1}
+_BLOCK = 128            # columns (and rows) of a block with one scale
+
+
+class _Scales(ctypes.Structure):
+    _fields_ = [("data", ctypes.c_void_p), ("row_stride", ctypes.c_longlong),
+                ("block_stride", ctypes.c_longlong), ("rows", ctypes.c_int)]
+
+
+class _Fp8Kind(ctypes.Structure):
+    _fields_ = [("x_type", ctypes.c_int), ("w_type", ctypes.c_int), ("out_dtype", ctypes.c_int),
+                ("act", ctypes.c_int)]
 
 _lib = None
 _check = None
 _call = None            # pgemm_block_call
 
 # The arguments of pgemm_block_call, by op (see layer_ops)
+_SCALES = "Pqqi0q"
 _PACK = (
     _struct("3i", "0q", _ROWS, "PPf", "0q", "PP", _ROWS, "P"),
     _struct("4i", _ROWS, _ROWS, "PPP", _ROWS, _ROWS, "PPPNP"),
+    _struct("4i", _WEIGHT, _ROWS, _SCALES, "P"),
+    _struct("7i", "0q", _ROWS, _SCALES, _ROWS, _SCALES, "P", _ROWS, _ROWS, _ROWS, "PNP"),
 )
-_LAYER_NORM, _LAYER_NORM_BACKWARD = range(2)
+_LAYER_NORM, _LAYER_NORM_BACKWARD, _QUANTIZE, _LINEAR_FP8 = range(4)
 
 
 def _bind(lib, check):
@@ -44,6 +61,10 @@ def _bind(lib, check):
         "pgemm_layer_norm": [i, i, i, _Rows, p, p, f, p, p, _Rows, p],
         "pgemm_layer_norm_backward": [i, i, i, i, _Rows, _Rows, p, p, p, _Rows, _Rows, p, p, p, z, p],
         "pgemm_layer_norm_backward_workspace": [i, i],
+        "pgemm_quantize": [i, i, i, i, _Weight, _Rows, _Scales, p],
+        "pgemm_linear_fp8": [_Fp8Kind, i, i, i, _Rows, _Scales, _Rows, _Scales, p, _Rows, _Rows, _Rows,
+                             p, z, p],
+        "pgemm_linear_fp8_workspace": [i, i, i],
     }
     for name, args in types.items():
         fn = getattr(lib, name)
@@ -106,3 +127,100 @@ def layer_norm_backward(dY, X, mean, rstd, *, weight=None, residual=None, dX=Non
 def layer_norm_backward_workspace(m, n) -> int:
     """Workspace bytes ``layer_norm_backward`` needs for dweight or dbias."""
     return _lib.pgemm_layer_norm_backward_workspace(m, n)
+
+
+# ---- 8-bit products ----------------------------------------------------------------
+
+def _fp8(t, name):
+    code = _FP8.get(t.dtype)
+    if code is None:
+        raise TypeError("%s is %s, expected float8_e4m3fn or float8_e5m2" % (name, t.dtype))
+    return code
+
+
+def _scales(t, name, rows, cols, device, written=False, by_row=False):
+    """(address, row stride, block stride, rows per scale) of the scales of a (rows,
+    cols) matrix: one for 128 columns of each row, or of 128 rows together."""
+    blocks = -(-cols // _BLOCK)
+    high = -(-rows // _BLOCK)
+    if t.dtype is not torch.float32 or t.get_device() != device:
+        _wrong(t, name, torch.float32, t.shape, device)
+    if t.shape == (rows, blocks):
+        by, n = 1, rows
+    elif not by_row and t.shape == (high, blocks):
+        by, n = _BLOCK, high
+    else:
+        raise ValueError("%s is %s, expected %s%s" % (name, tuple(t.shape), (rows, blocks),
+                                                      "" if by_row else " or %s" % ((high, blocks),)))
+    s0, s1 = t.stride()
+    if n <= 1:
+        s0 = blocks
+    if blocks <= 1:
+        s1 = 1
+    if written and n * blocks > 0 and not (
+            (n == 1 or s0 > 0) and (blocks == 1 or s1 > 0) and
+            (n == 1 or blocks == 1 or s0 >= blocks * s1 or s1 >= n * s0)):
+        raise ValueError("%s overlaps itself (strides %s)" % (name, t.stride()))
+    return t.data_ptr(), s0, s1, by
+
+
+def quantize(X, Q, scales, *, stream=None):
+    """Q <- X / scale in 8 bits, scales <- a scale for each block of 128 columns;
+    returns Q.
+
+    X (r, c) has contiguous rows or contiguous columns (a transposed view), Q (r, c)
+    float8_e4m3fn or float8_e5m2 contiguous rows.  scales, float32, is (r, c / 128)
+    for a scale of each row's block or (r / 128, c / 128) for one of 128 rows
+    together, sizes rounded up, with any strides.  The largest magnitude of a
+    block becomes the type's largest number; Q * scale stands for X.  A block
+    that holds an infinity or a NaN becomes NaN."""
+    dev = _device(X, "X")
+    r, c = _shape2(X, "X")
+    _shape2(scales, "scales")
+    code, q = _dtype(X, "X"), _fp8(Q, "Q")
+    st = _call(_QUANTIZE, _PACK[_QUANTIZE](
+        code, q, r, c, *_weight(X, "X", None, r, c, X.dtype, dev),
+        *_rows(Q, "Q", r, c, Q.dtype, dev), *_scales(scales, "scales", r, c, dev, written=True),
+        _stream(stream, dev)))
+    if st != 0:
+        _check(st, "quantize")
+    return Q
+
+
+def linear_fp8(X, x_scales, W, w_scales, Y, *, bias=None, act="none", residual=None, Z=None, ws=None,
+               stream=None):
+    """Y <- act(X @ W + bias) + residual for 8-bit X and W with scales, in place;
+    returns Y.
+
+    X (m, k) has contiguous rows; W (k, n) contiguous columns: the transposed view
+    of a weight kept as n x k.  Each is float8_e4m3fn or float8_e5m2.  x_scales
+    (m, k / 128) and w_scales (k / 128, n) or (k / 128, n / 128), sizes rounded up,
+    are float32 with any strides: ``quantize`` of the n x k weight gives W and
+    w_scales transposed.  Y, residual, Z (m, n) and bias (n,) have one dtype; Z, if
+    given, receives X @ W + bias.  ``ws`` (``linear_fp8_workspace`` bytes) lets
+    several workgroups share a long k."""
+    dev = _device(X, "X")
+    m, k = _shape2(X, "X")
+    n = _shape2(Y, "Y")[1]
+    T = Y.dtype
+    x, w, out = _fp8(X, "X"), _fp8(W, "W"), _dtype(Y, "Y")
+    _shape2(W, "W")
+    _shape2(x_scales, "x_scales")
+    _shape2(w_scales, "w_scales")
+    if W.shape != (k, n):
+        _wrong(W, "W", W.dtype, (k, n), dev)
+    st = _call(_LINEAR_FP8, _PACK[_LINEAR_FP8](
+        x, w, out, _act(act), m, n, k, *_rows(X, "X", m, k, X.dtype, dev),
+        *_scales(x_scales, "x_scales", m, k, dev, by_row=True),
+        *_rows(W.t(), "W's columns", n, k, W.dtype, dev),
+        *_scales(w_scales.t(), "w_scales transposed", n, k, dev), _flat(bias, "bias", (n,), T, dev),
+        *_rows(residual, "residual", m, n, T, dev), *_rows(Z, "Z", m, n, T, dev),
+        *_rows(Y, "Y", m, n, T, dev), *_space(ws, dev), _stream(stream, dev)))
+    if st != 0:
+        _check(st, "linear_fp8")
+    return Y
+
+
+def linear_fp8_workspace(m, n, k) -> int:
+    """Workspace bytes ``linear_fp8`` can use for this shape (0: none)."""
+    return _lib.pgemm_linear_fp8_workspace(m, n, k)

@@ -3,7 +3,9 @@
 
 #include <hip/hip_runtime.h>
 
+#include "fp8.hpp"
 #include "norm.hpp"
+#include "quantize.hpp"
 
 namespace pgemm {
 namespace blocks {
@@ -17,6 +19,17 @@ struct NormOps {
   hipError_t (*norm_columns)(const NormColumnArgs& a, hipStream_t s);
 };
 const NormOps& norm_ops(int dtype);
+
+// X of `dtype`, to 8 bits of `type` (Fp8); outer: X's columns are contiguous.
+hipError_t quantize_op(const QuantizeArgs& a, int dtype, int type, bool outer, hipStream_t s);
+
+// The product of a plan (and the sum of its splits), A of the type named, W of w_type,
+// for results of 16 bits and (wide) of 32, which have no tiles of 256 x 256.
+typedef hipError_t (*Prod8)(const Prod8Args& a, int w_type, int kernel, bool direct, hipStream_t s);
+hipError_t prod8_e4m3(const Prod8Args& a, int w_type, int kernel, bool direct, hipStream_t s);
+hipError_t prod8_e5m2(const Prod8Args& a, int w_type, int kernel, bool direct, hipStream_t s);
+hipError_t prod8_e4m3_wide(const Prod8Args& a, int w_type, int kernel, bool direct, hipStream_t s);
+hipError_t prod8_e5m2_wide(const Prod8Args& a, int w_type, int kernel, bool direct, hipStream_t s);
 
 }  // namespace blocks
 }  // namespace pgemm

@@ -97,7 +97,10 @@ inline ClassTime class_time(int kernel, int size) {
   static const ClassTime t32[3] = {{142e12, 6e-6, 1, {0, 0, 0, 0}},
                                    {130e12, 4e-6, 2, {0, 0.93, 0, 0}},
                                    {119e12, 3e-6, 4, {0, 0.8, 0.9, 0.95}}};
-  return (size == 2 ? t16 : t32)[kernel];
+  static const ClassTime t8[3] = {{2.4e15, 10e-6, 1, {0, 0, 0, 0}},
+                                  {1.9e15, 7e-6, 2, {0, 0.7, 0, 0}},
+                                  {1.0e15, 3.5e-6, 4, {0, 0.5, 0.75, 0.9}}};
+  return (size == 2 ? t16 : size == 1 ? t8 : t32)[kernel];
 }
 
 inline double tiles_time(const ClassTime& c, double tiles, double tile_flops) {

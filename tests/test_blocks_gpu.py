@@ -12,7 +12,7 @@ import pytest
 import torch
 
 import precision_gemm_02_amd as pg
-from layer_util import Guarded, half_step, ints
+from layer_util import Guarded, act64, half_step, ints
 
 pytestmark = [pytest.mark.gpu,
               pytest.mark.skipif(not torch.cuda.is_available(), reason="needs a GPU")]
@@ -246,3 +246,267 @@ def test_layer_norm_gradients_against_differences():
     for i in range(0, n, 5):
         assert abs(float(dw[i]) - diff(w, i, lambda t: loss(x, t, b))) < tol
         assert abs(float(db[i]) - diff(b, i, lambda t: loss(x, w, t))) < tol
+
+
+# ---- 8-bit products ------------------------------------------------------------------
+
+E4M3, E5M2 = torch.float8_e4m3fn, torch.float8_e5m2
+F8 = [E4M3, E5M2]
+LARGEST = {E4M3: 448.0, E5M2: 57344.0}
+ids8 = {E4M3: "e4m3", E5M2: "e5m2"}.get
+
+
+class Bytes:
+    """A (rows, cols) 8-bit tensor inside a larger buffer that has to survive."""
+
+    def __init__(self, rows, cols, dtype, pad=0, shift=0, data=None):
+        self.buf = torch.full(((rows + 1) * (cols + pad) + 64 + shift,), 0x5A, dtype=torch.uint8,
+                              device="cuda")
+        self.bytes = self.buf[32 + shift:].as_strided((rows, cols), (cols + pad, 1))
+        self.t = self.bytes.view(dtype)
+        if data is not None:
+            self.bytes.copy_(data.view(torch.uint8))
+        self.inside = torch.zeros_like(self.buf, dtype=torch.bool)
+        self.inside[32 + shift:].as_strided((rows, cols), (cols + pad, 1)).fill_(True)
+
+    def check(self, name=""):
+        assert bool((self.buf[~self.inside] == 0x5A).all()), "%s: written outside" % name
+
+
+def quantize_cpu(x, dtype, rows):
+    """8-bit values and scales of x (fp32, CPU), by loops over the blocks."""
+    r, c = x.shape
+    s = torch.empty(-(-r // rows), -(-c // 128))
+    q = torch.empty(r, c, dtype=torch.uint8)
+    low = torch.tensor(2.0 ** -126)
+    for i in range(s.shape[0]):
+        for b in range(s.shape[1]):
+            v = x[i * rows:(i + 1) * rows, b * 128:(b + 1) * 128]
+            top = v.abs().max()
+            s[i, b] = torch.maximum(top / LARGEST[dtype], low) if bool(v.isfinite().all()) else math.nan
+            q[i * rows:(i + 1) * rows, b * 128:(b + 1) * 128] = (v / s[i, b]).to(dtype).view(torch.uint8)
+    return q, s
+
+
+def same8(got, want, dtype):
+    """Equal bytes, any NaN for a NaN."""
+    a, b = got.cpu().view(torch.uint8), want.view(torch.uint8)
+    nan = want.view(dtype).float().isnan()
+    assert bool((got.cpu().view(dtype).float().isnan() == nan).all())
+    assert torch.equal(a[~nan], b[~nan])
+
+
+def same_or_nan(got, want):
+    got, nan = got.cpu(), want.isnan()
+    same = torch.equal(got.isnan(), nan) and torch.equal(got[~nan], want[~nan])
+    assert same
+
+
+QUANTS = [(1, 1), (1, 128), (3, 129), (16, 17), (128, 128), (129, 257), (200, 1000), (300, 17), (5, 2048)]
+
+
+@pytest.mark.parametrize("dtype", TYPES, ids=ids)
+@pytest.mark.parametrize("q", F8, ids=ids8)
+@pytest.mark.parametrize("shape", QUANTS, ids=str)
+@pytest.mark.parametrize("rows", [1, 128])
+@pytest.mark.parametrize("order,pad", [("rows", 0), ("rows", 3), ("columns", 0), ("columns", 5)])
+def test_quantize(dtype, q, shape, rows, order, pad):
+    r, c = shape
+    g = gen(r * 1009 + c)
+    x = torch.randn(r, c, generator=g) * torch.exp(3 * torch.randn(r, 1, generator=g))
+    x = x.to(dtype)
+    if order == "rows":
+        X = Guarded(r, c, dtype, pad=pad, shift=pad % 2, data=x).t
+    else:
+        X = Guarded(c, r, dtype, pad=pad, shift=pad % 2, data=x.t()).t.t()
+    Q = Bytes(r, c, q, pad=pad, shift=pad)
+    high, blocks = -(-r // rows), -(-c // 128)
+    S = Guarded(blocks, high, F32, pad=pad) if pad else Guarded(high, blocks, F32)
+    scales = S.t.t() if pad else S.t
+    assert pg.quantize(X, Q.t, scales) is Q.t
+    want_q, want_s = quantize_cpu(x.float(), q, rows)
+    same_or_nan(scales, want_s)                   # (in fp16 some rows hold an infinity)
+    same8(Q.bytes, want_q, q)
+    Q.check("Q")
+    S.check("scales")
+
+
+@pytest.mark.parametrize("q", F8, ids=ids8)
+@pytest.mark.parametrize("rows", [1, 128])
+@pytest.mark.parametrize("order", ["rows", "columns"])
+def test_quantize_extremes(q, rows, order):
+    """Blocks of zeros, of the smallest and the largest numbers, with an infinity and
+    with a NaN; ties between two 8-bit numbers."""
+    x = torch.zeros(256, 128 * 7)
+    x[:, 128:256] = 2.0 ** -149 * torch.arange(128)
+    x[:, 256:384] = 3.4e38
+    x[7, 400], x[8, 401], x[200, 402] = math.inf, math.nan, -math.inf
+    x[:, 512:640] = -torch.arange(128) / 8.0
+    x[:, 512] = LARGEST[q]                        # a scale of 1
+    x[:, 640:768] = 1.0 + torch.arange(128) / 256.0
+    x[:, 640] = LARGEST[q]
+    x[:, 768:] = torch.randn(256, 128, generator=gen(2)) * 1e-30
+    X = x.cuda() if order == "rows" else x.t().contiguous().cuda().t()
+    Q = torch.empty(256, x.shape[1], dtype=torch.uint8, device="cuda")
+    S = torch.empty(256 // rows, 7, device="cuda")
+    pg.quantize(X, Q.view(q), S)
+    want_q, want_s = quantize_cpu(x, q, rows)
+    same_or_nan(S, want_s)
+    same8(Q, want_q, q)
+
+
+def eights(g, *shape, dtype, hi=4):
+    """Small whole numbers as 8-bit bytes."""
+    return torch.randint(-hi, hi + 1, shape, generator=g).float().to(dtype)
+
+
+def powers(g, *shape):
+    return torch.exp2(torch.randint(-2, 3, shape, generator=g).float())
+
+
+def spread64(s, rows, cols):
+    """The scale of each element of a (rows, cols) matrix."""
+    s = s.double()
+    if s.shape[0] != rows:
+        s = s.repeat_interleave(128, 0)[:rows]
+    return s.repeat_interleave(128, 1)[:, :cols]
+
+
+# (m, n, k): few-rows kernels, tiles of every class, edges of each, odd k
+PRODUCTS = [(1, 1, 1), (1, 64, 128), (1, 257, 1023), (3, 17, 5), (16, 130, 272), (17, 64, 129),
+            (32, 72, 520), (33, 65, 31), (64, 64, 128), (65, 129, 64), (128, 256, 400), (200, 136, 1),
+            (300, 263, 264), (257, 520, 1040), (70, 1030, 2064)]
+
+
+@pytest.mark.parametrize("types", [(E4M3, E4M3), (E5M2, E4M3), (E4M3, E5M2), (E5M2, E5M2)],
+                         ids=lambda t: ids8(t[0]) + ids8(t[1]))
+@pytest.mark.parametrize("shape", PRODUCTS, ids=str)
+@pytest.mark.parametrize("rows", [1, 128])
+@pytest.mark.parametrize("pad", [0, 5, 16])
+def test_linear_fp8_exact(types, shape, rows, pad):
+    """Whole numbers and scales that are powers of two: exact sums."""
+    m, n, k = shape
+    g = gen(m + n + k)
+    X = Bytes(m, k, types[0], pad=pad, shift=pad % 16, data=eights(g, m, k, dtype=types[0]))
+    W = Bytes(n, k, types[1], pad=pad, shift=pad % 16, data=eights(g, n, k, dtype=types[1]))
+    kb, nb = -(-k // 128), -(-n // rows)
+    sx, sw = powers(g, m, kb).cuda(), powers(g, nb, kb).cuda()
+    if pad:                                       # scales in the other order
+        sx, sw = sx.t().contiguous().t(), sw.t().contiguous().t()
+    bias, R = ints(g, n).cuda(), ints(g, m, n).cuda()
+    Y, Z = Guarded(m, n, F32, pad=pad), Guarded(m, n, F32, pad=pad)
+    assert pg.linear_fp8(X.t, sx, W.t.t(), sw.t(), Y.t, bias=bias, act="relu", residual=R,
+                         Z=Z.t) is Y.t
+    x = X.t.cpu().double() * spread64(sx.cpu(), m, k)
+    w = W.t.cpu().double() * spread64(sw.cpu(), n, k)
+    z = x @ w.t() + bias.double().cpu()
+    same = torch.equal(Z.t.double().cpu(), z)
+    assert same
+    same = torch.equal(Y.t.double().cpu(), z.clamp(min=0) + R.double().cpu())
+    assert same
+    Y.check("Y")
+    Z.check("Z")
+    # 16-bit results are the exact values rounded once; with a workspace the summed
+    # index may be shared
+    ws = space(pg.linear_fp8_workspace(m, n, k))
+    for T in (BF16, F16):
+        y = Guarded(m, n, T, pad=pad)
+        pg.linear_fp8(X.t, sx, W.t.t(), sw.t(), y.t, bias=bias.to(T), ws=ws)
+        assert torch.equal(y.t.cpu(), z.to(T))
+        y.check("Y")
+
+
+@pytest.mark.parametrize("act", ["none", "relu", "gelu", "gelu_tanh", "silu"])
+@pytest.mark.parametrize("out", TYPES, ids=ids)
+@pytest.mark.parametrize("shape", [(7, 300, 700), (150, 270, 1030), (40, 48, 6000)], ids=str)
+@pytest.mark.parametrize("rows", [1, 128])
+def test_linear_fp8_of_quantized(act, out, shape, rows):
+    """Quantized random operands, as a program has them, against 64 bits."""
+    m, n, k = shape
+    g = gen(m * n + k)
+    x, w = torch.randn(m, k, generator=g).cuda(), (torch.randn(n, k, generator=g) * k ** -0.5).cuda()
+    kb, nb = -(-k // 128), -(-n // rows)
+    X, W = (torch.empty(*t.shape, dtype=E4M3, device="cuda") for t in (x, w))
+    sx, sw = torch.empty(m, kb, device="cuda"), torch.empty(nb, kb, device="cuda")
+    pg.quantize(x, X, sx)
+    pg.quantize(w, W, sw)
+    bias, R = (torch.randn(*s, generator=g).to(out).cuda() for s in ((n,), (m, n)))
+    Y, Z = torch.empty(m, n, dtype=out, device="cuda"), torch.empty(m, n, dtype=out, device="cuda")
+    pg.linear_fp8(X, sx, W.t(), sw.t(), Y, bias=bias, act=act, residual=R, Z=Z,
+                  ws=space(pg.linear_fp8_workspace(m, n, k)))
+    xd = X.cpu().double() * spread64(sx.cpu(), m, k)
+    wd = W.cpu().double() * spread64(sw.cpu(), n, k)
+    z = xd @ wd.t() + bias.double().cpu()
+    # 128 products of a block, each block's two scalings, the blocks' sum, the bias
+    e = (128 + kb + 8) * U * (xd.abs() @ wd.abs().t() + bias.double().cpu().abs())
+    if out is not F32:
+        # the 8-bit instructions cut seven of eight neighbouring products off at 2^-13 of
+        # the largest's power of two, or of its double: 7 2^-12 of the largest, at most
+        # the sum of what the largest factors make
+        p = torch.nn.functional.pad(xd.abs(), (0, -k % 8)).view(m, -1, 8)
+        q = torch.nn.functional.pad(wd.abs(), (0, -k % 8)).view(n, -1, 8)
+        e = e + 7 * 2.0 ** -12 * (p.amax(2) @ q.amax(2).t())
+    held(Z, z, e, "Z")
+    y = act64(z, act)
+    # an activation's slope is below 1.13; its own evaluation: see the layer operators'
+    ea = 1.13 * e + (z.abs() + 8) * 2 * U * z.abs() + U
+    held(Y, y + R.double().cpu(), ea + U * (y.abs() + R.double().cpu().abs()), "Y")
+
+
+def test_linear_fp8_scales_of_one_number():
+    """Scales are only read: one number for all of them, through strides of 0."""
+    g = gen(4)
+    X, W = (eights(g, *s, dtype=E4M3).cuda() for s in ((40, 300), (70, 300)))
+    one, half = torch.tensor([[1.0]], device="cuda"), torch.tensor([[0.5]], device="cuda")
+    Y = torch.empty(40, 70, device="cuda")
+    pg.linear_fp8(X, one.expand(40, 3), W.t(), half.expand(3, 70), Y)
+    assert torch.equal(Y.cpu().double(), 0.5 * X.cpu().double() @ W.cpu().double().t())
+
+
+def test_linear_fp8_without_inner_size():
+    X, W = torch.empty(5, 0, device="cuda").to(E4M3), torch.empty(9, 0, device="cuda").to(E4M3)
+    Y, R = torch.full((5, 9), math.nan, device="cuda"), torch.ones(5, 9, device="cuda")
+    bias = torch.arange(9.0, device="cuda") - 4
+    e = lambda *s: torch.empty(*s, device="cuda")
+    pg.linear_fp8(X, e(5, 0), W.t(), e(0, 9), Y, bias=bias, act="relu", residual=R)
+    assert torch.equal(Y, bias.clamp(min=0).expand(5, 9) + 1)
+
+
+def test_linear_fp8_gradients():
+    """The gradients of a product in 8 bits are the same product of operands quantized
+    along the other index: dX = dY W^T, dW = X^T dY."""
+    m, n, k = 150, 270, 520
+    g = gen(9)
+    x, w, d = (torch.randn(*s, generator=g).cuda() for s in ((m, k), (n, k), (m, n)))
+
+    def quantized(t, rows=1, dtype=E4M3):
+        q = torch.empty(*t.shape, dtype=dtype, device="cuda")
+        s = torch.empty(-(-t.shape[0] // rows), -(-t.shape[1] // 128), device="cuda")
+        pg.quantize(t, q, s)
+        return q, s
+
+    def value(q, s):
+        return q.cpu().double() * spread64(s.cpu(), *q.shape)
+
+    # dX(m, k): summed over n; the weight's transpose, in blocks of 128 x 128
+    dq, ds = quantized(d, dtype=E5M2)
+    wq, ws = quantized(w.t(), 128)
+    dX = torch.empty(m, k, device="cuda")
+    pg.linear_fp8(dq, ds, wq.t(), ws.t(), dX)
+    a, b = value(dq, ds), value(wq, ws)
+    held(dX, a @ b.t(), (128 + 3 + 8) * U * (a.abs() @ b.abs().t()), "dX")
+    # the weight's blocks are those of its transpose
+    assert torch.equal(ws, quantized(w, 128)[1].t())
+    # dW(n, k): summed over m
+    dt, dts = quantized(d.t(), dtype=E5M2)
+    xt, xts = quantized(x.t())
+    dW = torch.empty(n, k, device="cuda")
+    pg.linear_fp8(dt, dts, xt.t(), xts.t(), dW)
+    a, b = value(dt, dts), value(xt, xts)
+    held(dW, a @ b.t(), (128 + 2 + 8) * U * (a.abs() @ b.abs().t()), "dW")
+    # and near the products of the numbers themselves: each factor is off by at most
+    # half a step (2^-4, 2^-3 of the type) of itself, or of its block's smallest normal
+    want = d.double().cpu() @ w.double().cpu()
+    off = (dX.double().cpu() - want).abs()
+    assert bool((off <= (2 ** -4 + 2 ** -3 + 2 ** -7 + 0.02) * (d.double().cpu().abs() @
+                                                                w.double().cpu().abs())).all())

@@ -82,6 +82,50 @@ def test_layer_norm_workspace():
             assert b >= 8 * n and b % 256 == 0
 
 
+def S(data=FAKE, row=2, block=1, rows=1):
+    return bo._Scales(data, row, block, rows)
+
+
+QUANT = [2, 0, 200, 130, Wt(FAKE, 130), R(FAKE, 130), S(), None]
+
+
+def test_quantize_argument_codes():
+    refused(L.pgemm_quantize, QUANT,
+            [(1, 4), (2, 2), (3, -1), (3, TOP + 1), (4, -1), (5, Wt(None)), (5, Wt(FAKE, 129)),
+             (5, Wt(FAKE + 1, 130)), (5, Wt(FAKE, 130, 2)), (5, Wt(FAKE, 199, 1)), (6, R(None)),
+             (6, R(FAKE, 129)), (7, S(None)), (7, S(FAKE + 2)), (7, S(rows=64)), (7, S(row=1)),
+             (7, S(row=0)), (7, S(block=0)), (7, S(row=-2)), (7, S(row=1, block=199))])
+    none = R(None)
+    for r, c in ((0, 5), (5, 0)):
+        assert L.pgemm_quantize(2, 0, r, c, Wt(None), none, S(None), None) == 0
+
+
+FP8 = [bo._Fp8Kind(0, 1, 2, 4), 8, 200, 256, R(FAKE, 256), S(), R(FAKE, 256), S(rows=128), FAKE,
+       R(FAKE, 200), R(FAKE, 200), R(FAKE, 200), FAKE, 0, None]
+
+
+def test_linear_fp8_argument_codes():
+    kinds = [bo._Fp8Kind(*x) for x in ((2, 0, 2, 0), (0, -1, 2, 0), (0, 0, 3, 0), (0, 0, 2, 5))]
+    refused(L.pgemm_linear_fp8, FP8,
+            [(1, k) for k in kinds] +
+            [(2, -1), (3, TOP + 1), (4, -1), (5, R(None)), (5, R(FAKE, 255)), (6, S(None)),
+             (6, S(rows=128)), (6, S(row=-1)), (7, R(None)), (7, R(FAKE, 255)), (8, S(None)),
+             (8, S(rows=2)), (8, S(block=-1)), (9, FAKE + 1), (10, R(FAKE, 199)), (11, R(FAKE + 1)),
+             (12, R(None)), (12, R(FAKE, 199)), (13, FAKE + 8)])
+    none = R(None)
+    for m, n in ((0, 64), (8, 0)):
+        assert L.pgemm_linear_fp8(FP8[0], m, n, 64, none, S(None), none, S(None), None, none, none,
+                                  none, None, 0, None) == 0
+
+
+def test_linear_fp8_workspace():
+    assert pg.linear_fp8_workspace(8192, 8192, 4096) == 0
+    assert pg.linear_fp8_workspace(1, 512, 16384) > 0
+    for m in (0, 1, 33, 5000):
+        for n in (0, 1, 300):
+            assert pg.linear_fp8_workspace(m, n, 0) == 0
+
+
 # ---- packed calls ------------------------------------------------------------------
 
 def flat(args):
@@ -102,13 +146,15 @@ def changed(args, pos, value):
 
 
 CALLS = [(L.pgemm_layer_norm, changed(NORM, 10, R(FAKE, 3))),
-         (L.pgemm_layer_norm_backward, changed(NORM_BACK, 15, NEED - 1))]
+         (L.pgemm_layer_norm_backward, changed(NORM_BACK, 15, NEED - 1)),
+         (L.pgemm_quantize, changed(QUANT, 7, S(row=1))), (L.pgemm_linear_fp8, changed(FP8, 13, FAKE + 8))]
 
 
 def test_packed_calls_equal_the_functions():
     """Every argument reaches its place: a bad value gives the same code."""
     bad = {ctypes.c_int: -1, ctypes.c_float: -1.0, lo._Rows: R(FAKE + 1, 64),
-           lo._Weight: Wt(FAKE, 64, 9), lo._Kind: lo._Kind(7, 7, 0), ctypes.c_void_p: FAKE + 1}
+           lo._Weight: Wt(FAKE, 64, 9), lo._Kind: lo._Kind(7, 7, 0), ctypes.c_void_p: FAKE + 1,
+           bo._Scales: S(rows=3), bo._Fp8Kind: bo._Fp8Kind(9, 9, 9, 9)}
     for op, (fn, args) in enumerate(CALLS):
         assert -100 < fn(*args) < 0
         for pos, kind in enumerate(fn.argtypes[:-1]):
@@ -177,3 +223,42 @@ def test_layer_norm_backward_refusals(anywhere, change, error):
     args.update(change)
     with pytest.raises(error):
         pg.layer_norm_backward(**args)
+
+
+def f8(*shape, dtype=torch.float8_e4m3fn):
+    return torch.zeros(*shape, dtype=F32).to(dtype)
+
+
+def f(*shape):
+    return torch.zeros(*shape)
+
+
+@pytest.mark.parametrize("change,error", [
+    (dict(X=z(200, 130, dtype=torch.float64)), TypeError), (dict(X=z(200)), ValueError),
+    (dict(X=z(200, 260)[:, ::2]), ValueError), (dict(X=z(1, 130).expand(200, 130)), ValueError),
+    (dict(Q=z(200, 130)), TypeError), (dict(Q=f8(200, 131)), ValueError),
+    (dict(Q=f8(130, 200).t()), ValueError), (dict(scales=f(200)), ValueError),
+    (dict(scales=f(200, 1)), ValueError), (dict(scales=f(3, 2)), ValueError),
+    (dict(scales=z(200, 2)), TypeError), (dict(scales=f(1, 2).expand(200, 2)), ValueError),
+    (dict(scales=f(200, 1).expand(200, 2)), ValueError)])
+def test_quantize_refusals(anywhere, change, error):
+    args = dict(X=z(200, 130), Q=f8(200, 130), scales=f(200, 2))
+    args.update(change)
+    with pytest.raises(error):
+        pg.quantize(**args)
+
+
+@pytest.mark.parametrize("change,error", [
+    (dict(X=z(8, 130)), TypeError), (dict(X=f8(130, 8).t()), ValueError), (dict(X=f8(8)), ValueError),
+    (dict(W=f8(130, 200)), ValueError), (dict(W=f8(200, 131).t()), ValueError),
+    (dict(W=z(200, 130).t()), TypeError), (dict(x_scales=f(1, 2)), ValueError),
+    (dict(x_scales=f(8, 1)), ValueError), (dict(x_scales=z(8, 2)), TypeError),
+    (dict(w_scales=f(2, 3)), ValueError), (dict(w_scales=f(200, 2)), ValueError),
+    (dict(w_scales=f(2)), ValueError), (dict(Y=f8(8, 200)), TypeError), (dict(Y=z(9, 200)), ValueError),
+    (dict(bias=z(200, dtype=F32)), TypeError), (dict(residual=z(8, 200, dtype=F32)), TypeError),
+    (dict(Z=z(8, 201)), ValueError), (dict(act="tanh"), ValueError)])
+def test_linear_fp8_refusals(anywhere, change, error):
+    args = dict(X=f8(8, 130), x_scales=f(8, 2), W=f8(200, 130).t(), w_scales=f(2, 2), Y=z(8, 200))
+    args.update(change)
+    with pytest.raises(error):
+        pg.linear_fp8(**args)
