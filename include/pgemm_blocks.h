@@ -32,21 +32,67 @@ int pgemm_layer_norm(int dtype, int m, int n, pgemm_rows X, const void *weight, 
  * Its gradients: with h = (X - mean) * rstd and g = dY * weight,
  *   dX = rstd * (g - mean of g - h * mean of g h) + residual,
  *   dweight = the sum over rows of dY * h, dbias = the sum of dY's rows.
- *   arguments: 1 dtype (of dY, X, weight, residual and dX), 2 out_dtype (of dweight
- *   and dbias: dtype or PGEMM_F32), 3 m, 4 n, 5 dY, 6 X, 7 mean, 8 rstd (m, fp32,
- *   as pgemm_layer_norm kept them), 9 weight (or NULL: ones), 10 residual (the
- *   gradient that reaches X past the norm; data NULL: none; may be dX itself),
- *   11 dX (data NULL: not wanted), 12 dweight (or NULL), 13 dbias (or NULL),
- *   14 workspace, 15 workspace_bytes, 16 stream.
+ *   arguments: 1 kind (dtype of dY, X, weight, residual and dX; out_dtype of dweight
+ *   and dbias; act none), 2 m, 3 n, 4 dY, 5 X, 6 mean, 7 rstd (m, fp32, as
+ *   pgemm_layer_norm kept them), 8 weight (or NULL: ones), 9 residual (the gradient
+ *   that reaches X past the norm; data NULL: none; may be dX itself), 10 dX (data
+ *   NULL: not wanted), 11 dweight (or NULL), 12 dbias (or NULL), 13 workspace,
+ *   14 workspace_bytes, 15 stream.
  * m == 0 gives a zero dweight and dbias.  The workspace must have
  * pgemm_layer_norm_backward_workspace bytes where dweight or dbias is wanted
  * (partial sums).
  */
-int pgemm_layer_norm_backward(int dtype, int out_dtype, int m, int n, pgemm_rows dY, pgemm_rows X,
+int pgemm_layer_norm_backward(pgemm_kind kind, int m, int n, pgemm_rows dY, pgemm_rows X,
                               const float *mean, const float *rstd, const void *weight,
                               pgemm_rows residual, pgemm_rows dX, void *dweight, void *dbias,
                               void *workspace, size_t workspace_bytes, void *stream);
 size_t pgemm_layer_norm_backward_workspace(int m, int n);
+
+/* The two weights of a gated product, both in one order and with one ld (their stride
+ * is not used), and what belongs to each. */
+typedef struct {
+  pgemm_weight gate, up;
+} pgemm_gate_weights;
+typedef struct {
+  pgemm_rows gate, up;
+} pgemm_gate_rows;
+typedef struct {
+  void *gate, *up;
+} pgemm_gate_bias;
+
+/*
+ * Y(m x n) = act(Zg) * Zu with Zg = X(m x k) Wg(k x n) + bias g and Zu = X Wu + bias u,
+ * in one kernel.
+ *   arguments: 1 kind, 2 m, 3 n (at most 2^30 - 4096), 4 k, 5 X, 6 W, 7 bias (n each,
+ *   or NULL), 8 Z (data NULL: not kept), 9 Y, 10 workspace (or NULL),
+ *   11 workspace_bytes, 12 stream.
+ * Activation and product see the fp32 sums; Z is those rounded to T.  m == 0 or n ==
+ * 0: nothing is touched; k == 0: Z is the bias.  The workspace is as
+ * pgemm_linear's.
+ */
+int pgemm_gated_linear(pgemm_kind kind, int m, int n, int k, pgemm_rows X, pgemm_gate_weights W,
+                       pgemm_gate_bias bias, pgemm_gate_rows Z, pgemm_rows Y, void *workspace,
+                       size_t workspace_bytes, void *stream);
+size_t pgemm_gated_linear_workspace(int dtype, int m, int n, int k);
+
+/*
+ * Its gradients: with dZg = dY * Zu * act'(Zg) and dZu = dY * act(Zg),
+ *   dX = dZg Wg^T + dZu Wu^T (summed in fp32, rounded once), dW = X^T dZ of each,
+ *   dbias = the sum of dZ's rows of each.
+ *   arguments: 1 kind, 2 m, 3 n (as above), 4 k, 5 dY (T), 6 Z (T, as
+ *   pgemm_gated_linear kept them), 7 X, 8 W, 9 dX (T; data NULL: not wanted), 10 dW
+ *   (out_dtype, each in its own order; data NULL: not wanted), 11 dbias (out_dtype,
+ *   or NULL), 12 workspace, 13 workspace_bytes, 14 stream.
+ * W is read only for dX and X only for dW; m == 0 gives zero dW and dbias.  dZ is
+ * rounded to T before the products, as pgemm_linear_backward's.
+ * The workspace must have pgemm_gated_linear_backward_workspace bytes (it holds dZ
+ * of both, and partial sums).
+ */
+int pgemm_gated_linear_backward(pgemm_kind kind, int m, int n, int k, pgemm_rows dY,
+                                pgemm_gate_rows Z, pgemm_rows X, pgemm_gate_weights W,
+                                pgemm_rows dX, pgemm_gate_weights dW, pgemm_gate_bias dbias,
+                                void *workspace, size_t workspace_bytes, void *stream);
+size_t pgemm_gated_linear_backward_workspace(pgemm_kind kind, int m, int n, int k);
 
 /* 8-bit floating point: e4m3 without infinities (largest 448), e5m2 (largest 57344). */
 enum { PGEMM_E4M3 = 0, PGEMM_E5M2 = 1 };
@@ -109,7 +155,9 @@ enum {
   PGEMM_OP_LAYER_NORM = 0,
   PGEMM_OP_LAYER_NORM_BACKWARD = 1,
   PGEMM_OP_QUANTIZE = 2,
-  PGEMM_OP_LINEAR_FP8 = 3
+  PGEMM_OP_LINEAR_FP8 = 3,
+  PGEMM_OP_GATED_LINEAR = 4,
+  PGEMM_OP_GATED_LINEAR_BACKWARD = 5
 };
 int pgemm_block_call(int op, const void *args);
 

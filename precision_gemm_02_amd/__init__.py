@@ -352,6 +352,7 @@ from . import block_ops as _block_ops  # noqa: E402
 
 _block_ops._bind(_lib, _check)
 from .block_ops import (  # noqa: E402,F401
+    gated_linear, gated_linear_backward, gated_linear_backward_workspace, gated_linear_workspace,
     layer_norm, layer_norm_backward, layer_norm_backward_workspace, linear_fp8,
     linear_fp8_workspace, quantize)
 BLOCK_EXPORTS = _block_ops.EXPORTS

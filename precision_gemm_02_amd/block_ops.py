@@ -1,5 +1,5 @@
-"""Operators of a feed-forward block on GPU tensors: layer norm with its gradients, and
-products of 8-bit operands with their quantization.
+"""Operators of a feed-forward block on GPU tensors: layer norm and gated
+products with their gradients, products of 8-bit operands and their quantization.
 
 Thin ctypes binding over the entry points of ``include/pgemm_blocks.h``, with the
 conventions of ``layer_ops``: tensors on the current device with contiguous
@@ -14,12 +14,14 @@ import ctypes
 
 import torch
 
-from .layer_ops import (_DTYPES, _ROWS, _WEIGHT, _act, _device, _dtype, _flat, _grad_type, _Rows,
-                        _rows, _shape2, _space, _stream, _struct, _Weight, _weight, _wrong)
+from .layer_ops import (_DTYPES, _KIND, _NO_WEIGHT, _ROWS, _WEIGHT, _act, _device, _dtype, _flat,
+                        _grad_type, _Kind, _out, _Rows, _rows, _shape2, _space, _stream, _struct,
+                        _Weight, _weight, _wrong)
 
 # every entry point include/pgemm_blocks.h declares
 EXPORTS = ("pgemm_layer_norm", "pgemm_layer_norm_backward", "pgemm_layer_norm_backward_workspace",
-           "pgemm_quantize", "pgemm_linear_fp8", "pgemm_linear_fp8_workspace", "pgemm_block_call")
+           "pgemm_gated_linear", "pgemm_gated_linear_workspace", "pgemm_gated_linear_backward",
+           "pgemm_gated_linear_backward_workspace", "pgemm_quantize", "pgemm_linear_fp8", "pgemm_linear_fp8_workspace", "pgemm_block_call")
 
 _FP8 = {torch.float8_e4m3fn: 0, torch.float8_e5m2: 1}
 _BLOCK = 128            # columns (and rows) of a block with one scale
@@ -28,6 +30,14 @@ _BLOCK = 128            # columns (and rows) of a block with one scale
 class _Scales(ctypes.Structure):
     _fields_ = [("data", ctypes.c_void_p), ("row_stride", ctypes.c_longlong),
                 ("block_stride", ctypes.c_longlong), ("rows", ctypes.c_int)]
+
+
+def _pair(name, kind):
+    return type(name, (ctypes.Structure,), {"_fields_": [("gate", kind), ("up", kind)]})
+
+
+_GateWeights, _GateRows = _pair("_GateWeights", _Weight), _pair("_GateRows", _Rows)
+_GateBias = _pair("_GateBias", ctypes.c_void_p)
 
 
 class _Fp8Kind(ctypes.Structure):
@@ -42,11 +52,15 @@ _call = None            # pgemm_block_call
 _SCALES = "Pqqi0q"
 _PACK = (
     _struct("3i", "0q", _ROWS, "PPf", "0q", "PP", _ROWS, "P"),
-    _struct("4i", _ROWS, _ROWS, "PPP", _ROWS, _ROWS, "PPPNP"),
+    _struct(_KIND, "2i", "0q", _ROWS, _ROWS, "PPP", _ROWS, _ROWS, "PPPNP"),
     _struct("4i", _WEIGHT, _ROWS, _SCALES, "P"),
     _struct("7i", "0q", _ROWS, _SCALES, _ROWS, _SCALES, "P", _ROWS, _ROWS, _ROWS, "PNP"),
+    _struct(_KIND, "3i", _ROWS, _WEIGHT, _WEIGHT, "PP", _ROWS, _ROWS, _ROWS, "PNP"),
+    _struct(_KIND, "3i", _ROWS, _ROWS, _ROWS, _ROWS, _WEIGHT, _WEIGHT, _ROWS, _WEIGHT, _WEIGHT, "PP",
+            "PNP"),
 )
-_LAYER_NORM, _LAYER_NORM_BACKWARD, _QUANTIZE, _LINEAR_FP8 = range(4)
+(_LAYER_NORM, _LAYER_NORM_BACKWARD, _QUANTIZE, _LINEAR_FP8, _GATED_LINEAR,
+ _GATED_LINEAR_BACKWARD) = range(6)
 
 
 def _bind(lib, check):
@@ -59,8 +73,14 @@ def _bind(lib, check):
     i, f, p, z = ctypes.c_int, ctypes.c_float, ctypes.c_void_p, ctypes.c_size_t
     types = {
         "pgemm_layer_norm": [i, i, i, _Rows, p, p, f, p, p, _Rows, p],
-        "pgemm_layer_norm_backward": [i, i, i, i, _Rows, _Rows, p, p, p, _Rows, _Rows, p, p, p, z, p],
+        "pgemm_layer_norm_backward": [_Kind, i, i, _Rows, _Rows, p, p, p, _Rows, _Rows, p, p, p, z, p],
         "pgemm_layer_norm_backward_workspace": [i, i],
+        "pgemm_gated_linear": [_Kind, i, i, i, _Rows, _GateWeights, _GateBias, _GateRows, _Rows, p, z,
+                               p],
+        "pgemm_gated_linear_workspace": [i, i, i, i],
+        "pgemm_gated_linear_backward": [_Kind, i, i, i, _Rows, _GateRows, _Rows, _GateWeights, _Rows,
+                                        _GateWeights, _GateBias, p, z, p],
+        "pgemm_gated_linear_backward_workspace": [_Kind, i, i, i],
         "pgemm_quantize": [i, i, i, i, _Weight, _Rows, _Scales, p],
         "pgemm_linear_fp8": [_Fp8Kind, i, i, i, _Rows, _Scales, _Rows, _Scales, p, _Rows, _Rows, _Rows,
                              p, z, p],
@@ -115,7 +135,7 @@ def layer_norm_backward(dY, X, mean, rstd, *, weight=None, residual=None, dX=Non
     if mean is None or rstd is None:
         raise ValueError("mean and rstd are needed")
     st = _call(_LAYER_NORM_BACKWARD, _PACK[_LAYER_NORM_BACKWARD](
-        code, _DTYPES[out], m, n, *_rows(dY, "dY", m, n, T, dev), *_rows(X, "X", m, n, T, dev),
+        code, _DTYPES[out], 0, m, n, *_rows(dY, "dY", m, n, T, dev), *_rows(X, "X", m, n, T, dev),
         _flat(mean, "mean", (m,), f32, dev), _flat(rstd, "rstd", (m,), f32, dev),
         _flat(weight, "weight", (n,), T, dev), *_rows(residual, "residual", m, n, T, dev),
         *_rows(dX, "dX", m, n, T, dev), _flat(dweight, "dweight", (n,), out, dev),
@@ -127,6 +147,101 @@ def layer_norm_backward(dY, X, mean, rstd, *, weight=None, residual=None, dX=Non
 def layer_norm_backward_workspace(m, n) -> int:
     """Workspace bytes ``layer_norm_backward`` needs for dweight or dbias."""
     return _lib.pgemm_layer_norm_backward_workspace(m, n)
+
+
+# ---- gated products ----------------------------------------------------------------
+
+def _gate_weights(gate, up, k, n, dtype, device):
+    """Both weights' members: in one order and with one stride."""
+    g = _weight(gate, "W_gate", None, k, n, dtype, device)
+    u = _weight(up, "W_up", None, k, n, dtype, device)
+    if g[1:3] != u[1:3] and k > 0 and n > 0:
+        raise ValueError("W_gate with strides %s and W_up with strides %s must have the same"
+                         % (gate.stride(), up.stride()))
+    return g + u
+
+
+def gated_linear(X, W_gate, W_up, Y, *, bias_gate=None, bias_up=None, act="silu", Z_gate=None,
+                 Z_up=None, ws=None, stream=None):
+    """Y <- act(X @ W_gate + bias_gate) * (X @ W_up + bias_up), in place; returns Y.
+
+    X (m, k), the weights (k, n) in either order but both with the same strides, the
+    biases (n,) and Z (m, n) have one dtype; Y (m, n) has that dtype or float32.
+    Z_gate and Z_up, if given, receive X @ W + bias of each for
+    ``gated_linear_backward``.  ``ws`` (``gated_linear_workspace`` bytes) lets few
+    rows share a long k over more workgroups."""
+    dev = _device(X, "X")
+    m, k = _shape2(X, "X")
+    n = _shape2(Y, "Y")[1]
+    T = X.dtype
+    if W_gate is None or W_up is None:
+        raise ValueError("both weights are needed")
+    st = _call(_GATED_LINEAR, _PACK[_GATED_LINEAR](
+        _dtype(X, "X"), _out(Y, "Y", T), _act(act), m, n, k, *_rows(X, "X", m, k, T, dev),
+        *_gate_weights(W_gate, W_up, k, n, T, dev), _flat(bias_gate, "bias_gate", (n,), T, dev),
+        _flat(bias_up, "bias_up", (n,), T, dev), *_rows(Z_gate, "Z_gate", m, n, T, dev),
+        *_rows(Z_up, "Z_up", m, n, T, dev), *_rows(Y, "Y", m, n, Y.dtype, dev), *_space(ws, dev),
+        _stream(stream, dev)))
+    if st != 0:
+        _check(st, "gated_linear")
+    return Y
+
+
+def gated_linear_workspace(m, n, k, dtype) -> int:
+    """Workspace bytes ``gated_linear`` can use for this shape (0: none)."""
+    return _lib.pgemm_gated_linear_workspace(_DTYPES[dtype], m, n, k)
+
+
+def gated_linear_backward(dY, X, W_gate, W_up, Z_gate, Z_up, *, act="silu", dX=None, dW_gate=None,
+                          dW_up=None, dbias_gate=None, dbias_up=None, ws=None, stream=None):
+    """Gradients of ``gated_linear``: with dZ_gate = dY * Z_up * act'(Z_gate) and dZ_up
+    = dY * act(Z_gate), dX <- dZ_gate @ W_gate^T + dZ_up @ W_up^T, dW <- X^T @ dZ and
+    dbias <- the sum of dZ's rows of each; those given are written.
+
+    Z_gate and Z_up are what ``gated_linear`` kept.  dX has the inputs' dtype; the
+    dW (each in either order) and dbias have one dtype, the inputs' or float32.  The
+    weights may be None without dX, X without a dW.  ``ws`` has
+    ``gated_linear_backward_workspace`` bytes."""
+    dev = _device(dY, "dY")
+    m, n = _shape2(dY, "dY")
+    some = dX if dX is not None else X
+    if some is not None:
+        k = _shape2(some, "dX" if dX is not None else "X")[1]
+    else:
+        k = next((w.shape[0] for w in (dW_gate, dW_up, W_gate, W_up) if w is not None), 0)
+    T = dY.dtype
+    given = [t for t in (dW_gate, dW_up, dbias_gate, dbias_up) if t is not None]
+    out = given[0].dtype if given else T
+    code = _dtype(dY, "dY")
+    if any(t.dtype is not out for t in given) or (out is not T and out is not torch.float32):
+        raise TypeError("dW and dbias are %s, expected all %s or all float32"
+                        % (", ".join(str(t.dtype) for t in given), T))
+    if Z_gate is None or Z_up is None:
+        raise ValueError("Z_gate and Z_up are needed")
+    if W_gate is None or W_up is None:
+        if dX is not None:
+            raise ValueError("dX needs both weights")
+        W = _NO_WEIGHT + _NO_WEIGHT
+    else:
+        W = _gate_weights(W_gate, W_up, k, n, T, dev)
+    if X is None and (dW_gate is not None or dW_up is not None):
+        raise ValueError("a dW needs X")
+    st = _call(_GATED_LINEAR_BACKWARD, _PACK[_GATED_LINEAR_BACKWARD](
+        code, _DTYPES[out], _act(act), m, n, k, *_rows(dY, "dY", m, n, T, dev),
+        *_rows(Z_gate, "Z_gate", m, n, T, dev), *_rows(Z_up, "Z_up", m, n, T, dev),
+        *_rows(X, "X", m, k, T, dev), *W, *_rows(dX, "dX", m, k, T, dev),
+        *_weight(dW_gate, "dW_gate", None, k, n, out, dev),
+        *_weight(dW_up, "dW_up", None, k, n, out, dev),
+        _flat(dbias_gate, "dbias_gate", (n,), out, dev), _flat(dbias_up, "dbias_up", (n,), out, dev),
+        *_space(ws, dev), _stream(stream, dev)))
+    if st != 0:
+        _check(st, "gated_linear_backward")
+
+
+def gated_linear_backward_workspace(m, n, k, dtype) -> int:
+    """Workspace bytes ``gated_linear_backward`` needs."""
+    d = _DTYPES[dtype]
+    return _lib.pgemm_gated_linear_backward_workspace(_Kind(d, d, 0), m, n, k)
 
 
 # ---- 8-bit products ----------------------------------------------------------------

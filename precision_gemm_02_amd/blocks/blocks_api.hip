@@ -35,6 +35,99 @@ bool scales_ok(const pgemm_scales& s, bool need) {
   return vector_ok(s.data, 4, need) && s.row_stride >= 0 && s.block_stride >= 0;
 }
 
+// ---- gated products ------------------------------------------------------------
+
+constexpr int kMaxGated = (1 << 30) - 4096;      // columns: both weights' together fit
+
+bool gate_weights_ok(const pgemm_gate_weights& w, int k, int n, int size, bool need) {
+  if (!weight_ok(w.gate, k, n, size, need, 1) || !weight_ok(w.up, k, n, size, need, 1)) return false;
+  return !need || (w.gate.order == w.up.order && w.gate.ld == w.up.ld);
+}
+
+// Columns of each weight that a workgroup takes.
+int gate_columns(int kernel) {
+  if (kernel >= kFew16) return kernel >= kFew16Wide ? 32 : 16;
+  return kShape[kernel].bn / 2;
+}
+
+// The plan of a gated product: a product with 2 n columns, but for the columns of the
+// few-rows kernels.  Workspace as in plan_product.
+Plan gate_plan(int size, int m, int n, int k, int loading, size_t ws_bytes, bool any_ws) {
+  if (m > 32) return plan_product(size, kInner, kDense, m, 1, 2 * n, k, loading, ws_bytes, any_ws, true,
+                                  false);
+  Plan p;
+  p.loading = loading;
+  const bool wide = ceil_div(n, 32) >= 2 * kUnits;
+  p.kernel = wide ? (m <= 16 ? kFew16Wide : kFew32Wide) : (m <= 16 ? kFew16 : kFew32);
+  const int bk = 128 / size;
+  const long long groups = ceil_div(n, gate_columns(p.kernel));
+  // one split per free compute unit, each of 16 units of 128 bytes at least
+  long long s = kUnits / groups;
+  if (s > k / (16 * bk)) s = k / (16 * bk);
+  if (s > 64) s = 64;
+  if (s > 1) {
+    p.k_split = (int)round_up(ceil_div(k, s), bk);
+    p.splits = (int)ceil_div(k, p.k_split);
+    if (!any_ws && ws_bytes < split_space(p, kDense, m, 1, 2 * n)) p.splits = 1;
+  }
+  return p;
+}
+
+int pair_loading(const pgemm_gate_weights& w, int size, int inner) {
+  const int g = operand_loading(w.gate.data, w.gate.ld, size, inner, 0);
+  const int u = operand_loading(w.up.data, w.up.ld, size, inner, 0);
+  return g == u ? g : g == kThrough || u == kThrough ? kThrough : kRagged;
+}
+int both_loading(int a, int b) {
+  return a == kDirect && b == kDirect ? kDirect : a != kThrough && b != kThrough ? kRagged : kThrough;
+}
+
+// The parts of a gated backward call's workspace: dZ of both weights, then partial
+// sums (of the bias gradients, then of the products, in stream order).
+struct GateSpace {
+  size_t dz = 0, rest = 0;
+  int half = 0, chunks = 1;
+  size_t total() const { return dz + rest; }
+};
+
+GateSpace gate_space(const pgemm_kind& kind, int m, int n, int k) {
+  GateSpace g;
+  const int size = size_of(kind.dtype);
+  g.half = (int)round_up(n, 64);
+  g.dz = align256((size_t)m * 2 * (size_t)g.half * (size_t)size);
+  const int rows = m < 1 ? 1 : m;
+  g.chunks = slope_chunks(rows, 1, g.half);
+  g.rest = 2 * (size_t)g.chunks * (size_t)n * 4;
+  const size_t parts[3] = {split_bytes(size, kInner, kDense, rows, 1, k, 2 * g.half, false),
+                           split_bytes(size, kOuter, kDense, k, 1, n, rows),
+                           split_bytes(size, kOuter, kDense, n, 1, k, rows)};
+  for (const size_t x : parts)
+    if (x > g.rest) g.rest = x;
+  g.rest = align256(g.rest);
+  return g;
+}
+
+// The product for one weight's gradient, dW = X^T dZ.
+bool plan_dw(Product* p, const pgemm_kind& kind, int m, int n, int k, const pgemm_rows& X,
+             const void* dz, long long ldz, const pgemm_weight& dW, void* ws, size_t ws_bytes) {
+  const bool kn = dW.order == PGEMM_KN;
+  ProdArgs& a = p->a;
+  a.A = kn ? X.data : dz;
+  a.lda = kn ? X.ld : ldz;
+  a.B = kn ? dz : X.data;
+  a.ldb = kn ? ldz : X.ld;
+  a.D = const_cast<void*>(dW.data);
+  a.ldd = dW.ld;
+  a.out32 = kind.out_dtype == PGEMM_F32;
+  a.M = kn ? k : n;
+  a.N = kn ? n : k;
+  a.K = m;
+  p->dtype = kind.dtype;
+  p->la = p->lb = kOuter;
+  p->mode = kDense;
+  return plan_call(p, a.M, ws, ws_bytes);
+}
+
 }  // namespace
 }  // namespace blocks
 }  // namespace pgemm
@@ -74,31 +167,30 @@ int pgemm_layer_norm(int dtype, int m, int n, pgemm_rows X, const void* weight, 
   return status(norm_ops(dtype).norm(a, static_cast<hipStream_t>(stream)));
 }
 
-int pgemm_layer_norm_backward(int dtype, int out_dtype, int m, int n, pgemm_rows dY, pgemm_rows X,
+int pgemm_layer_norm_backward(pgemm_kind kind, int m, int n, pgemm_rows dY, pgemm_rows X,
                               const float* mean, const float* rstd, const void* weight,
                               pgemm_rows residual, pgemm_rows dX, void* dweight, void* dbias,
                               void* workspace, size_t workspace_bytes, void* stream) {
-  if (!known(dtype)) return -1;
-  if (out_dtype != dtype && out_dtype != PGEMM_F32) return -2;
-  if (!size_ok(m)) return -3;
-  if (!size_ok(n)) return -4;
+  if (!kind_ok(kind) || kind.act != PGEMM_ACT_NONE) return -1;
+  if (!size_ok(m)) return -2;
+  if (!size_ok(n)) return -3;
   const bool touch = m > 0 && n > 0, sums = dweight != nullptr || dbias != nullptr;
-  const int size = size_of(dtype), osize = size_of(out_dtype);
-  if (!rows_ok(dY, n, size, touch)) return -5;
-  if (!rows_ok(X, n, size, touch)) return -6;
-  if (!vector_ok(mean, 4, touch)) return -7;
-  if (!vector_ok(rstd, 4, touch)) return -8;
-  if (!vector_ok(weight, size, false)) return -9;
-  if (!rows_ok(residual, n, size, false)) return -10;
-  if (!rows_ok(dX, n, size, false)) return -11;
-  if (!vector_ok(dweight, osize, false)) return -12;
-  if (!vector_ok(dbias, osize, false)) return -13;
+  const int size = size_of(kind.dtype), osize = size_of(kind.out_dtype);
+  if (!rows_ok(dY, n, size, touch)) return -4;
+  if (!rows_ok(X, n, size, touch)) return -5;
+  if (!vector_ok(mean, 4, touch)) return -6;
+  if (!vector_ok(rstd, 4, touch)) return -7;
+  if (!vector_ok(weight, size, false)) return -8;
+  if (!rows_ok(residual, n, size, false)) return -9;
+  if (!rows_ok(dX, n, size, false)) return -10;
+  if (!vector_ok(dweight, osize, false)) return -11;
+  if (!vector_ok(dbias, osize, false)) return -12;
   if (sums && n > 0) {
-    if (workspace == nullptr || !aligned_to(workspace, 16)) return -14;
-    if (workspace_bytes < pgemm_layer_norm_backward_workspace(m, n)) return -15;
+    if (workspace == nullptr || !aligned_to(workspace, 16)) return -13;
+    if (workspace_bytes < pgemm_layer_norm_backward_workspace(m, n)) return -14;
   }
   if (n == 0) return PGEMM_OK;
-  const NormOps& ops = norm_ops(dtype);
+  const NormOps& ops = norm_ops(kind.dtype);
   const hipStream_t s = static_cast<hipStream_t>(stream);
   NormBackArgs a{};
   a.dY = dY.data;
@@ -127,7 +219,7 @@ int pgemm_layer_norm_backward(int dtype, int out_dtype, int m, int n, pgemm_rows
     const hipError_t e = ops.norm_sums(a, s);
     if (e != hipSuccess) return PGEMM_EHIP;
   }
-  const NormColumnArgs c = {partial, dweight, dbias, n, a.groups, out_dtype == PGEMM_F32};
+  const NormColumnArgs c = {partial, dweight, dbias, n, a.groups, kind.out_dtype == PGEMM_F32};
   return status(ops.norm_columns(c, s));
 }
 
@@ -237,6 +329,176 @@ size_t pgemm_linear_fp8_workspace(int m, int n, int k) {
   return split_bytes(1, kInner, kDense, m, 1, n, k);
 }
 
+int pgemm_gated_linear(pgemm_kind kind, int m, int n, int k, pgemm_rows X, pgemm_gate_weights W,
+                       pgemm_gate_bias bias, pgemm_gate_rows Z, pgemm_rows Y, void* workspace,
+                       size_t workspace_bytes, void* stream) {
+  if (!kind_ok(kind)) return -1;
+  if (!size_ok(m)) return -2;
+  if (n < 0 || n > kMaxGated) return -3;
+  if (!size_ok(k)) return -4;
+  const bool touch = m > 0 && n > 0, read = touch && k > 0;
+  const int size = size_of(kind.dtype);
+  if (!rows_ok(X, k, size, read)) return -5;
+  if (!gate_weights_ok(W, k, n, size, read)) return -6;
+  if (!vector_ok(bias.gate, size, false) || !vector_ok(bias.up, size, false)) return -7;
+  if (!rows_ok(Z.gate, n, size, false) || !rows_ok(Z.up, n, size, false)) return -8;
+  if (!rows_ok(Y, n, size_of(kind.out_dtype), touch)) return -9;
+  if (workspace != nullptr && !aligned_to(workspace, 16)) return -10;
+  if (!touch) return PGEMM_OK;
+  PairArgs args{};
+  ProdArgs& a = args.p;
+  a.A = X.data;
+  a.lda = X.ld;
+  a.B = W.gate.data;
+  a.ldb = W.gate.ld;
+  a.D = Y.data;
+  a.ldd = Y.ld;
+  a.M = m;
+  a.N = n;
+  a.K = k;
+  a.bias = bias.gate;
+  a.Z = Z.gate.data;
+  a.ldz = Z.gate.ld;
+  a.act = kind.act;
+  a.out32 = kind.out_dtype == PGEMM_F32;
+  args.B2 = W.up.data;
+  args.bias2 = bias.up;
+  args.Z2 = Z.up.data;
+  args.ldz2 = Z.up.ld;
+  const int lb = W.gate.order == PGEMM_KN ? kOuter : kInner;
+  const int loading = both_loading(operand_loading(X.data, X.ld, size, k, 0),
+                                   pair_loading(W, size, lb == kInner ? k : n));
+  const Plan plan =
+      gate_plan(size, m, n, k, loading, workspace == nullptr ? 0 : workspace_bytes, false);
+  if (plan.kernel < 0) return -2;
+  a.splits = plan.splits;
+  a.k_split = plan.k_split;
+  a.partial = static_cast<float*>(workspace);
+  a.tiles_m = plan.kernel >= kFew16 ? 1 : (int)ceil_div(m, kShape[plan.kernel].bm);
+  a.tiles_n = (int)ceil_div(n, gate_columns(plan.kernel));
+  return status(gate_ops(kind.dtype).pair(args, lb, kColumns, plan.kernel, loading,
+                                          static_cast<hipStream_t>(stream)));
+}
+
+size_t pgemm_gated_linear_workspace(int dtype, int m, int n, int k) {
+  if (!known(dtype) || m <= 0 || n <= 0 || n > kMaxGated || k <= 0) return 0;
+  size_t most = 0;
+  for (const int loading : {kThrough, kDirect}) {
+    const Plan p = gate_plan(size_of(dtype), m, n, k, loading, 0, true);
+    const size_t b = split_space(p, kDense, m, 1, 2 * n);
+    if (b > most) most = b;
+  }
+  return most;
+}
+
+int pgemm_gated_linear_backward(pgemm_kind kind, int m, int n, int k, pgemm_rows dY,
+                                pgemm_gate_rows Z, pgemm_rows X, pgemm_gate_weights W,
+                                pgemm_rows dX, pgemm_gate_weights dW, pgemm_gate_bias dbias,
+                                void* workspace, size_t workspace_bytes, void* stream) {
+  if (!kind_ok(kind)) return -1;
+  if (!size_ok(m)) return -2;
+  if (n < 0 || n > kMaxGated) return -3;
+  if (!size_ok(k)) return -4;
+  const bool read = m > 0 && n > 0;
+  const int size = size_of(kind.dtype), osize = size_of(kind.out_dtype);
+  const bool any_dw = dW.gate.data != nullptr || dW.up.data != nullptr;
+  if (!rows_ok(dY, n, size, read)) return -5;
+  if (!rows_ok(Z.gate, n, size, read) || !rows_ok(Z.up, n, size, read)) return -6;
+  if (!rows_ok(X, k, size, read && k > 0 && any_dw)) return -7;
+  if (!gate_weights_ok(W, k, n, size, read && k > 0 && dX.data != nullptr)) return -8;
+  if (!rows_ok(dX, k, size, false)) return -9;
+  if (!weight_ok(dW.gate, k, n, osize, false, 1) || !weight_ok(dW.up, k, n, osize, false, 1)) return -10;
+  if (!vector_ok(dbias.gate, osize, false) || !vector_ok(dbias.up, osize, false)) return -11;
+  const GateSpace space = gate_space(kind, m, n, k);
+  if (space.total() > 0 && (workspace == nullptr || !aligned_to(workspace, 16))) return -12;
+  if (workspace_bytes < space.total()) return -13;
+  const hipStream_t s = static_cast<hipStream_t>(stream);
+  const GateOps& ops = gate_ops(kind.dtype);
+  const bool bias = n > 0 && (dbias.gate != nullptr || dbias.up != nullptr);
+  const bool want_dx = dX.data != nullptr && m > 0 && k > 0;
+  const bool want_dw = any_dw && k > 0 && n > 0;
+  char* const dz = static_cast<char*>(workspace);
+  void* const rest = dz + space.dz;
+  const long long ldz = 2LL * space.half;
+  const void* const dzs[2] = {dz, dz + (size_t)space.half * (size_t)size};
+
+  // all of the call is planned before any of it is launched
+  PairArgs dx{};
+  Plan dx_plan;
+  int lb = kInner, loading = kThrough;
+  if (want_dx) {
+    ProdArgs& a = dx.p;
+    a.A = dz;
+    a.lda = ldz;
+    a.B = W.gate.data;
+    a.ldb = W.gate.ld;
+    a.D = dX.data;
+    a.ldd = dX.ld;
+    a.M = m;
+    a.N = k;
+    a.K = (int)ldz;
+    dx.B2 = W.up.data;
+    dx.half = space.half;
+    dx.inner = n;
+    lb = W.gate.order == PGEMM_KN ? kInner : kOuter;
+    loading = both_loading(operand_loading(dz, ldz, size, (int)ldz, 0),
+                           pair_loading(W, size, lb == kInner ? n : k));
+    dx_plan = plan_product(size, kInner, kDense, m, 1, k, (int)ldz, loading, space.rest, false, true,
+                           false);
+    if (dx_plan.kernel < 0) return -2;
+    a.splits = dx_plan.splits;
+    a.k_split = dx_plan.k_split;
+    a.partial = static_cast<float*>(rest);
+    set_tiles(&a, dx_plan.kernel, kDense, m);
+  }
+  Product dw[2] = {};
+  const pgemm_weight* const dws[2] = {&dW.gate, &dW.up};
+  for (int w = 0; w < 2; ++w)
+    if (want_dw && dws[w]->data != nullptr &&
+        !plan_dw(&dw[w], kind, m, n, k, X, dzs[w], ldz, *dws[w], rest, space.rest))
+      return -2;
+
+  if (n > 0 && (want_dx || want_dw || bias)) {
+    GateSlopeArgs a{};
+    a.dY = dY.data;
+    a.ldy = dY.ld;
+    a.Zg = Z.gate.data;
+    a.ldg = Z.gate.ld;
+    a.Zu = Z.up.data;
+    a.ldu = Z.up.ld;
+    a.dZ = dz;
+    a.ldd = ldz;
+    a.n = n;
+    a.half = space.half;
+    a.act = kind.act;
+    a.rows = m;
+    a.chunks = space.chunks;
+    a.tpr = threads_per_row(space.half, 64);
+    a.partial = bias ? static_cast<float*>(rest) : nullptr;
+    const bool out32 = kind.out_dtype == PGEMM_F32;
+    if (ops.slope(a, bias && out32, s) != hipSuccess) return PGEMM_EHIP;
+    void* const to[2] = {dbias.gate, dbias.up};
+    for (int w = 0; w < 2; ++w)
+      if (bias && to[w] != nullptr &&
+          ops_of(kind.dtype).column_sum(a.partial + (size_t)w * (size_t)a.chunks * (size_t)n, to[w], n,
+                                        1, a.chunks, out32, s) != hipSuccess)
+        return PGEMM_EHIP;
+  }
+  if (want_dx && ops.pair(dx, lb, kHalves, dx_plan.kernel, loading, s) != hipSuccess)
+    return PGEMM_EHIP;
+  for (int w = 0; w < 2; ++w)
+    if (want_dw && dws[w]->data != nullptr) {
+      const int st = launch_product(dw[w], s);
+      if (st != PGEMM_OK) return st;
+    }
+  return PGEMM_OK;
+}
+
+size_t pgemm_gated_linear_backward_workspace(pgemm_kind kind, int m, int n, int k) {
+  if (!kind_ok(kind) || !size_ok(m) || n <= 0 || n > kMaxGated || !size_ok(k)) return 0;
+  return gate_space(kind, m, n, k).total();
+}
+
 namespace {
 
 struct LayerNormCall {
@@ -251,7 +513,8 @@ struct LayerNormCall {
   void* stream;
 };
 struct LayerNormBackwardCall {
-  int dtype, out_dtype, m, n;
+  pgemm_kind kind;
+  int m, n;
   pgemm_rows dY, X;
   const float* mean;
   const float* rstd;
@@ -285,6 +548,33 @@ struct LinearFp8Call {
   void* stream;
 };
 
+struct GatedLinearCall {
+  pgemm_kind kind;
+  int m, n, k;
+  pgemm_rows X;
+  pgemm_gate_weights W;
+  pgemm_gate_bias bias;
+  pgemm_gate_rows Z;
+  pgemm_rows Y;
+  void* workspace;
+  size_t workspace_bytes;
+  void* stream;
+};
+struct GatedLinearBackwardCall {
+  pgemm_kind kind;
+  int m, n, k;
+  pgemm_rows dY;
+  pgemm_gate_rows Z;
+  pgemm_rows X;
+  pgemm_gate_weights W;
+  pgemm_rows dX;
+  pgemm_gate_weights dW;
+  pgemm_gate_bias dbias;
+  void* workspace;
+  size_t workspace_bytes;
+  void* stream;
+};
+
 }  // namespace
 
 int pgemm_block_call(int op, const void* args) {
@@ -297,8 +587,8 @@ int pgemm_block_call(int op, const void* args) {
     }
     case PGEMM_OP_LAYER_NORM_BACKWARD: {
       const LayerNormBackwardCall& c = *static_cast<const LayerNormBackwardCall*>(args);
-      return pgemm_layer_norm_backward(c.dtype, c.out_dtype, c.m, c.n, c.dY, c.X, c.mean, c.rstd,
-                                       c.weight, c.residual, c.dX, c.dweight, c.dbias, c.workspace,
+      return pgemm_layer_norm_backward(c.kind, c.m, c.n, c.dY, c.X, c.mean, c.rstd, c.weight,
+                                       c.residual, c.dX, c.dweight, c.dbias, c.workspace,
                                        c.workspace_bytes, c.stream);
     }
     case PGEMM_OP_QUANTIZE: {
@@ -309,6 +599,16 @@ int pgemm_block_call(int op, const void* args) {
       const LinearFp8Call& c = *static_cast<const LinearFp8Call*>(args);
       return pgemm_linear_fp8(c.kind, c.m, c.n, c.k, c.X, c.x_scales, c.W, c.w_scales, c.bias,
                               c.residual, c.Z, c.Y, c.workspace, c.workspace_bytes, c.stream);
+    }
+    case PGEMM_OP_GATED_LINEAR: {
+      const GatedLinearCall& c = *static_cast<const GatedLinearCall*>(args);
+      return pgemm_gated_linear(c.kind, c.m, c.n, c.k, c.X, c.W, c.bias, c.Z, c.Y, c.workspace,
+                                c.workspace_bytes, c.stream);
+    }
+    case PGEMM_OP_GATED_LINEAR_BACKWARD: {
+      const GatedLinearBackwardCall& c = *static_cast<const GatedLinearBackwardCall*>(args);
+      return pgemm_gated_linear_backward(c.kind, c.m, c.n, c.k, c.dY, c.Z, c.X, c.W, c.dX, c.dW,
+                                         c.dbias, c.workspace, c.workspace_bytes, c.stream);
     }
     default: return -1;
   }

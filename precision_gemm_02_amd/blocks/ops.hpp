@@ -4,6 +4,7 @@
 #include <hip/hip_runtime.h>
 
 #include "fp8.hpp"
+#include "gated.hpp"
 #include "norm.hpp"
 #include "quantize.hpp"
 
@@ -30,6 +31,18 @@ hipError_t prod8_e4m3(const Prod8Args& a, int w_type, int kernel, bool direct, h
 hipError_t prod8_e5m2(const Prod8Args& a, int w_type, int kernel, bool direct, hipStream_t s);
 hipError_t prod8_e4m3_wide(const Prod8Args& a, int w_type, int kernel, bool direct, hipStream_t s);
 hipError_t prod8_e5m2_wide(const Prod8Args& a, int w_type, int kernel, bool direct, hipStream_t s);
+
+struct GateOps {
+  // a gated product, or dX of one, and the sum of its splits
+  hipError_t (*pair)(const PairArgs& a, int lb, int pair, int kernel, int loading, hipStream_t s);
+  hipError_t (*slope)(const GateSlopeArgs& a, bool sums32, hipStream_t s);
+};
+const GateOps& gate_ops_f32();
+const GateOps& gate_ops_f16();
+const GateOps& gate_ops_bf16();
+inline const GateOps& gate_ops(int dtype) {
+  return dtype == 0 ? gate_ops_f32() : dtype == 1 ? gate_ops_f16() : gate_ops_bf16();
+}
 
 }  // namespace blocks
 }  // namespace pgemm

@@ -23,8 +23,10 @@ BLOCKS = os.path.join(HERE, "blocks")
 SOURCES = [os.path.join(CSRC, f) for f in ("api.hip", "sgemm.hip", "dgemm.hip")] + [
     os.path.join(LAYERS, f)
     for f in ("layers_api.hip", "prod_f32.hip", "prod_f16.hip", "prod_bf16.hip")] + [
-    os.path.join(BLOCKS, f) for f in ("blocks_api.hip", "norm.hip", "quantize.hip", "fp8_e4m3.hip", "fp8_e5m2.hip",
-                                     "fp8_e4m3_wide.hip", "fp8_e5m2_wide.hip")]
+    os.path.join(BLOCKS, f)
+    for f in ("blocks_api.hip", "norm.hip", "gated_f32.hip", "gated_f16.hip", "gated_bf16.hip",
+              "quantize.hip", "fp8_e4m3.hip", "fp8_e5m2.hip", "fp8_e4m3_wide.hip",
+              "fp8_e5m2_wide.hip")]
 ARCH = "gfx950"
 
 HIPCC = os.environ.get("HIPCC", shutil.which("hipcc") or "/opt/rocm/bin/hipcc")

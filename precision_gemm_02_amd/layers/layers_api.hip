@@ -11,24 +11,6 @@ namespace pgemm {
 namespace layers {
 namespace {
 
-// Threads per row of a row-wise kernel with 8 columns per thread.
-int threads_per_row(int n, int most) {
-  int t = 1;
-  while (t < most && t * 8 < n) t *= 2;
-  return t;
-}
-
-// Row chunks per group of the slope kernel: enough workgroups for every
-// compute unit, at least 16 rows of an average group each.
-int slope_chunks(long long rows, int groups, int n) {
-  if (n < 1) return 1;
-  const long long cols = ceil_div(n, threads_per_row(n, 64) * 8);
-  long long c = 4 * kUnits / (cols * groups);
-  const long long most = ceil_div(ceil_div(rows, groups), 16);
-  if (c > most) c = most;
-  return c < 1 ? 1 : (int)c;
-}
-
 // The parts of a backward call's workspace: dZ, then partial sums (column sums
 // of the bias gradient, then the products' splits, one after the other in
 // stream order).

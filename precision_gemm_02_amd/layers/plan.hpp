@@ -146,9 +146,10 @@ inline bool launch_fits(int kernel, int mode, long long rows, int groups, int n)
 // rows: the rows of D over all groups (how they are distributed is not known
 // here; any distribution is correct).  may_split: the summed index may be
 // shared by workgroups, through partial sums in `ws_bytes` bytes (any_ws: as
-// many as it takes).
+// many as it takes).  few: the few-rows kernels may be chosen.
 inline Plan plan_product(int size, int la, int mode, long long rows, int groups, int n, int k,
-                  int loading, size_t ws_bytes, bool any_ws, bool may_split = true) {
+                         int loading, size_t ws_bytes, bool any_ws, bool may_split = true,
+                         bool may_few = true) {
   Plan p;
   p.loading = loading;
   const int bk = 128 / size;
@@ -160,7 +161,7 @@ inline Plan plan_product(int size, int la, int mode, long long rows, int groups,
   const long long wide = ceil_div(n, 64) * (mode == kRows ? groups : 1);
   const int few = wide >= 2 * kUnits ? (per <= 16 ? kFew16Wide : kFew32Wide)
                                      : (per <= 16 ? kFew16 : kFew32);
-  if (la == kInner && per <= 32 && launch_fits(few, mode, rows, groups, n)) {
+  if (may_few && la == kInner && per <= 32 && launch_fits(few, mode, rows, groups, n)) {
     p.kernel = few;
     if (may_split && n > 0) {   // (no columns: the size of a workspace that is not used)
       // one split per free compute unit, each of 16 units of 128 bytes at least
@@ -206,16 +207,17 @@ inline Plan plan_product(int size, int la, int mode, long long rows, int groups,
     }
     const size_t need = split_space(p, mode, rows, groups, n);
     if (!any_ws && ws_bytes < need)   // the best plan that needs no space
-      return plan_product(size, la, mode, rows, groups, n, k, loading, 0, false, false);
+      return plan_product(size, la, mode, rows, groups, n, k, loading, 0, false, false, may_few);
   }
   return p;
 }
 
 // Workspace that plan_product may use for a product, over any alignment.
-inline size_t split_bytes(int size, int la, int mode, long long rows, int groups, int n, int k) {
+inline size_t split_bytes(int size, int la, int mode, long long rows, int groups, int n, int k,
+                          bool may_few = true) {
   size_t most = 0;
   for (const int loading : {kThrough, kDirect}) {
-    const Plan p = plan_product(size, la, mode, rows, groups, n, k, loading, 0, true);
+    const Plan p = plan_product(size, la, mode, rows, groups, n, k, loading, 0, true, true, may_few);
     const size_t b = split_space(p, mode, rows, groups, n);
     if (b > most) most = b;
   }
@@ -257,6 +259,24 @@ inline int launch_product(const Product& p, hipStream_t s) {
                  hipSuccess
              ? PGEMM_OK
              : PGEMM_EHIP;
+}
+
+// Threads per row of a row-wise kernel with 8 columns per thread.
+inline int threads_per_row(int n, int most) {
+  int t = 1;
+  while (t < most && t * 8 < n) t *= 2;
+  return t;
+}
+
+// Row chunks per group of the slope kernel: enough workgroups for every
+// compute unit, at least 16 rows of an average group each.
+inline int slope_chunks(long long rows, int groups, int n) {
+  if (n < 1) return 1;
+  const long long cols = ceil_div(n, threads_per_row(n, 64) * 8);
+  long long c = 4 * kUnits / (cols * groups);
+  const long long most = ceil_div(ceil_div(rows, groups), 16);
+  if (c > most) c = most;
+  return c < 1 ? 1 : (int)c;
 }
 
 }  // namespace layers

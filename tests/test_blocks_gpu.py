@@ -12,7 +12,7 @@ import pytest
 import torch
 
 import precision_gemm_02_amd as pg
-from layer_util import Guarded, act64, half_step, ints
+from layer_util import Guarded, act64, half_step, ints, slope64, weight
 
 pytestmark = [pytest.mark.gpu,
               pytest.mark.skipif(not torch.cuda.is_available(), reason="needs a GPU")]
@@ -246,6 +246,212 @@ def test_layer_norm_gradients_against_differences():
     for i in range(0, n, 5):
         assert abs(float(dw[i]) - diff(w, i, lambda t: loss(x, t, b))) < tol
         assert abs(float(db[i]) - diff(b, i, lambda t: loss(x, w, t))) < tol
+
+
+# ---- gated products ------------------------------------------------------------------
+
+# (m, n, k): few-rows kernels (m <= 32), tiles of every class, edges of each
+GATES = [(1, 1, 1), (1, 64, 64), (1, 257, 1023), (3, 17, 5), (16, 130, 72), (17, 64, 129), (32, 72, 520),
+         (33, 65, 31), (64, 64, 128), (65, 129, 64), (128, 256, 40), (200, 136, 1), (300, 263, 264),
+         (260, 520, 72)]
+
+
+@pytest.mark.parametrize("dtype", TYPES, ids=ids)
+@pytest.mark.parametrize("order", ["kn", "nk"])
+@pytest.mark.parametrize("shape", GATES, ids=str)
+@pytest.mark.parametrize("pad", [0, 5, 8])
+def test_gated_linear_exact_integers(dtype, order, shape, pad):
+    """Whole numbers: sums, biases and products are exact."""
+    m, n, k = shape
+    g = gen(m + n + k)
+    X = Guarded(m, k, dtype, pad=pad, shift=pad % 2, data=ints(g, m, k, hi=1).to(dtype))
+    Wg, Wu = (weight(g, (), k, n, order, dtype, integer=True, pad=pad) for _ in range(2))
+    bg, bu = (ints(g, n).to(dtype).cuda() for _ in range(2))
+    Y, Zg, Zu = Guarded(m, n, F32, pad=pad), Guarded(m, n, dtype, pad=pad), Guarded(m, n, dtype, pad=pad)
+    assert pg.gated_linear(X.t, Wg, Wu, Y.t, bias_gate=bg, bias_up=bu, act="relu", Z_gate=Zg.t,
+                           Z_up=Zu.t) is Y.t
+    x = X.t.double().cpu()
+    zg = x @ Wg.double().cpu() + bg.double().cpu()
+    zu = x @ Wu.double().cpu() + bu.double().cpu()
+    y = zg.clamp(min=0) * zu
+    same = torch.equal(Y.t.double().cpu(), y)
+    assert same
+    assert torch.equal(Zg.t.cpu(), zg.to(dtype)) and torch.equal(Zu.t.cpu(), zu.to(dtype))
+    for t, name in ((Y, "Y"), (Zg, "Z_gate"), (Zu, "Z_up")):
+        t.check(name)
+    # with the summed index shared between workgroups, in the inputs' type, one bias
+    ws = space(pg.gated_linear_workspace(m, n, k, dtype))
+    Y2 = Guarded(m, n, dtype, pad=pad)
+    pg.gated_linear(X.t, Wg, Wu, Y2.t, bias_gate=bg, act="relu", ws=ws)
+    assert torch.equal(Y2.t.cpu(), (zg.clamp(min=0) * (zu - bu.double().cpu())).to(dtype))
+    Y2.check("Y")
+
+
+@pytest.mark.parametrize("dtype", [F16, BF16], ids=ids)
+@pytest.mark.parametrize("order", ["kn", "nk"])
+@pytest.mark.parametrize("k", [66, 126, 130, 186, 188, 190, 194, 258, 1026])
+@pytest.mark.parametrize("shape", [(65, 40), (129, 66), (257, 514)], ids=str)
+def test_gated_linear_ragged_rows(dtype, order, k, shape):
+    """Rows at 4-byte boundaries, at inner sizes around the last whole tile."""
+    m, n = shape
+    g = gen(k)
+    X = Guarded(m, k, dtype, pad=2, shift=2, data=ints(g, m, k, hi=1).to(dtype))
+    rows, cols = (k, n) if order == "kn" else (n, k)
+    W = [Guarded(rows, cols, dtype, pad=2, shift=2, data=ints(g, rows, cols).to(dtype)) for _ in "gu"]
+    Wg, Wu = (w.t if order == "kn" else w.t.t() for w in W)
+    x = X.t.double().cpu()
+    want = (x @ Wg.double().cpu()) * (x @ Wu.double().cpu())
+    Y = Guarded(m, n, F32, pad=2, shift=2)
+    pg.gated_linear(X.t, Wg, Wu, Y.t, act="none")
+    same = torch.equal(Y.t.double().cpu(), want)
+    assert same
+    Y.check("Y")
+    # dX = dY (Wg + Wu of the others), with Z of ones and no activation
+    one = torch.ones(m, n, dtype=dtype, device="cuda")
+    D = Guarded(m, n, dtype, pad=2, shift=2, data=ints(g, m, n, hi=1).to(dtype))
+    dX = Guarded(m, k, dtype, pad=2, shift=2)
+    pg.gated_linear_backward(D.t, None, Wg, Wu, one, one, act="none", dX=dX.t,
+                             ws=space(pg.gated_linear_backward_workspace(m, n, k, dtype)))
+    d = D.t.double().cpu()
+    same = torch.equal(dX.t.cpu(), (d @ Wg.double().cpu().t() + d @ Wu.double().cpu().t()).to(dtype))
+    assert same
+    dX.check("dX")
+
+
+@pytest.mark.parametrize("dtype", TYPES, ids=ids)
+@pytest.mark.parametrize("order", ["kn", "nk"])
+@pytest.mark.parametrize("shape", GATES, ids=str)
+@pytest.mark.parametrize("pad,out", [(0, None), (5, F32), (8, None)])
+def test_gated_linear_backward_exact_integers(dtype, order, shape, pad, out):
+    m, n, k = shape
+    g = gen(m + n + k + 1)
+    X = Guarded(m, k, dtype, pad=pad, data=ints(g, m, k).to(dtype))
+    Wg, Wu = (weight(g, (), k, n, order, dtype, integer=True, pad=pad) for _ in range(2))
+    D, Zg, Zu = (Guarded(m, n, dtype, pad=pad, shift=pad % 2, data=ints(g, m, n, hi=2).to(dtype))
+                 for _ in range(3))
+    dX = Guarded(m, k, dtype, pad=pad, shift=pad % 2)
+    T = out or dtype
+    # the weights' gradients each in its own order
+    dWg = Guarded(k, n, T, pad=pad)
+    dWu = Guarded(n, k, T, pad=pad)
+    dbg, dbu = (torch.full((n,), math.nan, dtype=T, device="cuda") for _ in range(2))
+    ws = space(pg.gated_linear_backward_workspace(m, n, k, dtype))
+    pg.gated_linear_backward(D.t, X.t, Wg, Wu, Zg.t, Zu.t, act="relu", dX=dX.t, dW_gate=dWg.t,
+                             dW_up=dWu.t.t(), dbias_gate=dbg, dbias_up=dbu, ws=ws)
+    d, x, zg, zu = (t.t.double().cpu() for t in (D, X, Zg, Zu))
+    dzg, dzu = d * zu * (zg > 0), d * zg.clamp(min=0)
+    want = (dzg @ Wg.double().cpu().t() + dzu @ Wu.double().cpu().t()).to(dtype)
+    same = torch.equal(dX.t.cpu(), want)
+    assert same
+    assert torch.equal(dWg.t.cpu(), (x.t() @ dzg).to(T)) and torch.equal(dWu.t.cpu(), (dzu.t() @ x).to(T))
+    assert torch.equal(dbg.cpu(), dzg.sum(0).to(T)) and torch.equal(dbu.cpu(), dzu.sum(0).to(T))
+    for t, name in ((dX, "dX"), (dWg, "dW_gate"), (dWu, "dW_up")):
+        t.check(name)
+    # each alone
+    only = torch.full_like(dX.t, math.nan)
+    pg.gated_linear_backward(D.t, None, Wg, Wu, Zg.t, Zu.t, act="relu", dX=only, ws=ws)
+    assert torch.equal(only, dX.t)
+    only = torch.full((k, n), math.nan, dtype=T, device="cuda")
+    pg.gated_linear_backward(D.t, X.t, None, None, Zg.t, Zu.t, act="relu", dW_up=only, ws=ws)
+    assert torch.equal(only, dWu.t.t())
+    only = torch.full((n,), math.nan, dtype=T, device="cuda")
+    pg.gated_linear_backward(D.t, None, None, None, Zg.t, Zu.t, act="relu", dbias_up=only, ws=ws)
+    assert torch.equal(only, dbu)
+
+
+@pytest.mark.parametrize("act", ["none", "relu", "gelu", "gelu_tanh", "silu"])
+@pytest.mark.parametrize("dtype", TYPES, ids=ids)
+@pytest.mark.parametrize("shape", [(5, 70, 300), (70, 150, 260), (24, 40, 6000)], ids=str)
+def test_gated_linear_activations(act, dtype, shape):
+    """Random operands against 64 bits, both directions."""
+    m, n, k = shape
+    g = gen(m * n + k)
+    X = torch.randn(m, k, generator=g).to(dtype).cuda()
+    Wg, Wu = (weight(g, (), k, n, "nk", dtype, scale=k ** -0.5) for _ in range(2))
+    bg, bu = (torch.randn(n, generator=g).to(dtype).cuda() for _ in range(2))
+    Y, Zg, Zu = (torch.empty(m, n, dtype=dtype, device="cuda") for _ in range(3))
+    pg.gated_linear(X, Wg, Wu, Y, bias_gate=bg, bias_up=bu, act=act, Z_gate=Zg, Z_up=Zu,
+                    ws=space(pg.gated_linear_workspace(m, n, k, dtype)))
+    x, wg, wu, b1, b2 = (t.double().cpu() for t in (X, Wg, Wu, bg, bu))
+    zg, zu = x @ wg + b1, x @ wu + b2
+    eg = (k + 3) * U * (x.abs() @ wg.abs() + b1.abs())
+    eu = (k + 3) * U * (x.abs() @ wu.abs() + b2.abs())
+    held(Zg, zg, eg, "Z_gate")
+    held(Zu, zu, eu, "Z_up")
+    a = act64(zg, act)
+    # an activation's slope is below 1.13; its own evaluation: at most (|z| + 8) 2 U of z
+    # (the 16-bit forms a little more in the far tails, below their half step)
+    ea = 1.13 * eg + (zg.abs() + 8) * 2 * U * zg.abs() + (0 if dtype is F32 else 2e-5) * a.abs() + U
+    held(Y, a * zu, ea * (zu.abs() + eu) + a.abs() * eu + U * (a * zu).abs(), "Y")
+    # gradients
+    dY = torch.randn(m, n, generator=g).to(dtype).cuda()
+    dX, dWg, dWu = torch.empty_like(X), torch.empty_like(Wg), torch.empty_like(Wu)
+    dbg, dbu = torch.empty_like(bg), torch.empty_like(bu)
+    pg.gated_linear_backward(dY, X, Wg, Wu, Zg, Zu, act=act, dX=dX, dW_gate=dWg, dW_up=dWu,
+                             dbias_gate=dbg, dbias_up=dbu,
+                             ws=space(pg.gated_linear_backward_workspace(m, n, k, dtype)))
+    d, zg, zu = dY.double().cpu(), Zg.double().cpu(), Zu.double().cpu()
+    a, s = act64(zg, act), slope64(zg, act)
+    dzg, dzu = d * zu * s, d * a
+    # dZ: the slope's and the activation's evaluation (as above, slopes up to 1.13 and
+    # their z times a bell), then the rounding to the type
+    h = half_step(dtype)
+    ev = (zg.abs() + 8) * 4 * U * (1 + zg.abs()) + (0 if dtype is F32 else 2e-5)
+    e1 = (d * zu).abs() * (ev + 2 * U) + h * (dzg.abs() + (d * zu).abs() * ev) + 2.0 ** -25
+    e2 = d.abs() * (ev + 2 * U) + h * (dzu.abs() + d.abs() * ev) + 2.0 ** -25
+    held(dX, dzg @ wg.t() + dzu @ wu.t(),
+         (e1 + (2 * n + 3) * U * dzg.abs()) @ wg.abs().t() + (e2 + (2 * n + 3) * U * dzu.abs()) @ wu.abs().t(),
+         "dX")
+    held(dWg, x.t() @ dzg, x.abs().t() @ (e1 + (m + 3) * U * dzg.abs()), "dW_gate")
+    held(dWu, x.t() @ dzu, x.abs().t() @ (e2 + (m + 3) * U * dzu.abs()), "dW_up")
+    held(dbg, dzg.sum(0), (e1 + (m + 3) * U * dzg.abs()).sum(0), "dbias_gate")
+    held(dbu, dzu.sum(0), (e2 + (m + 3) * U * dzu.abs()).sum(0), "dbias_up")
+
+
+def test_gated_linear_gradients_against_differences():
+    m, n, k = 3, 9, 11
+    g = gen(6)
+    t64 = [torch.randn(*s, generator=g).double() for s in ((m, k), (k, n), (k, n), (n,), (n,))]
+    d = torch.randn(m, n, generator=g).double()
+
+    def loss(x, wg, wu, bg, bu):
+        return float((act64(x @ wg + bg, "gelu_tanh") * (x @ wu + bu) * d).sum())
+
+    X, Wg, Wu, bg, bu = (t.float().cuda() for t in t64)
+    Y, Zg, Zu = (torch.empty(m, n, device="cuda") for _ in range(3))
+    pg.gated_linear(X, Wg, Wu, Y, bias_gate=bg, bias_up=bu, act="gelu_tanh", Z_gate=Zg, Z_up=Zu)
+    grads = [torch.empty_like(t) for t in (X, Wg, Wu, bg, bu)]
+    pg.gated_linear_backward(d.float().cuda(), X, Wg, Wu, Zg, Zu, act="gelu_tanh", dX=grads[0],
+                             dW_gate=grads[1], dW_up=grads[2], dbias_gate=grads[3],
+                             dbias_up=grads[4], ws=space(pg.gated_linear_backward_workspace(m, n, k, F32)))
+    s = 1e-5
+    for which, grad in enumerate(grads):
+        for i in range(0, grad.numel(), 3):
+            up, down = [t.clone() for t in t64], [t.clone() for t in t64]
+            up[which].view(-1)[i] += s
+            down[which].view(-1)[i] -= s
+            want = (loss(*up) - loss(*down)) / (2 * s)
+            # fp32 sums of a few dozen terms of size 10 and less, and differences good to
+            # s^2 and 1e-16 / s
+            assert abs(float(grad.view(-1)[i]) - want) < 2e-4
+
+
+def test_gated_linear_empty_sizes():
+    e = lambda *s: torch.empty(*s, device="cuda")
+    nan = lambda *s: torch.full(s, math.nan, device="cuda")
+    Y, b = nan(4, 6), torch.arange(6.0, device="cuda")
+    pg.gated_linear(e(4, 0), e(0, 6), e(0, 6), Y, bias_gate=b, bias_up=b + 1, act="relu")
+    assert torch.equal(Y, (b * (b + 1)).expand(4, 6))
+    # no rows: zero gradients of what all rows share
+    dWg, dWu, dbg = nan(5, 6), nan(6, 5).t(), nan(6)
+    pg.gated_linear_backward(e(0, 6), e(0, 5), e(5, 6), e(5, 6), e(0, 6), e(0, 6), dX=e(0, 5), dW_gate=dWg,
+                             dW_up=dWu, dbias_gate=dbg,
+                             ws=space(pg.gated_linear_backward_workspace(0, 6, 5, F32)))
+    assert bool((dWg == 0).all()) and bool((dWu == 0).all()) and bool((dbg == 0).all())
+    # no columns: dX is a sum of nothing
+    dX = nan(3, 5)
+    pg.gated_linear_backward(e(3, 0), e(3, 5), e(5, 0), e(5, 0), e(3, 0), e(3, 0), dX=dX)
+    assert bool((dX == 0).all())
 
 
 # ---- 8-bit products ------------------------------------------------------------------

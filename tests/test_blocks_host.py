@@ -59,18 +59,19 @@ def test_layer_norm_argument_codes():
 
 
 NEED = L.pgemm_layer_norm_backward_workspace(8, 64)
-NORM_BACK = [2, 0, 8, 64, R(), R(), FAKE, FAKE, FAKE, R(), R(), FAKE, FAKE, FAKE, NEED, None]
+NORM_BACK = [lo._Kind(2, 0, 0), 8, 64, R(), R(), FAKE, FAKE, FAKE, R(), R(), FAKE, FAKE, FAKE, NEED, None]
 
 
 def test_layer_norm_backward_argument_codes():
+    kinds = [lo._Kind(*x) for x in ((7, 7, 0), (2, 1, 0), (2, 2, 1))]
     refused(L.pgemm_layer_norm_backward, NORM_BACK,
-            [(1, 7), (2, 1), (3, -1), (4, TOP + 1), (5, R(None)), (5, R(FAKE, 63)), (6, R(None)),
-             (7, None), (7, FAKE + 2), (8, None), (9, FAKE + 1), (10, R(FAKE, 3)),
-             (11, R(FAKE + 1)), (12, FAKE + 2), (13, FAKE + 2), (14, None), (14, FAKE + 8),
-             (15, NEED - 1)])
+            [(1, k) for k in kinds] +
+            [(2, -1), (3, TOP + 1), (4, R(None)), (4, R(FAKE, 63)), (5, R(None)), (6, None),
+             (6, FAKE + 2), (7, None), (8, FAKE + 1), (9, R(FAKE, 3)), (10, R(FAKE + 1)),
+             (11, FAKE + 2), (12, FAKE + 2), (13, None), (13, FAKE + 8), (14, NEED - 1)])
     args = list(NORM_BACK)
-    args[3] = 0                                 # no features: nothing is touched
-    args[4] = args[5] = R(None)
+    args[2] = 0                                 # no features: nothing is touched
+    args[3] = args[4] = R(None)
     assert L.pgemm_layer_norm_backward(*args) == 0
 
 
@@ -126,6 +127,65 @@ def test_linear_fp8_workspace():
             assert pg.linear_fp8_workspace(m, n, 0) == 0
 
 
+def GW(gate=FAKE, up=FAKE, ld=64, order=0, up_ld=None, up_order=None):
+    return bo._GateWeights(Wt(gate, ld, order), Wt(up, up_ld or ld, order if up_order is None else up_order))
+
+
+def GR(gate=FAKE, up=FAKE, ld=64):
+    return bo._GateRows(R(gate, ld), R(up, ld))
+
+
+def GB(gate=FAKE, up=FAKE):
+    return bo._GateBias(gate, up)
+
+
+KIND, SILU = lo._Kind(2, 2, 0), lo._Kind(2, 2, 4)
+WIDEST = (1 << 30) - 4096
+GATED = [SILU, 8, 64, 64, R(), GW(), GB(), GR(), R(), FAKE, 0, None]
+BAD_PAIRS = [GW(None), GW(up=None), GW(ld=63), GW(up_ld=65), GW(up_order=1), GW(order=3),
+             GW(up=FAKE + 1)]
+
+
+def test_gated_linear_argument_codes():
+    refused(L.pgemm_gated_linear, GATED,
+            [(1, lo._Kind(2, 1, 0)), (1, lo._Kind(2, 2, 5)), (2, -1), (3, -1), (3, WIDEST + 1), (4, -1),
+             (5, R(None)), (5, R(FAKE, 63))] + [(6, w) for w in BAD_PAIRS] +
+            [(7, GB(FAKE + 1)), (7, GB(up=FAKE + 1)), (8, GR(FAKE + 1)), (8, GR(ld=63)), (9, R(None)),
+             (9, R(FAKE, 63)), (10, FAKE + 8)])
+    none = R(None)
+    for m, n in ((0, 64), (8, 0)):
+        assert L.pgemm_gated_linear(SILU, m, n, 64, none, GW(None, None), GB(None, None),
+                                    GR(None, None), none, None, 0, None) == 0
+
+
+NEEDG = L.pgemm_gated_linear_backward_workspace(SILU, 8, 64, 64)
+GATED_BACK = [SILU, 8, 64, 64, R(), GR(), R(), GW(), R(), GW(), GB(), FAKE, NEEDG, None]
+
+
+def test_gated_linear_backward_argument_codes():
+    refused(L.pgemm_gated_linear_backward, GATED_BACK,
+            [(1, lo._Kind(2, 1, 0)), (2, -1), (3, WIDEST + 1), (4, -1), (5, R(None)), (6, GR(None)),
+             (6, GR(up=None)), (7, R(None)), (7, R(FAKE, 63))] + [(8, w) for w in BAD_PAIRS] +
+            [(9, R(FAKE, 63)), (10, GW(ld=63)), (10, GW(up_order=2)), (11, GB(FAKE + 1)),
+             (11, GB(up=FAKE + 1)), (12, None), (12, FAKE + 8), (13, NEEDG - 1)])
+    args = list(GATED_BACK)
+    args[2] = 0                                 # no columns, nothing wanted
+    args[8], args[11], args[12] = R(None), None, 0
+    assert L.pgemm_gated_linear_backward(*args) == 0
+
+
+def test_gated_workspaces():
+    assert pg.gated_linear_workspace(8192, 8192, 4096, BF) == 0
+    assert pg.gated_linear_workspace(1, 256, 8192, BF) > 0
+    for T in (BF, F16, F32):
+        for m in (0, 1, 16, 33, 5000):
+            for n in (0, 1, 65, 5000):
+                for k in (0, 1, 64, 5000):
+                    b = pg.gated_linear_backward_workspace(m, n, k, T)
+                    assert b >= 2 * m * n * T.itemsize
+                    assert pg.gated_linear_workspace(m, n, k, T) == 0 or m * n * k > 0
+
+
 # ---- packed calls ------------------------------------------------------------------
 
 def flat(args):
@@ -146,15 +206,18 @@ def changed(args, pos, value):
 
 
 CALLS = [(L.pgemm_layer_norm, changed(NORM, 10, R(FAKE, 3))),
-         (L.pgemm_layer_norm_backward, changed(NORM_BACK, 15, NEED - 1)),
-         (L.pgemm_quantize, changed(QUANT, 7, S(row=1))), (L.pgemm_linear_fp8, changed(FP8, 13, FAKE + 8))]
+         (L.pgemm_layer_norm_backward, changed(NORM_BACK, 14, NEED - 1)),
+         (L.pgemm_quantize, changed(QUANT, 7, S(row=1))), (L.pgemm_linear_fp8, changed(FP8, 13, FAKE + 8)),
+         (L.pgemm_gated_linear, changed(GATED, 10, FAKE + 8)),
+         (L.pgemm_gated_linear_backward, changed(GATED_BACK, 13, NEEDG - 1))]
 
 
 def test_packed_calls_equal_the_functions():
     """Every argument reaches its place: a bad value gives the same code."""
     bad = {ctypes.c_int: -1, ctypes.c_float: -1.0, lo._Rows: R(FAKE + 1, 64),
            lo._Weight: Wt(FAKE, 64, 9), lo._Kind: lo._Kind(7, 7, 0), ctypes.c_void_p: FAKE + 1,
-           bo._Scales: S(rows=3), bo._Fp8Kind: bo._Fp8Kind(9, 9, 9, 9)}
+           bo._Scales: S(rows=3), bo._Fp8Kind: bo._Fp8Kind(9, 9, 9, 9),
+           bo._GateWeights: GW(order=9), bo._GateRows: GR(up=FAKE + 1), bo._GateBias: GB(up=FAKE + 1)}
     for op, (fn, args) in enumerate(CALLS):
         assert -100 < fn(*args) < 0
         for pos, kind in enumerate(fn.argtypes[:-1]):
@@ -262,3 +325,31 @@ def test_linear_fp8_refusals(anywhere, change, error):
     args.update(change)
     with pytest.raises(error):
         pg.linear_fp8(**args)
+
+
+@pytest.mark.parametrize("change,error", [
+    (dict(W_up=z(3, 5)), ValueError), (dict(W_gate=z(3, 4, dtype=F32)), TypeError),
+    (dict(W_up=z(4, 3).t()), ValueError), (dict(W_up=z(3, 8)[:, :4]), ValueError),
+    (dict(W_gate=None), ValueError), (dict(W_up=None), ValueError), (dict(Y=z(2, 4, dtype=F16)), TypeError),
+    (dict(Y=z(3, 4)), ValueError), (dict(X=z(3, 2).t()), ValueError), (dict(bias_gate=z(5)), ValueError),
+    (dict(bias_up=z(4, dtype=F32)), TypeError), (dict(Z_gate=z(2, 5)), ValueError),
+    (dict(Z_up=z(2, 4, dtype=F32)), TypeError), (dict(act="tanh"), ValueError)])
+def test_gated_linear_refusals(anywhere, change, error):
+    args = dict(X=z(2, 3), W_gate=z(3, 4), W_up=z(3, 4), Y=z(2, 4))
+    args.update(change)
+    with pytest.raises(error):
+        pg.gated_linear(**args)
+
+
+@pytest.mark.parametrize("change,error", [
+    (dict(X=z(3, 3)), ValueError), (dict(W_up=z(4, 3).t()), ValueError), (dict(Z_up=None), ValueError),
+    (dict(Z_gate=z(2, 4, dtype=F32)), TypeError), (dict(dX=z(2, 3, dtype=F32)), TypeError),
+    (dict(dX=z(2, 3), W_gate=None), ValueError), (dict(dW_up=z(3, 4), X=None), ValueError),
+    (dict(dW_gate=z(3, 4), dW_up=z(3, 4, dtype=F32)), TypeError), (dict(dW_gate=z(4, 3)), ValueError),
+    (dict(dW_gate=z(3, 4), dbias_up=z(4, dtype=F32)), TypeError), (dict(dbias_up=z(5)), ValueError),
+    (dict(dX=z(2, 3)), pg.PgemmError), (dict(act="x"), ValueError)])
+def test_gated_linear_backward_refusals(anywhere, change, error):
+    args = dict(dY=z(2, 4), X=z(2, 3), W_gate=z(3, 4), W_up=z(3, 4), Z_gate=z(2, 4), Z_up=z(2, 4))
+    args.update(change)
+    with pytest.raises(error):
+        pg.gated_linear_backward(**args)
