@@ -253,28 +253,50 @@ def _fp8(t, name):
     return code
 
 
-def _scales(t, name, rows, cols, device, written=False, by_row=False):
+def _columns(t, name, rows, cols, device):
+    """(address, column stride) of a matrix with contiguous columns."""
+    if t.shape != (rows, cols) or t.get_device() != device:
+        _wrong(t, name, t.dtype, (rows, cols), device)
+    s0, s1 = t.stride()
+    if s0 == 1 and s1 >= rows and cols > 1:
+        return t.data_ptr(), s1 or 1
+    if rows == 0 or cols == 0:
+        return t.data_ptr(), max(1, rows)
+    if rows > 1 and s0 != 1:
+        raise ValueError("%s must have contiguous columns (strides %s): the transposed view of a weight "
+                         "kept as n x k" % (name, (s0, s1)))
+    if cols == 1:
+        s1 = rows
+    if s1 < rows:
+        raise ValueError("%s has overlapping columns (strides %s)" % (name, (s0, s1)))
+    return t.data_ptr(), s1
+
+
+def _scales(t, name, rows, cols, device, turned=False, by_row=False, written=False):
     """(address, row stride, block stride, rows per scale) of the scales of a (rows,
-    cols) matrix: one for 128 columns of each row, or of 128 rows together."""
-    blocks = -(-cols // _BLOCK)
-    high = -(-rows // _BLOCK)
+    cols) matrix: one for 128 columns of each row, or of 128 rows together.  turned:
+    the tensor is transposed."""
+    blocks = (cols + 127) // 128
     if t.dtype is not torch.float32 or t.get_device() != device:
         _wrong(t, name, torch.float32, t.shape, device)
-    if t.shape == (rows, blocks):
-        by, n = 1, rows
-    elif not by_row and t.shape == (high, blocks):
-        by, n = _BLOCK, high
+    if turned:
+        n1, n0 = t.shape
+        s1, s0 = t.stride()
     else:
-        raise ValueError("%s is %s, expected %s%s" % (name, tuple(t.shape), (rows, blocks),
-                                                      "" if by_row else " or %s" % ((high, blocks),)))
-    s0, s1 = t.stride()
-    if n <= 1:
+        n0, n1 = t.shape
+        s0, s1 = t.stride()
+    by = 1 if n0 == rows else _BLOCK
+    if n1 != blocks or (n0 != rows and (by_row or n0 != (rows + 127) // 128)):
+        want = [(rows, blocks)] + ([] if by_row else [((rows + 127) // 128, blocks)])
+        raise ValueError("%s is %s, expected %s" % (name, tuple(t.shape), " or ".join(
+            str(w[::-1] if turned else w) for w in want)))
+    if n0 <= 1:
         s0 = blocks
     if blocks <= 1:
         s1 = 1
-    if written and n * blocks > 0 and not (
-            (n == 1 or s0 > 0) and (blocks == 1 or s1 > 0) and
-            (n == 1 or blocks == 1 or s0 >= blocks * s1 or s1 >= n * s0)):
+    if written and n0 * blocks > 0 and not (
+            (n0 == 1 or s0 > 0) and (blocks == 1 or s1 > 0) and
+            (n0 == 1 or blocks == 1 or s0 >= blocks * s1 or s1 >= n0 * s0)):
         raise ValueError("%s overlaps itself (strides %s)" % (name, t.stride()))
     return t.data_ptr(), s0, s1, by
 
@@ -320,15 +342,12 @@ def linear_fp8(X, x_scales, W, w_scales, Y, *, bias=None, act="none", residual=N
     T = Y.dtype
     x, w, out = _fp8(X, "X"), _fp8(W, "W"), _dtype(Y, "Y")
     _shape2(W, "W")
-    _shape2(x_scales, "x_scales")
-    _shape2(w_scales, "w_scales")
-    if W.shape != (k, n):
-        _wrong(W, "W", W.dtype, (k, n), dev)
+    if x_scales.dim() != 2 or w_scales.dim() != 2:
+        raise ValueError("x_scales and w_scales must be 2-D")
     st = _call(_LINEAR_FP8, _PACK[_LINEAR_FP8](
         x, w, out, _act(act), m, n, k, *_rows(X, "X", m, k, X.dtype, dev),
         *_scales(x_scales, "x_scales", m, k, dev, by_row=True),
-        *_rows(W.t(), "W's columns", n, k, W.dtype, dev),
-        *_scales(w_scales.t(), "w_scales transposed", n, k, dev), _flat(bias, "bias", (n,), T, dev),
+        *_columns(W, "W", k, n, dev), *_scales(w_scales, "w_scales", n, k, dev, turned=True), _flat(bias, "bias", (n,), T, dev),
         *_rows(residual, "residual", m, n, T, dev), *_rows(Z, "Z", m, n, T, dev),
         *_rows(Y, "Y", m, n, T, dev), *_space(ws, dev), _stream(stream, dev)))
     if st != 0:

@@ -5,6 +5,7 @@
 #include "../layers/launch.hpp"
 #include "launch.hpp"
 #include "ops.hpp"
+#include "whole.hpp"
 
 namespace pgemm {
 namespace blocks {
@@ -27,6 +28,27 @@ hipError_t pair_tiles(const PairArgs& a, int kernel, dim3 grid, hipStream_t s) {
   return hipErrorInvalidValue;
 }
 
+template <typename T, int LB, int PAIR>
+hipError_t whole_tiles(const PairArgs& a, int kernel, dim3 grid, hipStream_t s) {
+  if (kernel == kTile256)
+    return launch(&pair_whole_kernel<T, LB, 256, 256, 2, 4, PAIR>, grid, prod_threads(kTile256), a, s);
+  if (kernel == kTile128)
+    return launch(&pair_whole_kernel<T, LB, 128, 128, 2, 2, PAIR>, grid, prod_threads(kTile128), a, s);
+  if (kernel == kTile64)
+    return launch(&pair_whole_kernel<T, LB, 64, 64, 2, 2, PAIR>, grid, prod_threads(kTile64), a, s);
+  return hipErrorInvalidValue;
+}
+
+// Whether pair_whole_kernel takes a product whose loads are direct: whole steps, and
+// offsets within a tile of at most 256 rows that fit 32 bits.
+template <typename T>
+bool whole(const PairArgs& a, int lb, int pair_) {
+  constexpr long long BK = 128 / sizeof(T), most = 0x7fffffffLL / 256 / sizeof(T);
+  if (pair_ == kColumns && lb != kInner) return false;
+  return a.p.K % BK == 0 && (pair_ == kColumns || a.inner == a.half) && a.p.lda < most &&
+         a.p.ldb < most;
+}
+
 template <typename T, int LB, int MB, int NB>
 hipError_t gate_rows(const PairArgs& a, dim3 grid, hipStream_t s) {
   static_assert(prod_threads(kFew16) == 512, "the checked launch");
@@ -45,6 +67,8 @@ hipError_t pair(const PairArgs& a, int kernel, int loading, hipStream_t s) {
           : kernel == kFew16Wide ? gate_rows<T, LB, 1, 4>(a, grid, s)
                                  : gate_rows<T, LB, 2, 4>(a, grid, s);
     }
+  } else if (loading == kDirect && whole<T>(a, LB, PAIR)) {
+    if constexpr (PAIR == kHalves || LB == kInner) e = whole_tiles<T, LB, PAIR>(a, kernel, grid, s);
   } else if (loading == kDirect) {
     e = pair_tiles<T, LB, PAIR, kDirect>(a, kernel, grid, s);
   } else if (sizeof(T) == 2 && loading == kRagged) {

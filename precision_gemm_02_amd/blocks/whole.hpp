@@ -1,0 +1,276 @@
+// The pair products' tile kernel for whole tiles: 16-byte aligned rows, and a summed
+// index of whole steps of 128 bytes.  Beside pair_tile_kernel it spends no vector
+// instruction on the loads' addresses: an operand's tile is a buffer descriptor whose
+// scalar base moves along the summed index, and each lane's 32-bit offsets within a
+// tile stay as they are.
+//
+// A tile of the summed index is 128 bytes of each row.  Of the LDS, three slots hold A's
+// tiles, two B's.  A wave's B operands of a whole tile stay in registers (CB x 8), read
+// at the end of the tile before, so that B's slot is free for the tile after next as
+// soon as every wave has passed barrier M behind its first block; A's blocks of 16
+// rows are read one ahead of their use, and its slot is free behind barrier E, before
+// the last block, which also waits for the next tile: both operands are loaded about
+// two tiles ahead.  A tile's code is repeated for the six places that the slots take
+// in turn, so that every LDS address is a constant.
+#pragma once
+
+#include "gated.hpp"
+
+namespace pgemm {
+namespace blocks {
+
+// A descriptor of everything from `base` on (offsets are in bounds by construction).
+__device__ __forceinline__ u32x4 descriptor(const char* base) {
+  const uint64_t a = reinterpret_cast<uint64_t>(base);
+  return u32x4{(uint32_t)a, (uint32_t)(a >> 32) & 0xffffu, 0xffffffffu, 0x00020000u};
+}
+
+// 16 bytes per lane straight to LDS: lane l of the wave writes at to + 16 l (an LDS
+// address, the same for all lanes).  As the instruction for load_to_lds's reasons.
+__device__ __forceinline__ void tile_load(u32x4 from, uint32_t offset, uint32_t to) {
+  asm volatile(
+      "s_mov_b32 m0, %0\n\t"
+      "s_nop 0\n\t"
+      "buffer_load_dwordx4 %1, %2, 0 offen lds"
+      :
+      : "s"(to), "v"(offset), "s"(from));
+}
+
+__device__ __forceinline__ uint32_t lds_address(const void* p) {
+  return (uint32_t)(uintptr_t)(__attribute__((address_space(3))) const char*)p;
+}
+
+// An operand's descriptor base and what moves it from tile to tile.  Past the last
+// tile it stays (the loads repeat it; nothing uses them).
+struct Walk {
+  const char* at;
+  long long step;
+  int left;                // tiles from `at` on
+  __device__ __forceinline__ void next(long long extra) {
+    if (--left > 0) at += step + extra;
+  }
+};
+
+template <typename T, int LB, int BM, int BN, int WGM, int WGN, int PAIR>
+__global__ __launch_bounds__(WGM* WGN * 64) void pair_whole_kernel(const PairArgs args) {
+  const ProdArgs& a = args.p;
+  constexpr int S = sizeof(T), NT = WGM * WGN * 64;
+  constexpr int WM = BM / WGM, WN = BN / WGN, RB = WM / 16, CB = WN / 16;
+  constexpr int BK = 128 / S;
+  constexpr int SLOT_A = BM * 128, SLOT_B = BN * 128;
+  constexpr int EPI_LD = WN + 4;
+  constexpr int EPI = WGM * WGN * 32 * EPI_LD * 4;   // 32 rows per wave
+  constexpr int LDS = 3 * SLOT_A + 2 * SLOT_B > EPI ? 3 * SLOT_A + 2 * SLOT_B : EPI;
+  static_assert(PAIR == kHalves || LB == kInner, "both weights' columns in one load");
+  __shared__ __attribute__((aligned(128))) char lds[LDS];
+
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
+  const int wm = (wave / WGN) * WM, wn = (wave % WGN) * WN;
+  constexpr int COLS = PAIR == kColumns ? BN / 2 : BN;   // results of a tile
+  int tm, tn, k_lo = 0, k_hi = a.K;
+  map_tile(blockIdx.x, a.tiles_m, a.tiles_n, &tm, &tn);
+  const int row0 = tm * BM, col0 = tn * COLS;
+  if (a.splits > 1) {
+    k_lo = blockIdx.y * a.k_split;
+    k_hi = k_lo + a.k_split < a.K ? k_lo + a.k_split : a.K;
+  }
+  const int nk = (k_hi - k_lo) / BK;
+
+  using TA = OperandTile<T, kInner, BM, NT>;
+  using TB = OperandTile<T, LB, BN, NT>;
+  constexpr int LA_ = TA::LOADS, LB_ = TB::LOADS;
+  uint32_t va[LA_], vb[LB_];
+#pragma unroll
+  for (int j = 0; j < LA_; ++j) {
+    int r, c;
+    TA::slot(j * NT + (int)threadIdx.x, &r, &c);
+    const int row = row0 + r < a.M ? r : a.M - 1 - row0;
+    va[j] = (uint32_t)row * (uint32_t)(a.lda * S) + c * 16;
+  }
+  // kColumns: rows of the tile that a wave's load covers belong to one weight
+  auto second = [&](int j) {
+    return PAIR == kColumns && (j * NT + wave * 64) / 8 / 16 % CB >= CB / 2;
+  };
+#pragma unroll
+  for (int j = 0; j < LB_; ++j) {
+    int r, c;
+    TB::slot(j * NT + (int)threadIdx.x, &r, &c);
+    if constexpr (LB == kInner) {
+      int col = r;
+      if constexpr (PAIR == kColumns) {
+        const int p = r / 16, in = p % CB;
+        col = (p / CB * (CB / 2) + in % (CB / 2)) * 16 + r % 16;
+      }
+      col = col0 + col < a.N ? col : a.N - 1 - col0;
+      vb[j] = (uint32_t)col * (uint32_t)(a.ldb * S) + c * 16;
+    } else {
+      vb[j] = (uint32_t)r * (uint32_t)(a.ldb * S) + (col0 + c * TB::V < a.N ? c * 16 : 0);
+    }
+  }
+  Walk wa, wb;
+  wa.at = static_cast<const char*>(a.A) + ((long long)row0 * a.lda + k_lo) * S;
+  wa.step = 128;
+  wb.step = LB == kInner ? 128 : BK * a.ldb * S;
+  wa.left = wb.left = nk;
+  const long long second_at = static_cast<const char*>(args.B2) - static_cast<const char*>(a.B);
+  long long jump = 0;
+  int before = -1;                 // kHalves: B's tiles left when the second weight begins
+  if constexpr (PAIR == kHalves) {
+    const bool on = k_lo >= args.half;
+    const int in = on ? k_lo - args.half : k_lo;
+    wb.at = static_cast<const char*>(on ? args.B2 : a.B) +
+            (LB == kInner ? (long long)col0 * a.ldb + in : in * a.ldb + col0) * S;
+    jump = second_at - (LB == kInner ? args.half : args.half * a.ldb) * S;
+    before = (k_hi - args.half) / BK;
+  } else {
+    wb.at = static_cast<const char*>(a.B) + ((long long)col0 * a.ldb + k_lo) * S;
+  }
+  const uint32_t lds_wave = lds_address(lds) + wave * 1024;
+
+  // loads J0 .. J1-1 of the next tile, into slot `to`
+  auto load_a = [&](auto j0, auto j1, int to) {
+    const u32x4 d = descriptor(wa.at);
+#pragma unroll
+    for (int j = decltype(j0)::value; j < decltype(j1)::value; ++j)
+      tile_load(d, va[j], lds_wave + to * SLOT_A + j * NT * 16);
+    if constexpr (decltype(j1)::value == LA_) wa.next(0);
+  };
+  auto load_b = [&](auto j0, auto j1, int to) {
+    const u32x4 d = descriptor(wb.at);
+    const u32x4 e = PAIR == kColumns ? descriptor(wb.at + second_at) : d;
+#pragma unroll
+    for (int j = decltype(j0)::value; j < decltype(j1)::value; ++j)
+      tile_load(second(j) ? e : d, vb[j], lds_wave + 3 * SLOT_A + to * SLOT_B + j * NT * 16);
+    if constexpr (decltype(j1)::value == LB_)
+      wb.next(PAIR == kHalves && wb.left - 1 == before ? jump : 0);
+  };
+
+  f32x4 acc[RB][CB];
+#pragma unroll
+  for (int r = 0; r < RB; ++r)
+#pragma unroll
+    for (int c = 0; c < CB; ++c) acc[r][c] = f32x4{0, 0, 0, 0};
+
+  if (nk > 0) {
+    constexpr std::integral_constant<int, 0> zero{};
+    constexpr std::integral_constant<int, LA_> all_a{};
+    constexpr std::integral_constant<int, LB_> all_b{};
+    load_a(zero, all_a, 0);
+    load_b(zero, all_b, 0);
+    load_a(zero, all_a, 1);
+    load_b(zero, all_b, 1);
+    load_a(zero, all_a, 2);
+    wait_loads<2 * LA_ + LB_>();
+    workgroup_barrier();
+
+    u32x4 fa[2][2], fb[CB][2];
+    auto read_a = [&](const char* from, int g) {
+      fa[g & 1][0] = TA::frag(from, wm, g, 0);
+      fa[g & 1][1] = TA::frag(from, wm, g, 1);
+    };
+    read_a(lds, 0);
+#pragma unroll
+    for (int c = 0; c < CB; ++c) {
+      fb[c][0] = TB::frag(lds + 3 * SLOT_A, wn, c, 0);
+      fb[c][1] = TB::frag(lds + 3 * SLOT_A, wn, c, 1);
+    }
+    auto tile = [&](auto place) {
+      constexpr int sa = decltype(place)::value % 3, sb = decltype(place)::value % 2;
+      const char* const a0 = lds + sa * SLOT_A;
+      const char* const a1 = lds + (sa + 1) % 3 * SLOT_A;
+      const char* const b1 = lds + 3 * SLOT_A + (sb ^ 1) * SLOT_B;
+      static_for<RB>([&](auto gc) {
+        constexpr int g = decltype(gc)::value;
+        constexpr bool M = g == 1, E = g == RB - 1;
+        if constexpr (E) {
+          // all but the tile after next (of which, in two blocks, B's is not yet asked for)
+          wait_loads<M ? LA_ : LA_ + LB_>();
+          workgroup_barrier();
+          read_a(a1, 0);                        // past the last tile: some LDS, never used
+        } else {
+          if constexpr (M) workgroup_barrier();
+          read_a(a0, g + 1);
+        }
+        // B's loads over the blocks behind M, A's in the last one
+        constexpr int PARTS = RB > 2 ? RB - 2 : 1;
+        constexpr int b0 = g >= 1 && (g < RB - 1 || RB == 2) ? LB_ * (g - 1) / PARTS : LB_;
+        constexpr int b_end = g >= 1 && (g < RB - 1 || RB == 2) ? LB_ * g / PARTS : LB_;
+        if constexpr (b0 < b_end)
+          load_b(std::integral_constant<int, b0>{}, std::integral_constant<int, b_end>{}, sb);
+        if constexpr (E) load_a(zero, all_a, sa);
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+          for (int c = 0; c < CB; ++c) {
+            acc[g][c] = Elem<T>::mfma(fb[c][h], fa[g & 1][h], acc[g][c]);
+            if constexpr (E) fb[c][h] = TB::frag(b1, wn, c, h);
+          }
+        __builtin_amdgcn_sched_barrier(0);
+      });
+    };
+#pragma unroll 1
+    for (int t = 0; t < nk; t += 6)
+      static_for<6>([&](auto i) {
+        if (t + decltype(i)::value < nk) tile(i);
+      });
+    wait_loads<0>();                            // the loads past the end
+  }
+  __syncthreads();   // the operands' LDS becomes the epilogue's
+
+  // Epilogue: as pair_tile_kernel's
+  float* stg = reinterpret_cast<float*>(lds) + wave * 32 * EPI_LD;
+  constexpr int WC = PAIR == kColumns ? WN / 2 : WN;               // results of a wave's row
+  constexpr int LPR = WC / 8, RPP = 64 / LPR, PASSES = 32 / RPP;   // lanes per row, rows per pass
+  const int col = (lane % LPR) * 8, n = col0 + (wn / WN) * WC + col;
+  float bg[8], bu[8];
+  if constexpr (PAIR == kColumns) {
+    if (a.splits <= 1) gate_bias<T>(args, n, bg, bu);
+  }
+#pragma unroll 1
+  for (int r = 0; r < RB / 2; ++r) {
+    const int m0 = row0 + wm + 32 * r + lane / LPR;
+    static_for<RB / 2>([&](auto rc) {
+      constexpr int q = decltype(rc)::value;
+      if (r == q) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+          for (int c = 0; c < CB; ++c)
+            *reinterpret_cast<f32x4*>(stg + (16 * h + (lane & 15)) * EPI_LD + 16 * c +
+                                      4 * (lane >> 4)) = acc[2 * q + h][c];
+      }
+    });
+    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+#pragma unroll
+    for (int p = 0; p < PASSES; ++p) {
+      const float* from = stg + (p * RPP + lane / LPR) * EPI_LD + col;
+      const int m = m0 + p * RPP;
+      if (m < a.M && n < a.N) {
+        float v[8], u[8];
+        *reinterpret_cast<f32x4*>(v) = *reinterpret_cast<const f32x4*>(from);
+        *reinterpret_cast<f32x4*>(v + 4) = *reinterpret_cast<const f32x4*>(from + 4);
+        if constexpr (PAIR == kColumns) {
+          *reinterpret_cast<f32x4*>(u) = *reinterpret_cast<const f32x4*>(from + WC);
+          *reinterpret_cast<f32x4*>(u + 4) = *reinterpret_cast<const f32x4*>(from + WC + 4);
+          if (a.splits > 1) {
+            put_partial(a, blockIdx.y, 0, m, n, v);
+            put_partial(a, blockIdx.y, 1, m, n, u);
+          } else {
+            finish_gate<T>(args, m, n, v, u, bg, bu);
+          }
+        } else if (a.splits > 1) {
+          put_row8<float>(a.partial, ((long long)blockIdx.y * a.M + m) * a.N, n, a.N, v);
+        } else {
+          put_row8<T>(a.D, m * a.ldd, n, a.N, v);
+        }
+      }
+    }
+    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+  }
+}
+
+}  // namespace blocks
+}  // namespace pgemm
