@@ -98,34 +98,91 @@ GateSpace gate_space(const pgemm_kind& kind, int m, int n, int k) {
   const int rows = m < 1 ? 1 : m;
   g.chunks = slope_chunks(rows, 1, g.half);
   g.rest = 2 * (size_t)g.chunks * (size_t)n * 4;
-  const size_t parts[3] = {split_bytes(size, kInner, kDense, rows, 1, k, 2 * g.half, false),
+  const int both = 2LL * k <= kMaxSize ? 2 * k : k;
+  const size_t parts[5] = {split_bytes(size, kInner, kDense, rows, 1, k, 2 * g.half, false),
                            split_bytes(size, kOuter, kDense, k, 1, n, rows),
-                           split_bytes(size, kOuter, kDense, n, 1, k, rows)};
+                           split_bytes(size, kOuter, kDense, n, 1, k, rows),
+                           split_bytes(size, kOuter, kDense, k, 1, 2 * n, rows),
+                           split_bytes(size, kOuter, kDense, n, 1, both, rows)};
   for (const size_t x : parts)
     if (x > g.rest) g.rest = x;
   g.rest = align256(g.rest);
   return g;
 }
 
-// The product for one weight's gradient, dW = X^T dZ.
-bool plan_dw(Product* p, const pgemm_kind& kind, int m, int n, int k, const pgemm_rows& X,
-             const void* dz, long long ldz, const pgemm_weight& dW, void* ws, size_t ws_bytes) {
-  const bool kn = dW.order == PGEMM_KN;
-  ProdArgs& a = p->a;
-  a.A = kn ? X.data : dz;
-  a.lda = kn ? X.ld : ldz;
-  a.B = kn ? dz : X.data;
-  a.ldb = kn ? ldz : X.ld;
-  a.D = const_cast<void*>(dW.data);
-  a.ldd = dW.ld;
-  a.out32 = kind.out_dtype == PGEMM_F32;
-  a.M = kn ? k : n;
-  a.N = kn ? n : k;
-  a.K = m;
-  p->dtype = kind.dtype;
-  p->la = p->lb = kOuter;
-  p->mode = kDense;
-  return plan_call(p, a.M, ws, ws_bytes);
+// Whether pair_whole_kernel takes operands whose loads are direct: offsets within a tile
+// of at most 256 rows fit 32 bits, and the summed index has whole steps.
+bool whole_tiles(int size, long long lda, long long ldb, int summed) {
+  const long long most = 0x7fffffffLL / (256 * size);
+  return lda < most && ldb < most && summed % (128 / size) == 0;
+}
+
+// The products for the weights' gradients, dW = X^T dZ of each: one launch for both
+// where pair_whole_kernel takes them, else one of `one` for each that is wanted.
+struct WeightGradients {
+  bool whole = false;
+  PairArgs args{};
+  int kernel = -1;
+  int count = 0;
+  Product one[2] = {};
+};
+
+bool plan_weights(WeightGradients* g, const pgemm_kind& kind, int m, int n, int k,
+                  const pgemm_rows& X, const void* const* dz, long long ldz,
+                  const pgemm_gate_weights& dW, void* ws, size_t ws_bytes) {
+  const int size = size_of(kind.dtype);
+  const pgemm_weight* const to[2] = {&dW.gate, &dW.up};
+  const pgemm_weight* first = nullptr;
+  bool alike = true;
+  for (int w = 0; w < 2; ++w) {
+    if (to[w]->data == nullptr) continue;
+    const bool kn = to[w]->order == PGEMM_KN;
+    if (first == nullptr) first = to[w];
+    alike = alike && to[w]->order == first->order && to[w]->ld == first->ld;
+    ProdArgs& a = g->one[g->count++].a;
+    a.A = kn ? X.data : dz[w];
+    a.lda = kn ? X.ld : ldz;
+    a.B = kn ? dz[w] : X.data;
+    a.ldb = kn ? ldz : X.ld;
+    a.D = const_cast<void*>(to[w]->data);
+    a.ldd = to[w]->ld;
+    a.out32 = kind.out_dtype == PGEMM_F32;
+    a.M = kn ? k : n;
+    a.N = kn ? n : k;
+    a.K = m;
+  }
+  // dZ's rows go on behind column n (see gate_slope_kernel): its loads are direct
+  if (alike && whole_tiles(size, X.ld, ldz, m) &&
+      operand_loading(X.data, X.ld, size, k, 0) == kDirect) {
+    g->args.p = g->one[0].a;
+    g->args.count = g->count;
+    g->args.A2 = g->one[g->count - 1].a.A;
+    g->args.B2 = g->one[g->count - 1].a.B;
+    g->args.D2 = g->one[g->count - 1].a.D;
+    ProdArgs& a = g->args.p;
+    const long long columns = (long long)a.N * g->count;
+    if (columns <= kMaxSize) {
+      const Plan p = plan_product(size, kOuter, kDense, a.M, 1, (int)columns, m, kDirect, ws_bytes,
+                                  false);
+      if (p.kernel >= 0) {
+        a.splits = p.splits;
+        a.k_split = p.k_split;
+        a.partial = static_cast<float*>(ws);
+        set_tiles(&a, p.kernel, kDense, a.M);
+        g->kernel = p.kernel;
+        g->whole = (long long)a.tiles_m * a.tiles_n * g->count <= kMaxThreads / prod_threads(p.kernel);
+      }
+    }
+  }
+  if (g->whole) return true;
+  for (int i = 0; i < g->count; ++i) {
+    Product& p = g->one[i];
+    p.dtype = kind.dtype;
+    p.la = p.lb = kOuter;
+    p.mode = kDense;
+    if (!plan_call(&p, p.a.M, ws, ws_bytes)) return false;
+  }
+  return true;
 }
 
 }  // namespace
@@ -377,6 +434,7 @@ int pgemm_gated_linear(pgemm_kind kind, int m, int n, int k, pgemm_rows X, pgemm
   a.tiles_m = plan.kernel >= kFew16 ? 1 : (int)ceil_div(m, kShape[plan.kernel].bm);
   a.tiles_n = (int)ceil_div(n, gate_columns(plan.kernel));
   return status(gate_ops(kind.dtype).pair(args, lb, kColumns, plan.kernel, loading,
+                                          loading == kDirect && whole_tiles(size, X.ld, W.gate.ld, k),
                                           static_cast<hipStream_t>(stream)));
 }
 
@@ -451,12 +509,8 @@ int pgemm_gated_linear_backward(pgemm_kind kind, int m, int n, int k, pgemm_rows
     a.partial = static_cast<float*>(rest);
     set_tiles(&a, dx_plan.kernel, kDense, m);
   }
-  Product dw[2] = {};
-  const pgemm_weight* const dws[2] = {&dW.gate, &dW.up};
-  for (int w = 0; w < 2; ++w)
-    if (want_dw && dws[w]->data != nullptr &&
-        !plan_dw(&dw[w], kind, m, n, k, X, dzs[w], ldz, *dws[w], rest, space.rest))
-      return -2;
+  WeightGradients dw;
+  if (want_dw && !plan_weights(&dw, kind, m, n, k, X, dzs, ldz, dW, rest, space.rest)) return -2;
 
   if (n > 0 && (want_dx || want_dw || bias)) {
     GateSlopeArgs a{};
@@ -484,13 +538,16 @@ int pgemm_gated_linear_backward(pgemm_kind kind, int m, int n, int k, pgemm_rows
                                         1, a.chunks, out32, s) != hipSuccess)
         return PGEMM_EHIP;
   }
-  if (want_dx && ops.pair(dx, lb, kHalves, dx_plan.kernel, loading, s) != hipSuccess)
+  if (want_dx && ops.pair(dx, lb, kHalves, dx_plan.kernel, loading,
+                          loading == kDirect && n == space.half &&
+                              whole_tiles(size, ldz, W.gate.ld, n),
+                          s) != hipSuccess)
     return PGEMM_EHIP;
-  for (int w = 0; w < 2; ++w)
-    if (want_dw && dws[w]->data != nullptr) {
-      const int st = launch_product(dw[w], s);
-      if (st != PGEMM_OK) return st;
-    }
+  if (dw.whole) return status(ops.apart(dw.args, dw.kernel, s));
+  for (int i = 0; i < dw.count; ++i) {
+    const int st = launch_product(dw.one[i], s);
+    if (st != PGEMM_OK) return st;
+  }
   return PGEMM_OK;
 }
 

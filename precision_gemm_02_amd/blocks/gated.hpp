@@ -15,11 +15,16 @@ namespace blocks {
 
 using namespace layers;
 
-enum Pair { kColumns = 0, kHalves = 1 };
+enum Pair { kColumns = 0, kHalves = 1, kApart = 2 };
 
 struct PairArgs {
   ProdArgs p;             // B: the first weight; N: outputs; K: summed (kHalves: of both)
   const void* B2;         // the second weight, in the first one's order and ld
+  // kApart (pair_whole_kernel alone): `count` (1, 2) products of one shape, the second of A2
+  // and B2 into D2
+  const void* A2;
+  void* D2;
+  int count;
   // kColumns: the second weight's bias and pre-activations
   const void* bias2;
   void* Z2;
@@ -600,11 +605,11 @@ __global__ __launch_bounds__(256) void gate_reduce_kernel(const PairArgs args) {
   finish_gate<T>(args, m, n, v[0], v[1], bg, bu);
 }
 
-// Sums the splits of dX.
+// Sums the splits of the other products (blockIdx.y: of the first or the second).
 template <typename T>
-__global__ __launch_bounds__(256) void halves_reduce_kernel(const PairArgs args) {
+__global__ __launch_bounds__(256) void pair_reduce_kernel(const PairArgs args) {
   const ProdArgs& a = args.p;
-  const int per_row = (a.N + 7) / 8;
+  const int per_row = (a.N + 7) / 8, count = gridDim.y, w = blockIdx.y;
   const long long id = (long long)blockIdx.x * 256 + threadIdx.x;
   if (id >= (long long)a.M * per_row) return;
   const long long m = id / per_row;
@@ -613,11 +618,13 @@ __global__ __launch_bounds__(256) void halves_reduce_kernel(const PairArgs args)
 #pragma unroll 4
   for (int s = 0; s < a.splits; ++s) {
     float x[8];
-    get_row8<float>(a.partial, (s * (long long)a.M + m) * a.N, n, a.N, x);
+    get_row8<float>(a.partial, (((long long)s * count + w) * a.M + m) * a.N, n, a.N, x);
 #pragma unroll
     for (int j = 0; j < 8; ++j) v[j] += x[j];
   }
-  put_row8<T>(a.D, m * a.ldd, n, a.N, v);
+  void* D = w == 0 ? a.D : args.D2;
+  if (a.out32) put_row8<float>(D, m * a.ldd, n, a.N, v);
+  else put_row8<T>(D, m * a.ldd, n, a.N, v);
 }
 
 struct GateSlopeArgs {

@@ -28,25 +28,24 @@ hipError_t pair_tiles(const PairArgs& a, int kernel, dim3 grid, hipStream_t s) {
   return hipErrorInvalidValue;
 }
 
-template <typename T, int LB, int PAIR>
+template <typename T, int LA, int LB, int PAIR>
 hipError_t whole_tiles(const PairArgs& a, int kernel, dim3 grid, hipStream_t s) {
   if (kernel == kTile256)
-    return launch(&pair_whole_kernel<T, LB, 256, 256, 2, 4, PAIR>, grid, prod_threads(kTile256), a, s);
+    return launch(&pair_whole_kernel<T, LA, LB, 256, 256, 2, 4, PAIR>, grid, prod_threads(kTile256), a,
+                  s);
   if (kernel == kTile128)
-    return launch(&pair_whole_kernel<T, LB, 128, 128, 2, 2, PAIR>, grid, prod_threads(kTile128), a, s);
+    return launch(&pair_whole_kernel<T, LA, LB, 128, 128, 2, 2, PAIR>, grid, prod_threads(kTile128), a,
+                  s);
   if (kernel == kTile64)
-    return launch(&pair_whole_kernel<T, LB, 64, 64, 2, 2, PAIR>, grid, prod_threads(kTile64), a, s);
+    return launch(&pair_whole_kernel<T, LA, LB, 64, 64, 2, 2, PAIR>, grid, prod_threads(kTile64), a, s);
   return hipErrorInvalidValue;
 }
 
-// Whether pair_whole_kernel takes a product whose loads are direct: whole steps, and
-// offsets within a tile of at most 256 rows that fit 32 bits.
 template <typename T>
-bool whole(const PairArgs& a, int lb, int pair_) {
-  constexpr long long BK = 128 / sizeof(T), most = 0x7fffffffLL / 256 / sizeof(T);
-  if (pair_ == kColumns && lb != kInner) return false;
-  return a.p.K % BK == 0 && (pair_ == kColumns || a.inner == a.half) && a.p.lda < most &&
-         a.p.ldb < most;
+hipError_t pair_reduce(const PairArgs& a, int count, hipStream_t s) {
+  const long long items = (long long)a.p.M * ((a.p.N + 7) / 8);
+  return launch(&pair_reduce_kernel<T>, dim3((unsigned)((items + 255) / 256), (unsigned)count), 256, a,
+                s);
 }
 
 template <typename T, int LB, int MB, int NB>
@@ -56,7 +55,7 @@ hipError_t gate_rows(const PairArgs& a, dim3 grid, hipStream_t s) {
 }
 
 template <typename T, int LB, int PAIR>
-hipError_t pair(const PairArgs& a, int kernel, int loading, hipStream_t s) {
+hipError_t pair(const PairArgs& a, int kernel, int loading, bool whole, hipStream_t s) {
   const ProdGrid g = prod_grid(a.p, kDense, kernel);
   const dim3 grid((unsigned)g.x, (unsigned)g.y);
   hipError_t e = hipErrorInvalidValue;
@@ -67,8 +66,8 @@ hipError_t pair(const PairArgs& a, int kernel, int loading, hipStream_t s) {
           : kernel == kFew16Wide ? gate_rows<T, LB, 1, 4>(a, grid, s)
                                  : gate_rows<T, LB, 2, 4>(a, grid, s);
     }
-  } else if (loading == kDirect && whole<T>(a, LB, PAIR)) {
-    if constexpr (PAIR == kHalves || LB == kInner) e = whole_tiles<T, LB, PAIR>(a, kernel, grid, s);
+  } else if (whole) {
+    e = whole_tiles<T, kInner, LB, PAIR>(a, kernel, grid, s);
   } else if (loading == kDirect) {
     e = pair_tiles<T, LB, PAIR, kDirect>(a, kernel, grid, s);
   } else if (sizeof(T) == 2 && loading == kRagged) {
@@ -77,19 +76,27 @@ hipError_t pair(const PairArgs& a, int kernel, int loading, hipStream_t s) {
     e = pair_tiles<T, LB, PAIR, kThrough>(a, kernel, grid, s);
   }
   if (e != hipSuccess || a.p.splits <= 1) return e;
+  if constexpr (PAIR == kHalves) return pair_reduce<T>(a, 1, s);
   const long long items = (long long)a.p.M * ((a.p.N + 7) / 8);
-  const dim3 groups((unsigned)((items + 255) / 256));
-  if constexpr (PAIR == kColumns) return launch(&gate_reduce_kernel<T>, groups, 256, a, s);
-  else return launch(&halves_reduce_kernel<T>, groups, 256, a, s);
+  return launch(&gate_reduce_kernel<T>, dim3((unsigned)((items + 255) / 256)), 256, a, s);
 }
 
 template <typename T>
-hipError_t pair(const PairArgs& a, int lb, int pair_, int kernel, int loading, hipStream_t s) {
+hipError_t pair(const PairArgs& a, int lb, int pair_, int kernel, int loading, bool whole,
+                hipStream_t s) {
   if (pair_ == kColumns)
-    return lb == kInner ? pair<T, kInner, kColumns>(a, kernel, loading, s)
-                        : pair<T, kOuter, kColumns>(a, kernel, loading, s);
-  return lb == kInner ? pair<T, kInner, kHalves>(a, kernel, loading, s)
-                      : pair<T, kOuter, kHalves>(a, kernel, loading, s);
+    return lb == kInner ? pair<T, kInner, kColumns>(a, kernel, loading, whole, s)
+                        : pair<T, kOuter, kColumns>(a, kernel, loading, whole, s);
+  return lb == kInner ? pair<T, kInner, kHalves>(a, kernel, loading, whole, s)
+                      : pair<T, kOuter, kHalves>(a, kernel, loading, whole, s);
+}
+
+template <typename T>
+hipError_t apart(const PairArgs& a, int kernel, hipStream_t s) {
+  const ProdGrid g = prod_grid(a.p, kDense, kernel);
+  const dim3 grid((unsigned)(g.x * a.count), (unsigned)g.y);
+  const hipError_t e = whole_tiles<T, kOuter, kOuter, kApart>(a, kernel, grid, s);
+  return e != hipSuccess || a.p.splits <= 1 ? e : pair_reduce<T>(a, a.count, s);
 }
 
 template <typename T>
@@ -102,7 +109,7 @@ hipError_t slope(const GateSlopeArgs& a, bool sums32, hipStream_t s) {
 
 template <typename T>
 const GateOps& ops() {
-  static const GateOps o = {&pair<T>, &slope<T>};
+  static const GateOps o = {&pair<T>, &apart<T>, &slope<T>};
   return o;
 }
 

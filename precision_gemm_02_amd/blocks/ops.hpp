@@ -33,8 +33,12 @@ hipError_t prod8_e4m3_wide(const Prod8Args& a, int w_type, int kernel, bool dire
 hipError_t prod8_e5m2_wide(const Prod8Args& a, int w_type, int kernel, bool direct, hipStream_t s);
 
 struct GateOps {
-  // a gated product, or dX of one, and the sum of its splits
-  hipError_t (*pair)(const PairArgs& a, int lb, int pair, int kernel, int loading, hipStream_t s);
+  // a gated product (kColumns), or dX of one (kHalves), and the sum of its splits; whole: by
+  // pair_whole_kernel
+  hipError_t (*pair)(const PairArgs& a, int lb, int pair, int kernel, int loading, bool whole,
+                     hipStream_t s);
+  // one or two products of outer-order operands (kApart), whole
+  hipError_t (*apart)(const PairArgs& a, int kernel, hipStream_t s);
   hipError_t (*slope)(const GateSlopeArgs& a, bool sums32, hipStream_t s);
 };
 const GateOps& gate_ops_f32();

@@ -51,7 +51,7 @@ struct Walk {
   }
 };
 
-template <typename T, int LB, int BM, int BN, int WGM, int WGN, int PAIR>
+template <typename T, int LA, int LB, int BM, int BN, int WGM, int WGN, int PAIR>
 __global__ __launch_bounds__(WGM* WGN * 64) void pair_whole_kernel(const PairArgs args) {
   const ProdArgs& a = args.p;
   constexpr int S = sizeof(T), NT = WGM * WGN * 64;
@@ -61,7 +61,6 @@ __global__ __launch_bounds__(WGM* WGN * 64) void pair_whole_kernel(const PairArg
   constexpr int EPI_LD = WN + 4;
   constexpr int EPI = WGM * WGN * 32 * EPI_LD * 4;   // 32 rows per wave
   constexpr int LDS = 3 * SLOT_A + 2 * SLOT_B > EPI ? 3 * SLOT_A + 2 * SLOT_B : EPI;
-  static_assert(PAIR == kHalves || LB == kInner, "both weights' columns in one load");
   __shared__ __attribute__((aligned(128))) char lds[LDS];
 
   const int lane = threadIdx.x & 63;
@@ -69,7 +68,9 @@ __global__ __launch_bounds__(WGM* WGN * 64) void pair_whole_kernel(const PairArg
   const int wm = (wave / WGN) * WM, wn = (wave % WGN) * WN;
   constexpr int COLS = PAIR == kColumns ? BN / 2 : BN;   // results of a tile
   int tm, tn, k_lo = 0, k_hi = a.K;
-  map_tile(blockIdx.x, a.tiles_m, a.tiles_n, &tm, &tn);
+  map_tile(blockIdx.x, a.tiles_m, PAIR == kApart ? a.tiles_n * args.count : a.tiles_n, &tm, &tn);
+  const bool other = PAIR == kApart && tn >= a.tiles_n;
+  if (other) tn -= a.tiles_n;
   const int row0 = tm * BM, col0 = tn * COLS;
   if (a.splits > 1) {
     k_lo = blockIdx.y * a.k_split;
@@ -77,54 +78,55 @@ __global__ __launch_bounds__(WGM* WGN * 64) void pair_whole_kernel(const PairArg
   }
   const int nk = (k_hi - k_lo) / BK;
 
-  using TA = OperandTile<T, kInner, BM, NT>;
-  using TB = OperandTile<T, LB, BN, NT>;
-  constexpr int LA_ = TA::LOADS, LB_ = TB::LOADS;
-  uint32_t va[LA_], vb[LB_];
+  // kColumns: B's slot holds a tile of either weight, half as wide
+  constexpr int SUBS = PAIR == kColumns ? 2 : 1, SUB = BN / SUBS, SUB_BYTES = SUB * 128;
+  using TA = OperandTile<T, LA, BM, NT>;
+  using TB = OperandTile<T, LB, SUB, NT>;
+  constexpr int NA = TA::LOADS, NB = SUBS * TB::LOADS;
+  // a lane's offsets from its operand's tile; rows and columns outside read the last row
+  // or the first chunk (they reach results that are never stored)
+  uint32_t va[NA], vb[TB::LOADS];
 #pragma unroll
-  for (int j = 0; j < LA_; ++j) {
+  for (int j = 0; j < NA; ++j) {
     int r, c;
     TA::slot(j * NT + (int)threadIdx.x, &r, &c);
-    const int row = row0 + r < a.M ? r : a.M - 1 - row0;
-    va[j] = (uint32_t)row * (uint32_t)(a.lda * S) + c * 16;
+    if constexpr (LA == kInner) {
+      const int row = row0 + r < a.M ? r : a.M - 1 - row0;
+      va[j] = (uint32_t)row * (uint32_t)(a.lda * S) + c * 16;
+    } else {
+      va[j] = (uint32_t)r * (uint32_t)(a.lda * S) + (row0 + c * TA::V < a.M ? c * 16 : 0);
+    }
   }
-  // kColumns: rows of the tile that a wave's load covers belong to one weight
-  auto second = [&](int j) {
-    return PAIR == kColumns && (j * NT + wave * 64) / 8 / 16 % CB >= CB / 2;
-  };
 #pragma unroll
-  for (int j = 0; j < LB_; ++j) {
+  for (int j = 0; j < TB::LOADS; ++j) {
     int r, c;
     TB::slot(j * NT + (int)threadIdx.x, &r, &c);
     if constexpr (LB == kInner) {
-      int col = r;
-      if constexpr (PAIR == kColumns) {
-        const int p = r / 16, in = p % CB;
-        col = (p / CB * (CB / 2) + in % (CB / 2)) * 16 + r % 16;
-      }
-      col = col0 + col < a.N ? col : a.N - 1 - col0;
+      const int col = col0 + r < a.N ? r : a.N - 1 - col0;
       vb[j] = (uint32_t)col * (uint32_t)(a.ldb * S) + c * 16;
     } else {
       vb[j] = (uint32_t)r * (uint32_t)(a.ldb * S) + (col0 + c * TB::V < a.N ? c * 16 : 0);
     }
   }
+  // element (output index, summed index) of an operand
+  auto place = [](const void* base, int order, long long ld, long long out, long long in) {
+    return static_cast<const char*>(base) + (order == kInner ? out * ld + in : in * ld + out) * S;
+  };
   Walk wa, wb;
-  wa.at = static_cast<const char*>(a.A) + ((long long)row0 * a.lda + k_lo) * S;
-  wa.step = 128;
+  wa.at = place(other ? args.A2 : a.A, LA, a.lda, row0, k_lo);
+  wa.step = LA == kInner ? 128 : BK * a.lda * S;
   wb.step = LB == kInner ? 128 : BK * a.ldb * S;
   wa.left = wb.left = nk;
-  const long long second_at = static_cast<const char*>(args.B2) - static_cast<const char*>(a.B);
+  const long long second = static_cast<const char*>(args.B2) - static_cast<const char*>(a.B);
   long long jump = 0;
   int before = -1;                 // kHalves: B's tiles left when the second weight begins
   if constexpr (PAIR == kHalves) {
     const bool on = k_lo >= args.half;
-    const int in = on ? k_lo - args.half : k_lo;
-    wb.at = static_cast<const char*>(on ? args.B2 : a.B) +
-            (LB == kInner ? (long long)col0 * a.ldb + in : in * a.ldb + col0) * S;
-    jump = second_at - (LB == kInner ? args.half : args.half * a.ldb) * S;
+    wb.at = place(on ? args.B2 : a.B, LB, a.ldb, col0, on ? k_lo - args.half : k_lo);
+    jump = second - (LB == kInner ? args.half : args.half * a.ldb) * S;
     before = (k_hi - args.half) / BK;
   } else {
-    wb.at = static_cast<const char*>(a.B) + ((long long)col0 * a.ldb + k_lo) * S;
+    wb.at = place(other ? args.B2 : a.B, LB, a.ldb, col0, k_lo);
   }
   const uint32_t lds_wave = lds_address(lds) + wave * 1024;
 
@@ -134,15 +136,16 @@ __global__ __launch_bounds__(WGM* WGN * 64) void pair_whole_kernel(const PairArg
 #pragma unroll
     for (int j = decltype(j0)::value; j < decltype(j1)::value; ++j)
       tile_load(d, va[j], lds_wave + to * SLOT_A + j * NT * 16);
-    if constexpr (decltype(j1)::value == LA_) wa.next(0);
+    if constexpr (decltype(j1)::value == NA) wa.next(0);
   };
   auto load_b = [&](auto j0, auto j1, int to) {
     const u32x4 d = descriptor(wb.at);
-    const u32x4 e = PAIR == kColumns ? descriptor(wb.at + second_at) : d;
+    const u32x4 e = PAIR == kColumns ? descriptor(wb.at + second) : d;
 #pragma unroll
     for (int j = decltype(j0)::value; j < decltype(j1)::value; ++j)
-      tile_load(second(j) ? e : d, vb[j], lds_wave + 3 * SLOT_A + to * SLOT_B + j * NT * 16);
-    if constexpr (decltype(j1)::value == LB_)
+      tile_load(j < TB::LOADS ? d : e, vb[j % TB::LOADS],
+                lds_wave + 3 * SLOT_A + to * SLOT_B + j * NT * 16);
+    if constexpr (decltype(j1)::value == NB)
       wb.next(PAIR == kHalves && wb.left - 1 == before ? jump : 0);
   };
 
@@ -154,29 +157,37 @@ __global__ __launch_bounds__(WGM* WGN * 64) void pair_whole_kernel(const PairArg
 
   if (nk > 0) {
     constexpr std::integral_constant<int, 0> zero{};
-    constexpr std::integral_constant<int, LA_> all_a{};
-    constexpr std::integral_constant<int, LB_> all_b{};
+    constexpr std::integral_constant<int, NA> all_a{};
+    constexpr std::integral_constant<int, NB> all_b{};
     load_a(zero, all_a, 0);
     load_b(zero, all_b, 0);
     load_a(zero, all_a, 1);
     load_b(zero, all_b, 1);
     load_a(zero, all_a, 2);
-    wait_loads<2 * LA_ + LB_>();
+    wait_loads<2 * NA + NB>();
     workgroup_barrier();
 
-    u32x4 fa[2][2], fb[CB][2];
+    // B's first halves of two tiles in turn: those of the next are read under the last
+    // block; its second halves follow as this tile's come free
+    u32x4 fa[2][2], fb0[2][CB], fb1[CB];
     auto read_a = [&](const char* from, int g) {
       fa[g & 1][0] = TA::frag(from, wm, g, 0);
       fa[g & 1][1] = TA::frag(from, wm, g, 1);
     };
+    auto read_b = [&](const char* from, int c, int half) {
+      if constexpr (PAIR == kColumns)
+        return TB::frag(from + (c >= CB / 2 ? SUB_BYTES : 0), wn / 2, c % (CB / 2), half);
+      else
+        return TB::frag(from, wn, c, half);
+    };
     read_a(lds, 0);
 #pragma unroll
     for (int c = 0; c < CB; ++c) {
-      fb[c][0] = TB::frag(lds + 3 * SLOT_A, wn, c, 0);
-      fb[c][1] = TB::frag(lds + 3 * SLOT_A, wn, c, 1);
+      fb0[0][c] = read_b(lds + 3 * SLOT_A, c, 0);
+      fb1[c] = read_b(lds + 3 * SLOT_A, c, 1);
     }
-    auto tile = [&](auto place) {
-      constexpr int sa = decltype(place)::value % 3, sb = decltype(place)::value % 2;
+    auto tile = [&](auto place_) {
+      constexpr int sa = decltype(place_)::value % 3, sb = decltype(place_)::value % 2;
       const char* const a0 = lds + sa * SLOT_A;
       const char* const a1 = lds + (sa + 1) % 3 * SLOT_A;
       const char* const b1 = lds + 3 * SLOT_A + (sb ^ 1) * SLOT_B;
@@ -185,27 +196,29 @@ __global__ __launch_bounds__(WGM* WGN * 64) void pair_whole_kernel(const PairArg
         constexpr bool M = g == 1, E = g == RB - 1;
         if constexpr (E) {
           // all but the tile after next (of which, in two blocks, B's is not yet asked for)
-          wait_loads<M ? LA_ : LA_ + LB_>();
+          wait_loads<M ? NA : NA + NB>();
           workgroup_barrier();
           read_a(a1, 0);                        // past the last tile: some LDS, never used
+#pragma unroll
+          for (int c = 0; c < CB; ++c) fb0[sb ^ 1][c] = read_b(b1, c, 0);
         } else {
           if constexpr (M) workgroup_barrier();
           read_a(a0, g + 1);
         }
         // B's loads over the blocks behind M, A's in the last one
         constexpr int PARTS = RB > 2 ? RB - 2 : 1;
-        constexpr int b0 = g >= 1 && (g < RB - 1 || RB == 2) ? LB_ * (g - 1) / PARTS : LB_;
-        constexpr int b_end = g >= 1 && (g < RB - 1 || RB == 2) ? LB_ * g / PARTS : LB_;
-        if constexpr (b0 < b_end)
-          load_b(std::integral_constant<int, b0>{}, std::integral_constant<int, b_end>{}, sb);
+        constexpr bool ask = g >= 1 && (g < RB - 1 || RB == 2);
+        constexpr int from = ask ? NB * (g - 1) / PARTS : 0, to = ask ? NB * g / PARTS : 0;
+        if constexpr (from < to)
+          load_b(std::integral_constant<int, from>{}, std::integral_constant<int, to>{}, sb);
         if constexpr (E) load_a(zero, all_a, sa);
 #pragma unroll
-        for (int h = 0; h < 2; ++h)
+        for (int c = 0; c < CB; ++c) acc[g][c] = Elem<T>::mfma(fb0[sb][c], fa[g & 1][0], acc[g][c]);
 #pragma unroll
-          for (int c = 0; c < CB; ++c) {
-            acc[g][c] = Elem<T>::mfma(fb[c][h], fa[g & 1][h], acc[g][c]);
-            if constexpr (E) fb[c][h] = TB::frag(b1, wn, c, h);
-          }
+        for (int c = 0; c < CB; ++c) {
+          acc[g][c] = Elem<T>::mfma(fb1[c], fa[g & 1][1], acc[g][c]);
+          if constexpr (E) fb1[c] = read_b(b1, c, 1);
+        }
         __builtin_amdgcn_sched_barrier(0);
       });
     };
@@ -261,9 +274,13 @@ __global__ __launch_bounds__(WGM* WGN * 64) void pair_whole_kernel(const PairArg
             finish_gate<T>(args, m, n, v, u, bg, bu);
           }
         } else if (a.splits > 1) {
-          put_row8<float>(a.partial, ((long long)blockIdx.y * a.M + m) * a.N, n, a.N, v);
+          const long long matrix = PAIR == kApart ? (long long)blockIdx.y * args.count + other
+                                                  : blockIdx.y;
+          put_row8<float>(a.partial, (matrix * a.M + m) * a.N, n, a.N, v);
         } else {
-          put_row8<T>(a.D, m * a.ldd, n, a.N, v);
+          void* D = other ? args.D2 : a.D;
+          if (a.out32) put_row8<float>(D, m * a.ldd, n, a.N, v);
+          else put_row8<T>(D, m * a.ldd, n, a.N, v);
         }
       }
     }

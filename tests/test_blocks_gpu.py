@@ -359,6 +359,45 @@ def test_gated_linear_backward_exact_integers(dtype, order, shape, pad, out):
     assert torch.equal(only, dbu)
 
 
+@pytest.mark.parametrize("dtype", TYPES, ids=ids)
+@pytest.mark.parametrize("order", ["kn", "nk"])
+@pytest.mark.parametrize("shape", [(4104, 4096, 192), (1024, 1032, 384), (320, 512, 640), (2048, 2056, 64),
+                                   (64, 64, 4096), (4160, 1096, 1000)], ids=str)
+def test_gated_linear_large(dtype, order, shape):
+    """Tiles of every class over several rounds, summed indices of one whole step to many,
+    whole and not; exact sums (64-bit products on the GPU)."""
+    m, n, k = shape
+    g = torch.Generator(device="cuda").manual_seed(m + n)
+
+    def ints_(*s, hi=2):
+        return torch.randint(-hi, hi + 1, s, generator=g, device="cuda").to(dtype)
+
+    X, D, Zg, Zu = ints_(m, k, hi=1), ints_(m, n), ints_(m, n), ints_(m, n)
+    Wg, Wu = ((ints_(k, n) if order == "kn" else ints_(n, k).t()) for _ in range(2))
+    Y = torch.full((m, n), math.nan, device="cuda")
+    pg.gated_linear(X, Wg, Wu, Y, act="relu")
+    x, wg, wu = X.double(), Wg.double(), Wu.double()
+    same = torch.equal(Y.double(), (x @ wg).clamp(min=0) * (x @ wu))
+    assert same
+    dX = torch.full((m, k), math.nan, dtype=dtype, device="cuda")
+    dWg, dWu = (torch.full_like(w, math.nan, dtype=F32) for w in (Wg, Wu))
+    ws = space(pg.gated_linear_backward_workspace(m, n, k, dtype))
+    pg.gated_linear_backward(D, X, Wg, Wu, Zg, Zu, act="relu", dX=dX, dW_gate=dWg, dW_up=dWu, ws=ws)
+    d, zg, zu = D.double(), Zg.double(), Zu.double()
+    dzg, dzu = d * zu * (zg > 0), d * zg.clamp(min=0)
+    same = torch.equal(dX, (dzg @ wg.t() + dzu @ wu.t()).to(dtype))
+    assert same
+    for got, dz in ((dWg, dzg), (dWu, dzu)):
+        same = torch.equal(got.double(), x.t() @ dz)
+        assert same
+    # one of both, in the other order and in the inputs' type
+    one = torch.full((n, k) if order == "kn" else (k, n), math.nan, dtype=dtype, device="cuda")
+    one = one.t() if order == "kn" else one
+    pg.gated_linear_backward(D, X, None, None, Zg, Zu, act="relu", dW_up=one, ws=ws)
+    same = torch.equal(one, dWu.to(dtype))
+    assert same
+
+
 @pytest.mark.parametrize("act", ["none", "relu", "gelu", "gelu_tanh", "silu"])
 @pytest.mark.parametrize("dtype", TYPES, ids=ids)
 @pytest.mark.parametrize("shape", [(5, 70, 300), (70, 150, 260), (24, 40, 6000)], ids=str)
