@@ -51,6 +51,20 @@ struct Walk {
   }
 };
 
+// Two blocks of results (lane 16 g + i: row i, columns 4 g .. 4 g + 3) as 8 consecutive
+// columns per lane: lane group g has columns 8 (g / 2) .. of block g % 2.
+__device__ __forceinline__ void join(f32x4 x, f32x4 y, float* v) {
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const float xj = x[j], yj = y[j];           // (a bit_cast of x[j] itself takes element 0)
+    const auto p = __builtin_amdgcn_permlane16_swap(__builtin_bit_cast(uint32_t, xj),
+                                                    __builtin_bit_cast(uint32_t, yj), false, false);
+    const uint32_t lo = p[0], hi = p[1];
+    v[j] = __builtin_bit_cast(float, lo);
+    v[4 + j] = __builtin_bit_cast(float, hi);
+  }
+}
+
 template <typename T, int LA, int LB, int BM, int BN, int WGM, int WGN, int PAIR>
 __global__ __launch_bounds__(WGM* WGN * 64) void pair_whole_kernel(const PairArgs args) {
   const ProdArgs& a = args.p;
@@ -58,10 +72,7 @@ __global__ __launch_bounds__(WGM* WGN * 64) void pair_whole_kernel(const PairArg
   constexpr int WM = BM / WGM, WN = BN / WGN, RB = WM / 16, CB = WN / 16;
   constexpr int BK = 128 / S;
   constexpr int SLOT_A = BM * 128, SLOT_B = BN * 128;
-  constexpr int EPI_LD = WN + 4;
-  constexpr int EPI = WGM * WGN * 32 * EPI_LD * 4;   // 32 rows per wave
-  constexpr int LDS = 3 * SLOT_A + 2 * SLOT_B > EPI ? 3 * SLOT_A + 2 * SLOT_B : EPI;
-  __shared__ __attribute__((aligned(128))) char lds[LDS];
+  __shared__ __attribute__((aligned(128))) char lds[3 * SLOT_A + 2 * SLOT_B];
 
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
@@ -229,63 +240,44 @@ __global__ __launch_bounds__(WGM* WGN * 64) void pair_whole_kernel(const PairArg
       });
     wait_loads<0>();                            // the loads past the end
   }
-  __syncthreads();   // the operands' LDS becomes the epilogue's
-
-  // Epilogue: as pair_tile_kernel's
-  float* stg = reinterpret_cast<float*>(lds) + wave * 32 * EPI_LD;
-  constexpr int WC = PAIR == kColumns ? WN / 2 : WN;               // results of a wave's row
-  constexpr int LPR = WC / 8, RPP = 64 / LPR, PASSES = 32 / RPP;   // lanes per row, rows per pass
-  const int col = (lane % LPR) * 8, n = col0 + (wn / WN) * WC + col;
-  float bg[8], bu[8];
-  if constexpr (PAIR == kColumns) {
-    if (a.splits <= 1) gate_bias<T>(args, n, bg, bu);
-  }
-#pragma unroll 1
-  for (int r = 0; r < RB / 2; ++r) {
-    const int m0 = row0 + wm + 32 * r + lane / LPR;
-    static_for<RB / 2>([&](auto rc) {
-      constexpr int q = decltype(rc)::value;
-      if (r == q) {
+  // Epilogue: 8 consecutive columns per lane, of two blocks beside each other, or (where a
+  // wave has one block of a weight) below each other.
+  constexpr int WC = PAIR == kColumns ? WN / 2 : WN, WCB = WC / 16;   // results of a wave's row
+  constexpr bool BELOW = WCB == 1;
+  constexpr int DR = BELOW ? 2 : 1, DC = BELOW ? 1 : 2;
+  const int i16 = lane & 15, half = lane >> 5, which = lane >> 4 & 1;
 #pragma unroll
-        for (int h = 0; h < 2; ++h)
+  for (int c = 0; c < WCB; c += DC) {
+    const int n = col0 + wn / WN * WC + 16 * (BELOW ? c : c + which) + 8 * half;
+    float bg[8], bu[8];
+    if constexpr (PAIR == kColumns) {
+      if (a.splits <= 1) gate_bias<T>(args, n, bg, bu);
+    }
 #pragma unroll
-          for (int c = 0; c < CB; ++c)
-            *reinterpret_cast<f32x4*>(stg + (16 * h + (lane & 15)) * EPI_LD + 16 * c +
-                                      4 * (lane >> 4)) = acc[2 * q + h][c];
-      }
-    });
-    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
-    __builtin_amdgcn_wave_barrier();
-#pragma unroll
-    for (int p = 0; p < PASSES; ++p) {
-      const float* from = stg + (p * RPP + lane / LPR) * EPI_LD + col;
-      const int m = m0 + p * RPP;
-      if (m < a.M && n < a.N) {
-        float v[8], u[8];
-        *reinterpret_cast<f32x4*>(v) = *reinterpret_cast<const f32x4*>(from);
-        *reinterpret_cast<f32x4*>(v + 4) = *reinterpret_cast<const f32x4*>(from + 4);
-        if constexpr (PAIR == kColumns) {
-          *reinterpret_cast<f32x4*>(u) = *reinterpret_cast<const f32x4*>(from + WC);
-          *reinterpret_cast<f32x4*>(u + 4) = *reinterpret_cast<const f32x4*>(from + WC + 4);
-          if (a.splits > 1) {
-            put_partial(a, blockIdx.y, 0, m, n, v);
-            put_partial(a, blockIdx.y, 1, m, n, u);
-          } else {
-            finish_gate<T>(args, m, n, v, u, bg, bu);
-          }
-        } else if (a.splits > 1) {
-          const long long matrix = PAIR == kApart ? (long long)blockIdx.y * args.count + other
-                                                  : blockIdx.y;
-          put_row8<float>(a.partial, (matrix * a.M + m) * a.N, n, a.N, v);
+    for (int r = 0; r < RB; r += DR) {
+      const int m = row0 + wm + 16 * (BELOW ? r + which : r) + i16;
+      float v[8], u[8];
+      join(acc[r][c], BELOW ? acc[r + DR - 1][c] : acc[r][c + DC - 1], v);
+      if constexpr (PAIR == kColumns)
+        join(acc[r][WCB + c], BELOW ? acc[r + DR - 1][WCB + c] : acc[r][WCB + c + DC - 1], u);
+      if (m >= a.M || n >= a.N) continue;
+      if constexpr (PAIR == kColumns) {
+        if (a.splits > 1) {
+          put_partial(a, blockIdx.y, 0, m, n, v);
+          put_partial(a, blockIdx.y, 1, m, n, u);
         } else {
-          void* D = other ? args.D2 : a.D;
-          if (a.out32) put_row8<float>(D, m * a.ldd, n, a.N, v);
-          else put_row8<T>(D, m * a.ldd, n, a.N, v);
+          finish_gate<T>(args, m, n, v, u, bg, bu);
         }
+      } else if (a.splits > 1) {
+        const long long matrix = PAIR == kApart ? (long long)blockIdx.y * args.count + other
+                                                : blockIdx.y;
+        put_row8<float>(a.partial, (matrix * a.M + m) * a.N, n, a.N, v);
+      } else {
+        void* D = other ? args.D2 : a.D;
+        if (a.out32) put_row8<float>(D, m * a.ldd, n, a.N, v);
+        else put_row8<T>(D, m * a.ldd, n, a.N, v);
       }
     }
-    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
-    __builtin_amdgcn_wave_barrier();
   }
 }
 
