@@ -378,7 +378,10 @@ int pgemm_linear_fp8(pgemm_fp8_kind kind, int m, int n, int k, pgemm_rows X, pge
   const hipStream_t s = static_cast<hipStream_t>(stream);
   const Prod8 prod = kind.x_type == PGEMM_E4M3 ? (wide ? prod8_e4m3_wide : prod8_e4m3)
                                                : (wide ? prod8_e5m2_wide : prod8_e5m2);
-  return status(prod(args, kind.w_type, plan.kernel, direct, s));
+  const long long far = 0x7fffffffLL / (256 * 4);   // scales' offsets within a tile fit 32 bits
+  const bool whole = direct && !wide && whole_tiles(1, X.ld, W.ld, k) && x_scales.row_stride < far &&
+                     w_scales.row_stride < far;
+  return status(prod(args, kind.w_type, plan.kernel, whole ? kWhole : direct ? kDirect : kThrough, s));
 }
 
 size_t pgemm_linear_fp8_workspace(int m, int n, int k) {

@@ -4,8 +4,8 @@
 namespace pgemm {
 namespace blocks {
 
-hipError_t prod8_e4m3(const Prod8Args& a, int w_type, int kernel, bool direct, hipStream_t s) {
-  return prod8_of<kE4M3, false>(a, w_type, kernel, direct, s);
+hipError_t prod8_e4m3(const Prod8Args& a, int w_type, int kernel, int loading, hipStream_t s) {
+  return prod8_of<kE4M3, false>(a, w_type, kernel, loading, s);
 }
 
 }  // namespace blocks

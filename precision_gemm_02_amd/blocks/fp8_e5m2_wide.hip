@@ -4,8 +4,8 @@
 namespace pgemm {
 namespace blocks {
 
-hipError_t prod8_e5m2_wide(const Prod8Args& a, int w_type, int kernel, bool direct, hipStream_t s) {
-  return prod8_of<kE5M2, true>(a, w_type, kernel, direct, s);
+hipError_t prod8_e5m2_wide(const Prod8Args& a, int w_type, int kernel, int loading, hipStream_t s) {
+  return prod8_of<kE5M2, true>(a, w_type, kernel, loading, s);
 }
 
 }  // namespace blocks

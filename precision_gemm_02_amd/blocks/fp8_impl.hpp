@@ -6,6 +6,7 @@
 #include "fp8.hpp"
 #include "launch.hpp"
 #include "ops.hpp"
+#include "whole8.hpp"
 
 namespace pgemm {
 namespace blocks {
@@ -19,6 +20,15 @@ hipError_t tile8(const Prod8Args& a, dim3 grid, hipStream_t s) {
                 WGM * WGN * 64, a, s);
 }
 
+template <int FA, int FB, bool COLS>
+hipError_t whole8(const Prod8Args& a, int kernel, dim3 grid, hipStream_t s) {
+  if (kernel == kTile256)
+    return launch(&prod8_whole_kernel<FA, FB, 256, 256, 2, 4, COLS>, grid, prod_threads(kTile256), a, s);
+  if (kernel == kTile128)
+    return launch(&prod8_whole_kernel<FA, FB, 128, 128, 2, 2, COLS>, grid, prod_threads(kTile128), a, s);
+  return launch(&prod8_whole_kernel<FA, FB, 64, 64, 2, 2, COLS>, grid, prod_threads(kTile64), a, s);
+}
+
 template <int FA, int FB, bool COLS, bool WIDE, int MB, int NB>
 hipError_t rows8(const Prod8Args& a, dim3 grid, hipStream_t s) {
   static_assert(prod_threads(kFew16) == 512, "the checked launch");
@@ -26,17 +36,19 @@ hipError_t rows8(const Prod8Args& a, dim3 grid, hipStream_t s) {
 }
 
 template <int FA, int FB, bool COLS, bool WIDE>
-hipError_t prod8(const Prod8Args& a, int kernel, bool direct, hipStream_t s) {
+hipError_t prod8(const Prod8Args& a, int kernel, int loading, hipStream_t s) {
   const ProdGrid g = prod_grid(a.p, kDense, kernel);
   const dim3 grid((unsigned)g.x, (unsigned)g.y);
   hipError_t e = hipErrorInvalidValue;
-  if (kernel == kTile256) {
+  if (!WIDE && loading == kWhole && kernel <= kTile64) {
+    if constexpr (!WIDE) e = whole8<FA, FB, COLS>(a, kernel, grid, s);
+  } else if (kernel == kTile256) {
     if constexpr (!WIDE) e = tile8<FA, FB, COLS, WIDE, kTile256, 2, 4, true>(a, grid, s);
   } else if (kernel == kTile128) {
-    e = direct ? tile8<FA, FB, COLS, WIDE, kTile128, 2, 2, true>(a, grid, s)
+    e = loading != kThrough ? tile8<FA, FB, COLS, WIDE, kTile128, 2, 2, true>(a, grid, s)
                : tile8<FA, FB, COLS, WIDE, kTile128, 2, 2, false>(a, grid, s);
   } else if (kernel == kTile64) {
-    e = direct ? tile8<FA, FB, COLS, WIDE, kTile64, 2, 2, true>(a, grid, s)
+    e = loading != kThrough ? tile8<FA, FB, COLS, WIDE, kTile64, 2, 2, true>(a, grid, s)
                : tile8<FA, FB, COLS, WIDE, kTile64, 2, 2, false>(a, grid, s);
   } else if (kernel == kFew16) {
     e = rows8<FA, FB, COLS, WIDE, 1, 1>(a, grid, s);
@@ -53,13 +65,13 @@ hipError_t prod8(const Prod8Args& a, int kernel, bool direct, hipStream_t s) {
 }
 
 template <int FA, bool WIDE>
-hipError_t prod8_of(const Prod8Args& a, int w_type, int kernel, bool direct, hipStream_t s) {
+hipError_t prod8_of(const Prod8Args& a, int w_type, int kernel, int loading, hipStream_t s) {
   const bool cols = a.w_shift == 0;
   if (w_type == kE4M3)
-    return cols ? prod8<FA, kE4M3, true, WIDE>(a, kernel, direct, s)
-                : prod8<FA, kE4M3, false, WIDE>(a, kernel, direct, s);
-  return cols ? prod8<FA, kE5M2, true, WIDE>(a, kernel, direct, s)
-              : prod8<FA, kE5M2, false, WIDE>(a, kernel, direct, s);
+    return cols ? prod8<FA, kE4M3, true, WIDE>(a, kernel, loading, s)
+                : prod8<FA, kE4M3, false, WIDE>(a, kernel, loading, s);
+  return cols ? prod8<FA, kE5M2, true, WIDE>(a, kernel, loading, s)
+              : prod8<FA, kE5M2, false, WIDE>(a, kernel, loading, s);
 }
 
 }  // namespace

@@ -25,12 +25,14 @@ const NormOps& norm_ops(int dtype);
 hipError_t quantize_op(const QuantizeArgs& a, int dtype, int type, bool outer, hipStream_t s);
 
 // The product of a plan (and the sum of its splits), A of the type named, W of w_type,
-// for results of 16 bits and (wide) of 32, which have no tiles of 256 x 256.
-typedef hipError_t (*Prod8)(const Prod8Args& a, int w_type, int kernel, bool direct, hipStream_t s);
-hipError_t prod8_e4m3(const Prod8Args& a, int w_type, int kernel, bool direct, hipStream_t s);
-hipError_t prod8_e5m2(const Prod8Args& a, int w_type, int kernel, bool direct, hipStream_t s);
-hipError_t prod8_e4m3_wide(const Prod8Args& a, int w_type, int kernel, bool direct, hipStream_t s);
-hipError_t prod8_e5m2_wide(const Prod8Args& a, int w_type, int kernel, bool direct, hipStream_t s);
+// for results of 16 bits and (wide) of 32, which have no tiles of 256 x 256.  loading: kDirect,
+// kThrough, or kWhole where prod8_whole_kernel takes its tiles (16-bit results).
+constexpr int kWhole = 3;
+typedef hipError_t (*Prod8)(const Prod8Args& a, int w_type, int kernel, int loading, hipStream_t s);
+hipError_t prod8_e4m3(const Prod8Args& a, int w_type, int kernel, int loading, hipStream_t s);
+hipError_t prod8_e5m2(const Prod8Args& a, int w_type, int kernel, int loading, hipStream_t s);
+hipError_t prod8_e4m3_wide(const Prod8Args& a, int w_type, int kernel, int loading, hipStream_t s);
+hipError_t prod8_e5m2_wide(const Prod8Args& a, int w_type, int kernel, int loading, hipStream_t s);
 
 struct GateOps {
   // a gated product (kColumns), or dX of one (kHalves), and the sum of its splits; whole: by

@@ -65,6 +65,22 @@ __device__ __forceinline__ void join(f32x4 x, f32x4 y, float* v) {
   }
 }
 
+// Row r of the blocks of results, by branches (r is the same for the wave).  The empty asm
+// keeps the compiler from making one indexed copy of them, through memory.
+template <int RB, int CB>
+__device__ __forceinline__ void take(const f32x4 (&acc)[RB][CB], int r, f32x4 (&row)[CB]) {
+  static_for<RB>([&](auto q) {
+    if (r == decltype(q)::value) {
+#pragma unroll
+      for (int c = 0; c < CB; ++c) {
+        f32x4 t = acc[decltype(q)::value][c];
+        asm volatile("" : "+v"(t));
+        row[c] = t;
+      }
+    }
+  });
+}
+
 template <typename T, int LA, int LB, int BM, int BN, int WGM, int WGN, int PAIR>
 __global__ __launch_bounds__(WGM* WGN * 64) void pair_whole_kernel(const PairArgs args) {
   const ProdArgs& a = args.p;
@@ -244,29 +260,34 @@ __global__ __launch_bounds__(WGM* WGN * 64) void pair_whole_kernel(const PairArg
   // wave has one block of a weight) below each other.
   constexpr int WC = PAIR == kColumns ? WN / 2 : WN, WCB = WC / 16;   // results of a wave's row
   constexpr bool BELOW = WCB == 1;
-  constexpr int DR = BELOW ? 2 : 1, DC = BELOW ? 1 : 2;
-  const int i16 = lane & 15, half = lane >> 5, which = lane >> 4 & 1;
+  const int which = lane >> 4 & 1;
+  const int n0 = col0 + wn / WN * WC + (BELOW ? 0 : 16 * which) + 8 * (lane >> 5);
+  float bg[WCB / 2 + 1][8], bu[WCB / 2 + 1][8];
+  if constexpr (PAIR == kColumns) {
 #pragma unroll
-  for (int c = 0; c < WCB; c += DC) {
-    const int n = col0 + wn / WN * WC + 16 * (BELOW ? c : c + which) + 8 * half;
-    float bg[8], bu[8];
-    if constexpr (PAIR == kColumns) {
-      if (a.splits <= 1) gate_bias<T>(args, n, bg, bu);
-    }
+    for (int c = 0; c < WCB; c += 2)
+      if (a.splits <= 1) gate_bias<T>(args, n0 + 16 * c, bg[c / 2], bu[c / 2]);
+  }
+#pragma unroll 1
+  for (int r = 0; r < RB; r += BELOW ? 2 : 1) {
+    const int m = row0 + wm + 16 * (BELOW ? r + which : r) + (lane & 15);
+    f32x4 row[CB], below[CB];
+    take<RB, CB>(acc, r, row);
+    if constexpr (BELOW) take<RB, CB>(acc, r + 1, below);
 #pragma unroll
-    for (int r = 0; r < RB; r += DR) {
-      const int m = row0 + wm + 16 * (BELOW ? r + which : r) + i16;
+    for (int c = 0; c < WCB; c += 2) {
+      const int n = n0 + 16 * c;
       float v[8], u[8];
-      join(acc[r][c], BELOW ? acc[r + DR - 1][c] : acc[r][c + DC - 1], v);
+      join(row[c], BELOW ? below[c] : row[c + 1 - BELOW], v);
       if constexpr (PAIR == kColumns)
-        join(acc[r][WCB + c], BELOW ? acc[r + DR - 1][WCB + c] : acc[r][WCB + c + DC - 1], u);
+        join(row[WCB + c], BELOW ? below[WCB + c] : row[WCB + c + 1 - BELOW], u);
       if (m >= a.M || n >= a.N) continue;
       if constexpr (PAIR == kColumns) {
         if (a.splits > 1) {
           put_partial(a, blockIdx.y, 0, m, n, v);
           put_partial(a, blockIdx.y, 1, m, n, u);
         } else {
-          finish_gate<T>(args, m, n, v, u, bg, bu);
+          finish_gate<T>(args, m, n, v, u, bg[c / 2], bu[c / 2]);
         }
       } else if (a.splits > 1) {
         const long long matrix = PAIR == kApart ? (long long)blockIdx.y * args.count + other

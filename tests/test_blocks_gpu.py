@@ -661,6 +661,38 @@ def test_linear_fp8_exact(types, shape, rows, pad):
         y.check("Y")
 
 
+@pytest.mark.parametrize("rows", [1, 128])
+@pytest.mark.parametrize("shape", [(4104, 4096, 256), (1024, 1032, 384), (320, 512, 640), (2048, 2056, 128),
+                                   (64, 64, 8192), (4160, 1096, 1040), (520, 1000, 8320)], ids=str)
+@pytest.mark.parametrize("types", [(E4M3, E4M3), (E5M2, E4M3)], ids=lambda t: ids8(t[0]) + ids8(t[1]))
+def test_linear_fp8_large(types, shape, rows):
+    """Tiles of every class over several rounds, one block to many, whole and not; exact
+    sums (64-bit products on the GPU)."""
+    m, n, k = shape
+    g = torch.Generator(device="cuda").manual_seed(m + n)
+
+    def numbers(*s, dtype):
+        return torch.randint(-2, 3, s, generator=g, device="cuda").float().to(dtype)
+
+    def scale(*s):
+        return torch.exp2(torch.randint(-1, 2, s, generator=g, device="cuda").float())
+
+    X, W = numbers(m, k, dtype=types[0]), numbers(n, k, dtype=types[1])
+    kb, nb = -(-k // 128), -(-n // rows)
+    sx, sw = scale(m, kb), scale(nb, kb)
+    bias = torch.randint(-3, 4, (n,), generator=g, device="cuda").float()
+    R = torch.randint(-3, 4, (m, n), generator=g, device="cuda").float()
+    z = (X.double() * spread64(sx, m, k)) @ (W.double() * spread64(sw, n, k)).t() + bias.double()
+    ws = space(pg.linear_fp8_workspace(m, n, k))
+    for out in (BF16, F16, F32):
+        for space_ in (None, ws):
+            Y, Z = (torch.full((m, n), math.nan, dtype=out, device="cuda") for _ in range(2))
+            pg.linear_fp8(X, sx, W.t(), sw.t(), Y, bias=bias.to(out), act="relu", residual=R.to(out),
+                          Z=Z, ws=space_)
+            same = torch.equal(Z, z.to(out)) and torch.equal(Y, (z.clamp(min=0) + R.double()).to(out))
+            assert same
+
+
 @pytest.mark.parametrize("act", ["none", "relu", "gelu", "gelu_tanh", "silu"])
 @pytest.mark.parametrize("out", TYPES, ids=ids)
 @pytest.mark.parametrize("shape", [(7, 300, 700), (150, 270, 1030), (40, 48, 6000)], ids=str)
