@@ -246,6 +246,7 @@ __global__ __launch_bounds__(WGM* WGN * 64) void pair_whole_kernel(const PairArg
           acc[g][c] = Elem<T>::mfma(fb1[c], fa[g & 1][1], acc[g][c]);
           if constexpr (E) fb1[c] = read_b(b1, c, 1);
         }
+        spread<2 * TA::READS + (E ? 2 * CB * TB::READS : 0), 2 * CB * Elem<T>::kMfmas, 0>();
         __builtin_amdgcn_sched_barrier(0);
       });
     };
