@@ -16,12 +16,15 @@ using namespace layers;
 int status(hipError_t e) { return e == hipSuccess ? PGEMM_OK : PGEMM_EHIP; }
 
 // Workgroups along the rows of a norm's gradients.  Each writes its column sums
-// (8 n bytes) once, so that it should have a few rows; and each thread adds its
-// rows one after the other, so that it should not have too many (as far as a launch
-// of norm_sums_kernel goes: 2^24 workgroups).
+// (8 n bytes) once, so that it should have a few rows, and one of 1024 threads on
+// each compute unit is enough (8192 x 4096 bf16: 256 of them 51 us, 512 of 512 threads
+// 52, 1024 of 256 threads 78); and each thread adds its rows one after the other, so
+// that it should not have too many (as far as a launch of norm_sums_kernel goes: 2^24
+// workgroups).
 int norm_groups(int m, int n) {
-  const long long few = ceil_div(m, 4), long_sum = ceil_div(m, 1024);
-  long long g = few < 2 * kUnits ? few : 2 * kUnits;
+  const long long few = ceil_div(m, 2), long_sum = ceil_div(m, 1024);
+  const long long cap = n <= 2048 ? 2 * kUnits : kUnits;
+  long long g = few < cap ? few : cap;
   if (g < long_sum) g = long_sum;
   const long long most = (1LL << 23) / ceil_div(n, 512);
   if (g > most) g = most;
@@ -50,27 +53,43 @@ int gate_columns(int kernel) {
   return kShape[kernel].bn / 2;
 }
 
-// The plan of a gated product: a product with 2 n columns, but for the columns of the
-// few-rows kernels.  Workspace as in plan_product.
-Plan gate_plan(int size, int m, int n, int k, int loading, size_t ws_bytes, bool any_ws) {
-  if (m > 32) return plan_product(size, kInner, kDense, m, 1, 2 * n, k, loading, ws_bytes, any_ws, true,
-                                  false);
+// The plan of a few-rows kernel (at most 32 rows), whose workgroups take `wide` columns where
+// that gives every compute unit one, else 16.  `results`: partial sums of a row and split.
+// (No kernel if one launch does not take them.)
+Plan few_plan(int size, int m, int n, int wide, int results, int k, int loading, size_t ws_bytes,
+              bool any_ws) {
   Plan p;
   p.loading = loading;
-  const bool wide = ceil_div(n, 32) >= 2 * kUnits;
-  p.kernel = wide ? (m <= 16 ? kFew16Wide : kFew32Wide) : (m <= 16 ? kFew16 : kFew32);
+  const bool is_wide = ceil_div(n, wide) >= kUnits;
+  if (m > 32 || ceil_div(n, is_wide ? wide : 16) > kMaxThreads / prod_threads(kFew16)) return p;
+  p.kernel = is_wide ? (m <= 16 ? kFew16Wide : kFew32Wide) : (m <= 16 ? kFew16 : kFew32);
   const int bk = 128 / size;
-  const long long groups = ceil_div(n, gate_columns(p.kernel));
   // one split per free compute unit, each of 16 units of 128 bytes at least
-  long long s = kUnits / groups;
+  long long s = kUnits / ceil_div(n, is_wide ? wide : 16);
   if (s > k / (16 * bk)) s = k / (16 * bk);
   if (s > 64) s = 64;
   if (s > 1) {
     p.k_split = (int)round_up(ceil_div(k, s), bk);
     p.splits = (int)ceil_div(k, p.k_split);
-    if (!any_ws && ws_bytes < split_space(p, kDense, m, 1, 2 * n)) p.splits = 1;
+    if (!any_ws && ws_bytes < split_space(p, kDense, m, 1, results)) p.splits = 1;
   }
   return p;
+}
+
+// The plan of a gated product: a product with 2 n columns, but for few rows.  Workspace as in
+// plan_product.
+Plan gate_plan(int size, int m, int n, int k, int loading, size_t ws_bytes, bool any_ws) {
+  const Plan p = few_plan(size, m, n, gate_columns(kFew16Wide), 2 * n, k, loading, ws_bytes, any_ws);
+  if (p.kernel >= 0) return p;
+  return plan_product(size, kInner, kDense, m, 1, 2 * n, k, loading, ws_bytes, any_ws, true, false);
+}
+
+// The plan of a product in 8 bits (kThrough: no tiles of 256 x 256).
+constexpr int kFewWide8 = 32;                     // columns of its wide few-rows kernels
+Plan plan8(int m, int n, int k, int loading, size_t ws_bytes, bool any_ws) {
+  const Plan p = few_plan(1, m, n, kFewWide8, n, k, loading, ws_bytes, any_ws);
+  if (p.kernel >= 0) return p;
+  return plan_product(1, kInner, kDense, m, 1, n, k, loading, ws_bytes, any_ws, true, false);
 }
 
 int pair_loading(const pgemm_gate_weights& w, int size, int inner) {
@@ -90,13 +109,23 @@ struct GateSpace {
   size_t total() const { return dz + rest; }
 };
 
+// Row chunks of the slope kernel: two workgroups for every compute unit's four, at least
+// 8 rows each.
+int gate_chunks(int rows, int half) {
+  if (half < 1) return 1;
+  long long c = 8 * kUnits / ceil_div(half, threads_per_row(half, 64) * 8);
+  const long long most = ceil_div(rows, 8);
+  if (c > most) c = most;
+  return c < 1 ? 1 : (int)c;
+}
+
 GateSpace gate_space(const pgemm_kind& kind, int m, int n, int k) {
   GateSpace g;
   const int size = size_of(kind.dtype);
   g.half = (int)round_up(n, 64);
   g.dz = align256((size_t)m * 2 * (size_t)g.half * (size_t)size);
   const int rows = m < 1 ? 1 : m;
-  g.chunks = slope_chunks(rows, 1, g.half);
+  g.chunks = gate_chunks(rows, g.half);
   g.rest = 2 * (size_t)g.chunks * (size_t)n * 4;
   const int both = 2LL * k <= kMaxSize ? 2 * k : k;
   const size_t parts[5] = {split_bytes(size, kInner, kDense, rows, 1, k, 2 * g.half, false),
@@ -267,7 +296,10 @@ int pgemm_layer_norm_backward(pgemm_kind kind, int m, int n, pgemm_rows dY, pgem
   float* partial = sums ? static_cast<float*>(workspace) : nullptr;
   if (dX.data != nullptr && m > 0) {
     if (n <= kSumMost) a.partial = partial;
+    const int groups = a.groups;
+    if (a.partial == nullptr) a.groups = m < 8 * kUnits ? m : 8 * kUnits;   // (no column sums)
     const hipError_t e = ops.norm_back(a, s);
+    a.groups = groups;
     if (e != hipSuccess) return PGEMM_EHIP;
   }
   if (!sums) return PGEMM_OK;
@@ -367,14 +399,14 @@ int pgemm_linear_fp8(pgemm_fp8_kind kind, int m, int n, int k, pgemm_rows X, pge
   const bool direct = operand_loading(X.data, X.ld, 1, k, 0) == kDirect &&
                       operand_loading(W.data, W.ld, 1, k, 0) == kDirect;
   const bool wide = kind.out_dtype == PGEMM_F32;
-  // (kThrough: no tiles of 256 x 256)
-  const Plan plan = plan_product(1, kInner, kDense, m, 0, n, k, direct && !wide ? kDirect : kThrough,
-                                 workspace == nullptr ? 0 : workspace_bytes, false);
+  const Plan plan = plan8(m, n, k, direct && !wide ? kDirect : kThrough,
+                          workspace == nullptr ? 0 : workspace_bytes, false);
   if (plan.kernel < 0) return -2;
   a.splits = plan.splits;
   a.k_split = plan.k_split;
   a.partial = static_cast<float*>(workspace);
   set_tiles(&a, plan.kernel, kDense, m);
+  if (plan.kernel >= kFew16Wide) a.tiles_n = (int)ceil_div(n, kFewWide8);
   const hipStream_t s = static_cast<hipStream_t>(stream);
   const Prod8 prod = kind.x_type == PGEMM_E4M3 ? (wide ? prod8_e4m3_wide : prod8_e4m3)
                                                : (wide ? prod8_e5m2_wide : prod8_e5m2);
@@ -386,7 +418,12 @@ int pgemm_linear_fp8(pgemm_fp8_kind kind, int m, int n, int k, pgemm_rows X, pge
 
 size_t pgemm_linear_fp8_workspace(int m, int n, int k) {
   if (m <= 0 || n <= 0 || k <= 0) return 0;
-  return split_bytes(1, kInner, kDense, m, 1, n, k);
+  size_t most = 0;
+  for (const int loading : {kThrough, kDirect}) {
+    const size_t b = split_space(plan8(m, n, k, loading, 0, true), kDense, m, 1, n);
+    if (b > most) most = b;
+  }
+  return most;
 }
 
 int pgemm_gated_linear(pgemm_kind kind, int m, int n, int k, pgemm_rows X, pgemm_gate_weights W,

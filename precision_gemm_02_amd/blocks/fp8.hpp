@@ -369,16 +369,17 @@ __global__ __launch_bounds__(WGM* WGN * 64) void prod8_tile_kernel(const Prod8Ar
 // workgroup takes 16 NB columns; its waves take blocks of 128 of the summed index
 // in turn (U of them in flight), from memory straight into the matrix
 // instruction's registers, each adding into its own sums, which are added over
-// the waves through LDS in a fixed order.
+// the waves through LDS in a fixed order.  The scales of all its blocks are read
+// once into LDS, under the first blocks' loads (one by one, each row's would be a
+// cache line for itself), where they fit.
 template <int FA, int FB, int MB, int NB, int WAVES, bool COLS, bool WIDE>
 __global__ __launch_bounds__(WAVES * 64) void prod8_rows_kernel(const Prod8Args args) {
   const ProdArgs& a = args.p;
   constexpr int BN = 16 * NB, U = NB == 1 && MB == 1 ? 2 : 1;
   constexpr int V = 16, BK = 128, RED_LD = BN + 4;
-  // the next units' loads before the current ones' use, where registers hold both (with
-  // a scale for each of 64 columns 192 would be spilled)
-  constexpr bool AHEAD = !(COLS && NB == 4);
+  constexpr int XS = 16 * MB, WS = COLS ? BN : 1, ROOM = 4096;   // rows of scales; their room
   __shared__ __attribute__((aligned(128))) float red[WAVES * MB * 16 * RED_LD];
+  __shared__ float scales[ROOM];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, i = lane & 15, g = lane >> 4;
   const int col0 = map_range(blockIdx.x, gridDim.x) * BN;
   int k_lo = 0, k_hi = a.K;
@@ -387,6 +388,8 @@ __global__ __launch_bounds__(WAVES * 64) void prod8_rows_kernel(const Prod8Args 
     k_hi = k_lo + a.k_split < a.K ? k_lo + a.k_split : a.K;
   }
   const int units = (k_hi - k_lo + BK - 1) / BK, whole = (k_hi - k_lo) / BK, b_lo = k_lo / BK;
+  const int pitch = units | 1;                   // (odd: a column's 16 rows lie in 16 banks)
+  const bool staged = (long long)pitch * (XS + WS) <= ROOM;
   // rows and columns outside read the last one (their results are never stored)
   const uint8_t* wrow[NB];
 #pragma unroll
@@ -394,15 +397,20 @@ __global__ __launch_bounds__(WAVES * 64) void prod8_rows_kernel(const Prod8Args 
     const int n = col0 + 16 * c + i;
     wrow[c] = static_cast<const uint8_t*>(a.B) + (long long)(n < a.N ? n : a.N - 1) * a.ldb;
   }
+  auto w_scale = [&](int n, int unit) {
+    return args.sw[((n < a.N ? n : a.N - 1) >> args.w_shift) * args.sw_row +
+                   (b_lo + unit) * args.sw_block];
+  };
 
   for (int m0 = 0; m0 < a.M; m0 += 16 * MB) {
+    auto x_scale = [&](int r, int unit) {
+      return args.sx[(m0 + r < a.M ? m0 + r : a.M - 1) * args.sx_row + (b_lo + unit) * args.sx_block];
+    };
     const uint8_t* arow[MB];
-    const float* as[MB];
 #pragma unroll
     for (int b = 0; b < MB; ++b) {
       const int m = m0 + 16 * b + i < a.M ? m0 + 16 * b + i : a.M - 1;
       arow[b] = static_cast<const uint8_t*>(a.A) + m * a.lda;
-      as[b] = args.sx + m * args.sx_row;
     }
     f32x4 acc[MB][NB];
 #pragma unroll
@@ -412,22 +420,19 @@ __global__ __launch_bounds__(WAVES * 64) void prod8_rows_kernel(const Prod8Args 
 
     struct Unit {
       u32x4 w[NB][2], x[MB][2];
-      float sx[MB], sw[COLS ? NB : 1][COLS ? 4 : 1];
     };
-    auto load_scales = [&](int unit, Unit& u) {
-      const long long kb = b_lo + unit;
+    auto use = [&](const Unit& u, int unit) {
+      float sx[MB], sw[WS == 1 ? 1 : NB][COLS ? 4 : 1];
 #pragma unroll
-      for (int b = 0; b < MB; ++b) u.sx[b] = as[b][kb * args.sx_block];
+      for (int b = 0; b < MB; ++b)
+        sx[b] = staged ? scales[(16 * b + i) * pitch + unit] : x_scale(16 * b + i, unit);
 #pragma unroll
       for (int c = 0; c < (COLS ? NB : 1); ++c)
 #pragma unroll
         for (int j = 0; j < (COLS ? 4 : 1); ++j) {
-          const int n = COLS ? col0 + 16 * c + 4 * g + j : col0;
-          u.sw[c][j] = args.sw[((n < a.N ? n : a.N - 1) >> args.w_shift) * args.sw_row +
-                               kb * args.sw_block];
+          const int n = COLS ? 16 * c + 4 * g + j : 0;
+          sw[c][j] = staged ? scales[(XS + n) * pitch + unit] : w_scale(col0 + n, unit);
         }
-    };
-    auto use = [&](const Unit& u) {
       Part<WIDE> x[MB];
 #pragma unroll
       for (int b = 0; b < MB; ++b) x[b] = part<WIDE, FA>(u.x[b][0], u.x[b][1]);
@@ -439,7 +444,7 @@ __global__ __launch_bounds__(WAVES * 64) void prod8_rows_kernel(const Prod8Args 
           const f32x4 t = block_sum<WIDE, FB, FA>(w, x[b]);
 #pragma unroll
           for (int j = 0; j < 4; ++j)
-            acc[b][c][j] += t[j] * (u.sx[b] * u.sw[COLS ? c : 0][COLS ? j : 0]);
+            acc[b][c][j] += t[j] * (sx[b] * sw[COLS ? c : 0][COLS ? j : 0]);
         }
       }
     };
@@ -458,31 +463,29 @@ __global__ __launch_bounds__(WAVES * 64) void prod8_rows_kernel(const Prod8Args 
 #pragma unroll
           for (int b = 0; b < MB; ++b) us[q].x[b][kk] = load16(arow[b] + k0 + (4 * kk + g) * V);
         }
-        load_scales(unit, us[q]);
       }
     };
     auto use_all = [&](int u0, Unit(&us)[U]) {
 #pragma unroll
       for (int q = 0; q < U; ++q) {
         if (u0 + q * WAVES >= whole) break;
-        use(us[q]);
+        use(us[q], u0 + q * WAVES);
       }
     };
-    if constexpr (AHEAD) {
-      load(wave, xs);
-#pragma unroll 1
-      for (int u0 = wave; u0 < whole; u0 += 2 * STEP) {
-        load(u0 + STEP, ys);
-        use_all(u0, xs);
-        load(u0 + 2 * STEP, xs);
-        use_all(u0 + STEP, ys);
+    load(wave, xs);
+    if (staged) {
+      for (int t = threadIdx.x; t < (XS + WS) * units; t += WAVES * 64) {
+        const int r = t / units, unit = t - r * units;
+        scales[r * pitch + unit] = r < XS ? x_scale(r, unit) : w_scale(col0 + r - XS, unit);
       }
-    } else {
+      __syncthreads();
+    }
 #pragma unroll 1
-      for (int u0 = wave; u0 < whole; u0 += STEP) {
-        load(u0, xs);
-        use_all(u0, xs);
-      }
+    for (int u0 = wave; u0 < whole; u0 += 2 * STEP) {
+      load(u0 + STEP, ys);
+      use_all(u0, xs);
+      load(u0 + 2 * STEP, xs);
+      use_all(u0 + STEP, ys);
     }
     if (whole < units && whole % WAVES == wave) {     // the last, partly filled block
       Unit u;
@@ -494,8 +497,7 @@ __global__ __launch_bounds__(WAVES * 64) void prod8_rows_kernel(const Prod8Args 
 #pragma unroll
         for (int b = 0; b < MB; ++b) u.x[b][kk] = load_guarded(arow[b], k0 + (4 * kk + g) * V, k_hi);
       }
-      load_scales(whole, u);
-      use(u);
+      use(u, whole);
     }
 
     // sum over the waves, then 8 columns per thread

@@ -55,9 +55,9 @@ hipError_t prod8(const Prod8Args& a, int kernel, int loading, hipStream_t s) {
   } else if (kernel == kFew32) {
     e = rows8<FA, FB, COLS, WIDE, 2, 1>(a, grid, s);
   } else if (kernel == kFew16Wide) {
-    e = rows8<FA, FB, COLS, WIDE, 1, 4>(a, grid, s);
+    e = rows8<FA, FB, COLS, WIDE, 1, 2>(a, grid, s);
   } else {
-    e = rows8<FA, FB, COLS, WIDE, 2, 4>(a, grid, s);
+    e = rows8<FA, FB, COLS, WIDE, 2, 2>(a, grid, s);
   }
   if (e != hipSuccess || a.p.splits <= 1) return e;
   const long long items = (long long)a.p.M * ((a.p.N + 7) / 8);

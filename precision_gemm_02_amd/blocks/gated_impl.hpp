@@ -48,10 +48,10 @@ hipError_t pair_reduce(const PairArgs& a, int count, hipStream_t s) {
                 s);
 }
 
-template <typename T, int LB, int MB, int NB>
+template <typename T, int LB, int MB, int NB, int WAVES>
 hipError_t gate_rows(const PairArgs& a, dim3 grid, hipStream_t s) {
-  static_assert(prod_threads(kFew16) == 512, "the checked launch");
-  return launch(&gate_rows_kernel<T, LB, MB, NB, 8>, grid, 512, a, s);
+  static_assert(prod_threads(kFew16) >= WAVES * 64, "the checked launch");
+  return launch(&gate_rows_kernel<T, LB, MB, NB, WAVES>, grid, WAVES * 64, a, s);
 }
 
 template <typename T, int LB, int PAIR>
@@ -61,10 +61,10 @@ hipError_t pair(const PairArgs& a, int kernel, int loading, bool whole, hipStrea
   hipError_t e = hipErrorInvalidValue;
   if (kernel >= kFew16) {
     if constexpr (PAIR == kColumns) {
-      e = kernel == kFew16       ? gate_rows<T, LB, 1, 2>(a, grid, s)
-          : kernel == kFew32     ? gate_rows<T, LB, 2, 2>(a, grid, s)
-          : kernel == kFew16Wide ? gate_rows<T, LB, 1, 4>(a, grid, s)
-                                 : gate_rows<T, LB, 2, 4>(a, grid, s);
+      e = kernel == kFew16       ? gate_rows<T, LB, 1, 2, 4>(a, grid, s)
+          : kernel == kFew32     ? gate_rows<T, LB, 2, 2, 4>(a, grid, s)
+          : kernel == kFew16Wide ? gate_rows<T, LB, 1, 4, 2>(a, grid, s)
+                                 : gate_rows<T, LB, 2, 4, 2>(a, grid, s);
     }
   } else if (whole) {
     e = whole_tiles<T, kInner, LB, PAIR>(a, kernel, grid, s);

@@ -45,7 +45,7 @@ hipError_t norm(const NormArgs& a, hipStream_t s) {
   if (a.n <= 1024) return norm_as<T, 64, 2, 256>(a, s);
   if (a.n <= 2048) return norm_as<T, 256, 1, 256>(a, s);
   if (a.n <= 4096) return norm_as<T, 256, 2, 256>(a, s);
-  if (a.n <= 8192) return norm_as<T, 256, 4, 256>(a, s);
+  if (a.n <= 8192) return norm_as<T, 512, 2, 512>(a, s);
   if (a.n <= 16384) return norm_as<T, 1024, 2, 1024>(a, s);
   if (a.n <= kRowMost) return norm_as<T, 1024, 4, 1024>(a, s);
   return norm_parts<T>(&norm_long_kernel<T>, 1, 1024, a, s);
@@ -65,11 +65,10 @@ hipError_t norm_back(const NormBackArgs& a, hipStream_t s) {
   if (a.n <= 128) return norm_back_as<T, 16, 1, 256>(a, s);
   if (a.n <= 512) return norm_back_as<T, 64, 1, 256>(a, s);
   if (a.n <= 1024) return norm_back_as<T, 64, 2, 256>(a, s);
-  if (a.n <= 2048) return norm_back_as<T, 256, 1, 256>(a, s);
-  if (a.n <= 4096) return norm_back_as<T, 512, 1, 512>(a, s);
+  if (a.n <= 2048) return norm_back_as<T, 256, 1, 512>(a, s);
+  if (a.n <= 4096) return norm_back_as<T, 512, 1, 1024>(a, s);
   if (a.n <= 8192) return norm_back_as<T, 1024, 1, 1024>(a, s);
-  if (a.n <= 16384) return norm_back_as<T, 1024, 2, 1024>(a, s);
-  if (a.n <= kRowMost) return norm_back_as<T, 1024, 4, 1024>(a, s);
+  if (a.n <= kBackMost) return norm_back_as<T, 1024, 2, 1024>(a, s);
   for (long long r = 0; r < a.m; r += kMostGroups) {
     NormBackArgs b = a;
     b.m = (int)(a.m - r < kMostGroups ? a.m - r : kMostGroups);

@@ -20,6 +20,7 @@ namespace blocks {
 
 using layers::get_row8;
 using layers::put_row8;
+using layers::u32x4;
 
 struct NormArgs {
   const void* X;
@@ -54,9 +55,9 @@ struct NormColumnArgs {
   int n, groups, out32;
 };
 
-// Rows of up to kRowMost elements stay in registers, in the gradients with column
-// sums up to kSumMost (their sums take as many registers again, twice).
-constexpr int kRowMost = 1024 * 8 * 4, kSumMost = 1024 * 8 * 2;
+// Rows of up to kRowMost elements stay in registers, in the gradients up to kBackMost,
+// with column sums up to kSumMost (their sums take as many registers again, twice).
+constexpr int kRowMost = 1024 * 8 * 4, kBackMost = 1024 * 8 * 2, kSumMost = 1024 * 8;
 
 // N sums over the TPR threads of a row, the same bits for all of them, with one
 // barrier.  Calls that follow each other take other parts of `lds`.
@@ -183,75 +184,141 @@ __global__ __launch_bounds__(1024) void norm_long_kernel(const NormArgs a) {
   }
 }
 
+// Eight elements of a row as they are stored, zeros behind its end.
+template <typename T>
+struct Stored8 {
+  u32x4 v[sizeof(T) / 2];
+};
+template <typename T>
+__device__ __forceinline__ Stored8<T> stored8(const void* base, long long row, int c, int n) {
+  Stored8<T> s;
+  const T* p = static_cast<const T*>(base) + row + c;
+  if (c + 8 <= n) {
+#pragma unroll
+    for (int k = 0; k < (int)sizeof(T) / 2; ++k) s.v[k] = layers::load16(p + k * 16 / sizeof(T));
+  } else {
+    T t[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) t[j] = c + j < n ? p[j] : (T)0.0f;
+    __builtin_memcpy(&s, t, sizeof(s));
+  }
+  return s;
+}
+template <typename T>
+__device__ __forceinline__ void widen8(const Stored8<T>& s, float* v) {
+  T t[8];
+  __builtin_memcpy(t, &s, sizeof(s));
+#pragma unroll
+  for (int j = 0; j < 8; ++j) v[j] = (float)t[j];
+}
+
 // dX and, with SUMS, the column sums of this workgroup's rows: row group by row
 // group, each thread adds its columns in order; the groups of one workgroup
-// are then added in order through LDS.
+// are then added in order through LDS.  The next row is asked for before the sums
+// of this one, where the registers hold both; rows are kept as they are stored (16-bit
+// ones in half the registers).  Rows over 8192 take the column sums apart: with them
+// 75 to 135 registers were spilled (4096 rows of 16384, bf16: 190 us).
 template <typename T, int TPR, int C, int NT, bool SUMS>
 __global__ __launch_bounds__(NT) void norm_back_kernel(const NormBackArgs a) {
   constexpr int ROWS = NT / TPR;
+  constexpr bool AHEAD = C == 1;
   __shared__ float lds[4][16];
   __shared__ float cols[SUMS && ROWS > 1 ? NT * 8 : 1];
   const int t = threadIdx.x % TPR, mine = threadIdx.x / TPR;
   const float inv = 1.0f / (float)a.n;
-  float w[C][8], sw[SUMS ? C : 1][8], sb[SUMS ? C : 1][8];
+  Stored8<T> w[C];
+  float sw[SUMS ? C : 1][8], sb[SUMS ? C : 1][8];
 #pragma unroll
   for (int c = 0; c < C; ++c) {
-    if (a.W != nullptr) {
-      get_row8<T>(a.W, 0, (c * TPR + t) * 8, a.n, w[c]);
-    } else {
-#pragma unroll
-      for (int j = 0; j < 8; ++j) w[c][j] = 1.0f;
-    }
+    if (a.W != nullptr) w[c] = stored8<T>(a.W, 0, (c * TPR + t) * 8, a.n);
     if constexpr (SUMS) {
 #pragma unroll
       for (int j = 0; j < 8; ++j) sw[c][j] = sb[c][j] = 0.0f;
     }
   }
-  int slot = 0;
-  for (long long r0 = (long long)blockIdx.x * ROWS; r0 < a.m; r0 += (long long)a.groups * ROWS) {
-    const bool live = r0 + mine < a.m;
-    const long long row = live ? r0 + mine : a.m - 1;
-    const float mean = a.mean[row], rstd = a.rstd[row];
-    float x[C][8], d[C][8];
+  struct Row {
+    Stored8<T> x[C], d[C], r[AHEAD ? C : 1];
+    float mean, rstd;
+  };
+  auto load = [&](long long r0) {
+    const long long row = r0 + mine < a.m ? r0 + mine : a.m - 1;
+    Row v;
+    v.mean = a.mean[row];
+    v.rstd = a.rstd[row];
 #pragma unroll
     for (int c = 0; c < C; ++c) {
-      get_row8<T>(a.X, row * a.ldx, (c * TPR + t) * 8, a.n, x[c]);
-      get_row8<T>(a.dY, row * a.ldy, (c * TPR + t) * 8, a.n, d[c]);
+      v.x[c] = stored8<T>(a.X, row * a.ldx, (c * TPR + t) * 8, a.n);
+      v.d[c] = stored8<T>(a.dY, row * a.ldy, (c * TPR + t) * 8, a.n);
+      if (AHEAD && a.R != nullptr) v.r[c] = stored8<T>(a.R, row * a.ldr, (c * TPR + t) * 8, a.n);
     }
+    return v;
+  };
+  // h and g of chunk c
+  auto values = [&](const Row& v, int c, float* h, float* g) {
+    float x[8];
+    widen8<T>(v.x[c], x);
+    widen8<T>(v.d[c], g);
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+      h[j] = (c * TPR + t) * 8 + j < a.n ? (x[j] - v.mean) * v.rstd : 0.0f;
+  };
+  auto weigh = [&](int c, float* g) {
+    if (a.W == nullptr) return;
+    float k[8];
+    widen8<T>(w[c], k);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) g[j] *= k[j];
+  };
+  const long long step = (long long)a.groups * ROWS;
+  long long r0 = (long long)blockIdx.x * ROWS;
+  int slot = 0;
+  Row next;
+  if (AHEAD && r0 < a.m) next = load(r0);
+#pragma unroll 1
+  for (; r0 < a.m; r0 += step) {
+    if (!AHEAD) next = load(r0);
+    const Row v = next;
+    const bool live = r0 + mine < a.m;
+    if (AHEAD && r0 + step < a.m) next = load(r0 + step);
     float s[2] = {0.0f, 0.0f};
 #pragma unroll
-    for (int c = 0; c < C; ++c)
+    for (int c = 0; c < C; ++c) {
+      float h[8], g[8];
+      values(v, c, h, g);
+      if constexpr (SUMS) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          sw[c][j] += live ? g[j] * h[j] : 0.0f;
+          sb[c][j] += live ? g[j] : 0.0f;
+        }
+      }
+      weigh(c, g);
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
-        const bool in = (c * TPR + t) * 8 + j < a.n;
-        const float h = in ? (x[c][j] - mean) * rstd : 0.0f;
-        x[c][j] = h;
-        if constexpr (SUMS) {
-          sw[c][j] += live ? d[c][j] * h : 0.0f;
-          sb[c][j] += live ? d[c][j] : 0.0f;
-        }
-        const float g = d[c][j] * w[c][j];
-        d[c][j] = g;
-        s[0] += g;
-        s[1] += g * h;
+        s[0] += g[j];
+        s[1] += g[j] * h[j];
       }
+    }
     row_sums<TPR>(s, lds + slot);
     slot ^= 2;
     const float s1 = s[0] * inv, s2 = s[1] * inv;
     if (live) {
+      const long long row = r0 + mine;
 #pragma unroll
       for (int c = 0; c < C; ++c) {
         const int col = (c * TPR + t) * 8;
         if (col >= a.n) break;
-        float res[8];
-        if (a.R != nullptr) get_row8<T>(a.R, row * a.ldr, col, a.n, res);
+        float h[8], g[8], res[8];
+        values(v, c, h, g);
+        weigh(c, g);
+        if (a.R != nullptr)
+          widen8<T>(AHEAD ? v.r[AHEAD ? c : 0] : stored8<T>(a.R, row * a.ldr, col, a.n), res);
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
-          float v = rstd * (d[c][j] - s1 - x[c][j] * s2);
-          if (a.R != nullptr) v += res[j];
-          d[c][j] = v;
+          g[j] = v.rstd * (g[j] - s1 - h[j] * s2);
+          if (a.R != nullptr) g[j] += res[j];
         }
-        put_row8<T>(a.dX, row * a.ldd, col, a.n, d[c]);
+        put_row8<T>(a.dX, row * a.ldd, col, a.n, g);
       }
     }
   }
