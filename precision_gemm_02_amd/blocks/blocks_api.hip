@@ -122,7 +122,7 @@ int gate_chunks(int rows, int half) {
 GateSpace gate_space(const pgemm_kind& kind, int m, int n, int k) {
   GateSpace g;
   const int size = size_of(kind.dtype);
-  g.half = (int)round_up(n, 64);
+  g.half = (int)round_up(n, 128 / size);       // whole steps of the kernels
   g.dz = align256((size_t)m * 2 * (size_t)g.half * (size_t)size);
   const int rows = m < 1 ? 1 : m;
   g.chunks = gate_chunks(rows, g.half);
@@ -140,10 +140,10 @@ GateSpace gate_space(const pgemm_kind& kind, int m, int n, int k) {
 }
 
 // Whether pair_whole_kernel takes operands whose loads are direct: offsets within a tile
-// of at most 256 rows fit 32 bits, and the summed index has whole steps.
-bool whole_tiles(int size, long long lda, long long ldb, int summed) {
-  const long long most = 0x7fffffffLL / (256 * size);
-  return lda < most && ldb < most && summed % (128 / size) == 0;
+// of at most 256 rows fit 31 bits.
+bool whole_tiles(int size, long long lda, long long ldb) {
+  const long long most = 0x7fffffffLL / (256 * size) - 16;
+  return lda < most && ldb < most;
 }
 
 // The products for the weights' gradients, dW = X^T dZ of each: one launch for both
@@ -181,7 +181,7 @@ bool plan_weights(WeightGradients* g, const pgemm_kind& kind, int m, int n, int 
     a.K = m;
   }
   // dZ's rows go on behind column n (see gate_slope_kernel): its loads are direct
-  if (alike && whole_tiles(size, X.ld, ldz, m) &&
+  if (alike && whole_tiles(size, X.ld, ldz) &&
       operand_loading(X.data, X.ld, size, k, 0) == kDirect) {
     g->args.p = g->one[0].a;
     g->args.count = g->count;
@@ -411,7 +411,7 @@ int pgemm_linear_fp8(pgemm_fp8_kind kind, int m, int n, int k, pgemm_rows X, pge
   const Prod8 prod = kind.x_type == PGEMM_E4M3 ? (wide ? prod8_e4m3_wide : prod8_e4m3)
                                                : (wide ? prod8_e5m2_wide : prod8_e5m2);
   const long long far = 0x7fffffffLL / (256 * 4);   // scales' offsets within a tile fit 32 bits
-  const bool whole = direct && !wide && whole_tiles(1, X.ld, W.ld, k) && x_scales.row_stride < far &&
+  const bool whole = direct && !wide && whole_tiles(1, X.ld, W.ld) && x_scales.row_stride < far &&
                      w_scales.row_stride < far;
   return status(prod(args, kind.w_type, plan.kernel, whole ? kWhole : direct ? kDirect : kThrough, s));
 }
@@ -474,7 +474,7 @@ int pgemm_gated_linear(pgemm_kind kind, int m, int n, int k, pgemm_rows X, pgemm
   a.tiles_m = plan.kernel >= kFew16 ? 1 : (int)ceil_div(m, kShape[plan.kernel].bm);
   a.tiles_n = (int)ceil_div(n, gate_columns(plan.kernel));
   return status(gate_ops(kind.dtype).pair(args, lb, kColumns, plan.kernel, loading,
-                                          loading == kDirect && whole_tiles(size, X.ld, W.gate.ld, k),
+                                          loading == kDirect && whole_tiles(size, X.ld, W.gate.ld),
                                           static_cast<hipStream_t>(stream)));
 }
 
@@ -579,9 +579,7 @@ int pgemm_gated_linear_backward(pgemm_kind kind, int m, int n, int k, pgemm_rows
         return PGEMM_EHIP;
   }
   if (want_dx && ops.pair(dx, lb, kHalves, dx_plan.kernel, loading,
-                          loading == kDirect && n == space.half &&
-                              whole_tiles(size, ldz, W.gate.ld, n),
-                          s) != hipSuccess)
+                          loading == kDirect && whole_tiles(size, ldz, W.gate.ld), s) != hipSuccess)
     return PGEMM_EHIP;
   if (dw.whole) return status(ops.apart(dw.args, dw.kernel, s));
   for (int i = 0; i < dw.count; ++i) {

@@ -20,13 +20,16 @@ hipError_t tile8(const Prod8Args& a, dim3 grid, hipStream_t s) {
                 WGM * WGN * 64, a, s);
 }
 
-template <int FA, int FB, bool COLS>
+template <int FA, int FB, bool COLS, bool TAIL>
 hipError_t whole8(const Prod8Args& a, int kernel, dim3 grid, hipStream_t s) {
   if (kernel == kTile256)
-    return launch(&prod8_whole_kernel<FA, FB, 256, 256, 2, 4, COLS>, grid, prod_threads(kTile256), a, s);
+    return launch(&prod8_whole_kernel<FA, FB, 256, 256, 2, 4, COLS, TAIL>, grid,
+                  prod_threads(kTile256), a, s);
   if (kernel == kTile128)
-    return launch(&prod8_whole_kernel<FA, FB, 128, 128, 2, 2, COLS>, grid, prod_threads(kTile128), a, s);
-  return launch(&prod8_whole_kernel<FA, FB, 64, 64, 2, 2, COLS>, grid, prod_threads(kTile64), a, s);
+    return launch(&prod8_whole_kernel<FA, FB, 128, 128, 2, 2, COLS, TAIL>, grid,
+                  prod_threads(kTile128), a, s);
+  return launch(&prod8_whole_kernel<FA, FB, 64, 64, 2, 2, COLS, TAIL>, grid, prod_threads(kTile64), a,
+                s);
 }
 
 template <int FA, int FB, bool COLS, bool WIDE, int MB, int NB>
@@ -41,7 +44,9 @@ hipError_t prod8(const Prod8Args& a, int kernel, int loading, hipStream_t s) {
   const dim3 grid((unsigned)g.x, (unsigned)g.y);
   hipError_t e = hipErrorInvalidValue;
   if (!WIDE && loading == kWhole && kernel <= kTile64) {
-    if constexpr (!WIDE) e = whole8<FA, FB, COLS>(a, kernel, grid, s);
+    if constexpr (!WIDE)
+      e = a.p.K % 128 ? whole8<FA, FB, COLS, true>(a, kernel, grid, s)
+                      : whole8<FA, FB, COLS, false>(a, kernel, grid, s);
   } else if (kernel == kTile256) {
     if constexpr (!WIDE) e = tile8<FA, FB, COLS, WIDE, kTile256, 2, 4, true>(a, grid, s);
   } else if (kernel == kTile128) {

@@ -28,17 +28,25 @@ hipError_t pair_tiles(const PairArgs& a, int kernel, dim3 grid, hipStream_t s) {
   return hipErrorInvalidValue;
 }
 
+template <typename T, int LA, int LB, int PAIR, bool TAIL>
+hipError_t whole_tile(const PairArgs& a, int kernel, dim3 grid, hipStream_t s) {
+  if (kernel == kTile256)
+    return launch(&pair_whole_kernel<T, LA, LB, 256, 256, 2, 4, PAIR, TAIL>, grid,
+                  prod_threads(kTile256), a, s);
+  if (kernel == kTile128)
+    return launch(&pair_whole_kernel<T, LA, LB, 128, 128, 2, 2, PAIR, TAIL>, grid,
+                  prod_threads(kTile128), a, s);
+  if (kernel == kTile64)
+    return launch(&pair_whole_kernel<T, LA, LB, 64, 64, 2, 2, PAIR, TAIL>, grid,
+                  prod_threads(kTile64), a, s);
+  return hipErrorInvalidValue;
+}
+
 template <typename T, int LA, int LB, int PAIR>
 hipError_t whole_tiles(const PairArgs& a, int kernel, dim3 grid, hipStream_t s) {
-  if (kernel == kTile256)
-    return launch(&pair_whole_kernel<T, LA, LB, 256, 256, 2, 4, PAIR>, grid, prod_threads(kTile256), a,
-                  s);
-  if (kernel == kTile128)
-    return launch(&pair_whole_kernel<T, LA, LB, 128, 128, 2, 2, PAIR>, grid, prod_threads(kTile128), a,
-                  s);
-  if (kernel == kTile64)
-    return launch(&pair_whole_kernel<T, LA, LB, 64, 64, 2, 2, PAIR>, grid, prod_threads(kTile64), a, s);
-  return hipErrorInvalidValue;
+  const int along = PAIR == kHalves ? a.inner : a.p.K;
+  return along % (int)(128 / sizeof(T)) ? whole_tile<T, LA, LB, PAIR, true>(a, kernel, grid, s)
+                                        : whole_tile<T, LA, LB, PAIR, false>(a, kernel, grid, s);
 }
 
 template <typename T>

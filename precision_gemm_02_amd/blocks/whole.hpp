@@ -1,8 +1,9 @@
-// The pair products' tile kernel for whole tiles: 16-byte aligned rows, and a summed
-// index of whole steps of 128 bytes.  Beside pair_tile_kernel it spends no vector
-// instruction on the loads' addresses: an operand's tile is a buffer descriptor whose
-// scalar base moves along the summed index, and each lane's 32-bit offsets within a
-// tile stay as they are.
+// The pair products' tile kernel for operands in whole 16-byte chunks (aligned rows).
+// Beside pair_tile_kernel it spends no vector instruction on the loads' addresses: an
+// operand's tile is a buffer descriptor whose scalar base moves along the summed index,
+// and each lane's 32-bit offsets within a tile stay as they are.  In a last, partly
+// filled tile of the summed index, lanes outside take an offset behind the descriptor's
+// end, for which the load writes zeros to LDS.
 //
 // A tile of the summed index is 128 bytes of each row.  Of the LDS, three slots hold A's
 // tiles, two B's.  A wave's B operands of a whole tile stay in registers (CB x 8), read
@@ -19,10 +20,12 @@
 namespace pgemm {
 namespace blocks {
 
-// A descriptor of everything from `base` on (offsets are in bounds by construction).
+// A descriptor of 2^31 bytes from `base` on.  Offsets below are in bounds of the operand by
+// construction; kOutside is behind it.
+constexpr uint32_t kOutside = 0x80000000u;
 __device__ __forceinline__ u32x4 descriptor(const char* base) {
   const uint64_t a = reinterpret_cast<uint64_t>(base);
-  return u32x4{(uint32_t)a, (uint32_t)(a >> 32) & 0xffffu, 0xffffffffu, 0x00020000u};
+  return u32x4{(uint32_t)a, (uint32_t)(a >> 32) & 0xffffu, kOutside, 0x00020000u};
 }
 
 // 16 bytes per lane straight to LDS: lane l of the wave writes at to + 16 l (an LDS
@@ -81,7 +84,7 @@ __device__ __forceinline__ void take(const f32x4 (&acc)[RB][CB], int r, f32x4 (&
   });
 }
 
-template <typename T, int LA, int LB, int BM, int BN, int WGM, int WGN, int PAIR>
+template <typename T, int LA, int LB, int BM, int BN, int WGM, int WGN, int PAIR, bool TAIL>
 __global__ __launch_bounds__(WGM* WGN * 64) void pair_whole_kernel(const PairArgs args) {
   const ProdArgs& a = args.p;
   constexpr int S = sizeof(T), NT = WGM * WGN * 64;
@@ -103,7 +106,7 @@ __global__ __launch_bounds__(WGM* WGN * 64) void pair_whole_kernel(const PairArg
     k_lo = blockIdx.y * a.k_split;
     k_hi = k_lo + a.k_split < a.K ? k_lo + a.k_split : a.K;
   }
-  const int nk = (k_hi - k_lo) / BK;
+  const int nk = (k_hi - k_lo + BK - 1) / BK;
 
   // kColumns: B's slot holds a tile of either weight, half as wide
   constexpr int SUBS = PAIR == kColumns ? 2 : 1, SUB = BN / SUBS, SUB_BYTES = SUB * 128;
@@ -113,10 +116,16 @@ __global__ __launch_bounds__(WGM* WGN * 64) void pair_whole_kernel(const PairArg
   // a lane's offsets from its operand's tile; rows and columns outside read the last row
   // or the first chunk (they reach results that are never stored)
   uint32_t va[NA], vb[TB::LOADS];
+  // TAIL: summed indices of a partly filled last tile (0: it is whole), and the loads outside
+  // them; kHalves: of B alone, in both halves (dZ's rows hold zeros there)
+  const int tail = !TAIL ? 0 : (PAIR == kHalves ? args.inner : a.K) % BK;
+  const bool ends = k_hi == a.K || (PAIR == kHalves && k_hi == args.half);
+  uint32_t out_a = 0, out_b = 0;   // bit 31 - j: a lane's load j is outside (inner: all alike)
 #pragma unroll
   for (int j = 0; j < NA; ++j) {
     int r, c;
     TA::slot(j * NT + (int)threadIdx.x, &r, &c);
+    if (PAIR != kHalves && (LA == kInner ? c * TA::V : r) >= tail) out_a |= kOutside >> j;
     if constexpr (LA == kInner) {
       const int row = row0 + r < a.M ? r : a.M - 1 - row0;
       va[j] = (uint32_t)row * (uint32_t)(a.lda * S) + c * 16;
@@ -128,6 +137,7 @@ __global__ __launch_bounds__(WGM* WGN * 64) void pair_whole_kernel(const PairArg
   for (int j = 0; j < TB::LOADS; ++j) {
     int r, c;
     TB::slot(j * NT + (int)threadIdx.x, &r, &c);
+    if ((LB == kInner ? c * TB::V : r) >= tail) out_b |= kOutside >> j;
     if constexpr (LB == kInner) {
       const int col = col0 + r < a.N ? r : a.N - 1 - col0;
       vb[j] = (uint32_t)col * (uint32_t)(a.ldb * S) + c * 16;
@@ -160,17 +170,22 @@ __global__ __launch_bounds__(WGM* WGN * 64) void pair_whole_kernel(const PairArg
   // loads J0 .. J1-1 of the next tile, into slot `to`
   auto load_a = [&](auto j0, auto j1, int to) {
     const u32x4 d = descriptor(wa.at);
+    const uint32_t cut = TAIL && tail > 0 && ends && wa.left <= 1 ? kOutside : 0;
 #pragma unroll
     for (int j = decltype(j0)::value; j < decltype(j1)::value; ++j)
-      tile_load(d, va[j], lds_wave + to * SLOT_A + j * NT * 16);
+      tile_load(d, PAIR == kHalves ? va[j] : va[j] | ((LA == kInner ? out_a : out_a << j) & cut),
+                lds_wave + to * SLOT_A + j * NT * 16);
     if constexpr (decltype(j1)::value == NA) wa.next(0);
   };
   auto load_b = [&](auto j0, auto j1, int to) {
     const u32x4 d = descriptor(wb.at);
     const u32x4 e = PAIR == kColumns ? descriptor(wb.at + second) : d;
+    const uint32_t cut =
+        TAIL && tail > 0 && (wb.left <= 1 ? ends : wb.left - 1 == before) ? kOutside : 0;
 #pragma unroll
     for (int j = decltype(j0)::value; j < decltype(j1)::value; ++j)
-      tile_load(j < TB::LOADS ? d : e, vb[j % TB::LOADS],
+      tile_load(j < TB::LOADS ? d : e,
+                vb[j % TB::LOADS] | ((LB == kInner ? out_b : out_b << j % TB::LOADS) & cut),
                 lds_wave + 3 * SLOT_A + to * SLOT_B + j * NT * 16);
     if constexpr (decltype(j1)::value == NB)
       wb.next(PAIR == kHalves && wb.left - 1 == before ? jump : 0);

@@ -1,6 +1,6 @@
-// The 8-bit products' tile kernel for whole tiles (16-byte aligned rows, a summed index
-// of whole blocks of 128) and 16-bit results: prod8_tile_kernel with its loads through
-// buffer descriptors, as pair_whole_kernel has them.
+// The 8-bit products' tile kernel for operands in whole 16-byte chunks (aligned rows) and
+// 16-bit results: prod8_tile_kernel with its loads through buffer descriptors, as
+// pair_whole_kernel has them.
 #pragma once
 
 #include "fp8.hpp"
@@ -19,7 +19,7 @@ __device__ __forceinline__ void tile_load4(u32x4 from, uint32_t offset, uint32_t
       : "s"(to), "v"(offset), "s"(from));
 }
 
-template <int FA, int FB, int BM, int BN, int WGM, int WGN, bool COLS>
+template <int FA, int FB, int BM, int BN, int WGM, int WGN, bool COLS, bool TAIL>
 __global__ __launch_bounds__(WGM* WGN * 64) void prod8_whole_kernel(const Prod8Args args) {
   const ProdArgs& a = args.p;
   constexpr int NT = WGM * WGN * 64;
@@ -40,17 +40,22 @@ __global__ __launch_bounds__(WGM* WGN * 64) void prod8_whole_kernel(const Prod8A
     k_lo = blockIdx.y * a.k_split;
     k_hi = k_lo + a.k_split < a.K ? k_lo + a.k_split : a.K;
   }
-  const int row0 = tm * BM, col0 = tn * BN, nk = (k_hi - k_lo) / BK;
+  const int row0 = tm * BM, col0 = tn * BN, nk = (k_hi - k_lo + BK - 1) / BK;
 
   using TA = OperandTile<uint8_t, kInner, BM, NT>;
   using TB = OperandTile<uint8_t, kInner, BN, NT>;
   constexpr int NA = TA::LOADS, NB = TB::LOADS;
   // a lane's offsets from its operand's tile; rows outside read the last one
   uint32_t va[NA], vb[NB], vs;
+  // TAIL: summed indices of a partly filled last tile (0: it is whole); this lane's chunk (the same
+  // of every row) is outside them
+  const int tail = TAIL ? a.K % BK : 0;
+  uint32_t out = 0;
 #pragma unroll
   for (int j = 0; j < NA; ++j) {
     int r, c;
     TA::slot(j * NT + (int)threadIdx.x, &r, &c);
+    out = c * 16 >= tail ? kOutside : 0;
     va[j] = (uint32_t)(row0 + r < a.M ? r : a.M - 1 - row0) * (uint32_t)a.lda + c * 16;
   }
 #pragma unroll
@@ -80,8 +85,10 @@ __global__ __launch_bounds__(WGM* WGN * 64) void prod8_whole_kernel(const Prod8A
   // A and the scales of the next tile, into place `to`
   auto load_a = [&](int to) {
     const u32x4 d = descriptor(wa.at);
+    const uint32_t cut = TAIL && tail > 0 && k_hi == a.K && wa.left <= 1 ? kOutside : 0;
 #pragma unroll
-    for (int j = 0; j < NA; ++j) tile_load(d, va[j], lds_wave + to * SLOT_A + j * NT * 16);
+    for (int j = 0; j < NA; ++j)
+      tile_load(d, va[j] | (cut & out), lds_wave + to * SLOT_A + j * NT * 16);
     if (BM + BN == NT || wave * 64 < BM + BN)
       tile_load4(descriptor(ws.at), vs, lds_address(lds) + AT_S + to * SCALES + wave * 256);
     wa.next(0);
@@ -89,9 +96,10 @@ __global__ __launch_bounds__(WGM* WGN * 64) void prod8_whole_kernel(const Prod8A
   };
   auto load_b = [&](auto j0, auto j1, int to) {
     const u32x4 d = descriptor(wb.at);
+    const uint32_t cut = TAIL && tail > 0 && k_hi == a.K && wb.left <= 1 ? kOutside : 0;
 #pragma unroll
     for (int j = decltype(j0)::value; j < decltype(j1)::value; ++j)
-      tile_load(d, vb[j], lds_wave + AT_B + to * SLOT_B + j * NT * 16);
+      tile_load(d, vb[j] | (cut & out), lds_wave + AT_B + to * SLOT_B + j * NT * 16);
     if constexpr (decltype(j1)::value == NB) wb.next(0);
   };
 
