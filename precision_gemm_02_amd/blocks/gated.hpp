@@ -8,7 +8,7 @@
 #pragma once
 
 #include "../layers/prod_rows.hpp"
-#include "../layers/rows.hpp"
+#include "rows8.hpp"
 
 namespace pgemm {
 namespace blocks {
@@ -652,10 +652,19 @@ __global__ __launch_bounds__(256) void gate_slope_kernel(const GateSlopeArgs a) 
   if (c < a.half) {
 #pragma unroll 2
     for (int r = r0 + threadIdx.x / a.tpr; r < r1; r += rpb) {
+      Stored8<T> raw[3];
+      rows8<T>(a.n, [&](auto get) {
+        raw[0] = get(a.dY, (long long)r * a.ldy, c);
+        raw[1] = get(a.Zg, (long long)r * a.ldg, c);
+        raw[2] = get(a.Zu, (long long)r * a.ldu, c);
+      });
       float d[8], g[8], u[8];
-      get_row8<T>(a.dY, (long long)r * a.ldy, c, a.n, d);
-      get_row8<T>(a.Zg, (long long)r * a.ldg, c, a.n, g);
-      get_row8<T>(a.Zu, (long long)r * a.ldu, c, a.n, u);
+      settle8<T>(raw[0], c, a.n);
+      settle8<T>(raw[1], c, a.n);
+      settle8<T>(raw[2], c, a.n);
+      widen8<T>(raw[0], d);
+      widen8<T>(raw[1], g);
+      widen8<T>(raw[2], u);
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
         const float z = g[j], dj = d[j];

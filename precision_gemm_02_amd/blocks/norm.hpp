@@ -13,7 +13,7 @@
 #pragma once
 
 #include "../layers/prod.hpp"
-#include "../layers/rows.hpp"
+#include "rows8.hpp"
 
 namespace pgemm {
 namespace blocks {
@@ -91,9 +91,17 @@ __global__ __launch_bounds__(NT) void norm_kernel(const NormArgs a) {
   const long long row = (long long)blockIdx.x * ROWS + threadIdx.x / TPR;
   const bool live = row < a.m;
   const long long at = (live ? row : a.m - 1) * a.ldx;
+  Stored8<T> raw[C];
+  rows8<T>(a.n, [&](auto get) {
+#pragma unroll
+    for (int c = 0; c < C; ++c) raw[c] = get(a.X, at, (c * TPR + t) * 8);
+  });
   float x[C][8];
 #pragma unroll
-  for (int c = 0; c < C; ++c) get_row8<T>(a.X, at, (c * TPR + t) * 8, a.n, x[c]);
+  for (int c = 0; c < C; ++c) {
+    settle8<T>(raw[c], (c * TPR + t) * 8, a.n);
+    widen8<T>(raw[c], x[c]);
+  }
   float s[1] = {0.0f};
 #pragma unroll
   for (int c = 0; c < C; ++c)
@@ -184,34 +192,6 @@ __global__ __launch_bounds__(1024) void norm_long_kernel(const NormArgs a) {
   }
 }
 
-// Eight elements of a row as they are stored, zeros behind its end.
-template <typename T>
-struct Stored8 {
-  u32x4 v[sizeof(T) / 2];
-};
-template <typename T>
-__device__ __forceinline__ Stored8<T> stored8(const void* base, long long row, int c, int n) {
-  Stored8<T> s;
-  const T* p = static_cast<const T*>(base) + row + c;
-  if (c + 8 <= n) {
-#pragma unroll
-    for (int k = 0; k < (int)sizeof(T) / 2; ++k) s.v[k] = layers::load16(p + k * 16 / sizeof(T));
-  } else {
-    T t[8];
-#pragma unroll
-    for (int j = 0; j < 8; ++j) t[j] = c + j < n ? p[j] : (T)0.0f;
-    __builtin_memcpy(&s, t, sizeof(s));
-  }
-  return s;
-}
-template <typename T>
-__device__ __forceinline__ void widen8(const Stored8<T>& s, float* v) {
-  T t[8];
-  __builtin_memcpy(t, &s, sizeof(s));
-#pragma unroll
-  for (int j = 0; j < 8; ++j) v[j] = (float)t[j];
-}
-
 // dX and, with SUMS, the column sums of this workgroup's rows: row group by row
 // group, each thread adds its columns in order; the groups of one workgroup
 // are then added in order through LDS.  The next row is asked for before the sums
@@ -228,9 +208,16 @@ __global__ __launch_bounds__(NT) void norm_back_kernel(const NormBackArgs a) {
   const float inv = 1.0f / (float)a.n;
   Stored8<T> w[C];
   float sw[SUMS ? C : 1][8], sb[SUMS ? C : 1][8];
+  if (a.W != nullptr) {
+    rows8<T>(a.n, [&](auto get) {
+#pragma unroll
+      for (int c = 0; c < C; ++c) w[c] = get(a.W, 0, (c * TPR + t) * 8);
+    });
+#pragma unroll
+    for (int c = 0; c < C; ++c) settle8<T>(w[c], (c * TPR + t) * 8, a.n);
+  }
 #pragma unroll
   for (int c = 0; c < C; ++c) {
-    if (a.W != nullptr) w[c] = stored8<T>(a.W, 0, (c * TPR + t) * 8, a.n);
     if constexpr (SUMS) {
 #pragma unroll
       for (int j = 0; j < 8; ++j) sw[c][j] = sb[c][j] = 0.0f;
@@ -245,13 +232,23 @@ __global__ __launch_bounds__(NT) void norm_back_kernel(const NormBackArgs a) {
     Row v;
     v.mean = a.mean[row];
     v.rstd = a.rstd[row];
+    rows8<T>(a.n, [&](auto get) {
+#pragma unroll
+      for (int c = 0; c < C; ++c) {
+        v.x[c] = get(a.X, row * a.ldx, (c * TPR + t) * 8);
+        v.d[c] = get(a.dY, row * a.ldy, (c * TPR + t) * 8);
+        if (AHEAD && a.R != nullptr) v.r[c] = get(a.R, row * a.ldr, (c * TPR + t) * 8);
+      }
+    });
+    return v;
+  };
+  auto settle = [&](Row& v) {
 #pragma unroll
     for (int c = 0; c < C; ++c) {
-      v.x[c] = stored8<T>(a.X, row * a.ldx, (c * TPR + t) * 8, a.n);
-      v.d[c] = stored8<T>(a.dY, row * a.ldy, (c * TPR + t) * 8, a.n);
-      if (AHEAD && a.R != nullptr) v.r[c] = stored8<T>(a.R, row * a.ldr, (c * TPR + t) * 8, a.n);
+      settle8<T>(v.x[c], (c * TPR + t) * 8, a.n);
+      settle8<T>(v.d[c], (c * TPR + t) * 8, a.n);
+      if (AHEAD && a.R != nullptr) settle8<T>(v.r[c], (c * TPR + t) * 8, a.n);
     }
-    return v;
   };
   // h and g of chunk c
   auto values = [&](const Row& v, int c, float* h, float* g) {
@@ -277,9 +274,10 @@ __global__ __launch_bounds__(NT) void norm_back_kernel(const NormBackArgs a) {
 #pragma unroll 1
   for (; r0 < a.m; r0 += step) {
     if (!AHEAD) next = load(r0);
-    const Row v = next;
+    Row v = next;
     const bool live = r0 + mine < a.m;
     if (AHEAD && r0 + step < a.m) next = load(r0 + step);
+    settle(v);
     float s[2] = {0.0f, 0.0f};
 #pragma unroll
     for (int c = 0; c < C; ++c) {
@@ -311,8 +309,10 @@ __global__ __launch_bounds__(NT) void norm_back_kernel(const NormBackArgs a) {
         float h[8], g[8], res[8];
         values(v, c, h, g);
         weigh(c, g);
-        if (a.R != nullptr)
-          widen8<T>(AHEAD ? v.r[AHEAD ? c : 0] : stored8<T>(a.R, row * a.ldr, col, a.n), res);
+        if (a.R != nullptr) {
+          if constexpr (AHEAD) widen8<T>(v.r[c], res);
+          else get_row8<T>(a.R, row * a.ldr, col, a.n, res);
+        }
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
           g[j] = v.rstd * (g[j] - s1 - h[j] * s2);
@@ -402,9 +402,16 @@ __global__ __launch_bounds__(256) void norm_sums_kernel(const NormBackArgs a) {
   if (c < a.n) {
     for (long long r = (long long)group * 4 + mine; r < a.m; r += (long long)a.groups * 4) {
       const float mean = a.mean[r], rstd = a.rstd[r];
+      Stored8<T> raw[2];
+      rows8<T>(a.n, [&](auto get) {
+        raw[0] = get(a.X, r * a.ldx, (int)c);
+        raw[1] = get(a.dY, r * a.ldy, (int)c);
+      });
       float x[8], d[8];
-      get_row8<T>(a.X, r * a.ldx, (int)c, a.n, x);
-      get_row8<T>(a.dY, r * a.ldy, (int)c, a.n, d);
+      settle8<T>(raw[0], (int)c, a.n);
+      settle8<T>(raw[1], (int)c, a.n);
+      widen8<T>(raw[0], x);
+      widen8<T>(raw[1], d);
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
         sw[j] += d[j] * ((x[j] - mean) * rstd);

@@ -12,14 +12,23 @@ constexpr long long kMost = 1 << 22;
 
 template <typename T, int F>
 hipError_t quantize(const QuantizeArgs& all, bool outer, hipStream_t s) {
+  QuantizeArgs a = all;
   if (!outer && !all.together) {
-    const long long groups = ((long long)all.r * all.blocks + 15) / 16;
-    return launch(&quantize_rows_kernel<T, F>, dim3((unsigned)(groups < kMost ? groups : kMost)), 256,
-                  all, s);
+    // as many blocks beside each other as leave less than an eighth of them without work
+    a.beside = 4;
+    while (a.beside > 0 && (-all.blocks & ((1 << a.beside) - 1)) > all.blocks / 8) --a.beside;
+    const long long across = (all.blocks + (1 << a.beside) - 1) >> a.beside;
+    const long long high = (16 >> a.beside) * kRowsAhead, total = (all.r + high - 1) / high;
+    const long long most = kMost / across < 65535 ? kMost / across : 65535;
+    for (a.first = 0; a.first < total; a.first += most) {
+      const dim3 grid((unsigned)across, (unsigned)(total - a.first < most ? total - a.first : most));
+      const hipError_t e = launch(&quantize_rows_kernel<T, F>, grid, 256, a, s);
+      if (e != hipSuccess) return e;
+    }
+    return hipSuccess;
   }
   const long long total = ((long long)all.r + kScaleBlock - 1) / kScaleBlock * all.blocks;
   for (long long at = 0; at < total; at += kMost) {
-    QuantizeArgs a = all;
     a.first = at;
     const dim3 grid((unsigned)(total - at < kMost ? total - at : kMost));
     const hipError_t e =
