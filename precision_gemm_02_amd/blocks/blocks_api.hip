@@ -76,12 +76,44 @@ Plan few_plan(int size, int m, int n, int wide, int results, int k, int loading,
   return p;
 }
 
+// The times of this file's tile kernels (see ClassTimes), fitted to 24 shapes of 64 to 8192
+// rows, every class timed on each alone and split 2, 4 and 8 ways.  The class and split that
+// they choose take 1.00 to 1.01 times the best one's time in the mean; with the layer
+// operators' times it was 1.05 for whole 16-bit tiles (1000 x 2048 x 1024: 15.4 us, now
+// 12.4), 1.03 for 8 bits (128 x 2048 x 2048: 12.4 us, now 9.4).
+const ClassTimes* pair_times(int size, int loading) {
+  static const ClassTimes whole16 = {{{1.98e15, 10.5e-6, 1, {0, 0, 0, 0}},
+                                      {1.26e15, 5e-6, 2, {0, 1.0, 0, 0}},
+                                      {0.73e15, 3.5e-6, 4, {0, 0.57, 0.92, 0.92}}}, 6.4e-6, 8.1e12};
+  static const ClassTimes through16 = {{{0, 0, 1, {0, 0, 0, 0}},        // (has no largest tiles)
+                                        {0.82e15, 5.3e-6, 2, {0, 0.79, 0, 0}},
+                                        {0.43e15, 3.3e-6, 4, {0, 0.75, 0.93, 1.0}}}, 3.8e-6, 6.4e12};
+  static const ClassTimes any32 = {{{150e12, 2.9e-6, 1, {0, 0, 0, 0}},
+                                    {160e12, 5.3e-6, 2, {0, 0.89, 0, 0}},
+                                    {155e12, 5.2e-6, 4, {0, 0.965, 0.994, 0.994}}}, 4.3e-6, 5.9e12};
+  static const ClassTimes whole8 = {{{2.77e15, 12.2e-6, 1, {0, 0, 0, 0}},
+                                     {2.19e15, 8.7e-6, 2, {0, 0.92, 0, 0}},
+                                     {1.39e15, 6.6e-6, 4, {0, 0.84, 0.84, 1.0}}}, 3.8e-6, 8.5e12};
+  static const ClassTimes wide8 = {{{0, 0, 1, {0, 0, 0, 0}},            // (nor have these)
+                                    {1.20e15, 9.5e-6, 2, {0, 0.70, 0, 0}},
+                                    {0.81e15, 7.5e-6, 4, {0, 0.92, 0.92, 0.98}}}, 2e-6, 7.6e12};
+  if (size == 4) return &any32;
+  if (size == 2) return loading == kDirect ? &whole16 : &through16;
+  return loading == kDirect ? &whole8 : &wide8;
+}
+
+// A plan that takes none of the layer operators' kernels.
+Plan plan_pair(int size, int la, int rows, int n, int k, int loading, size_t ws_bytes, bool any_ws) {
+  return plan_product(size, la, kDense, rows, 1, n, k, loading, ws_bytes, any_ws, true, false,
+                      pair_times(size, loading));
+}
+
 // The plan of a gated product: a product with 2 n columns, but for few rows.  Workspace as in
 // plan_product.
 Plan gate_plan(int size, int m, int n, int k, int loading, size_t ws_bytes, bool any_ws) {
   const Plan p = few_plan(size, m, n, gate_columns(kFew16Wide), 2 * n, k, loading, ws_bytes, any_ws);
   if (p.kernel >= 0) return p;
-  return plan_product(size, kInner, kDense, m, 1, 2 * n, k, loading, ws_bytes, any_ws, true, false);
+  return plan_pair(size, kInner, m, 2 * n, k, loading, ws_bytes, any_ws);
 }
 
 // The plan of a product in 8 bits (kThrough: no tiles of 256 x 256).
@@ -89,7 +121,7 @@ constexpr int kFewWide8 = 32;                     // columns of its wide few-row
 Plan plan8(int m, int n, int k, int loading, size_t ws_bytes, bool any_ws) {
   const Plan p = few_plan(1, m, n, kFewWide8, n, k, loading, ws_bytes, any_ws);
   if (p.kernel >= 0) return p;
-  return plan_product(1, kInner, kDense, m, 1, n, k, loading, ws_bytes, any_ws, true, false);
+  return plan_pair(1, kInner, m, n, k, loading, ws_bytes, any_ws);
 }
 
 int pair_loading(const pgemm_gate_weights& w, int size, int inner) {
@@ -128,11 +160,18 @@ GateSpace gate_space(const pgemm_kind& kind, int m, int n, int k) {
   g.chunks = gate_chunks(rows, g.half);
   g.rest = 2 * (size_t)g.chunks * (size_t)n * 4;
   const int both = 2LL * k <= kMaxSize ? 2 * k : k;
-  const size_t parts[5] = {split_bytes(size, kInner, kDense, rows, 1, k, 2 * g.half, false),
-                           split_bytes(size, kOuter, kDense, k, 1, n, rows),
-                           split_bytes(size, kOuter, kDense, n, 1, k, rows),
-                           split_bytes(size, kOuter, kDense, k, 1, 2 * n, rows),
-                           split_bytes(size, kOuter, kDense, n, 1, both, rows)};
+  auto pair = [&](int la, int height, int width, int along, int loading) {
+    return split_space(plan_pair(size, la, height, width, along, loading, 0, true), kDense, height, 1,
+                       width);
+  };
+  const size_t parts[] = {pair(kInner, rows, k, 2 * g.half, kThrough),
+                          pair(kInner, rows, k, 2 * g.half, kDirect),
+                          pair(kOuter, k, n, rows, kDirect),
+                          pair(kOuter, n, k, rows, kDirect),
+                          pair(kOuter, k, 2 * n, rows, kDirect),
+                          pair(kOuter, n, both, rows, kDirect),
+                          split_bytes(size, kOuter, kDense, k, 1, n, rows),
+                          split_bytes(size, kOuter, kDense, n, 1, k, rows)};
   for (const size_t x : parts)
     if (x > g.rest) g.rest = x;
   g.rest = align256(g.rest);
@@ -191,8 +230,7 @@ bool plan_weights(WeightGradients* g, const pgemm_kind& kind, int m, int n, int 
     ProdArgs& a = g->args.p;
     const long long columns = (long long)a.N * g->count;
     if (columns <= kMaxSize) {
-      const Plan p = plan_product(size, kOuter, kDense, a.M, 1, (int)columns, m, kDirect, ws_bytes,
-                                  false);
+      const Plan p = plan_pair(size, kOuter, a.M, (int)columns, m, kDirect, ws_bytes, false);
       if (p.kernel >= 0) {
         a.splits = p.splits;
         a.k_split = p.k_split;
@@ -541,8 +579,7 @@ int pgemm_gated_linear_backward(pgemm_kind kind, int m, int n, int k, pgemm_rows
     lb = W.gate.order == PGEMM_KN ? kInner : kOuter;
     loading = both_loading(operand_loading(dz, ldz, size, (int)ldz, 0),
                            pair_loading(W, size, lb == kInner ? n : k));
-    dx_plan = plan_product(size, kInner, kDense, m, 1, k, (int)ldz, loading, space.rest, false, true,
-                           false);
+    dx_plan = plan_pair(size, kInner, m, k, (int)ldz, loading, space.rest, false);
     if (dx_plan.kernel < 0) return -2;
     a.splits = dx_plan.splits;
     a.k_split = dx_plan.k_split;
@@ -571,12 +608,10 @@ int pgemm_gated_linear_backward(pgemm_kind kind, int m, int n, int k, pgemm_rows
     a.partial = bias ? static_cast<float*>(rest) : nullptr;
     const bool out32 = kind.out_dtype == PGEMM_F32;
     if (ops.slope(a, bias && out32, s) != hipSuccess) return PGEMM_EHIP;
-    void* const to[2] = {dbias.gate, dbias.up};
-    for (int w = 0; w < 2; ++w)
-      if (bias && to[w] != nullptr &&
-          ops_of(kind.dtype).column_sum(a.partial + (size_t)w * (size_t)a.chunks * (size_t)n, to[w], n,
-                                        1, a.chunks, out32, s) != hipSuccess)
-        return PGEMM_EHIP;
+    if (bias) {
+      const NormColumnArgs c = {a.partial, dbias.gate, dbias.up, n, a.chunks, out32};
+      if (norm_ops(kind.dtype).norm_columns(c, s) != hipSuccess) return PGEMM_EHIP;
+    }
   }
   if (want_dx && ops.pair(dx, lb, kHalves, dx_plan.kernel, loading,
                           loading == kDirect && whole_tiles(size, ldz, W.gate.ld), s) != hipSuccess)

@@ -636,7 +636,7 @@ struct GateSlopeArgs {
   int n, half, act, rows;
   int chunks;             // row chunks (grid y)
   int tpr;                // threads per row (a power of two, at most 64)
-  float* partial;         // [weight][chunk][n] column sums (nullptr: not wanted)
+  float* partial;         // [chunk][weight][n] column sums (nullptr: not wanted)
 };
 
 // dZg = dY Zu act'(Zg) and dZu = dY act(Zg), each rounded once, zeros behind column n,
@@ -691,7 +691,7 @@ __global__ __launch_bounds__(256) void gate_slope_kernel(const GateSlopeArgs a) 
       if (n >= a.n) break;
       float v = 0.0f;
       for (int r = 0; r < rpb; ++r) v += sums[r * width + x];
-      a.partial[((long long)w * a.chunks + blockIdx.y) * a.n + n] = v;
+      a.partial[((long long)blockIdx.y * 2 + w) * a.n + n] = v;
     }
   }
 }

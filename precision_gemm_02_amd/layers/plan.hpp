@@ -90,17 +90,19 @@ struct ClassTime {
   int together;
   double part[4];          // by workgroups left over (0: unused)
 };
-inline ClassTime class_time(int kernel, int size) {
-  static const ClassTime t16[3] = {{1.35e15, 10e-6, 1, {0, 0, 0, 0}},
-                                   {1.10e15, 7e-6, 2, {0, 0.7, 0, 0}},
-                                   {0.60e15, 3.5e-6, 4, {0, 0.5, 0.75, 0.9}}};
-  static const ClassTime t32[3] = {{142e12, 6e-6, 1, {0, 0, 0, 0}},
-                                   {130e12, 4e-6, 2, {0, 0.93, 0, 0}},
-                                   {119e12, 3e-6, 4, {0, 0.8, 0.9, 0.95}}};
-  static const ClassTime t8[3] = {{2.4e15, 10e-6, 1, {0, 0, 0, 0}},
-                                  {1.9e15, 7e-6, 2, {0, 0.7, 0, 0}},
-                                  {1.0e15, 3.5e-6, 4, {0, 0.5, 0.75, 0.9}}};
-  return (size == 2 ? t16 : size == 1 ? t8 : t32)[kernel];
+// The three classes', and what a split adds: its launch, and the partial sums' traffic.
+struct ClassTimes {
+  ClassTime of[3];
+  double reduce, bandwidth;
+};
+inline const ClassTimes& class_times(int size) {
+  static const ClassTimes t16 = {{{1.35e15, 10e-6, 1, {0, 0, 0, 0}},
+                                  {1.10e15, 7e-6, 2, {0, 0.7, 0, 0}},
+                                  {0.60e15, 3.5e-6, 4, {0, 0.5, 0.75, 0.9}}}, 4e-6, 6e12};
+  static const ClassTimes t32 = {{{142e12, 6e-6, 1, {0, 0, 0, 0}},
+                                  {130e12, 4e-6, 2, {0, 0.93, 0, 0}},
+                                  {119e12, 3e-6, 4, {0, 0.8, 0.9, 0.95}}}, 4e-6, 6e12};
+  return size == 2 ? t16 : t32;
 }
 
 inline double tiles_time(const ClassTime& c, double tiles, double tile_flops) {
@@ -146,10 +148,12 @@ inline bool launch_fits(int kernel, int mode, long long rows, int groups, int n)
 // rows: the rows of D over all groups (how they are distributed is not known
 // here; any distribution is correct).  may_split: the summed index may be
 // shared by workgroups, through partial sums in `ws_bytes` bytes (any_ws: as
-// many as it takes).  few: the few-rows kernels may be chosen.
+// many as it takes).  may_few: the few-rows kernels may be chosen.  times: of the kernels
+// that take the product (nullptr: the layer operators').
 inline Plan plan_product(int size, int la, int mode, long long rows, int groups, int n, int k,
                          int loading, size_t ws_bytes, bool any_ws, bool may_split = true,
-                         bool may_few = true) {
+                         bool may_few = true, const ClassTimes* times = nullptr) {
+  if (times == nullptr) times = &class_times(size);
   Plan p;
   p.loading = loading;
   const int bk = 128 / size;
@@ -184,13 +188,12 @@ inline Plan plan_product(int size, int la, int mode, long long rows, int groups,
       if (mode == kRows) tiles *= groups * (per / bm > 0.5 ? per / bm + 0.5 : 1.0);
       else tiles *= (double)ceil_div(rows, bm) * (mode == kSums ? groups : 1);
       const double depth = mode == kSums ? (double)k / groups : (double)k;
-      const ClassTime ct = class_time(c, size);
+      const ClassTime& ct = times->of[c];
       const double matrix = (double)rows * n * (mode == kSums ? groups : 1);
       for (const int s : {1, 2, 3, 4, 5, 6, 8, 10, 12, 16, 24, 32, 48, 64}) {
         // (beyond 16 pieces per compute unit nothing is left to balance)
         if (s > 1 && (!may_split || depth / s < 4 * bk || tiles * s > 16.0 * kUnits)) break;
-        // the partial sums' traffic, and the launch that adds them
-        const double split = s > 1 ? 4e-6 + s * matrix * 8 / 6e12 : 0;
+        const double split = s > 1 ? times->reduce + s * matrix * 8 / times->bandwidth : 0;
         const double t = tiles_time(ct, tiles * s, 2.0 * bm * bn * depth / s) + split;
         if (best == 0 || t < best) {
           best = t;
@@ -207,7 +210,8 @@ inline Plan plan_product(int size, int la, int mode, long long rows, int groups,
     }
     const size_t need = split_space(p, mode, rows, groups, n);
     if (!any_ws && ws_bytes < need)   // the best plan that needs no space
-      return plan_product(size, la, mode, rows, groups, n, k, loading, 0, false, false, may_few);
+      return plan_product(size, la, mode, rows, groups, n, k, loading, 0, false, false, may_few,
+                          times);
   }
   return p;
 }
