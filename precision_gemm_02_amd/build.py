@@ -69,6 +69,11 @@ def layer_digest(extra_flags=()) -> str:
     return _digest(LAYERS, "pgemm_layers.h", extra_flags)
 
 
+def block_digest(extra_flags=()) -> str:
+    """The same of the block operators: blocks/ and pgemm_blocks.h."""
+    return _digest(BLOCKS, "pgemm_blocks.h", extra_flags)
+
+
 def _compile(src: str, extra) -> str:
     name = os.path.splitext(os.path.basename(src))[0]
     obj = os.path.join(BUILD_DIR, name + ".o")
