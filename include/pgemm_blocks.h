@@ -86,7 +86,8 @@ size_t pgemm_gated_linear_workspace(int dtype, int m, int n, int k);
  * W is read only for dX and X only for dW; m == 0 gives zero dW and dbias.  dZ is
  * rounded to T before the products, as pgemm_linear_backward's.
  * The workspace must have pgemm_gated_linear_backward_workspace bytes (it holds dZ
- * of both, and partial sums).
+ * of both, partial sums, and copies of X and W where n or k is not a multiple of 16
+ * bytes' elements).
  */
 int pgemm_gated_linear_backward(pgemm_kind kind, int m, int n, int k, pgemm_rows dY,
                                 pgemm_gate_rows Z, pgemm_rows X, pgemm_gate_weights W,

@@ -133,12 +133,26 @@ int both_loading(int a, int b) {
   return a == kDirect && b == kDirect ? kDirect : a != kThrough && b != kThrough ? kRagged : kThrough;
 }
 
-// The parts of a gated backward call's workspace: dZ of both weights, then partial
-// sums (of the bias gradients, then of the products, in stream order).
+// Rows of a gated backward call from which operands whose rows are not whole chunks of 16
+// bytes are copied into rows that are, for the whole-tile kernels, rather than taken through
+// registers (us, bf16 and fp32; k x n weights).  X, which also brings both weights' gradients
+// into one launch: 64 rows of 1001 x 1001 27.9 and 28 (fp32 38.6, 38), 128 of 501 x 500 30.6
+// and 24.8, 1000 of 1001 x 1001 60 and 42.  The weights, whose copy does not shrink with the
+// rows: beside X's 300 rows of 1001 x 1001 30.1 and 33.9 (fp32 54.2, 52.5), 512 of 2047 x 2047
+// 61 and 58 (fp32 181, 163), 4000 of them 177 and 159; in a launch of their own 512 of 1024 x
+// 2047 37 and 40 (fp32 100, 93), 2000 68 and 65.
+constexpr int kPadRows = 64;
+int pad_weight_rows(int size, bool beside) {
+  if (size == 4) return beside ? 256 : 512;
+  return beside ? 512 : 2048;
+}
+
+// The parts of a gated backward call's workspace: dZ of both weights, partial sums (of the
+// bias gradients, then of the products, in stream order), padded copies of X and the weights.
 struct GateSpace {
-  size_t dz = 0, rest = 0;
+  size_t dz = 0, rest = 0, x = 0, w = 0;
   int half = 0, chunks = 1;
-  size_t total() const { return dz + rest; }
+  size_t total() const { return dz + rest + x + 2 * w; }
 };
 
 // Row chunks of the slope kernel: two workgroups for every compute unit's four, at least
@@ -175,6 +189,15 @@ GateSpace gate_space(const pgemm_kind& kind, int m, int n, int k) {
   for (const size_t x : parts)
     if (x > g.rest) g.rest = x;
   g.rest = align256(g.rest);
+  const int per = 16 / size;
+  if (m >= kPadRows && n > 0 && k > 0) {
+    if (k % per) g.x = align256((size_t)m * (size_t)round_up(k, 8) * (size_t)size);
+    if (m >= pad_weight_rows(size, k % per != 0)) {
+      const size_t kn = n % per ? align256((size_t)k * (size_t)round_up(n, 8) * (size_t)size) : 0;
+      const size_t nk = k % per ? align256((size_t)n * (size_t)round_up(k, 8) * (size_t)size) : 0;
+      g.w = kn > nk ? kn : nk;
+    }
+  }
   return g;
 }
 
@@ -197,7 +220,7 @@ struct WeightGradients {
 
 bool plan_weights(WeightGradients* g, const pgemm_kind& kind, int m, int n, int k,
                   const pgemm_rows& X, const void* const* dz, long long ldz,
-                  const pgemm_gate_weights& dW, void* ws, size_t ws_bytes) {
+                  const pgemm_gate_weights& dW, int x_cols, void* ws, size_t ws_bytes) {
   const int size = size_of(kind.dtype);
   const pgemm_weight* const to[2] = {&dW.gate, &dW.up};
   const pgemm_weight* first = nullptr;
@@ -221,7 +244,7 @@ bool plan_weights(WeightGradients* g, const pgemm_kind& kind, int m, int n, int 
   }
   // dZ's rows go on behind column n (see gate_slope_kernel): its loads are direct
   if (alike && whole_tiles(size, X.ld, ldz) &&
-      operand_loading(X.data, X.ld, size, k, 0) == kDirect) {
+      operand_loading(X.data, X.ld, size, x_cols, 0) == kDirect) {
     g->args.p = g->one[0].a;
     g->args.count = g->count;
     g->args.A2 = g->one[g->count - 1].a.A;
@@ -559,6 +582,31 @@ int pgemm_gated_linear_backward(pgemm_kind kind, int m, int n, int k, pgemm_rows
   const void* const dzs[2] = {dz, dz + (size_t)space.half * (size_t)size};
 
   // all of the call is planned before any of it is launched
+  PadRowsArgs pads{};
+  int padded = 0;
+  auto pad = [&](const void** at, long long* ld, int height, int width, char* to) {
+    const long long wide = round_up(width, 8);
+    pads.of[padded++] = {*at, to, *ld, wide, height, width, threads_per_row((int)wide, 256)};
+    *at = to;
+    *ld = wide;
+  };
+  char* const copies = dz + space.dz + space.rest;
+  const int per = 16 / size;
+  const bool kn = W.gate.order == PGEMM_KN;
+  int inner = kn ? n : k, x_cols = k;          // columns that may be read
+  if (want_dx && n > 0 && m >= pad_weight_rows(size, k % per != 0)) {
+    if (inner % per && pair_loading(W, size, inner) != kDirect) {
+      pad(&W.gate.data, &W.gate.ld, kn ? k : n, inner, copies + space.x);
+      pad(&W.up.data, &W.up.ld, kn ? k : n, inner, copies + space.x + space.w);
+      inner = (int)W.gate.ld;
+    }
+  }
+  if (want_dw && m >= kPadRows && k % per && operand_loading(X.data, X.ld, size, k, 0) != kDirect) {
+    const void* at = X.data;
+    pad(&at, &X.ld, m, k, copies);
+    X.data = const_cast<void*>(at);
+    x_cols = (int)X.ld;
+  }
   PairArgs dx{};
   Plan dx_plan;
   int lb = kInner, loading = kThrough;
@@ -576,9 +624,8 @@ int pgemm_gated_linear_backward(pgemm_kind kind, int m, int n, int k, pgemm_rows
     dx.B2 = W.up.data;
     dx.half = space.half;
     dx.inner = n;
-    lb = W.gate.order == PGEMM_KN ? kInner : kOuter;
-    loading = both_loading(operand_loading(dz, ldz, size, (int)ldz, 0),
-                           pair_loading(W, size, lb == kInner ? n : k));
+    lb = kn ? kInner : kOuter;
+    loading = both_loading(operand_loading(dz, ldz, size, (int)ldz, 0), pair_loading(W, size, inner));
     dx_plan = plan_pair(size, kInner, m, k, (int)ldz, loading, space.rest, false);
     if (dx_plan.kernel < 0) return -2;
     a.splits = dx_plan.splits;
@@ -587,8 +634,10 @@ int pgemm_gated_linear_backward(pgemm_kind kind, int m, int n, int k, pgemm_rows
     set_tiles(&a, dx_plan.kernel, kDense, m);
   }
   WeightGradients dw;
-  if (want_dw && !plan_weights(&dw, kind, m, n, k, X, dzs, ldz, dW, rest, space.rest)) return -2;
+  if (want_dw && !plan_weights(&dw, kind, m, n, k, X, dzs, ldz, dW, x_cols, rest, space.rest))
+    return -2;
 
+  if (padded > 0 && ops.pad(pads, padded, s) != hipSuccess) return PGEMM_EHIP;
   if (n > 0 && (want_dx || want_dw || bias)) {
     GateSlopeArgs a{};
     a.dY = dY.data;

@@ -696,5 +696,32 @@ __global__ __launch_bounds__(256) void gate_slope_kernel(const GateSlopeArgs a) 
   }
 }
 
+// Matrices (blockIdx.y) with rows of ld elements into rows of ldt, a multiple of eight, zeros
+// behind the columns: a workgroup takes 256 / tpr rows at once.
+struct PadRowsArgs {
+  struct {
+    const void* from;
+    void* to;
+    long long ld, ldt;
+    int rows, cols;
+    int tpr;                // threads per row (a power of two, at most 256)
+  } of[3];
+};
+template <typename T>
+__global__ __launch_bounds__(256) void pad_rows_kernel(const PadRowsArgs args) {
+  const auto& a = args.of[blockIdx.y];
+  const int per = 256 / a.tpr, t = threadIdx.x & (a.tpr - 1);
+  for (long long r = (long long)blockIdx.x * per + threadIdx.x / a.tpr; r < a.rows;
+       r += (long long)gridDim.x * per)
+    for (long long c = t * 8; c < a.ldt; c += a.tpr * 8) {
+      Stored8<T> x;
+      rows8<T>(a.cols, [&](auto get) { x = get(a.from, r * a.ld, (int)c); });
+      settle8<T>(x, (int)c, a.cols);
+      T* const to = static_cast<T*>(a.to) + r * a.ldt + c;
+#pragma unroll
+      for (int k = 0; k < (int)sizeof(T) / 2; ++k) layers::store16(to + k * 16 / sizeof(T), x.v[k]);
+    }
+}
+
 }  // namespace blocks
 }  // namespace pgemm

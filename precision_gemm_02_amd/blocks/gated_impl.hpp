@@ -116,8 +116,13 @@ hipError_t slope(const GateSlopeArgs& a, bool sums32, hipStream_t s) {
 }
 
 template <typename T>
+hipError_t pad(const PadRowsArgs& a, int count, hipStream_t s) {
+  return launch(&pad_rows_kernel<T>, dim3(2048, (unsigned)count), 256, a, s);
+}
+
+template <typename T>
 const GateOps& ops() {
-  static const GateOps o = {&pair<T>, &apart<T>, &slope<T>};
+  static const GateOps o = {&pair<T>, &apart<T>, &slope<T>, &pad<T>};
   return o;
 }
 

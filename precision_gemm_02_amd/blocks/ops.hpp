@@ -42,6 +42,7 @@ struct GateOps {
   // one or two products of outer-order operands (kApart), whole
   hipError_t (*apart)(const PairArgs& a, int kernel, hipStream_t s);
   hipError_t (*slope)(const GateSlopeArgs& a, bool sums32, hipStream_t s);
+  hipError_t (*pad)(const PadRowsArgs& a, int count, hipStream_t s);
 };
 const GateOps& gate_ops_f32();
 const GateOps& gate_ops_f16();

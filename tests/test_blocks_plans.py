@@ -23,7 +23,7 @@ using namespace pgemm::layers;
 struct Launch {
   long long what, kernel, whole, M, N, K, splits, k_split, threads, partial, count, step;
 };
-enum { kNorm, kNormBack, kNormSums, kNormColumns, kQuantize, kFp8, kPair, kApartBoth, kSlope, kLayer };
+enum { kNorm, kNormBack, kNormSums, kNormColumns, kQuantize, kFp8, kPair, kApartBoth, kSlope, kLayer, kPad };
 static Launch log_[64];
 static int count_;
 static hipError_t note(Launch l) {
@@ -69,7 +69,15 @@ static hipError_t prod8(const Prod8Args& a, int, int kernel, int loading, hipStr
 static hipError_t no_sum(const float*, void*, int, int, int, int, hipStream_t) { return hipErrorInvalidValue; }
 static const TypeOps kLayers = {&layer, nullptr, &no_sum, nullptr, nullptr, nullptr, nullptr};
 static const NormOps kNorms = {&norm, &norm_back, &norm_sums, &norm_columns};
-static const GateOps kGates = {&pair, &apart, &slope};
+static hipError_t pad(const PadRowsArgs& a, int count, hipStream_t) {
+  Launch l{kPad};
+  for (int i = 0; i < count; ++i) {
+    if (a.of[i].ldt < a.of[i].cols || a.of[i].ldt % 8) return hipErrorInvalidValue;
+    l.M = (long long)(uintptr_t)a.of[i].to + a.of[i].rows * a.of[i].ldt * size_;    // the copies' end
+  }
+  return note(l);
+}
+static const GateOps kGates = {&pair, &apart, &slope, &pad};
 namespace pgemm {
 namespace layers {
 const TypeOps& ops_f32() { return kLayers; }
@@ -104,7 +112,7 @@ extern "C" int launches(Launch* to) {
 extern "C" void type_size(int size) { size_ = size; }
 """
 
-(NORM, NORM_BACK, NORM_SUMS, NORM_COLUMNS, QUANTIZE, FP8, PAIR, APART, SLOPE, LAYER) = range(10)
+(NORM, NORM_BACK, NORM_SUMS, NORM_COLUMNS, QUANTIZE, FP8, PAIR, APART, SLOPE, LAYER, PAD) = range(11)
 TOP = (1 << 31) - 4096
 i, f, p, q, z = ctypes.c_int, ctypes.c_float, ctypes.c_void_p, ctypes.c_longlong, ctypes.c_size_t
 
@@ -231,6 +239,8 @@ def drive(L, seed, times):
         half = -(-n // (128 // es)) * (128 // es)
         sound(got, need - -(-m * 2 * half * es // 256) * 256)
         if st[-1] == 0 and got and n > 0:
+            if got[0].what == PAD:            # copies behind the rest, inside the workspace
+                assert m >= 64 and got.pop(0).M <= (1 << 20) + need
             assert got[0].what == SLOPE and got[0].K == half
         assert all(-15 <= s <= 0 for s in st), st
         taken += sum(s == 0 for s in st)
@@ -306,6 +316,14 @@ def test_aligned_operands_take_the_whole_tile_kernels(lib, order):
             pair_of(k, n, order), Biases(1 << 20, 1 << 20), 1 << 20, need, None) == 0
         got = lib.launched()
         assert [x.what for x in got] == [SLOPE, NORM_COLUMNS, PAIR, APART] and got[2].whole
+    # rows that are not whole chunks are copied first, where there are enough
+    m, n, k = 555, 265, 1001
+    need = lib.pgemm_gated_linear_backward_workspace(kind, m, n, k)
+    assert lib.pgemm_gated_linear_backward(
+        kind, m, n, k, rows(n), Pairs(rows(n), rows(n)), rows(k), pair_of(k, n, order), rows(k),
+        pair_of(k, n, order), Biases(None, None), 1 << 20, need, None) == 0
+    got = lib.launched()
+    assert [x.what for x in got] == [PAD, SLOPE, PAIR, APART] and got[2].whole
     # rows too far apart for a tile's 32-bit offsets, and unaligned ones
     for ld in (1 << 24, 4097):
         assert lib.pgemm_gated_linear(Kind(2, 2, 0), 300, 512, 4096, rows(ld), pair_of(4096, 512),

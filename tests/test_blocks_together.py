@@ -392,3 +392,33 @@ def test_quotients_are_rounded_once():
         q, want = quantize_cpu(x, dtype, 1)
         assert torch.equal(s.cpu(), want)
         same8(Q, q.view(dtype), dtype)
+
+
+@pytest.mark.parametrize("dtype", TYPES, ids=ids)
+@pytest.mark.parametrize("order", ["kn", "nk"])
+@pytest.mark.parametrize("shape", [(64, 70, 33), (530, 131, 129), (300, 7, 9), (2100, 67, 64), (513, 64, 5)],
+                         ids=str)
+def test_gradients_of_rows_copied_into_whole_chunks(dtype, order, shape):
+    """Odd rows with NaN around them, which the copies must not take in."""
+    m, n, k = shape
+    g = gen(m + n + k)
+
+    def numbers(r, c):
+        return Guarded(r, c, dtype, pad=3, shift=1, data=ints(g, r, c, hi=1))
+    X, dY, Zg, Zu = numbers(m, k), numbers(m, n), numbers(m, n), numbers(m, n)
+    W = [numbers(*((k, n) if order == "kn" else (n, k))) for _ in range(2)]
+    dW = [Guarded(*((k, n) if order == "kn" else (n, k)), F32, pad=1) for _ in range(2)]
+    w, dw = ([t.t if order == "kn" else t.t.t() for t in s] for s in (W, dW))
+    dX = Guarded(m, k, dtype, pad=3, shift=1)
+    need = pg.gated_linear_backward_workspace(m, n, k, dtype)
+    ws = torch.full((need + 64,), 0x7F, dtype=torch.uint8, device="cuda")
+    pg.gated_linear_backward(dY.t, X.t, *w, Zg.t, Zu.t, act="relu", dX=dX.t, dW_gate=dw[0], dW_up=dw[1],
+                             ws=ws[:need])
+    x, d, a, b, wg, wu = (t.double().cpu() for t in (X.t, dY.t, Zg.t, Zu.t, *w))
+    dz = [d * b * (a > 0), d * a.clamp(min=0)]
+    assert torch.equal(dX.t.cpu(), (dz[0] @ wg.t() + dz[1] @ wu.t()).float().to(dtype))
+    for j in range(2):
+        assert torch.equal(dw[j].cpu().double(), x.t() @ dz[j])
+    for t in (X, dY, Zg, Zu, dX, *W, *dW):
+        t.check()
+    assert bool((ws[need:] == 0x7F).all())
