@@ -21,7 +21,8 @@ from .layer_ops import (_DTYPES, _KIND, _NO_WEIGHT, _ROWS, _WEIGHT, _act, _devic
 # every entry point include/pgemm_blocks.h declares
 EXPORTS = ("pgemm_layer_norm", "pgemm_layer_norm_backward", "pgemm_layer_norm_backward_workspace",
            "pgemm_gated_linear", "pgemm_gated_linear_workspace", "pgemm_gated_linear_backward",
-           "pgemm_gated_linear_backward_workspace", "pgemm_quantize", "pgemm_linear_fp8", "pgemm_linear_fp8_workspace", "pgemm_block_call")
+           "pgemm_gated_linear_backward_workspace", "pgemm_quantize", "pgemm_linear_fp8",
+           "pgemm_linear_fp8_workspace", "pgemm_block_call")
 
 _FP8 = {torch.float8_e4m3fn: 0, torch.float8_e5m2: 1}
 _BLOCK = 128            # columns (and rows) of a block with one scale
@@ -347,7 +348,8 @@ def linear_fp8(X, x_scales, W, w_scales, Y, *, bias=None, act="none", residual=N
     st = _call(_LINEAR_FP8, _PACK[_LINEAR_FP8](
         x, w, out, _act(act), m, n, k, *_rows(X, "X", m, k, X.dtype, dev),
         *_scales(x_scales, "x_scales", m, k, dev, by_row=True),
-        *_columns(W, "W", k, n, dev), *_scales(w_scales, "w_scales", n, k, dev, turned=True), _flat(bias, "bias", (n,), T, dev),
+        *_columns(W, "W", k, n, dev), *_scales(w_scales, "w_scales", n, k, dev, turned=True),
+        _flat(bias, "bias", (n,), T, dev),
         *_rows(residual, "residual", m, n, T, dev), *_rows(Z, "Z", m, n, T, dev),
         *_rows(Y, "Y", m, n, T, dev), *_space(ws, dev), _stream(stream, dev)))
     if st != 0:

@@ -142,7 +142,9 @@ __device__ __forceinline__ void finish8_any(const Prod8Args& args, long long m, 
 // the tile after next may be in flight).
 //
 // A block's sums are scaled and added while the matrix cores run the next
-// block's, so that neither waits for the other.
+// block's, so that neither waits for the other.  fp32 results of 4096^3 take 143 us
+// (0.96 PFLOP/s of the 16-bit instructions' 2.5, with widening in the vector units), 16-bit
+// ones prod8_whole_kernel's 66.
 template <int FA, int FB, int BM, int BN, int WGM, int WGN, bool DIRECT, bool COLS, bool WIDE>
 __global__ __launch_bounds__(WGM* WGN * 64) void prod8_tile_kernel(const Prod8Args args) {
   const ProdArgs& a = args.p;
@@ -371,7 +373,8 @@ __global__ __launch_bounds__(WGM* WGN * 64) void prod8_tile_kernel(const Prod8Ar
 // instruction's registers, each adding into its own sums, which are added over
 // the waves through LDS in a fixed order.  The scales of all its blocks are read
 // once into LDS, under the first blocks' loads (one by one, each row's would be a
-// cache line for itself), where they fit.
+// cache line for itself), where they fit.  16 x 4096 x 4096 8.4 us (17 MB of W: 2 TB/s; a
+// launch alone takes 6).
 template <int FA, int FB, int MB, int NB, int WAVES, bool COLS, bool WIDE>
 __global__ __launch_bounds__(WAVES * 64) void prod8_rows_kernel(const Prod8Args args) {
   const ProdArgs& a = args.p;

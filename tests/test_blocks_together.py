@@ -367,6 +367,22 @@ def test_random_8_bit_products(seed):
     Z.check("Z")
 
 
+@pytest.mark.parametrize("out", TYPES, ids=ids)
+@pytest.mark.parametrize("shape", [(7, 300, 700), (150, 264, 528), (64, 64, 8192), (600, 520, 256)], ids=str)
+def test_8_bit_residual_in_place(out, shape):
+    """The residual may be the result itself, in every class of kernel, split or not."""
+    m, n, k = shape
+    g = gen(48)
+    X, W = eights(g, m, k, dtype=E4M3, hi=1).cuda(), eights(g, n, k, dtype=E4M3, hi=1).cuda()
+    sx, sw = powers(g, m, -(-k // 128)).cuda(), powers(g, n, -(-k // 128)).cuda()
+    R = ints(g, m, n).to(out).cuda()
+    for ws in (None, space(pg.linear_fp8_workspace(m, n, k))):
+        Y, want = R.clone(), torch.empty_like(R)
+        pg.linear_fp8(X, sx, W.t(), sw.t(), want, residual=R, ws=ws)
+        pg.linear_fp8(X, sx, W.t(), sw.t(), Y, residual=Y, ws=ws)
+        assert torch.equal(Y, want)
+
+
 def test_quotients_are_rounded_once():
     """Quantized numbers next to the middles between 8-bit numbers, where a quotient off by one
     step of fp32 shows: from scales with full significands, every middle of the type and the
