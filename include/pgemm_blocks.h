@@ -67,8 +67,11 @@ typedef struct {
  *   or NULL), 8 Z (data NULL: not kept), 9 Y, 10 workspace (or NULL),
  *   11 workspace_bytes, 12 stream.
  * Activation and product see the fp32 sums; Z is those rounded to T.  m == 0 or n ==
- * 0: nothing is touched; k == 0: Z is the bias.  The workspace is as
- * pgemm_linear's.
+ * 0: nothing is touched; k == 0: Z is the bias.  With a workspace of
+ * pgemm_gated_linear_workspace bytes the summed index may be shared by several
+ * workgroups, and operands whose rows are not whole chunks of 16 bytes may be copied
+ * into rows that are; NULL or a smaller one never changes more than the order of the
+ * sums.
  */
 int pgemm_gated_linear(pgemm_kind kind, int m, int n, int k, pgemm_rows X, pgemm_gate_weights W,
                        pgemm_gate_bias bias, pgemm_gate_rows Z, pgemm_rows Y, void *workspace,

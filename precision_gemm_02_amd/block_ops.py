@@ -169,8 +169,9 @@ def gated_linear(X, W_gate, W_up, Y, *, bias_gate=None, bias_up=None, act="silu"
     X (m, k), the weights (k, n) in either order but both with the same strides, the
     biases (n,) and Z (m, n) have one dtype; Y (m, n) has that dtype or float32.
     Z_gate and Z_up, if given, receive X @ W + bias of each for
-    ``gated_linear_backward``.  ``ws`` (``gated_linear_workspace`` bytes) lets few
-    rows share a long k over more workgroups."""
+    ``gated_linear_backward``.  ``ws`` (``gated_linear_workspace`` bytes) lets
+    workgroups share a long k, and rows that are not whole chunks of 16 bytes be
+    copied into such."""
     dev = _device(X, "X")
     m, k = _shape2(X, "X")
     n = _shape2(Y, "Y")[1]

@@ -147,6 +147,28 @@ int pad_weight_rows(int size, bool beside) {
   return beside ? 512 : 2048;
 }
 
+// Bytes of a copy of X (m x k), and of one weight in either order, into whole chunks; 0 where
+// sizes alone do not ask for one.
+size_t pad_bytes(int size, int height, int width) {
+  return width % (16 / size) ? align256((size_t)height * (size_t)round_up(width, 8) * (size_t)size) : 0;
+}
+size_t pad_weight_bytes(int size, int k, int n) {
+  const size_t kn = pad_bytes(size, k, n), nk = pad_bytes(size, n, k);
+  return kn > nk ? kn : nk;
+}
+
+// The copies that a call makes before its products.
+struct Copies {
+  PadRowsArgs args{};
+  int count = 0;
+  void add(const void** at, long long* ld, int height, int width, char* to) {
+    const long long wide = round_up(width, 8);
+    args.of[count++] = {*at, to, *ld, wide, height, width, threads_per_row((int)wide, 256)};
+    *at = to;
+    *ld = wide;
+  }
+};
+
 // The parts of a gated backward call's workspace: dZ of both weights, partial sums (of the
 // bias gradients, then of the products, in stream order), padded copies of X and the weights.
 struct GateSpace {
@@ -163,6 +185,24 @@ int gate_chunks(int rows, int half) {
   const long long most = ceil_div(rows, 8);
   if (c > most) c = most;
   return c < 1 ? 1 : (int)c;
+}
+
+// The copies of a forward call, behind its partial sums.  Through registers k x n weights of odd
+// rows cost most (us, bf16 and fp32: 64 rows of 1001 x 1001 15.0 and with copies 15.6, fp32 19.3
+// and 22.8; 128 of 2047 x 2047 25.8, 25.2 and 51, 39; 300 of 1001 x 1000 18.3, 11.4 and 38, 24;
+// 4000 of 2047 x 2047 113, 69), n x k weights least (512 of 2047 x 2047 23.4, 27.4 and 81, 79;
+// 2000 of 1001 x 1001 21.1, 23.9; 1000 of 2047 x 2047 34.7, 29.6 and 142, 138; 4000 105, 68).
+struct GateCopies {
+  size_t x = 0, w = 0;
+  size_t total() const { return x + 2 * w; }
+};
+GateCopies gate_copies(int size, int m, int n, int k, bool kn) {
+  GateCopies c;
+  const double items = (double)m * n * k;
+  if (n < 1 || k < 1 || (kn ? m < 128 : size != 2 || m < 512 || items < 3e9)) return c;
+  c.x = pad_bytes(size, m, k);
+  c.w = kn ? pad_bytes(size, k, n) : pad_bytes(size, n, k);
+  return c;
 }
 
 GateSpace gate_space(const pgemm_kind& kind, int m, int n, int k) {
@@ -191,12 +231,8 @@ GateSpace gate_space(const pgemm_kind& kind, int m, int n, int k) {
   g.rest = align256(g.rest);
   const int per = 16 / size;
   if (m >= kPadRows && n > 0 && k > 0) {
-    if (k % per) g.x = align256((size_t)m * (size_t)round_up(k, 8) * (size_t)size);
-    if (m >= pad_weight_rows(size, k % per != 0)) {
-      const size_t kn = n % per ? align256((size_t)k * (size_t)round_up(n, 8) * (size_t)size) : 0;
-      const size_t nk = k % per ? align256((size_t)n * (size_t)round_up(k, 8) * (size_t)size) : 0;
-      g.w = kn > nk ? kn : nk;
-    }
+    g.x = pad_bytes(size, m, k);
+    if (m >= pad_weight_rows(size, k % per != 0)) g.w = pad_weight_bytes(size, k, n);
   }
   return g;
 }
@@ -503,6 +539,26 @@ int pgemm_gated_linear(pgemm_kind kind, int m, int n, int k, pgemm_rows X, pgemm
   if (!rows_ok(Y, n, size_of(kind.out_dtype), touch)) return -9;
   if (workspace != nullptr && !aligned_to(workspace, 16)) return -10;
   if (!touch) return PGEMM_OK;
+  const int lb = W.gate.order == PGEMM_KN ? kOuter : kInner;
+  int x_cols = k, inner = lb == kInner ? k : n;          // columns that may be read
+  Copies pads;
+  size_t space = workspace == nullptr ? 0 : workspace_bytes;
+  const GateCopies copies = gate_copies(size, m, n, k, lb == kOuter);
+  if (copies.total() > 0 && space >= pgemm_gated_linear_workspace(kind.dtype, m, n, k)) {
+    space -= copies.total();
+    char* const to = static_cast<char*>(workspace) + space / 16 * 16;
+    if (copies.x > 0 && operand_loading(X.data, X.ld, size, k, 0) != kDirect) {
+      const void* at = X.data;
+      pads.add(&at, &X.ld, m, k, to);
+      X.data = const_cast<void*>(at);
+      x_cols = (int)X.ld;
+    }
+    if (copies.w > 0 && pair_loading(W, size, inner) != kDirect) {
+      pads.add(&W.gate.data, &W.gate.ld, lb == kInner ? n : k, inner, to + copies.x);
+      pads.add(&W.up.data, &W.up.ld, lb == kInner ? n : k, inner, to + copies.x + copies.w);
+      inner = (int)W.gate.ld;
+    }
+  }
   PairArgs args{};
   ProdArgs& a = args.p;
   a.A = X.data;
@@ -523,20 +579,20 @@ int pgemm_gated_linear(pgemm_kind kind, int m, int n, int k, pgemm_rows X, pgemm
   args.bias2 = bias.up;
   args.Z2 = Z.up.data;
   args.ldz2 = Z.up.ld;
-  const int lb = W.gate.order == PGEMM_KN ? kOuter : kInner;
-  const int loading = both_loading(operand_loading(X.data, X.ld, size, k, 0),
-                                   pair_loading(W, size, lb == kInner ? k : n));
-  const Plan plan =
-      gate_plan(size, m, n, k, loading, workspace == nullptr ? 0 : workspace_bytes, false);
+  const int loading = both_loading(operand_loading(X.data, X.ld, size, x_cols, 0),
+                                   pair_loading(W, size, inner));
+  const Plan plan = gate_plan(size, m, n, k, loading, space, false);
   if (plan.kernel < 0) return -2;
   a.splits = plan.splits;
   a.k_split = plan.k_split;
   a.partial = static_cast<float*>(workspace);
   a.tiles_m = plan.kernel >= kFew16 ? 1 : (int)ceil_div(m, kShape[plan.kernel].bm);
   a.tiles_n = (int)ceil_div(n, gate_columns(plan.kernel));
-  return status(gate_ops(kind.dtype).pair(args, lb, kColumns, plan.kernel, loading,
-                                          loading == kDirect && whole_tiles(size, X.ld, W.gate.ld),
-                                          static_cast<hipStream_t>(stream)));
+  const GateOps& ops = gate_ops(kind.dtype);
+  const hipStream_t s = static_cast<hipStream_t>(stream);
+  if (pads.count > 0 && ops.pad(pads.args, pads.count, s) != hipSuccess) return PGEMM_EHIP;
+  return status(ops.pair(args, lb, kColumns, plan.kernel, loading,
+                         loading == kDirect && whole_tiles(size, X.ld, W.gate.ld), s));
 }
 
 size_t pgemm_gated_linear_workspace(int dtype, int m, int n, int k) {
@@ -547,7 +603,9 @@ size_t pgemm_gated_linear_workspace(int dtype, int m, int n, int k) {
     const size_t b = split_space(p, kDense, m, 1, 2 * n);
     if (b > most) most = b;
   }
-  return most;
+  const size_t kn = gate_copies(size_of(dtype), m, n, k, true).total();
+  const size_t nk = gate_copies(size_of(dtype), m, n, k, false).total();
+  return align256(most) + (kn > nk ? kn : nk);
 }
 
 int pgemm_gated_linear_backward(pgemm_kind kind, int m, int n, int k, pgemm_rows dY,
@@ -582,28 +640,21 @@ int pgemm_gated_linear_backward(pgemm_kind kind, int m, int n, int k, pgemm_rows
   const void* const dzs[2] = {dz, dz + (size_t)space.half * (size_t)size};
 
   // all of the call is planned before any of it is launched
-  PadRowsArgs pads{};
-  int padded = 0;
-  auto pad = [&](const void** at, long long* ld, int height, int width, char* to) {
-    const long long wide = round_up(width, 8);
-    pads.of[padded++] = {*at, to, *ld, wide, height, width, threads_per_row((int)wide, 256)};
-    *at = to;
-    *ld = wide;
-  };
+  Copies pads;
   char* const copies = dz + space.dz + space.rest;
   const int per = 16 / size;
   const bool kn = W.gate.order == PGEMM_KN;
   int inner = kn ? n : k, x_cols = k;          // columns that may be read
   if (want_dx && n > 0 && m >= pad_weight_rows(size, k % per != 0)) {
     if (inner % per && pair_loading(W, size, inner) != kDirect) {
-      pad(&W.gate.data, &W.gate.ld, kn ? k : n, inner, copies + space.x);
-      pad(&W.up.data, &W.up.ld, kn ? k : n, inner, copies + space.x + space.w);
+      pads.add(&W.gate.data, &W.gate.ld, kn ? k : n, inner, copies + space.x);
+      pads.add(&W.up.data, &W.up.ld, kn ? k : n, inner, copies + space.x + space.w);
       inner = (int)W.gate.ld;
     }
   }
   if (want_dw && m >= kPadRows && k % per && operand_loading(X.data, X.ld, size, k, 0) != kDirect) {
     const void* at = X.data;
-    pad(&at, &X.ld, m, k, copies);
+    pads.add(&at, &X.ld, m, k, copies);
     X.data = const_cast<void*>(at);
     x_cols = (int)X.ld;
   }
@@ -637,7 +688,7 @@ int pgemm_gated_linear_backward(pgemm_kind kind, int m, int n, int k, pgemm_rows
   if (want_dw && !plan_weights(&dw, kind, m, n, k, X, dzs, ldz, dW, x_cols, rest, space.rest))
     return -2;
 
-  if (padded > 0 && ops.pad(pads, padded, s) != hipSuccess) return PGEMM_EHIP;
+  if (pads.count > 0 && ops.pad(pads.args, pads.count, s) != hipSuccess) return PGEMM_EHIP;
   if (n > 0 && (want_dx || want_dw || bias)) {
     GateSlopeArgs a{};
     a.dY = dY.data;

@@ -5,9 +5,9 @@
 // those of prod_tile.hpp.
 //
 // Large products are bound by the matrix cores at the power-limited clock, as there.  The
-// kernels here take what pair_whole_kernel does not: rows that are not whole chunks, through
-// registers (1023 x 2047 x 1024, k x n: 24.5 us, 0.35 PFLOP/s; whole rows of 1000 x 2048 x
-// 1024 11.9), and strides beyond its offsets.
+// tile kernel here takes what pair_whole_kernel does not: rows that are not whole chunks and
+// that are not copied into such, through registers (512 x 2047 x 2047 n x k 23.4 us, 0.37
+// PFLOP/s), and strides beyond its offsets.
 #pragma once
 
 #include "../layers/prod_rows.hpp"

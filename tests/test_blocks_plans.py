@@ -347,3 +347,22 @@ def test_products_of_too_many_tiles_are_refused(lib):
             Kind(2, 2, 0), m, n, k, rows(n), Pairs(rows(n), rows(n)), rows(k), pair_of(k, n), rows(k),
             pair_of(k, n), Biases(None, None), 1 << 20, need, None) == -2
     assert lib.launched() == []
+
+
+def test_forward_copies_only_with_their_workspace(lib):
+    """Odd rows are copied into whole chunks where the workspace has the room; with less
+    they go through registers."""
+    lib.type_size(2)
+    none, kind = Pairs(Rows(None, 1), Rows(None, 1)), Kind(2, 2, 4)
+    for m, n, k, order, copied in ((130, 129, 64, 0, True), (130, 136, 65, 0, True), (127, 129, 64, 0, False),
+                                   (130, 136, 65, 1, False), (1000, 2047, 2047, 1, True)):
+        need = lib.pgemm_gated_linear_workspace(2, m, n, k)
+        for give, first in ((need, PAD if copied else PAIR), (need - 1, PAIR), (0, PAIR)):
+            assert lib.pgemm_gated_linear(
+                kind, m, n, k, rows(k), pair_of(k, n, order), Biases(None, None), none, rows(n),
+                (1 << 20) if give > 0 else None, max(0, give), None) == 0
+            got = lib.launched()
+            assert got[0].what == first, (m, n, k, order, give)
+            if first == PAD:
+                assert got[0].M <= (1 << 20) + need and got[1].whole
+                assert got[1].partial <= got[0].M - (1 << 20)

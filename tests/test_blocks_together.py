@@ -438,3 +438,31 @@ def test_gradients_of_rows_copied_into_whole_chunks(dtype, order, shape):
     for t in (X, dY, Zg, Zu, dX, *W, *dW):
         t.check()
     assert bool((ws[need:] == 0x7F).all())
+
+
+@pytest.mark.parametrize("dtype", TYPES, ids=ids)
+@pytest.mark.parametrize("order,shape", [("kn", (130, 131, 129)), ("kn", (300, 7, 64)), ("kn", (257, 64, 33)),
+                                         ("kn", (200, 45, 4105)), ("nk", (640, 2050, 2305))], ids=str)
+def test_gated_products_of_rows_copied_into_whole_chunks(dtype, order, shape):
+    """Forward, with NaN around the odd rows; the same without the workspace."""
+    m, n, k = shape
+    g = gen(m * n + k)
+
+    def numbers(r, c):
+        return Guarded(r, c, dtype, pad=3, shift=1, data=ints(g, r, c, hi=1))
+    X, W = numbers(m, k), [numbers(*((k, n) if order == "kn" else (n, k))) for _ in range(2)]
+    w = [t.t if order == "kn" else t.t.t() for t in W]
+    need = pg.gated_linear_workspace(m, n, k, dtype)
+    ws = torch.full((need + 64,), 0x7F, dtype=torch.uint8, device="cuda")
+    z = [X.t.double() @ t.double() for t in w]
+    assert z[0].abs().max() < 2 ** 11 and z[1].abs().max() < 2 ** 11
+    want = (z[0].clamp(min=0) * z[1]).float().to(dtype)
+    for give in (None, ws[:need], ws[:need // 2 // 16 * 16]):
+        Y, Z = Guarded(m, n, dtype, pad=1), [Guarded(m, n, dtype, pad=1) for _ in range(2)]
+        pg.gated_linear(X.t, *w, Y.t, act="relu", Z_gate=Z[0].t, Z_up=Z[1].t, ws=give)
+        assert torch.equal(Y.t, want)
+        for a, b in zip(Z, z):
+            assert torch.equal(a.t, b.to(dtype))
+        for t in (Y, X, *Z, *W):
+            t.check()
+    assert bool((ws[need:] == 0x7F).all())
