@@ -544,16 +544,20 @@ int pgemm_gated_linear(pgemm_kind kind, int m, int n, int k, pgemm_rows X, pgemm
   Copies pads;
   size_t space = workspace == nullptr ? 0 : workspace_bytes;
   const GateCopies copies = gate_copies(size, m, n, k, lb == kOuter);
-  if (copies.total() > 0 && space >= pgemm_gated_linear_workspace(kind.dtype, m, n, k)) {
+  const bool x_whole = operand_loading(X.data, X.ld, size, k, 0) == kDirect;
+  const bool w_whole = pair_loading(W, size, inner) == kDirect;
+  // (both operands have to become whole)
+  if (copies.total() > 0 && (x_whole || copies.x > 0) && (w_whole || copies.w > 0) &&
+      space >= pgemm_gated_linear_workspace(kind.dtype, m, n, k)) {
     space -= copies.total();
     char* const to = static_cast<char*>(workspace) + space / 16 * 16;
-    if (copies.x > 0 && operand_loading(X.data, X.ld, size, k, 0) != kDirect) {
+    if (!x_whole) {
       const void* at = X.data;
       pads.add(&at, &X.ld, m, k, to);
       X.data = const_cast<void*>(at);
       x_cols = (int)X.ld;
     }
-    if (copies.w > 0 && pair_loading(W, size, inner) != kDirect) {
+    if (!w_whole) {
       pads.add(&W.gate.data, &W.gate.ld, lb == kInner ? n : k, inner, to + copies.x);
       pads.add(&W.up.data, &W.up.ld, lb == kInner ? n : k, inner, to + copies.x + copies.w);
       inner = (int)W.gate.ld;

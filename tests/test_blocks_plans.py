@@ -366,3 +366,8 @@ def test_forward_copies_only_with_their_workspace(lib):
             if first == PAD:
                 assert got[0].M <= (1 << 20) + need and got[1].whole
                 assert got[1].partial <= got[0].M - (1 << 20)
+    # an X that no copy makes whole (its address): the weights are not copied for nothing
+    need = lib.pgemm_gated_linear_workspace(2, 300, 129, 64)
+    assert lib.pgemm_gated_linear(kind, 300, 129, 64, rows(64, (1 << 20) + 2), pair_of(64, 129, 0),
+                                  Biases(None, None), none, rows(129), 1 << 20, need, None) == 0
+    assert [x.what for x in lib.launched()] == [PAIR]
