@@ -88,6 +88,8 @@ size_t pgemm_gated_linear_workspace(int dtype, int m, int n, int k);
  *   or NULL), 12 workspace, 13 workspace_bytes, 14 stream.
  * W is read only for dX and X only for dW; m == 0 gives zero dW and dbias.  dZ is
  * rounded to T before the products, as pgemm_linear_backward's.
+ * Where a kept Z is infinite (fp16 sums beyond 65504), act and act' have their limits,
+ * and a product with an exact 0 (of dY, act or act') is 0; a NaN stays one.
  * The workspace must have pgemm_gated_linear_backward_workspace bytes (it holds dZ
  * of both, partial sums, and copies of X and W where n or k is not a multiple of 16
  * bytes' elements).

@@ -646,6 +646,12 @@ struct GateSlopeArgs {
 // dZg = dY Zu act'(Zg) and dZu = dY act(Zg), each rounded once, zeros behind column n,
 // and the column sums of a chunk of rows (before the rounding): see slope_kernel.  Bound by
 // memory: 8192 x 8192 bf16 143 us (671 MB: 4.7 TB/s); two rows asked for at once 144.
+//
+// A kept pre-activation may be infinite although the result was finite (an fp16 sum
+// beyond 65504).  Its products then take their limits: an activation far below 0 is 0, and
+// what is multiplied by an exact 0 (of the slope or of dY) is 0, not NaN.  (3 us of the 832
+// of 8192 x 4096 x 4096's gradients.  A branch around it where a chunk has no infinity, and
+// a second pass over its rows for a thread whose sums became NaN, cost 2 to 4.)
 template <typename T, int F>
 __global__ __launch_bounds__(256) void gate_slope_kernel(const GateSlopeArgs a) {
   __shared__ float sums[256 * 8];
@@ -653,6 +659,8 @@ __global__ __launch_bounds__(256) void gate_slope_kernel(const GateSlopeArgs a) 
   const int r1 = (int)((long long)a.rows * (blockIdx.y + 1) / a.chunks);
   const int c = (blockIdx.x * a.tpr + threadIdx.x % a.tpr) * 8;
   const int rpb = 256 / a.tpr;
+  const float inf = __builtin_inff();
+  const float lowest = a.act == kNone ? -inf : -3.402823466e38f;   // where act_value has its limit
   float sg[8] = {0, 0, 0, 0, 0, 0, 0, 0}, su[8] = {0, 0, 0, 0, 0, 0, 0, 0};
   if (c < a.half) {
 #pragma unroll 2
@@ -673,8 +681,9 @@ __global__ __launch_bounds__(256) void gate_slope_kernel(const GateSlopeArgs a) 
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
         const float z = g[j], dj = d[j];
-        g[j] = dj * u[j] * act_slope<F>(z, a.act);
-        u[j] = dj * act_value<F>(z, a.act);
+        const float s = act_slope<F>(z, a.act), v = act_value<F>(z < lowest ? lowest : z, a.act);
+        g[j] = fabsf(u[j]) == inf && dj * s == 0.0f ? 0.0f : dj * u[j] * s;
+        u[j] = fabsf(v) == inf && dj == 0.0f ? 0.0f : dj * v;
         if (c + j >= a.n) g[j] = u[j] = 0.0f;
         sg[j] += g[j];
         su[j] += u[j];
