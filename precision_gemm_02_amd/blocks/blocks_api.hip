@@ -69,8 +69,8 @@ Plan few_plan(int size, int m, int n, int wide, int results, int k, int loading,
   if (s > k / (16 * bk)) s = k / (16 * bk);
   if (s > 64) s = 64;
   if (s > 1) {
-    p.k_split = (int)round_up(ceil_div(k, s), bk);
-    p.splits = (int)ceil_div(k, p.k_split);
+    p.splits = (int)s;
+    share_inner(&p, k, bk);
     if (!any_ws && ws_bytes < split_space(p, kDense, m, 1, results)) p.splits = 1;
   }
   return p;

@@ -145,6 +145,18 @@ inline bool launch_fits(int kernel, int mode, long long rows, int groups, int n)
   return prod_grid(a, mode, kernel).x <= kMaxThreads / prod_threads(kernel);
 }
 
+// Shares k summed indices between p->splits workgroups, in whole steps of bk: as many as have
+// work, the last of whose ends, rounded up, has to stay within the kernels' 32 bits.
+inline void share_inner(Plan* p, int k, int bk) {
+  for (int s = p->splits; ; --s) {
+    const long long each = round_up(ceil_div(k, s), bk), n = ceil_div(k, each);
+    if (s > 1 && n * each > 0x7fffffffLL) continue;
+    p->k_split = (int)each;
+    p->splits = (int)n;
+    return;
+  }
+}
+
 // rows: the rows of D over all groups (how they are distributed is not known
 // here; any distribution is correct).  may_split: the summed index may be
 // shared by workgroups, through partial sums in `ws_bytes` bytes (any_ws: as
@@ -204,10 +216,7 @@ inline Plan plan_product(int size, int la, int mode, long long rows, int groups,
     }
   }
   if (p.splits > 1) {
-    if (mode == kDense) {
-      p.k_split = (int)round_up(ceil_div(k, p.splits), bk);
-      p.splits = (int)ceil_div(k, p.k_split);
-    }
+    if (mode == kDense) share_inner(&p, k, bk);
     const size_t need = split_space(p, mode, rows, groups, n);
     if (!any_ws && ws_bytes < need)   // the best plan that needs no space
       return plan_product(size, la, mode, rows, groups, n, k, loading, 0, false, false, may_few,

@@ -93,3 +93,32 @@ def test_gated_slopes_far_out(act, dtype, rows, out32):
     pg.gated_linear_backward(d, X, Wg, Wu, zg, zu, act=act, dX=dX, dW_gate=dWg, dW_up=dWu, ws=ws)
     for t in (dX, dWg, dWu):
         assert bool((t == 0).all())
+
+
+# ---- the longest rows of 8 bits ----------------------------------------------------------
+
+def x_at(t, at):
+    return t.view(torch.uint8)[:, at].view(t.dtype).cpu().double()
+
+
+@pytest.mark.parametrize("k", [(1 << 31) - 4096, (1 << 31) - 4097])
+def test_linear_fp8_longest_rows(k):
+    """The largest summed index, shared between workgroups and not: numbers in the first
+    and last blocks of the splits and of the rows."""
+    m, n = 2, 3
+    X, W = (torch.zeros(r, k, dtype=torch.uint8, device="cuda") for r in (m, n))
+    at = torch.cat([torch.arange(0, k, k // 61), torch.arange(k - 200, k)]).cuda()
+    g = gen(3)
+    x, w = (torch.randint(-4, 5, (r, len(at)), generator=g).float().to(torch.float8_e4m3fn).cuda()
+            for r in (m, n))
+    X[:, at], W[:, at] = x.view(torch.uint8), w.view(torch.uint8)
+    X, W = X.view(torch.float8_e4m3fn), W.view(torch.float8_e4m3fn)
+    at = at.unique()                         # (of a place named twice one number is left)
+    want = x_at(X, at) @ x_at(W, at).t()
+    one = torch.ones(1, 1, device="cuda")
+    blocks = -(-k // 128)
+    for out in (F32, BF16):
+        for ws in (None, space(pg.linear_fp8_workspace(m, n, k))):
+            Y = torch.full((m, n), NAN, dtype=out, device="cuda")
+            pg.linear_fp8(X, one.expand(m, blocks), W.t(), one.expand(blocks, n), Y, ws=ws)
+            assert torch.equal(Y.cpu(), want.to(out))
