@@ -177,14 +177,17 @@ struct GateSpace {
   size_t total() const { return dz + rest + x + 2 * w; }
 };
 
-// Row chunks of the slope kernel: two workgroups for every compute unit's four, at least
-// 8 rows each.
+// Row chunks of the slope kernel (its grid's y): two workgroups for every compute unit's four,
+// at least 8 rows each; and as norm_groups has it, no thread should add more than 1024 rows one
+// after the other.
 int gate_chunks(int rows, int half) {
   if (half < 1) return 1;
-  long long c = 8 * kUnits / ceil_div(half, threads_per_row(half, 64) * 8);
-  const long long most = ceil_div(rows, 8);
+  const int tpr = threads_per_row(half, 64);
+  long long c = 8 * kUnits / ceil_div(half, tpr * 8);
+  const long long most = ceil_div(rows, 8), long_sum = ceil_div(rows, 1024LL * (256 / tpr));
   if (c > most) c = most;
-  return c < 1 ? 1 : (int)c;
+  if (c < long_sum) c = long_sum;
+  return c < 1 ? 1 : c > 65535 ? 65535 : (int)c;
 }
 
 // The copies of a forward call, behind its partial sums.  Through registers k x n weights of odd

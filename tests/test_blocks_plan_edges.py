@@ -30,3 +30,30 @@ def test_ends_of_splits_stay_within_32_bits(lib, m, n, out):
         for x in lib.launched():
             if x.what == PAIR and x.splits > 1:
                 assert (x.splits - 1) * x.k_split < k <= x.splits * x.k_split < 1 << 31
+
+
+@pytest.mark.parametrize("n", [1, 63, 500, 8192, 100000, 1 << 19, 1 << 20, (1 << 28) + 1])
+@pytest.mark.parametrize("dtype", [0, 2])
+def test_bias_gradients_add_few_rows_one_after_the_other(lib, dtype, n):
+    """However wide the rows: a thread of the gated gradients adds at most 1024 (and what
+    the chunks' rounding adds), as one of the norm's gradients does; a launch takes the chunks."""
+    size = 4 if dtype == 0 else 2
+    lib.type_size(size)
+    kind = Kind(dtype, 0, 0)
+    half = -(-n // (128 // size)) * (128 // size)
+    tpr = 1
+    while tpr < 64 and tpr * 8 < half:
+        tpr *= 2
+    for m in (1, 7, 1000, 40000, 1 << 20, (1 << 24) + 3, TOP):
+        if 3 * m * n * size > 288e9:             # (dY and Z do not fit a card)
+            continue
+        need = lib.pgemm_gated_linear_backward_workspace(kind, m, n, 8)
+        assert lib.pgemm_gated_linear_backward(
+            kind, m, n, 8, rows(n), Pairs(rows(n), rows(n)), Rows(None, 1), pair_of(8, n), Rows(None, 1),
+            Weights(Weight(None, 1, 0, 0), Weight(None, 1, 0, 0)), Biases(1 << 20, 1 << 20), 1 << 20, need,
+            None) == 0
+        slope, sums = lib.launched()
+        assert slope.what == SLOPE and sums.what == NORM_COLUMNS
+        chunks = slope.count
+        assert 1 <= chunks <= 65535 and slope.partial <= need - -(-m * 2 * half * size // 256) * 256
+        assert -(-(-(-m // chunks)) // (256 // tpr)) <= 1025, (m, chunks)
