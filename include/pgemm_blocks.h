@@ -23,7 +23,8 @@ extern "C" {
  *   NULL: ones), 6 bias (n, or NULL: zeros), 7 eps (at least 0), 8 mean (m, fp32,
  *   or NULL: not kept), 9 rstd (the same), 10 Y, 11 stream.
  * m == 0 or n == 0: nothing is touched.  The variance is the mean square of what
- * is left of the mean (not the difference of two sums).
+ * is left of the mean (not the difference of two sums), in 64 bits for rows whose
+ * squares leave fp32's range.
  */
 int pgemm_layer_norm(int dtype, int m, int n, pgemm_rows X, const void *weight, const void *bias,
                      float eps, float *mean, float *rstd, pgemm_rows Y, void *stream);
@@ -38,8 +39,8 @@ int pgemm_layer_norm(int dtype, int m, int n, pgemm_rows X, const void *weight, 
  *   that reaches X past the norm; data NULL: none; may be dX itself), 10 dX (data
  *   NULL: not wanted), 11 dweight (or NULL), 12 dbias (or NULL), 13 workspace,
  *   14 workspace_bytes, 15 stream.
- * m == 0 gives a zero dweight and dbias.  The workspace must have
- * pgemm_layer_norm_backward_workspace bytes where dweight or dbias is wanted
+ * m == 0 gives a zero dweight and dbias.  X - mean and h are fp32.  The workspace must
+ * have pgemm_layer_norm_backward_workspace bytes where dweight or dbias is wanted
  * (partial sums).
  */
 int pgemm_layer_norm_backward(pgemm_kind kind, int m, int n, pgemm_rows dY, pgemm_rows X,

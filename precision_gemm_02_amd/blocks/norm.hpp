@@ -12,7 +12,8 @@
 // A row lives in the registers of TPR threads, C chunks of 8 elements each, so
 // that it is read once; longer rows are read again, from the caches.
 // Everything is fp32 in between (64 bits where a thread adds more than a few
-// dozen numbers of one row), each result rounded once.
+// dozen numbers of one row, and for a row whose squares leave fp32's range), each result
+// rounded once.
 #pragma once
 
 #include "../layers/prod.hpp"
@@ -86,13 +87,58 @@ __device__ __forceinline__ void row_sums(S (&v)[N], S (*lds)[16]) {
   }
 }
 
+// One row in 64 bits, by TPR threads of which this is t, read three times.
+template <typename T, int TPR>
+__device__ __forceinline__ void norm_row(const NormArgs& a, long long row, int t, double (*lds)[16]) {
+  double s[1] = {0.0};
+  for (uint32_t c = t * 8; c < (uint32_t)a.n; c += TPR * 8) {
+    float x[8];
+    get_row8<T>(a.X, row * a.ldx, (int)c, a.n, x);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) s[0] += x[j];
+  }
+  row_sums<TPR>(s, lds);
+  const double mean = s[0] / a.n;
+  s[0] = 0.0;
+  for (uint32_t c = t * 8; c < (uint32_t)a.n; c += TPR * 8) {
+    float x[8];
+    get_row8<T>(a.X, row * a.ldx, (int)c, a.n, x);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const double d = (int)c + j < a.n ? x[j] - mean : 0.0;
+      s[0] += d * d;
+    }
+  }
+  row_sums<TPR>(s, lds + 1);
+  const double rstd = 1.0 / sqrt(s[0] / a.n + (double)a.eps);
+  if (t == 0) {
+    if (a.mean != nullptr) a.mean[row] = (float)mean;
+    if (a.rstd != nullptr) a.rstd[row] = (float)rstd;
+  }
+  for (uint32_t c = t * 8; c < (uint32_t)a.n; c += TPR * 8) {
+    float x[8], w[8], b[8];
+    get_row8<T>(a.X, row * a.ldx, (int)c, a.n, x);
+    if (a.W != nullptr) get_row8<T>(a.W, 0, (int)c, a.n, w);
+    if (a.B != nullptr) get_row8<T>(a.B, 0, (int)c, a.n, b);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      float y = (float)((x[j] - mean) * rstd);
+      if (a.W != nullptr) y *= w[j];
+      if (a.B != nullptr) y += b[j];
+      x[j] = y;
+    }
+    put_row8<T>(a.Y, row * a.ldy, (int)c, a.n, x);
+  }
+}
+
 template <typename T, int TPR, int C, int NT>
 __global__ __launch_bounds__(NT) void norm_kernel(const NormArgs a) {
   __shared__ float lds[3][16];
+  __shared__ double wide[2][16];
   constexpr int ROWS = NT / TPR;
   const int t = threadIdx.x % TPR;
-  const long long row = (long long)blockIdx.x * ROWS + threadIdx.x / TPR;
-  const bool live = row < a.m;
+  const long long row = ROWS == 1 ? blockIdx.x : (long long)blockIdx.x * ROWS + threadIdx.x / TPR;
+  const bool live = ROWS == 1 || row < a.m;
   const long long at = (live ? row : a.m - 1) * a.ldx;
   Stored8<T> raw[C];
   rows8<T>(a.n, [&](auto get) {
@@ -125,8 +171,16 @@ __global__ __launch_bounds__(NT) void norm_kernel(const NormArgs a) {
     }
   row_sums<TPR>(q, lds + 1);
   const float d1 = q[0] * inv, var = q[1] * inv - d1 * d1;
-  const float rstd = 1.0f / sqrtf((var > 0.0f || var != var ? var : 0.0f) + a.eps);
   if (!live) return;
+  // squares beyond fp32 (or a NaN), or where what they lose below it matters (where waves have
+  // one row the branch is a scalar one, so that the row's registers are free behind it)
+  int far = !(var < 3e38f && (var > 0.0f ? var : 0.0f) + a.eps > 1e-30f);
+  if constexpr (TPR >= 64) far = __builtin_amdgcn_readfirstlane(far);
+  if (far) {
+    norm_row<T, TPR>(a, row, t, wide);
+    return;
+  }
+  const float rstd = 1.0f / sqrtf((var > 0.0f ? var : 0.0f) + a.eps);
   if (t == 0) {
     if (a.mean != nullptr) a.mean[row] = mean + d1;
     if (a.rstd != nullptr) a.rstd[row] = rstd;
@@ -149,50 +203,11 @@ __global__ __launch_bounds__(NT) void norm_kernel(const NormArgs a) {
   }
 }
 
-// One row per workgroup, read three times.
+// Rows longer than registers hold, one per workgroup.
 template <typename T>
 __global__ __launch_bounds__(1024) void norm_long_kernel(const NormArgs a) {
   __shared__ double lds[2][16];
-  const long long row = blockIdx.x;
-  double s[1] = {0.0};
-  for (long long c = threadIdx.x * 8; c < a.n; c += 8192) {
-    float x[8];
-    get_row8<T>(a.X, row * a.ldx, (int)c, a.n, x);
-#pragma unroll
-    for (int j = 0; j < 8; ++j) s[0] += x[j];
-  }
-  row_sums<1024>(s, lds);
-  const double mean = s[0] / a.n;
-  s[0] = 0.0;
-  for (long long c = threadIdx.x * 8; c < a.n; c += 8192) {
-    float x[8];
-    get_row8<T>(a.X, row * a.ldx, (int)c, a.n, x);
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      const double d = c + j < a.n ? x[j] - mean : 0.0;
-      s[0] += d * d;
-    }
-  }
-  row_sums<1024>(s, lds + 1);
-  const float rstd = (float)(1.0 / sqrt(s[0] / a.n + (double)a.eps));
-  if (threadIdx.x == 0) {
-    if (a.mean != nullptr) a.mean[row] = (float)mean;
-    if (a.rstd != nullptr) a.rstd[row] = rstd;
-  }
-  for (long long c = threadIdx.x * 8; c < a.n; c += 8192) {
-    float x[8], w[8], b[8];
-    get_row8<T>(a.X, row * a.ldx, (int)c, a.n, x);
-    if (a.W != nullptr) get_row8<T>(a.W, 0, (int)c, a.n, w);
-    if (a.B != nullptr) get_row8<T>(a.B, 0, (int)c, a.n, b);
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      float y = (float)(x[j] - mean) * rstd;
-      if (a.W != nullptr) y *= w[j];
-      if (a.B != nullptr) y += b[j];
-      x[j] = y;
-    }
-    put_row8<T>(a.Y, row * a.ldy, (int)c, a.n, x);
-  }
+  norm_row<T, 1024>(a, blockIdx.x, threadIdx.x, lds);
 }
 
 // dX and, with SUMS, the column sums of this workgroup's rows: row group by row

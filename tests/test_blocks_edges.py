@@ -122,3 +122,66 @@ def test_linear_fp8_longest_rows(k):
             Y = torch.full((m, n), NAN, dtype=out, device="cuda")
             pg.linear_fp8(X, one.expand(m, blocks), W.t(), one.expand(blocks, n), Y, ws=ws)
             assert torch.equal(Y.cpu(), want.to(out))
+
+
+# ---- rows whose squares leave fp32 ---------------------------------------------------------
+
+def norm64(x, eps):
+    mean = x.mean(1, keepdim=True)
+    rstd = 1 / torch.sqrt(((x - mean) ** 2).mean(1, keepdim=True) + eps)
+    return mean, rstd, (x - mean) * rstd
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16], ids=ids)
+@pytest.mark.parametrize("n", [40, 128, 500, 900, 2000, 2999, 8000, 16000, 30001, 40000])
+@pytest.mark.parametrize("eps,powers", [(1e-5, (0, 62, 64, 70, 100, 125, 3)), (0.0, (0, -50, -60, -80, -100, 70))])
+def test_layer_norm_of_huge_and_tiny_rows(dtype, n, eps, powers):
+    """The definition holds over the types' whole range, row by row, also where a row's sum
+    of squares is infinite in fp32, or nothing."""
+    g = gen(n)
+    x = torch.randn(3 * len(powers), n, generator=g) + torch.randn(3 * len(powers), 1, generator=g)
+    x *= torch.exp2(torch.tensor(powers, dtype=torch.float32)).repeat(3)[:, None]
+    X = x.to(dtype).cuda()
+    w, b = (torch.randn(n, generator=g).to(dtype).cuda() for _ in range(2))
+    Y = torch.full_like(X, NAN)
+    mean, rstd = (torch.full((X.shape[0],), NAN, device="cuda") for _ in range(2))
+    pg.layer_norm(X, Y, weight=w, bias=b, eps=eps, mean=mean, rstd=rstd)
+    x = X.double().cpu()
+    mu, r, h = norm64(x, eps)
+    # the statistics: a sum of n numbers of which a thread adds at most 64 one after the other,
+    # its parts by halves (at most 26 steps): 90 u of their magnitude, that of what is left of the
+    # mean once more; rstd 60 u and the mean's part squared.  Then x - mean, times rstd, times
+    # weight, plus bias: a rounding each, and Y's own.
+    mag, left = x.abs().mean(1, keepdim=True), (x - mu).abs().mean(1, keepdim=True)
+    e_mean = 2 * U * mag + 92 * U * (left + 90 * U * mag)
+    e_rstd = r * (60 * U) + r * (90 * U * mag * r) ** 2
+    w, b = w.double().cpu(), b.double().cpu()
+    e = ((x - mu).abs() * (3 * U * r + e_rstd) + r * (e_mean + 2 * U * (x.abs() + mu.abs()))) * w.abs()
+    y = h * w + b
+    e += 2 * U * ((h * w).abs() + y.abs() + b.abs())
+    half = torch.finfo(dtype).eps / 2
+    assert bool(((Y.double().cpu() - y).abs() <= e * (1 + half) + half * y.abs()).all())
+    assert bool(((mean.double().cpu() - mu[:, 0]).abs() <= (e_mean + U * mu.abs())[:, 0]).all())
+    assert bool(((rstd.double().cpu() - r[:, 0]).abs() <= (e_rstd + U * r)[:, 0]).all())
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16], ids=ids)
+@pytest.mark.parametrize("n", [40, 500, 3000, 20000, 40000])
+def test_layer_norm_of_the_largest_numbers(dtype, n):
+    """Rows of one number, whose sum is infinite in fp32, beside an ordinary one, one with an
+    infinity, and one that goes from end to end of the range."""
+    top = torch.finfo(dtype).max
+    X = torch.full((5, n), top, dtype=dtype, device="cuda")
+    X[1] = torch.randn(n, generator=gen(1)).to(dtype)
+    X[2, n // 2] = INF
+    X[3] = -top
+    X[4, : n // 2] = -top
+    Y, alone = torch.full_like(X, NAN), torch.full_like(X[1:2], NAN)
+    mean, rstd = (torch.full((5,), NAN, device="cuda") for _ in range(2))
+    pg.layer_norm(X, Y, eps=0.25, mean=mean, rstd=rstd)
+    pg.layer_norm(X[1:2], alone, eps=0.25)
+    assert torch.equal(Y[1:2], alone)
+    assert bool((Y[0] == 0).all()) and bool((Y[3] == 0).all()) and bool(Y[2].isnan().any())
+    assert float(mean[0]) == top and float(mean[3]) == -top and float(rstd[0]) == 2 == float(rstd[3])
+    # half the numbers each: the mean is 0, the spread the number itself
+    assert float(mean[4]) == 0 and bool((Y[4].double().cpu().abs() - 1).abs().max() <= 4 * U)
