@@ -6,6 +6,7 @@ import pytest
 import torch
 
 import precision_gemm_02_amd as pg
+from layer_util import Guarded, ints, weight
 
 pytestmark = [pytest.mark.gpu,
               pytest.mark.skipif(not torch.cuda.is_available(), reason="needs a GPU")]
@@ -185,3 +186,93 @@ def test_layer_norm_of_the_largest_numbers(dtype, n):
     assert float(mean[0]) == top and float(mean[3]) == -top and float(rstd[0]) == 2 == float(rstd[3])
     # half the numbers each: the mean is 0, the spread the number itself
     assert float(mean[4]) == 0 and bool((Y[4].double().cpu().abs() - 1).abs().max() <= 4 * U)
+
+
+# ---- few rows: wide products, long rows of 8 bits --------------------------------------------
+
+E4M3, E5M2 = torch.float8_e4m3fn, torch.float8_e5m2
+ids8 = {E4M3: "e4m3", E5M2: "e5m2"}.get
+# columns that fill the chip with workgroups of twice the width, with and without a partly
+# filled last one (test_blocks_plan_edges.py holds that these sizes take those kernels)
+WIDE = [(8161, 1001), (8200, 1032), (8191, 72)]
+
+
+@pytest.mark.parametrize("dtype", TYPES, ids=ids)
+@pytest.mark.parametrize("order", ["kn", "nk"])
+@pytest.mark.parametrize("m", [1, 16, 17, 32])
+@pytest.mark.parametrize("n,k", WIDE)
+def test_wide_gated_products_of_few_rows(dtype, order, m, n, k):
+    """Whole numbers: exact sums and products."""
+    g = gen(m + n + k)
+    pad = n % 8
+    X = Guarded(m, k, dtype, pad=pad, data=ints(g, m, k, hi=1).to(dtype))
+    Wg, Wu = (weight(g, (), k, n, order, dtype, integer=True, pad=pad) for _ in range(2))
+    bg, bu = (ints(g, n).to(dtype).cuda() for _ in range(2))
+    Y, Zg, Zu = Guarded(m, n, F32, pad=pad), Guarded(m, n, dtype, pad=pad), Guarded(m, n, dtype, pad=pad)
+    pg.gated_linear(X.t, Wg, Wu, Y.t, bias_gate=bg, bias_up=bu, act="relu", Z_gate=Zg.t, Z_up=Zu.t,
+                    ws=space(pg.gated_linear_workspace(m, n, k, dtype)))
+    x = X.t.double().cpu()
+    zg, zu = (x @ w.double().cpu() + b.double().cpu() for w, b in ((Wg, bg), (Wu, bu)))
+    assert torch.equal(Y.t.double().cpu(), zg.clamp(min=0) * zu)
+    assert torch.equal(Zg.t.cpu(), zg.to(dtype)) and torch.equal(Zu.t.cpu(), zu.to(dtype))
+    for t in (Y, Zg, Zu):
+        t.check()
+    Y = Guarded(m, n, dtype)
+    pg.gated_linear(X.t, Wg, Wu, Y.t, act="none")
+    want = (zg - bg.double().cpu()) * (zu - bu.double().cpu())
+    assert torch.equal(Y.t.cpu(), want.to(dtype))
+    Y.check()
+
+
+def eights(g, r, c, dtype, pad):
+    """Small whole numbers in 8 bits, NaN around their rows."""
+    buf = torch.full((r, c + pad), 0x7F, dtype=torch.uint8)
+    buf[:, :c] = torch.randint(-4, 5, (r, c), generator=g).float().to(dtype).view(torch.uint8)
+    return buf.cuda()[:, :c].view(dtype)
+
+
+def spread64(s, rows, cols):
+    s = s.double().cpu()
+    if s.shape[0] != rows:
+        s = s.repeat_interleave(128, 0)[:rows]
+    return s.repeat_interleave(128, 1)[:, :cols]
+
+
+def held_exactly(m, n, k, tx, tw, rows, pad):
+    """linear_fp8 of whole numbers and scales that are powers of two, with each type of
+    result, with and without a workspace."""
+    g = gen(m + n + k + rows)
+    X, W = eights(g, m, k, tx, pad), eights(g, n, k, tw, pad)
+    sx, sw = (torch.exp2(torch.randint(-1, 2, (r, -(-k // 128)), generator=g).float()).cuda()
+              for r in (m, -(-n // rows)))
+    bias, R = ints(g, n), ints(g, m, n)
+    xd, wd = X.cpu().double() * spread64(sx, m, k), W.cpu().double() * spread64(sw, n, k)
+    z = xd @ wd.t() + bias.double()
+    # multiples of 1/4 (of two scales) below 2^22, also without cancellation: exact in fp32
+    assert float((xd.abs() @ wd.abs().t()).max()) < 2 ** 22 - 3
+    for out in TYPES:
+        for ws in (None, space(pg.linear_fp8_workspace(m, n, k))):
+            Y, Z = Guarded(m, n, out, pad=pad), Guarded(m, n, out, pad=pad)
+            pg.linear_fp8(X, sx, W.t(), sw.t(), Y.t, bias=bias.to(out).cuda(), act="relu",
+                          residual=R.to(out).cuda(), Z=Z.t, ws=ws)
+            assert torch.equal(Z.t.cpu(), z.to(out))
+            assert torch.equal(Y.t.cpu(), (z.clamp(min=0) + R.double()).to(out))
+            Y.check("Y")
+            Z.check("Z")
+
+
+@pytest.mark.parametrize("types", [(E4M3, E4M3), (E5M2, E4M3), (E4M3, E5M2)], ids=lambda t: ids8(t[0]) + ids8(t[1]))
+@pytest.mark.parametrize("rows", [1, 128])
+@pytest.mark.parametrize("m", [1, 16, 17, 32])
+@pytest.mark.parametrize("n,k", WIDE)
+def test_wide_8_bit_products_of_few_rows(types, rows, m, n, k):
+    held_exactly(m, n, k, *types, rows, pad=n % 8)
+
+
+# shared between workgroups and not; more blocks than a workgroup's room for scales
+# (16384 with 16 rows and a scale for each column, 30720 with block scales)
+@pytest.mark.parametrize("k", [4096, 4224, 8320, 8337, 11000, 16512, 16517, 30848, 31000])
+@pytest.mark.parametrize("rows", [1, 128])
+@pytest.mark.parametrize("m,n", [(1, 1), (1, 72), (16, 40), (17, 16), (32, 129)])
+def test_long_8_bit_products_of_few_rows(rows, k, m, n):
+    held_exactly(m, n, k, E4M3, E4M3, rows, pad=k % 2 * 3)

@@ -57,3 +57,43 @@ def test_bias_gradients_add_few_rows_one_after_the_other(lib, dtype, n):
         chunks = slope.count
         assert 1 <= chunks <= 65535 and slope.partial <= need - -(-m * 2 * half * size // 256) * 256
         assert -(-(-(-m // chunks)) // (256 // tpr)) <= 1025, (m, chunks)
+
+
+# layers/launch.hpp's kernels for 16 and 32 rows, and their forms of twice the width
+FEW, WIDE = {16: 3, 32: 4}, {16: 5, 32: 6}
+
+
+@pytest.mark.parametrize("m", [1, 16, 17, 32])
+def test_kernels_of_few_rows(lib, m):
+    """Which sizes take the wide kernels, split or not: the sizes of the GPU tests."""
+    top, none, one = 16 if m <= 16 else 32, Pairs(Rows(None, 1), Rows(None, 1)), Scales(1 << 20, 1, 1, 1)
+
+    def gated(n, k, order, dtype):
+        lib.type_size(4 if dtype == 0 else 2)
+        need = lib.pgemm_gated_linear_workspace(dtype, m, n, k)
+        assert lib.pgemm_gated_linear(Kind(dtype, dtype, 4), m, n, k, rows(k), pair_of(k, n, order),
+                                      Biases(None, None), none, rows(n), 1 << 20, need, None) == 0
+        return lib.launched()
+
+    def fp8(n, k, out, split):
+        need = lib.pgemm_linear_fp8_workspace(m, n, k) if split else 0
+        assert lib.pgemm_linear_fp8(Kind8(0, 0, out, 0), m, n, k, rows(k), one, rows(k), one, None, Rows(None, 1),
+                                    Rows(None, 1), rows(n), (1 << 20) if need else None, need, None) == 0
+        return lib.launched()
+
+    for n, k in ((8161, 1001), (8200, 1032), (8191, 72)):
+        for order in (0, 1):
+            for dtype in (0, 1, 2):
+                got = gated(n, k, order, dtype)
+                assert [x.what for x in got] == [PAIR] and got[0].kernel == WIDE[top] and got[0].splits == 1
+        for out in (0, 1, 2):
+            got = fp8(n, k, out, True)
+            assert len(got) == 1 and got[0].kernel == WIDE[top] and got[0].splits == 1
+    assert gated(8160, 72, 1, 2)[0].kernel == FEW[top]
+    for n in (1, 16, 40, 72, 129):
+        for k in (4096, 4224, 8320, 8337, 11000, 16512, 16517, 30848, 31000):
+            for out in (0, 2):
+                got = fp8(n, k, out, True)
+                assert got[0].kernel == FEW[top] and got[0].splits == -(-k // got[0].k_split) > 1
+                got = fp8(n, k, out, False)
+                assert got[0].kernel == FEW[top] and got[0].splits == 1
