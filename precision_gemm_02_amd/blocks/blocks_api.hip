@@ -53,9 +53,9 @@ int gate_columns(int kernel) {
   return kShape[kernel].bn / 2;
 }
 
-// The plan of a few-rows kernel (at most 32 rows), whose workgroups take `wide` columns where
-// that gives every compute unit one, else 16.  `results`: partial sums of a row and split.
-// (No kernel if one launch does not take them.)
+// The plan of a few-rows kernel (of 16 or 32, which is all that the kernels take), whose
+// workgroups take `wide` columns where that gives every compute unit one, else 16.
+// `results`: partial sums of a row and split.  (No kernel if one launch does not take them.)
 Plan few_plan(int size, int m, int n, int wide, int results, int k, int loading, size_t ws_bytes,
               bool any_ws) {
   Plan p;

@@ -367,7 +367,7 @@ __global__ __launch_bounds__(WGM* WGN * 64) void prod8_tile_kernel(const Prod8Ar
   }
 }
 
-// Few rows: up to 16 MB of them against all of W, bound by reading W once.  A
+// Few rows: M of at most 16 MB (few_plan) against all of W, bound by reading W once.  A
 // workgroup takes 16 NB columns; its waves take blocks of 128 of the summed index
 // in turn (U of them in flight), from memory straight into the matrix
 // instruction's registers, each adding into its own sums, which are added over
@@ -405,127 +405,124 @@ __global__ __launch_bounds__(WAVES * 64) void prod8_rows_kernel(const Prod8Args 
                    (b_lo + unit) * args.sw_block];
   };
 
-  for (int m0 = 0; m0 < a.M; m0 += 16 * MB) {
-    auto x_scale = [&](int r, int unit) {
-      return args.sx[(m0 + r < a.M ? m0 + r : a.M - 1) * args.sx_row + (b_lo + unit) * args.sx_block];
-    };
-    const uint8_t* arow[MB];
+  auto x_scale = [&](int r, int unit) {
+    return args.sx[(r < a.M ? r : a.M - 1) * args.sx_row + (b_lo + unit) * args.sx_block];
+  };
+  const uint8_t* arow[MB];
 #pragma unroll
-    for (int b = 0; b < MB; ++b) {
-      const int m = m0 + 16 * b + i < a.M ? m0 + 16 * b + i : a.M - 1;
-      arow[b] = static_cast<const uint8_t*>(a.A) + m * a.lda;
-    }
-    f32x4 acc[MB][NB];
+  for (int b = 0; b < MB; ++b) {
+    const int m = 16 * b + i < a.M ? 16 * b + i : a.M - 1;
+    arow[b] = static_cast<const uint8_t*>(a.A) + m * a.lda;
+  }
+  f32x4 acc[MB][NB];
+#pragma unroll
+  for (int b = 0; b < MB; ++b)
+#pragma unroll
+    for (int c = 0; c < NB; ++c) acc[b][c] = f32x4{0, 0, 0, 0};
+
+  struct Unit {
+    u32x4 w[NB][2], x[MB][2];
+  };
+  auto use = [&](const Unit& u, int unit) {
+    float sx[MB], sw[WS == 1 ? 1 : NB][COLS ? 4 : 1];
 #pragma unroll
     for (int b = 0; b < MB; ++b)
+      sx[b] = staged ? scales[(16 * b + i) * pitch + unit] : x_scale(16 * b + i, unit);
 #pragma unroll
-      for (int c = 0; c < NB; ++c) acc[b][c] = f32x4{0, 0, 0, 0};
-
-    struct Unit {
-      u32x4 w[NB][2], x[MB][2];
-    };
-    auto use = [&](const Unit& u, int unit) {
-      float sx[MB], sw[WS == 1 ? 1 : NB][COLS ? 4 : 1];
+    for (int c = 0; c < (COLS ? NB : 1); ++c)
 #pragma unroll
-      for (int b = 0; b < MB; ++b)
-        sx[b] = staged ? scales[(16 * b + i) * pitch + unit] : x_scale(16 * b + i, unit);
-#pragma unroll
-      for (int c = 0; c < (COLS ? NB : 1); ++c)
-#pragma unroll
-        for (int j = 0; j < (COLS ? 4 : 1); ++j) {
-          const int n = COLS ? 16 * c + 4 * g + j : 0;
-          sw[c][j] = staged ? scales[(XS + n) * pitch + unit] : w_scale(col0 + n, unit);
-        }
-      Part<WIDE> x[MB];
-#pragma unroll
-      for (int b = 0; b < MB; ++b) x[b] = part<WIDE, FA>(u.x[b][0], u.x[b][1]);
-#pragma unroll
-      for (int c = 0; c < NB; ++c) {
-        const Part<WIDE> w = part<WIDE, FB>(u.w[c][0], u.w[c][1]);
-#pragma unroll
-        for (int b = 0; b < MB; ++b) {
-          const f32x4 t = block_sum<WIDE, FB, FA>(w, x[b]);
-#pragma unroll
-          for (int j = 0; j < 4; ++j)
-            acc[b][c][j] += t[j] * (sx[b] * sw[COLS ? c : 0][COLS ? j : 0]);
-        }
+      for (int j = 0; j < (COLS ? 4 : 1); ++j) {
+        const int n = COLS ? 16 * c + 4 * g + j : 0;
+        sw[c][j] = staged ? scales[(XS + n) * pitch + unit] : w_scale(col0 + n, unit);
       }
-    };
-    constexpr int STEP = U * WAVES;
-    Unit xs[U], ys[U];
-    auto load = [&](int u0, Unit(&us)[U]) {
+    Part<WIDE> x[MB];
 #pragma unroll
-      for (int q = 0; q < U; ++q) {
-        const int unit = u0 + q * WAVES;
-        if (unit >= whole) break;
-        const int k0 = k_lo + unit * BK;
+    for (int b = 0; b < MB; ++b) x[b] = part<WIDE, FA>(u.x[b][0], u.x[b][1]);
 #pragma unroll
-        for (int kk = 0; kk < 2; ++kk) {
+    for (int c = 0; c < NB; ++c) {
+      const Part<WIDE> w = part<WIDE, FB>(u.w[c][0], u.w[c][1]);
 #pragma unroll
-          for (int c = 0; c < NB; ++c) us[q].w[c][kk] = load16(wrow[c] + k0 + (4 * kk + g) * V);
+      for (int b = 0; b < MB; ++b) {
+        const f32x4 t = block_sum<WIDE, FB, FA>(w, x[b]);
 #pragma unroll
-          for (int b = 0; b < MB; ++b) us[q].x[b][kk] = load16(arow[b] + k0 + (4 * kk + g) * V);
-        }
+        for (int j = 0; j < 4; ++j)
+          acc[b][c][j] += t[j] * (sx[b] * sw[COLS ? c : 0][COLS ? j : 0]);
       }
-    };
-    auto use_all = [&](int u0, Unit(&us)[U]) {
-#pragma unroll
-      for (int q = 0; q < U; ++q) {
-        if (u0 + q * WAVES >= whole) break;
-        use(us[q], u0 + q * WAVES);
-      }
-    };
-    load(wave, xs);
-    if (staged) {
-      for (int t = threadIdx.x; t < (XS + WS) * units; t += WAVES * 64) {
-        const int r = t / units, unit = t - r * units;
-        scales[r * pitch + unit] = r < XS ? x_scale(r, unit) : w_scale(col0 + r - XS, unit);
-      }
-      __syncthreads();
     }
-#pragma unroll 1
-    for (int u0 = wave; u0 < whole; u0 += 2 * STEP) {
-      load(u0 + STEP, ys);
-      use_all(u0, xs);
-      load(u0 + 2 * STEP, xs);
-      use_all(u0 + STEP, ys);
-    }
-    if (whole < units && whole % WAVES == wave) {     // the last, partly filled block
-      Unit u;
-      const int k0 = k_lo + whole * BK;
+  };
+  constexpr int STEP = U * WAVES;
+  Unit xs[U], ys[U];
+  auto load = [&](int u0, Unit(&us)[U]) {
+#pragma unroll
+    for (int q = 0; q < U; ++q) {
+      const int unit = u0 + q * WAVES;
+      if (unit >= whole) break;
+      const int k0 = k_lo + unit * BK;
 #pragma unroll
       for (int kk = 0; kk < 2; ++kk) {
 #pragma unroll
-        for (int c = 0; c < NB; ++c) u.w[c][kk] = load_guarded(wrow[c], k0 + (4 * kk + g) * V, k_hi);
+        for (int c = 0; c < NB; ++c) us[q].w[c][kk] = load16(wrow[c] + k0 + (4 * kk + g) * V);
 #pragma unroll
-        for (int b = 0; b < MB; ++b) u.x[b][kk] = load_guarded(arow[b], k0 + (4 * kk + g) * V, k_hi);
+        for (int b = 0; b < MB; ++b) us[q].x[b][kk] = load16(arow[b] + k0 + (4 * kk + g) * V);
       }
-      use(u, whole);
     }
+  };
+  auto use_all = [&](int u0, Unit(&us)[U]) {
+#pragma unroll
+    for (int q = 0; q < U; ++q) {
+      if (u0 + q * WAVES >= whole) break;
+      use(us[q], u0 + q * WAVES);
+    }
+  };
+  load(wave, xs);
+  if (staged) {
+    for (int t = threadIdx.x; t < (XS + WS) * units; t += WAVES * 64) {
+      const int r = t / units, unit = t - r * units;
+      scales[r * pitch + unit] = r < XS ? x_scale(r, unit) : w_scale(col0 + r - XS, unit);
+    }
+    __syncthreads();
+  }
+#pragma unroll 1
+  for (int u0 = wave; u0 < whole; u0 += 2 * STEP) {
+    load(u0 + STEP, ys);
+    use_all(u0, xs);
+    load(u0 + 2 * STEP, xs);
+    use_all(u0 + STEP, ys);
+  }
+  if (whole < units && whole % WAVES == wave) {     // the last, partly filled block
+    Unit u;
+    const int k0 = k_lo + whole * BK;
+#pragma unroll
+    for (int kk = 0; kk < 2; ++kk) {
+#pragma unroll
+      for (int c = 0; c < NB; ++c) u.w[c][kk] = load_guarded(wrow[c], k0 + (4 * kk + g) * V, k_hi);
+#pragma unroll
+      for (int b = 0; b < MB; ++b) u.x[b][kk] = load_guarded(arow[b], k0 + (4 * kk + g) * V, k_hi);
+    }
+    use(u, whole);
+  }
 
-    // sum over the waves, then 8 columns per thread
-    __syncthreads();
+  // sum over the waves, then 8 columns per thread
+  __syncthreads();
 #pragma unroll
-    for (int b = 0; b < MB; ++b)
+  for (int b = 0; b < MB; ++b)
 #pragma unroll
-      for (int c = 0; c < NB; ++c)
-        *reinterpret_cast<f32x4*>(red + ((wave * MB + b) * 16 + i) * RED_LD + 16 * c + 4 * g) =
-            acc[b][c];
-    __syncthreads();
-    for (int t = threadIdx.x; t < MB * 16 * (BN / 8); t += WAVES * 64) {
-      const int row = t / (BN / 8), n = col0 + (t % (BN / 8)) * 8, m = m0 + row;
-      if (m < a.M && n < a.N) {
-        float v[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+    for (int c = 0; c < NB; ++c)
+      *reinterpret_cast<f32x4*>(red + ((wave * MB + b) * 16 + i) * RED_LD + 16 * c + 4 * g) =
+          acc[b][c];
+  __syncthreads();
+  for (int t = threadIdx.x; t < MB * 16 * (BN / 8); t += WAVES * 64) {
+    const int m = t / (BN / 8), n = col0 + (t % (BN / 8)) * 8;
+    if (m < a.M && n < a.N) {
+      float v[8] = {0, 0, 0, 0, 0, 0, 0, 0};
 #pragma unroll
-        for (int w = 0; w < WAVES; ++w) {
-          const float* from = red + (w * MB * 16 + row) * RED_LD + (t % (BN / 8)) * 8;
+      for (int w = 0; w < WAVES; ++w) {
+        const float* from = red + (w * MB * 16 + m) * RED_LD + (t % (BN / 8)) * 8;
 #pragma unroll
-          for (int j = 0; j < 8; ++j) v[j] += from[j];
-        }
-        finish8_any<WIDE>(args, m, n, v, blockIdx.y);
+        for (int j = 0; j < 8; ++j) v[j] += from[j];
       }
+      finish8_any<WIDE>(args, m, n, v, blockIdx.y);
     }
-    __syncthreads();   // before the next row block reuses the LDS
   }
 }
 

@@ -401,7 +401,7 @@ __global__ __launch_bounds__(WGM* WGN * 64) void pair_tile_kernel(const PairArgs
   }
 }
 
-// Few rows: up to 16 MB of them against both weights, bound by reading those once.  A
+// Few rows: M of at most 16 MB (few_plan) against both weights, bound by reading those once.  A
 // workgroup takes 8 NB columns of each (NB / 2 blocks of 16 of either); see
 // prod_rows_kernel, which it follows.  One row, 4096 to 8192, bf16: 25.5 us (134 MB of
 // weights: 5.3 TB/s, where a copy reaches 5.0).
@@ -449,139 +449,135 @@ __global__ __launch_bounds__(WAVES * 64) void gate_rows_kernel(const PairArgs ar
     }
   }
 
-  for (int m0 = 0; m0 < a.M; m0 += 16 * MB) {
-    const T* arow[MB];
+  const T* arow[MB];
 #pragma unroll
-    for (int b = 0; b < MB; ++b) {
-      const int m = m0 + 16 * b + i;
-      arow[b] = static_cast<const T*>(a.A) + (long long)(m < a.M ? m : a.M - 1) * a.lda;
-    }
-    f32x4 acc[MB][NB];
+  for (int b = 0; b < MB; ++b) {
+    const int m = 16 * b + i;
+    arow[b] = static_cast<const T*>(a.A) + (long long)(m < a.M ? m : a.M - 1) * a.lda;
+  }
+  f32x4 acc[MB][NB];
 #pragma unroll
-    for (int b = 0; b < MB; ++b)
+  for (int b = 0; b < MB; ++b)
 #pragma unroll
-      for (int c = 0; c < NB; ++c) acc[b][c] = f32x4{0, 0, 0, 0};
+    for (int c = 0; c < NB; ++c) acc[b][c] = f32x4{0, 0, 0, 0};
 
-    // multiply one unit's operands (outer order: through the wave's own LDS)
-    auto use = [&](u32x4(&rb)[BL], u32x4(&ra)[MB][2]) {
-      if constexpr (LB == kInner) {
+  // multiply one unit's operands (outer order: through the wave's own LDS)
+  auto use = [&](u32x4(&rb)[BL], u32x4(&ra)[MB][2]) {
+    if constexpr (LB == kInner) {
 #pragma unroll
-        for (int kk = 0; kk < 2; ++kk)
+      for (int kk = 0; kk < 2; ++kk)
 #pragma unroll
-          for (int c = 0; c < NB; ++c)
+        for (int c = 0; c < NB; ++c)
 #pragma unroll
-            for (int b = 0; b < MB; ++b)
-              acc[b][c] = Elem<T>::mfma(rb[2 * c + kk], ra[b][kk], acc[b][c]);
-      } else {
-        char* mine = lds + wave * BN * 128;
+          for (int b = 0; b < MB; ++b)
+            acc[b][c] = Elem<T>::mfma(rb[2 * c + kk], ra[b][kk], acc[b][c]);
+    } else {
+      char* mine = lds + wave * BN * 128;
 #pragma unroll
-        for (int j = 0; j < BL; ++j)
-          *reinterpret_cast<u32x4*>(mine + (j * 64 + lane) * 16) = rb[j];
-        __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
-        __builtin_amdgcn_wave_barrier();
+      for (int j = 0; j < BL; ++j)
+        *reinterpret_cast<u32x4*>(mine + (j * 64 + lane) * 16) = rb[j];
+      __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+      __builtin_amdgcn_wave_barrier();
 #pragma unroll
-        for (int kk = 0; kk < 2; ++kk)
+      for (int kk = 0; kk < 2; ++kk)
 #pragma unroll
-          for (int c = 0; c < NB; ++c) {
-            const u32x4 f = TB::frag(mine, 0, c, kk);
+        for (int c = 0; c < NB; ++c) {
+          const u32x4 f = TB::frag(mine, 0, c, kk);
 #pragma unroll
-            for (int b = 0; b < MB; ++b) acc[b][c] = Elem<T>::mfma(f, ra[b][kk], acc[b][c]);
-          }
-        __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
-        __builtin_amdgcn_wave_barrier();
-      }
-    };
-    constexpr int STEP = U * WAVES;
-    u32x4 xb[U][BL], xa[U][MB][2], yb[U][BL], ya[U][MB][2];
-    auto load = [&](int u0, u32x4(&rb)[U][BL], u32x4(&ra)[U][MB][2]) {
-#pragma unroll
-      for (int u = 0; u < U; ++u) {
-        const int unit = u0 + u * WAVES;
-        if (unit >= whole) break;
-        const int k0 = k_lo + unit * BK;
-#pragma unroll
-        for (int j = 0; j < BL; ++j) {
-          if constexpr (LB == kInner) rb[u][j] = load16(bptr[j >> 1] + k0 + (4 * (j & 1) + g) * V);
-          else rb[u][j] = load16(bptr[j] + (long long)k0 * a.ldb);
+          for (int b = 0; b < MB; ++b) acc[b][c] = Elem<T>::mfma(f, ra[b][kk], acc[b][c]);
         }
-#pragma unroll
-        for (int b = 0; b < MB; ++b)
-#pragma unroll
-          for (int kk = 0; kk < 2; ++kk) ra[u][b][kk] = load16(arow[b] + k0 + (4 * kk + g) * V);
-      }
-    };
-    auto use_all = [&](int u0, u32x4(&rb)[U][BL], u32x4(&ra)[U][MB][2]) {
-#pragma unroll
-      for (int u = 0; u < U; ++u) {
-        if (u0 + u * WAVES >= whole) break;
-        use(rb[u], ra[u]);
-      }
-    };
-    load(wave, xb, xa);
-#pragma unroll 1
-    for (int u0 = wave; u0 < whole; u0 += 2 * STEP) {
-      load(u0 + STEP, yb, ya);
-      use_all(u0, xb, xa);
-      load(u0 + 2 * STEP, xb, xa);
-      use_all(u0 + STEP, yb, ya);
+      __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+      __builtin_amdgcn_wave_barrier();
     }
-#pragma unroll 1
-    for (int unit = whole + wave; unit < units; unit += WAVES) {
-      const int k0 = k_lo + unit * BK;
-      u32x4 rb[BL], ra[MB][2];
+  };
+  constexpr int STEP = U * WAVES;
+  u32x4 xb[U][BL], xa[U][MB][2], yb[U][BL], ya[U][MB][2];
+  auto load = [&](int u0, u32x4(&rb)[U][BL], u32x4(&ra)[U][MB][2]) {
 #pragma unroll
-      for (int q = 0; q < BL; ++q) {
-        if constexpr (LB == kInner) {
-          rb[q] = load_guarded(bptr[q >> 1], k0 + (4 * (q & 1) + g) * V, k_hi);
-        } else {
-          int r, c;
-          TB::slot(q * 64 + lane, &r, &c);
-          const T* row = k0 + r < k_hi ? weight(c * V / 16) + (long long)(k0 + r) * a.ldb : nullptr;
-          rb[q] = load_guarded(row, column(c * V), a.N);
-        }
+    for (int u = 0; u < U; ++u) {
+      const int unit = u0 + u * WAVES;
+      if (unit >= whole) break;
+      const int k0 = k_lo + unit * BK;
+#pragma unroll
+      for (int j = 0; j < BL; ++j) {
+        if constexpr (LB == kInner) rb[u][j] = load16(bptr[j >> 1] + k0 + (4 * (j & 1) + g) * V);
+        else rb[u][j] = load16(bptr[j] + (long long)k0 * a.ldb);
       }
 #pragma unroll
       for (int b = 0; b < MB; ++b)
 #pragma unroll
-        for (int kk = 0; kk < 2; ++kk) ra[b][kk] = load_guarded(arow[b], k0 + (4 * kk + g) * V, k_hi);
-      use(rb, ra);
+        for (int kk = 0; kk < 2; ++kk) ra[u][b][kk] = load16(arow[b] + k0 + (4 * kk + g) * V);
     }
-
-    // sum over the waves, then 8 columns of both weights per thread
-    __syncthreads();
-    float* red = reinterpret_cast<float*>(lds);
+  };
+  auto use_all = [&](int u0, u32x4(&rb)[U][BL], u32x4(&ra)[U][MB][2]) {
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      if (u0 + u * WAVES >= whole) break;
+      use(rb[u], ra[u]);
+    }
+  };
+  load(wave, xb, xa);
+#pragma unroll 1
+  for (int u0 = wave; u0 < whole; u0 += 2 * STEP) {
+    load(u0 + STEP, yb, ya);
+    use_all(u0, xb, xa);
+    load(u0 + 2 * STEP, xb, xa);
+    use_all(u0 + STEP, yb, ya);
+  }
+#pragma unroll 1
+  for (int unit = whole + wave; unit < units; unit += WAVES) {
+    const int k0 = k_lo + unit * BK;
+    u32x4 rb[BL], ra[MB][2];
+#pragma unroll
+    for (int q = 0; q < BL; ++q) {
+      if constexpr (LB == kInner) {
+        rb[q] = load_guarded(bptr[q >> 1], k0 + (4 * (q & 1) + g) * V, k_hi);
+      } else {
+        int r, c;
+        TB::slot(q * 64 + lane, &r, &c);
+        const T* row = k0 + r < k_hi ? weight(c * V / 16) + (long long)(k0 + r) * a.ldb : nullptr;
+        rb[q] = load_guarded(row, column(c * V), a.N);
+      }
+    }
 #pragma unroll
     for (int b = 0; b < MB; ++b)
 #pragma unroll
-      for (int c = 0; c < NB; ++c)
-        *reinterpret_cast<f32x4*>(red + ((wave * MB + b) * 16 + i) * RED_LD + 16 * c + 4 * g) =
-            acc[b][c];
-    __syncthreads();
-    for (int t = threadIdx.x; t < MB * 16 * (COLS / 8); t += WAVES * 64) {
-      const int row = t / (COLS / 8), col = (t % (COLS / 8)) * 8;
-      const int m = m0 + row, n = col0 + col;
-      if (m < a.M && n < a.N) {
-        float v[8] = {0, 0, 0, 0, 0, 0, 0, 0}, u[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+      for (int kk = 0; kk < 2; ++kk) ra[b][kk] = load_guarded(arow[b], k0 + (4 * kk + g) * V, k_hi);
+    use(rb, ra);
+  }
+
+  // sum over the waves, then 8 columns of both weights per thread
+  __syncthreads();
+  float* red = reinterpret_cast<float*>(lds);
 #pragma unroll
-        for (int w = 0; w < WAVES; ++w) {
-          const float* from = red + (w * MB * 16 + row) * RED_LD + col;
+  for (int b = 0; b < MB; ++b)
 #pragma unroll
-          for (int j = 0; j < 8; ++j) {
-            v[j] += from[j];
-            u[j] += from[COLS + j];
-          }
-        }
-        if (a.splits > 1) {
-          put_partial(a, blockIdx.y, 0, m, n, v);
-          put_partial(a, blockIdx.y, 1, m, n, u);
-        } else {
-          float bg[8], bu[8];
-          gate_bias<T>(args, n, bg, bu);
-          finish_gate<T>(args, m, n, v, u, bg, bu);
+    for (int c = 0; c < NB; ++c)
+      *reinterpret_cast<f32x4*>(red + ((wave * MB + b) * 16 + i) * RED_LD + 16 * c + 4 * g) =
+          acc[b][c];
+  __syncthreads();
+  for (int t = threadIdx.x; t < MB * 16 * (COLS / 8); t += WAVES * 64) {
+    const int m = t / (COLS / 8), col = (t % (COLS / 8)) * 8, n = col0 + col;
+    if (m < a.M && n < a.N) {
+      float v[8] = {0, 0, 0, 0, 0, 0, 0, 0}, u[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+#pragma unroll
+      for (int w = 0; w < WAVES; ++w) {
+        const float* from = red + (w * MB * 16 + m) * RED_LD + col;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          v[j] += from[j];
+          u[j] += from[COLS + j];
         }
       }
+      if (a.splits > 1) {
+        put_partial(a, blockIdx.y, 0, m, n, v);
+        put_partial(a, blockIdx.y, 1, m, n, u);
+      } else {
+        float bg[8], bu[8];
+        gate_bias<T>(args, n, bg, bu);
+        finish_gate<T>(args, m, n, v, u, bg, bu);
+      }
     }
-    __syncthreads();   // before the next row block reuses the LDS
   }
 }
 
