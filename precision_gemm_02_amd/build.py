@@ -40,13 +40,13 @@ CFLAGS = [
 ]
 
 
-def _digest(folder: str, header: str, extra_flags) -> str:
+def _digest(folders, headers, extra_flags) -> str:
     import hashlib
     h = hashlib.sha256()
     h.update(" ".join([ARCH, *[f for f in CFLAGS if not f.startswith("-I")],
                        *extra_flags]).encode())
-    files = sorted(os.path.join(folder, f) for f in os.listdir(folder))
-    files.append(os.path.join(INCLUDE, header))
+    files = [p for folder in folders for p in sorted(os.path.join(folder, f) for f in os.listdir(folder))]
+    files += [os.path.join(INCLUDE, h) for h in headers]
     for path in files:
         h.update(os.path.basename(path).encode() + b"\0")
         with open(path, "rb") as f:
@@ -61,17 +61,18 @@ def source_digest(extra_flags=()) -> str:
     pgemm.h (the layer operators are compiled apart, from layers/).  Unlike a
     hash of libpgemm.so it does not depend on the directory the library is built
     in (hipcc derives per-file symbols from the path)."""
-    return _digest(CSRC, "pgemm.h", extra_flags)
+    return _digest([CSRC], ["pgemm.h"], extra_flags)
 
 
 def layer_digest(extra_flags=()) -> str:
     """The same of the layer operators: layers/ and pgemm_layers.h."""
-    return _digest(LAYERS, "pgemm_layers.h", extra_flags)
+    return _digest([LAYERS], ["pgemm_layers.h"], extra_flags)
 
 
 def block_digest(extra_flags=()) -> str:
-    """The same of the block operators: blocks/ and pgemm_blocks.h."""
-    return _digest(BLOCKS, "pgemm_blocks.h", extra_flags)
+    """The same of the block operators, which are built on the layer operators' sources:
+    blocks/, layers/ and both headers."""
+    return _digest([BLOCKS, LAYERS], ["pgemm_blocks.h", "pgemm_layers.h"], extra_flags)
 
 
 def _compile(src: str, extra) -> str:
