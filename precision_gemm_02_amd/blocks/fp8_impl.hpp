@@ -4,7 +4,6 @@
 
 #include "../layers/launch.hpp"
 #include "fp8.hpp"
-#include "launch.hpp"
 #include "ops.hpp"
 #include "whole8.hpp"
 

@@ -3,7 +3,6 @@
 #pragma once
 
 #include "../layers/launch.hpp"
-#include "launch.hpp"
 #include "ops.hpp"
 #include "whole.hpp"
 

@@ -1,11 +1,13 @@
 // Layer norm's launches, for each type.
-#include "launch.hpp"
+#include "../layers/launch.hpp"
 #include "ops.hpp"
 #include "pgemm_layers.h"
 
 namespace pgemm {
 namespace blocks {
 namespace {
+
+using layers::launch;
 
 // Workgroups of up to 1024 threads in one launch; more rows take several (a launch
 // has less than 2^32 threads).

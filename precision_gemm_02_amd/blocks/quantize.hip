@@ -1,11 +1,13 @@
 // The launches of the quantization, for each type.
-#include "launch.hpp"
+#include "../layers/launch.hpp"
 #include "ops.hpp"
 #include "pgemm_layers.h"
 
 namespace pgemm {
 namespace blocks {
 namespace {
+
+using layers::launch;
 
 // Workgroups of one launch (which has less than 2^32 threads).
 constexpr long long kMost = 1 << 22;

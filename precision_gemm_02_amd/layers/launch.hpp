@@ -11,6 +11,14 @@
 namespace pgemm {
 namespace layers {
 
+// A kernel's launch, its arguments in one struct.
+template <typename A>
+hipError_t launch(void (*kernel)(const A), dim3 grid, int threads, const A& a, hipStream_t s) {
+  A copy = a;
+  void* args[] = {&copy};
+  return hipLaunchKernel(reinterpret_cast<const void*>(kernel), grid, dim3(threads), args, 0, s);
+}
+
 // The tile classes and the few-rows kernels of the products.
 enum Kernel {
   kTile256 = 0,

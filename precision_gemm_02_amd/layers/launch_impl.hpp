@@ -9,13 +9,6 @@ namespace pgemm {
 namespace layers {
 namespace {
 
-template <typename A>
-hipError_t launch(void (*kernel)(const A), dim3 grid, int threads, const A& a, hipStream_t s) {
-  A copy = a;
-  void* args[] = {&copy};
-  return hipLaunchKernel(reinterpret_cast<const void*>(kernel), grid, dim3(threads), args, 0, s);
-}
-
 inline dim3 grid_of(const ProdArgs& a, int mode, int kernel) {
   const ProdGrid g = prod_grid(a, mode, kernel);
   return dim3((unsigned)g.x, (unsigned)g.y);

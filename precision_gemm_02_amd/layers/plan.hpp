@@ -226,11 +226,10 @@ inline Plan plan_product(int size, int la, int mode, long long rows, int groups,
 }
 
 // Workspace that plan_product may use for a product, over any alignment.
-inline size_t split_bytes(int size, int la, int mode, long long rows, int groups, int n, int k,
-                          bool may_few = true) {
+inline size_t split_bytes(int size, int la, int mode, long long rows, int groups, int n, int k) {
   size_t most = 0;
   for (const int loading : {kThrough, kDirect}) {
-    const Plan p = plan_product(size, la, mode, rows, groups, n, k, loading, 0, true, true, may_few);
+    const Plan p = plan_product(size, la, mode, rows, groups, n, k, loading, 0, true);
     const size_t b = split_space(p, mode, rows, groups, n);
     if (b > most) most = b;
   }
