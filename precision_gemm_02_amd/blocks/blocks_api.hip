@@ -91,15 +91,26 @@ const ClassTimes* pair_times(int size, int loading) {
   static const ClassTimes any32 = {{{150e12, 2.9e-6, 1, {0, 0, 0, 0}},
                                     {160e12, 5.3e-6, 2, {0, 0.89, 0, 0}},
                                     {155e12, 5.2e-6, 4, {0, 0.965, 0.994, 0.994}}}, 4.3e-6, 5.9e12};
+  return size == 4 ? &any32 : loading == kDirect ? &whole16 : &through16;
+}
+
+// The 8-bit tile kernels' times (whole8 and wide8 fitted so too).  wide8, of fp32 results, serves 16-bit results of rows that are
+// not whole chunks too: of 10 shapes with either kind of scales the choice took 1.00 to 1.05
+// times the best class's time.  Of such rows with fp32 results it took up to 1.79 times
+// (8191 x 8192 x 4095 in tiles of 128 2130 us, of 64 1255; 4096^2 x 4095 534 and 320; 2000 x 2048 x
+// 4095 137 and 84), hence odd32.
+const ClassTimes* times8(bool direct, bool wide) {
   static const ClassTimes whole8 = {{{2.77e15, 12.2e-6, 1, {0, 0, 0, 0}},
                                      {2.19e15, 8.7e-6, 2, {0, 0.92, 0, 0}},
                                      {1.39e15, 6.6e-6, 4, {0, 0.84, 0.84, 1.0}}}, 3.8e-6, 8.5e12};
-  static const ClassTimes wide8 = {{{0, 0, 1, {0, 0, 0, 0}},            // (nor have these)
+  static const ClassTimes wide8 = {{{0, 0, 1, {0, 0, 0, 0}},            // (have no largest tiles)
                                     {1.20e15, 9.5e-6, 2, {0, 0.70, 0, 0}},
                                     {0.81e15, 7.5e-6, 4, {0, 0.92, 0.92, 0.98}}}, 2e-6, 7.6e12};
-  if (size == 4) return &any32;
-  if (size == 2) return loading == kDirect ? &whole16 : &through16;
-  return loading == kDirect ? &whole8 : &wide8;
+  static const ClassTimes odd32 = {{{0, 0, 1, {0, 0, 0, 0}},
+                                    {0.26e15, 2e-6, 2, {0, 0.99, 0, 0}},
+                                    {0.46e15, 6e-6, 4, {0, 0.45, 0.67, 0.9}}}, 2e-6, 7.6e12};
+  if (!direct && wide) return &odd32;
+  return direct && !wide ? &whole8 : &wide8;
 }
 
 // A plan that takes none of the layer operators' kernels.
@@ -116,12 +127,15 @@ Plan gate_plan(int size, int m, int n, int k, int loading, size_t ws_bytes, bool
   return plan_pair(size, kInner, m, 2 * n, k, loading, ws_bytes, any_ws);
 }
 
-// The plan of a product in 8 bits (kThrough: no tiles of 256 x 256).
+// The plan of a product in 8 bits, of rows in whole chunks (direct) and with fp32 results (wide) or
+// not; only the first with 16-bit results have tiles of 256 x 256.
 constexpr int kFewWide8 = 32;                     // columns of its wide few-rows kernels
-Plan plan8(int m, int n, int k, int loading, size_t ws_bytes, bool any_ws) {
+Plan plan8(int m, int n, int k, bool direct, bool wide, size_t ws_bytes, bool any_ws) {
+  const int loading = direct && !wide ? kDirect : kThrough;
   const Plan p = few_plan(1, m, n, kFewWide8, n, k, loading, ws_bytes, any_ws);
   if (p.kernel >= 0) return p;
-  return plan_pair(1, kInner, m, n, k, loading, ws_bytes, any_ws);
+  return plan_product(1, kInner, kDense, m, 1, n, k, loading, ws_bytes, any_ws, true, false,
+                      times8(direct, wide));
 }
 
 int pair_loading(const pgemm_gate_weights& w, int size, int inner) {
@@ -499,8 +513,7 @@ int pgemm_linear_fp8(pgemm_fp8_kind kind, int m, int n, int k, pgemm_rows X, pge
   const bool direct = operand_loading(X.data, X.ld, 1, k, 0) == kDirect &&
                       operand_loading(W.data, W.ld, 1, k, 0) == kDirect;
   const bool wide = kind.out_dtype == PGEMM_F32;
-  const Plan plan = plan8(m, n, k, direct && !wide ? kDirect : kThrough,
-                          workspace == nullptr ? 0 : workspace_bytes, false);
+  const Plan plan = plan8(m, n, k, direct, wide, workspace == nullptr ? 0 : workspace_bytes, false);
   if (plan.kernel < 0) return -2;
   a.splits = plan.splits;
   a.k_split = plan.k_split;
@@ -519,10 +532,11 @@ int pgemm_linear_fp8(pgemm_fp8_kind kind, int m, int n, int k, pgemm_rows X, pge
 size_t pgemm_linear_fp8_workspace(int m, int n, int k) {
   if (m <= 0 || n <= 0 || k <= 0) return 0;
   size_t most = 0;
-  for (const int loading : {kThrough, kDirect}) {
-    const size_t b = split_space(plan8(m, n, k, loading, 0, true), kDense, m, 1, n);
-    if (b > most) most = b;
-  }
+  for (const bool direct : {false, true})
+    for (const bool wide : {false, true}) {
+      const size_t b = split_space(plan8(m, n, k, direct, wide, 0, true), kDense, m, 1, n);
+      if (b > most) most = b;
+    }
   return most;
 }
 

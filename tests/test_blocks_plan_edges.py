@@ -97,3 +97,15 @@ def test_kernels_of_few_rows(lib, m):
                 assert got[0].kernel == FEW[top] and got[0].splits == -(-k // got[0].k_split) > 1
                 got = fp8(n, k, out, False)
                 assert got[0].kernel == FEW[top] and got[0].splits == 1
+
+
+def test_8_bit_products_of_odd_rows_with_fp32_results(lib):
+    """Through registers and with fp32 results the small tiles are the faster ones."""
+    one = Scales(1 << 20, 1, 1, 1)
+    for m, n, k in ((2000, 2048, 4095), (4096, 4096, 4095), (8191, 8192, 4095)):
+        for ld, out, want in ((k, 0, 2), (k + 1, 0, 1), (k, 2, 1)):
+            need = lib.pgemm_linear_fp8_workspace(m, n, k)
+            assert lib.pgemm_linear_fp8(Kind8(0, 0, out, 0), m, n, ld if ld % 16 == 0 else k, rows(ld), one, rows(ld),
+                                        one, None, Rows(None, 1), Rows(None, 1), rows(n), 1 << 20, need, None) == 0
+            got = lib.launched()
+            assert got[0].kernel == want and got[0].partial <= need, (m, n, k, ld, out)
