@@ -209,6 +209,10 @@ int gate_chunks(int rows, int half) {
 // and 22.8; 128 of 2047 x 2047 25.8, 25.2 and 51, 39; 300 of 1001 x 1000 18.3, 11.4 and 38, 24;
 // 4000 of 2047 x 2047 113, 69), n x k weights least (512 of 2047 x 2047 23.4, 27.4 and 81, 79;
 // 2000 of 1001 x 1001 21.1, 23.9; 1000 of 2047 x 2047 34.7, 29.6 and 142, 138; 4000 105, 68).
+// The rule for k x n weights goes by the rows alone.  From about 500 x 500 on the copies win (128 rows
+// of 501 x 501 11.6, 10.2 and 21.4, 15.8); in smaller ones they are a launch too many (130 rows of
+// 129 x 64 4.5, 9.6 and 8.1, 9.0; 130 to 8000 rows of 33 x 33 8.3, 9.9 in either; 1000 of 257 x 257
+// 8.8, 10.1 and 14.4, 12.9): there a call without the workspace is the faster one.
 struct GateCopies {
   size_t x = 0, w = 0;
   size_t total() const { return x + 2 * w; }

@@ -142,9 +142,11 @@ __device__ __forceinline__ void finish8_any(const Prod8Args& args, long long m, 
 // the tile after next may be in flight).
 //
 // A block's sums are scaled and added while the matrix cores run the next
-// block's, so that neither waits for the other.  fp32 results of 4096^3 take 143 us
-// (0.96 PFLOP/s of the 16-bit instructions' 2.5, with widening in the vector units), 16-bit
-// ones prod8_whole_kernel's 66.
+// block's, so that neither waits for the other.  fp32 results of 4096^3 take 143 to 155 us
+// (0.9 to 0.96 PFLOP/s of the 16-bit instructions' 2.5, with widening in the vector units),
+// 16-bit ones prod8_whole_kernel's 66.  Rows that are not whole chunks (DIRECT false) are loaded
+// through guards and stored at once, a memory latency a tile: 8191 x 8192 x 4095 948 us, fp32
+// results 1255; 1000 x 1000 x 1001 14.7 and 16.5, where k = 1008 takes 9.0 and 9.3.
 template <int FA, int FB, int BM, int BN, int WGM, int WGN, bool DIRECT, bool COLS, bool WIDE>
 __global__ __launch_bounds__(WGM* WGN * 64) void prod8_tile_kernel(const Prod8Args args) {
   const ProdArgs& a = args.p;
@@ -373,8 +375,10 @@ __global__ __launch_bounds__(WGM* WGN * 64) void prod8_tile_kernel(const Prod8Ar
 // instruction's registers, each adding into its own sums, which are added over
 // the waves through LDS in a fixed order.  The scales of all its blocks are read
 // once into LDS, under the first blocks' loads (one by one, each row's would be a
-// cache line for itself), where they fit.  16 x 4096 x 4096 8.4 us (17 MB of W: 2 TB/s; a
-// launch alone takes 6).
+// cache line for itself), where they fit.  16 x 4096 x 4096 8.7 us back to back, 8.0 in a trace
+// (17 MB of W: 2 TB/s; there a launch of one workgroup over a row takes 2.7, the bf16 product
+// of these sizes 11.2): latency, since a wave's second blocks are asked for behind the
+// barrier of the scales, and each workgroup reads X as well, as many bytes as its part of W.
 template <int FA, int FB, int MB, int NB, int WAVES, bool COLS, bool WIDE>
 __global__ __launch_bounds__(WAVES * 64) void prod8_rows_kernel(const Prod8Args args) {
   const ProdArgs& a = args.p;

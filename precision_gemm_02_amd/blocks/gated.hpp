@@ -403,8 +403,9 @@ __global__ __launch_bounds__(WGM* WGN * 64) void pair_tile_kernel(const PairArgs
 
 // Few rows: M of at most 16 MB (few_plan) against both weights, bound by reading those once.  A
 // workgroup takes 8 NB columns of each (NB / 2 blocks of 16 of either); see
-// prod_rows_kernel, which it follows.  One row, 4096 to 8192, bf16: 25.5 us (134 MB of
-// weights: 5.3 TB/s, where a copy reaches 5.0).
+// prod_rows_kernel, which it follows.  One row, 4096 to 8192, bf16: 24.9 us (134 MB of
+// weights: 5.4 TB/s, part of it from the last-level cache; three pairs of weights in turn,
+// which that cache does not hold, 28.9 us and 4.6, where a copy reaches 5.0).
 template <typename T, int LB, int MB, int NB, int WAVES>
 __global__ __launch_bounds__(WAVES * 64) void gate_rows_kernel(const PairArgs args) {
   const ProdArgs& a = args.p;

@@ -214,8 +214,10 @@ __global__ __launch_bounds__(1024) void norm_long_kernel(const NormArgs a) {
 // group, each thread adds its columns in order; the groups of one workgroup
 // are then added in order through LDS.  The next row is asked for before the sums
 // of this one, where the registers hold both; rows are kept as they are stored (16-bit
-// ones in half the registers).  Rows over 8192 take the column sums apart: with them
-// 75 to 135 registers were spilled (4096 rows of 16384, bf16: 190 us).
+// ones in half the registers).  Rows over 8192 take the column sums apart, in a second pass over
+// X and dY (4096 rows of 16384, bf16: 139 us for a floor of 80): with the sums in registers 75
+// to 135 of them were spilled (190 us).  Sums in LDS, 128 KB of them for 16384 features, have
+// not been tried.
 template <typename T, int TPR, int C, int NT, bool SUMS>
 __global__ __launch_bounds__(NT) void norm_back_kernel(const NormBackArgs a) {
   constexpr int ROWS = NT / TPR;

@@ -15,8 +15,8 @@
 // in turn, so that every LDS address is a constant.
 //
 // Bound by the matrix cores at the power-limited clock: 8192 x 8192 x 4096 bf16 with both Z
-// 800 us (1.37 PFLOP/s), where a library product of 8192 x 16384 x 4096 without an epilogue
-// takes 719; of 8192 x 4096 x 4096 dX 381 and both dW 381 (1.44).  With 16384 summed indices the loops are
+// 800 to 824 us by the card (1.33 to 1.37 PFLOP/s), where a library product of 8192 x 16384 x
+// 4096 without an epilogue takes 719; of 8192 x 4096 x 4096 dX 381 and both dW 381 (1.44).  With 16384 summed indices the loops are
 // level; what is left is each tile's prologue and epilogue.  Tried and slower: four waves of
 // 128 x 128 (843 us against 797 then), one barrier a tile, B's reads earlier.
 #pragma once

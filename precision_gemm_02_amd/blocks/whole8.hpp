@@ -2,8 +2,9 @@
 // 16-bit results: prod8_tile_kernel with its loads through buffer descriptors, as
 // pair_whole_kernel has them.
 //
-// 8192 x 8192 x 4096 262 us (2.1 PFLOP/s), 315 with a scale for each column of W; of zeros,
-// which need little power, 227.  LDS, the vector units and the matrix cores share a tile's
+// 8192 x 8192 x 4096 over the same operands again and again 252 to 262 us (2.1 PFLOP/s; others in
+// turn, with an epilogue 272 to 287 by the card), 313 with a scale for each column of W; of
+// zeros, which need little power, 227.  LDS, the vector units and the matrix cores share a tile's
 // time: with a quarter of A's LDS reads 218 us, with a quarter of the multiply-adds 244.  A
 // wave's tile of 128 x 64 reads 24 KB for its 32 matrix instructions, and a larger one does
 // not fit the registers, since the sums that the vector units add to cannot lie in the

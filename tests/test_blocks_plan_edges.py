@@ -2,8 +2,8 @@
 test_blocks_plans.py, whose recording library this uses)."""
 import pytest
 
-from test_blocks_plans import (APART, FP8, LAYER, NORM_COLUMNS, PAIR, PAD, SLOPE, TOP, Biases, Kind, Kind8,
-                               Pairs, Rows, Scales, Weight, Weights, lib, pair_of, rows)  # noqa: F401
+from test_blocks_plans import (FP8, NORM_COLUMNS, PAIR, SLOPE, TOP, Biases, Kind, Kind8, Pairs, Rows,
+                               Scales, Weight, Weights, lib, pair_of, rows)  # noqa: F401
 
 
 @pytest.mark.parametrize("m,n", [(1, 1), (16, 16), (17, 64), (32, 9000), (33, 64), (200, 200)])
