@@ -94,11 +94,11 @@ const ClassTimes* pair_times(int size, int loading) {
   return size == 4 ? &any32 : loading == kDirect ? &whole16 : &through16;
 }
 
-// The 8-bit tile kernels' times (whole8 and wide8 fitted so too).  wide8, of fp32 results, serves 16-bit results of rows that are
-// not whole chunks too: of 10 shapes with either kind of scales the choice took 1.00 to 1.05
-// times the best class's time.  Of such rows with fp32 results it took up to 1.79 times
-// (8191 x 8192 x 4095 in tiles of 128 2130 us, of 64 1255; 4096^2 x 4095 534 and 320; 2000 x 2048 x
-// 4095 137 and 84), hence odd32.
+// The 8-bit tile kernels' times (whole8 and wide8 fitted so too).  wide8, of fp32 results,
+// serves 16-bit results of rows that are not whole chunks too: of 10 shapes with either kind of
+// scales the choice took 1.00 to 1.07 times the best class's time.  Of such rows with fp32
+// results it took up to 1.79 times (8191 x 8192 x 4095 in tiles of 128 2130 us, of 64 1255;
+// 4096^2 x 4095 534 and 320; 2000 x 2048 x 4095 137 and 84), hence odd32.
 const ClassTimes* times8(bool direct, bool wide) {
   static const ClassTimes whole8 = {{{2.77e15, 12.2e-6, 1, {0, 0, 0, 0}},
                                      {2.19e15, 8.7e-6, 2, {0, 0.92, 0, 0}},
@@ -127,8 +127,8 @@ Plan gate_plan(int size, int m, int n, int k, int loading, size_t ws_bytes, bool
   return plan_pair(size, kInner, m, 2 * n, k, loading, ws_bytes, any_ws);
 }
 
-// The plan of a product in 8 bits, of rows in whole chunks (direct) and with fp32 results (wide) or
-// not; only the first with 16-bit results have tiles of 256 x 256.
+// The plan of a product in 8 bits, of rows in whole chunks (direct) or not, with fp32 results
+// (wide) or 16-bit ones; only 16-bit results of whole chunks have tiles of 256 x 256.
 constexpr int kFewWide8 = 32;                     // columns of its wide few-rows kernels
 Plan plan8(int m, int n, int k, bool direct, bool wide, size_t ws_bytes, bool any_ws) {
   const int loading = direct && !wide ? kDirect : kThrough;
@@ -209,10 +209,10 @@ int gate_chunks(int rows, int half) {
 // and 22.8; 128 of 2047 x 2047 25.8, 25.2 and 51, 39; 300 of 1001 x 1000 18.3, 11.4 and 38, 24;
 // 4000 of 2047 x 2047 113, 69), n x k weights least (512 of 2047 x 2047 23.4, 27.4 and 81, 79;
 // 2000 of 1001 x 1001 21.1, 23.9; 1000 of 2047 x 2047 34.7, 29.6 and 142, 138; 4000 105, 68).
-// The rule for k x n weights goes by the rows alone.  From about 500 x 500 on the copies win (128 rows
-// of 501 x 501 11.6, 10.2 and 21.4, 15.8); in smaller ones they are a launch too many (130 rows of
-// 129 x 64 4.5, 9.6 and 8.1, 9.0; 130 to 8000 rows of 33 x 33 8.3, 9.9 in either; 1000 of 257 x 257
-// 8.8, 10.1 and 14.4, 12.9): there a call without the workspace is the faster one.
+// The rule for k x n weights goes by the rows alone.  From about 500 x 500 on the copies win (128
+// rows of 501 x 501 11.6, 10.2 and 21.4, 15.8); in smaller ones they are a launch too many (130
+// rows of 129 x 64 4.5, 9.6 and 8.1, 9.0; 130 to 8000 rows of 33 x 33 8.3, 9.9 in either; 1000
+// of 257 x 257 8.8, 10.1 and 14.4, 12.9): there a call without the workspace is faster.
 struct GateCopies {
   size_t x = 0, w = 0;
   size_t total() const { return x + 2 * w; }
